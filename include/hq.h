@@ -297,6 +297,99 @@ int hq_srft_encode(const void *x, int32_t dtype, uint64_t n, uint64_t seed, cons
 int hq_srft_decode(const void *codes, const void *scales, uint64_t n, uint64_t seed, const float *lambda,
                    int32_t bits, void *out, int32_t out_dtype, hq_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The paged SRFT cache of one layer: the SRFT codec's codes and scales, kept by page so that a serving
+ * loop can append tokens, attend over the codes, and evict tokens.
+ *
+ * data: DEVICE, [pages][heads][page bytes], 16-byte aligned.  A page holds `page` tokens (a power of two,
+ * 16 to 4096) of one KV head, 128 values each.  With E = `bits` (4 or 8) bytes for a group's 8 codes:
+ *   K codes [page][16][E] | K scales [page][16] binary16 |
+ *   V codes [page/4][16][4][E] | V scales [page/4][16][4] binary16
+ * (values lie in blocks of four tokens, group by group), in all page * 2 * (16 E + 32) bytes.  Codes,
+ * scales and the treatment of non-finite vectors are those of hq_srft_encode with the same seed and
+ * lambda (lambda_k for keys, lambda_v for values; HOST, 128 binary32 values or NULL for ones).
+ * A slot is page * P + offset.  Token t of sequence b is slot offset t mod P of page
+ * table[b * table_width + t / P]; a table entry outside [0, pages) is an absent page, whose tokens take
+ * no part.  All calls below are asynchronous on `stream`, allocate nothing and may be captured. */
+typedef struct {
+  void *data;
+  uint32_t pages, heads, page;
+  int32_t bits;
+  uint64_t seed;
+  const float *lambda_k, *lambda_v;
+} hq_kv_cache;
+
+/* Encodes the K and V vectors of `tokens` tokens into their slots.  k, v: DEVICE, value c of head h of
+ * token i at k[i strides[0] + h strides[1] + c] and v[i strides[2] + h strides[3] + c] (strides in
+ * values; 16-byte aligned rows are read fastest).  slots: DEVICE, int64; a slot outside [0, pages * page)
+ * writes nothing; the slots of one call must differ.  Codes and scales equal hq_srft_encode's.
+ * HQ_ERR_INVALID_ARG: null or misaligned pointers, a bad cache, dtype or lambda, over 2^31 tokens. */
+int hq_kv_append(const hq_kv_cache *cache, const void *k, const void *v, int32_t dtype, uint64_t tokens,
+                 const int64_t strides[4], const int64_t *slots, hq_stream_t stream);
+
+/* Decodes slots into k and v (DEVICE, [tokens][heads][128] of out_dtype, 16-byte aligned; one may be
+ * NULL), as hq_srft_decode does.  A slot outside the cache reads as zeros.  Errors as hq_kv_append. */
+int hq_kv_read(const hq_kv_cache *cache, const int64_t *slots, uint64_t tokens, void *k, void *v,
+               int32_t out_dtype, hq_stream_t stream);
+
+/* Softmax attention of queries over the cache.  Query i of a sequence's m queries stands at position
+ * n - m + i of its n = lens[b] cached tokens (its own token is cached first); it sees tokens up to its
+ * position (all tokens when causal == 0), and with window > 0 only the last `window` of those up to its
+ * position.  Scores are scale q.k, then softcap tanh(score / softcap) when softcap > 0; a row that sees
+ * nothing gives 0.  Query head j reads KV head j / (q_heads / heads).  Products and softmax statistics
+ * are binary32 sums of binary16 products (relative error about 2^-11 of a value; about 2^-20 of a score
+ * when weights are asked for). */
+typedef struct {
+  const void *q;            /* DEVICE, value c of head j of query i at q[i stride_token + j stride_head + c] */
+  void *out;                /* DEVICE, [total_q][q_heads][128], 16-byte aligned                              */
+  int32_t q_dtype, out_dtype;
+  int64_t q_stride_token, q_stride_head;
+  uint64_t total_q;
+  uint32_t q_heads;         /* a multiple of the cache's heads                                             */
+  uint32_t seqs;
+  uint32_t max_q;           /* most queries of a sequence; further ones are not computed                    */
+  uint32_t max_len;         /* most tokens of a sequence; a larger length counts as this                    */
+  const int32_t *q_start;   /* DEVICE, seqs + 1 query offsets; NULL: total_q / seqs queries each            */
+  const int32_t *table;     /* DEVICE, [seqs][table_width]                                                  */
+  uint32_t table_width;
+  const int32_t *lens;      /* DEVICE, [seqs]; a negative length counts as 0                                */
+  float scale, softcap;
+  int32_t causal;
+  uint32_t window;          /* 0: none                                                                      */
+  float *weights;           /* DEVICE or NULL: weights[(b heads + h) weights_stride + t] += the softmax
+                               weights of token t summed over the rows of KV head h, in a fixed order       */
+  uint64_t weights_stride;  /* at least max_len                                                             */
+} hq_kv_attend_args;
+
+/* Workspace bytes of hq_kv_attend for these sizes (host only; pointers are not read).  The workspace
+ * needs no initialisation, is 256-byte aligned, and serves one call in flight. */
+int hq_kv_attend_workspace_size(const hq_kv_cache *cache, const hq_kv_attend_args *args, size_t *bytes);
+
+/* HQ_ERR_INVALID_ARG: null or misaligned pointers, sizes outside their ranges, q_heads not a multiple of
+ * heads, q_start == NULL with total_q not a multiple of seqs, a scale or softcap that is not finite, a
+ * negative softcap, weights_stride < max_len, or a workspace that is too small. */
+int hq_kv_attend(const hq_kv_cache *cache, const hq_kv_attend_args *args, void *workspace,
+                 size_t workspace_bytes, hq_stream_t stream);
+
+/* Eviction by accumulated weight.  Of each (sequence, head)'s n tokens, m = min(n, budget) stay: the first
+ * `sink`, the last `recent`, and of the others those of most weight (ties to the lowest index; NaN counts
+ * least).  They move, in order, to tokens 0..m-1 of the pages of dst_table, which must not be pages that
+ * any table of the call reads; slots past m are not written. */
+typedef struct {
+  const int32_t *table;      /* DEVICE, [seqs][table_width]                                */
+  const int32_t *lens;       /* DEVICE, [seqs]                                             */
+  const float *weights;      /* DEVICE, as hq_kv_attend's                                  */
+  uint64_t weights_stride;
+  uint32_t seqs, table_width, max_len;
+  uint32_t budget, sink, recent;   /* sink + recent <= budget <= dst_width * page           */
+  const int32_t *dst_table;  /* DEVICE, [seqs][dst_width]                                  */
+  uint32_t dst_width;
+  int32_t *kept;             /* DEVICE, [seqs][heads][budget]: indices that stay, then -1  */
+  int32_t *new_lens;         /* DEVICE, [seqs]: m                                          */
+  float *new_weights;        /* DEVICE or NULL, [seqs][heads][budget]: their weights, then 0 */
+} hq_kv_evict_args;
+int hq_kv_evict(const hq_kv_cache *cache, const hq_kv_evict_args *args, hq_stream_t stream);
+
 /* Diagnostic front half of the encoder at a fixed step (components 1 and 2 of "Methodology: the
  * HyperQuant pipeline", with component 4's dither when params->dither is set; the integer codes
  * before component 3's stripping): per-value integer lattice codes (int32;

@@ -6,7 +6,8 @@ fallback: if the library is missing the calls raise.
 
 Entry points mirror the C ABI: ``hq_encode``, ``hq_decode``, ``hq_rate``, ``hq_codes``,
 ``hq_status``, ``hq_fallbacks``, ``hq_workspace_size``, ``hq_stream_fixed_bytes``, ``hq_encode_bound``,
-``hq_version``, ``hq_strerror``.
+``hq_version``, ``hq_strerror``; the paged SRFT cache: ``hq_kv_cache``, ``hq_kv_append``, ``hq_kv_read``,
+``hq_kv_attend``, ``hq_kv_evict``.
 """
 from __future__ import annotations
 
@@ -25,7 +26,8 @@ LATTICES = {"z": HQ_Z, "d4": HQ_D4, "e8": HQ_E8, "a2": HQ_A2}
 EXPORTS = ("hq_version", "hq_strerror", "hq_workspace_size", "hq_stream_fixed_bytes", "hq_encode_bound", "hq_rate",
            "hq_encode", "hq_encode_noalloc", "hq_decode", "hq_status", "hq_fallbacks", "hq_codes",
            "hq_gemv_workspace_size", "hq_gemv",
-           "hq_haar_matrix", "hq_rotate", "hq_srft_encode", "hq_srft_decode")
+           "hq_haar_matrix", "hq_rotate", "hq_srft_encode", "hq_srft_decode",
+           "hq_kv_append", "hq_kv_read", "hq_kv_attend_workspace_size", "hq_kv_attend", "hq_kv_evict")
 
 
 class HqParams(ctypes.Structure):
@@ -41,6 +43,29 @@ class HqInfo(ctypes.Structure):
 
     def as_dict(self):
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class HqKvCache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_uint32), ("heads", ctypes.c_uint32),
+                ("page", ctypes.c_uint32), ("bits", ctypes.c_int32), ("seed", ctypes.c_uint64),
+                ("lambda_k", ctypes.c_void_p), ("lambda_v", ctypes.c_void_p)]
+
+
+class HqKvAttendArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("q_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("q_stride_token", ctypes.c_int64), ("q_stride_head", ctypes.c_int64), ("total_q", ctypes.c_uint64),
+                ("q_heads", ctypes.c_uint32), ("seqs", ctypes.c_uint32), ("max_q", ctypes.c_uint32), ("max_len", ctypes.c_uint32),
+                ("q_start", ctypes.c_void_p), ("table", ctypes.c_void_p), ("table_width", ctypes.c_uint32),
+                ("lens", ctypes.c_void_p), ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_uint32), ("weights", ctypes.c_void_p), ("weights_stride", ctypes.c_uint64)]
+
+
+class HqKvEvictArgs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("weights_stride", ctypes.c_uint64), ("seqs", ctypes.c_uint32), ("table_width", ctypes.c_uint32),
+                ("max_len", ctypes.c_uint32), ("budget", ctypes.c_uint32), ("sink", ctypes.c_uint32), ("recent", ctypes.c_uint32),
+                ("dst_table", ctypes.c_void_p), ("dst_width", ctypes.c_uint32), ("kept", ctypes.c_void_p),
+                ("new_lens", ctypes.c_void_p), ("new_weights", ctypes.c_void_p)]
 
 
 class HqError(RuntimeError):
@@ -79,6 +104,11 @@ def lib():
         L.hq_rotate.argtypes = [P, u64, P, i32, P, P]
         L.hq_srft_encode.argtypes = [P, i32, u64, u64, P, i32, P, P, P]
         L.hq_srft_decode.argtypes = [P, P, u64, u64, P, i32, P, i32, P]
+        L.hq_kv_append.argtypes = [P, P, P, i32, u64, P, P, P]
+        L.hq_kv_read.argtypes = [P, P, u64, P, P, i32, P]
+        L.hq_kv_attend_workspace_size.argtypes = [P, P, ctypes.POINTER(sz)]
+        L.hq_kv_attend.argtypes = [P, P, P, sz, P]
+        L.hq_kv_evict.argtypes = [P, P, P]
         for name in EXPORTS:
             getattr(L, name).restype = getattr(L, name).restype or ctypes.c_int
         _lib = L
@@ -338,6 +368,157 @@ def hq_srft_decode(codes, scales, n: int, seed: int = 0, bits: int = 4, lam=None
                                 int(seed), lp, int(bits), ctypes.c_void_p(out.data_ptr()), _dtype_code(out),
                                 _stream_handle(stream)), "hq_srft_decode")
     return out
+
+
+# ---- the paged SRFT cache ---------------------------------------------------------------------------
+
+def hq_kv_token_bytes(bits: int = 4) -> int:
+    """Bytes of one token of one head, K and V."""
+    return 2 * (16 * bits + 32)
+
+
+def hq_kv_cache(pages: int, heads: int, page: int = 64, bits: int = 4, device="cuda"):
+    """A layer's empty paged cache: uint8 [pages][heads][page bytes] (layout in include/hq.h)."""
+    torch = _torch()
+    if bits not in (4, 8) or page < 16 or page > 4096 or page & (page - 1):
+        raise ValueError("bits is 4 or 8, page a power of two from 16 to 4096")
+    return torch.zeros(pages, heads, page * hq_kv_token_bytes(bits), dtype=torch.uint8, device=device)
+
+
+def _cache_arg(cache, bits, seed, lam_k, lam_v):
+    """The C description of a cache tensor, and what has to outlive the call."""
+    torch = _torch()
+    if not (cache.is_cuda and cache.is_contiguous() and cache.dtype == torch.uint8 and cache.dim() == 3):
+        raise TypeError("cache must be a contiguous uint8 CUDA tensor [pages][heads][page bytes]")
+    if bits not in (4, 8):
+        raise ValueError("bits is 4 or 8")
+    pages, heads, size = cache.shape
+    page, rest = divmod(size, hq_kv_token_bytes(bits))
+    if rest:
+        raise ValueError("the cache's last dimension is not a whole number of tokens at these bits")
+    keep_k, pk = _host_lambda(lam_k)
+    keep_v, pv = _host_lambda(lam_v)
+    return HqKvCache(cache.data_ptr(), pages, heads, page, bits, seed, pk, pv), (keep_k, keep_v)
+
+
+def _check_tensor(t, name, dtype, shape, device):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _check_rows(t, name, heads, device):
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128 or (t.stride(2) != 1 and t.numel()) or t.device != device:
+        raise ValueError(f"{name} must be [tokens][{heads}][128] on {device}, its last dimension contiguous")
+
+
+def hq_kv_append(cache, k, v, slots, bits: int = 4, seed: int = 0, lam_k=None, lam_v=None, stream=None):
+    """Encode K and V of new tokens ([tokens][heads][128] bf16 or float32, any token and head strides) into
+    their slots (int64 [tokens]: page * P + offset; a slot outside the cache, -1 say, writes nothing)."""
+    torch = _torch()
+    c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
+    dev = cache.device
+    _check_rows(k, "k", c.heads, dev)
+    _check_rows(v, "v", c.heads, dev)
+    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have one type and length")
+    _check_tensor(slots, "slots", torch.int64, (k.shape[0],), dev)
+    strides = (ctypes.c_int64 * 4)(k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+    _check(lib().hq_kv_append(ctypes.byref(c), k.data_ptr(), v.data_ptr(), _dtype_code(k), k.shape[0], strides,
+                              slots.data_ptr(), _stream_handle(stream)), "hq_kv_append")
+    return cache
+
+
+def hq_kv_read(cache, slots, bits: int = 4, seed: int = 0, lam_k=None, lam_v=None, out_dtype=None, k=None, v=None,
+               stream=None):
+    """Decode slots (int64 [tokens]) into (k, v), each [tokens][heads][128] bf16 (default) or float32; a slot
+    outside the cache reads as zeros."""
+    torch = _torch()
+    c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
+    _check_tensor(slots, "slots", torch.int64, (slots.numel(),), cache.device)
+    shape, dt = (slots.numel(), c.heads, 128), out_dtype or torch.bfloat16
+    k = torch.empty(shape, dtype=dt, device=cache.device) if k is None else k
+    v = torch.empty(shape, dtype=dt, device=cache.device) if v is None else v
+    _check_tensor(k, "k", dt, shape, cache.device)
+    _check_tensor(v, "v", dt, shape, cache.device)
+    _check(lib().hq_kv_read(ctypes.byref(c), slots.data_ptr(), slots.numel(), k.data_ptr(), v.data_ptr(), _dtype_code(k),
+                            _stream_handle(stream)), "hq_kv_read")
+    return k, v
+
+
+def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, bits: int = 4, seed: int = 0, lam_k=None,
+                 lam_v=None, scale=None, causal: bool = True, window: int = 0, softcap: float = 0.0, weights=None, out=None,
+                 ws=None, stream=None):
+    """Softmax attention of q ([queries][q heads][128] bf16 or float32, any strides but the last) over the cache.
+
+    table int32 [seqs][width], lens int32 [seqs] (tokens cached, the queries' own among them); q_start int32
+    [seqs + 1] offsets of each sequence's queries (None: as many each); max_q, max_len bounds on a sequence's
+    queries and tokens (None: all queries, the table's width).  weights float32 [seqs][heads][>= max_len] gets each
+    token's softmax weights added.  Returns out ([queries][q heads][128], bf16 unless given)."""
+    torch = _torch()
+    c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
+    dev = cache.device
+    if q.dim() != 3 or q.shape[1] == 0 or q.shape[1] % c.heads:
+        raise ValueError("q must be [queries][q heads][128], q heads a multiple of the cache's heads")
+    _check_rows(q, "q", q.shape[1], dev)
+    total, heads = q.shape[0], q.shape[1]
+    seqs, width = lens.numel(), table.shape[-1]
+    _check_tensor(lens, "lens", torch.int32, (seqs,), dev)
+    _check_tensor(table, "table", torch.int32, (seqs, width), dev)
+    if q_start is not None:
+        _check_tensor(q_start, "q_start", torch.int32, (seqs + 1,), dev)
+    if max_q is None:
+        max_q = total if q_start is not None else total // max(seqs, 1)
+    if max_len is None:
+        max_len = width * c.page
+    if out is None:
+        out = torch.empty((total, heads, 128), dtype=torch.bfloat16, device=dev)
+    _check_tensor(out, "out", out.dtype, (total, heads, 128), dev)
+    stride = 0
+    if weights is not None:
+        if weights.dim() != 3:
+            raise ValueError("weights must be [seqs][heads][tokens]")
+        stride = weights.shape[2]
+        _check_tensor(weights, "weights", torch.float32, (seqs, c.heads, stride), dev)
+    a = HqKvAttendArgs(q.data_ptr(), out.data_ptr(), _dtype_code(q), _dtype_code(out), q.stride(0), q.stride(1), total, heads, seqs,
+                       max_q, max_len, q_start.data_ptr() if q_start is not None else None, table.data_ptr(), width,
+                       lens.data_ptr(), 128 ** -0.5 if scale is None else scale, softcap, 1 if causal else 0, window,
+                       weights.data_ptr() if weights is not None else None, stride)
+    L, need = lib(), ctypes.c_size_t(0)
+    if ws is None:
+        _check(L.hq_kv_attend_workspace_size(ctypes.byref(c), ctypes.byref(a), ctypes.byref(need)), "hq_kv_attend")
+        ws = torch.empty(max(need.value, 256), dtype=torch.uint8, device=dev)
+    elif not (ws.is_contiguous() and ws.device == dev and ws.dtype == torch.uint8):
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+    _check(L.hq_kv_attend(ctypes.byref(c), ctypes.byref(a), ws.data_ptr(), ws.numel(), _stream_handle(stream)), "hq_kv_attend")
+    return out
+
+
+def hq_kv_evict(cache, table, lens, weights, budget: int, sink: int, recent: int, dst_table, bits: int = 4, max_len=None,
+                kept=None, new_lens=None, new_weights=None, stream=None):
+    """Keep, of each (sequence, head)'s tokens, at most `budget`: the first `sink`, the last `recent`, and the
+    others of most weight (ties to the lowest index), moved in order into the pages of dst_table (int32 [seqs][width],
+    none of them in `table`).  Returns (kept int32 [seqs][heads][budget], -1 past the end; new_lens int32 [seqs];
+    new_weights float32 [seqs][heads][budget])."""
+    torch = _torch()
+    c, _ = _cache_arg(cache, bits, 0, None, None)
+    dev, seqs, width, top = cache.device, lens.numel(), table.shape[-1], weights.shape[-1]
+    _check_tensor(lens, "lens", torch.int32, (seqs,), dev)
+    _check_tensor(table, "table", torch.int32, (seqs, width), dev)
+    _check_tensor(weights, "weights", torch.float32, (seqs, c.heads, top), dev)
+    _check_tensor(dst_table, "dst_table", torch.int32, (seqs, dst_table.shape[-1]), dev)
+    if min(budget, sink, recent) < 0:
+        raise ValueError("budget, sink and recent are not negative")
+    kept = torch.empty((seqs, c.heads, budget), dtype=torch.int32, device=dev) if kept is None else kept
+    new_lens = torch.empty(seqs, dtype=torch.int32, device=dev) if new_lens is None else new_lens
+    new_weights = torch.empty((seqs, c.heads, budget), dtype=torch.float32, device=dev) if new_weights is None else new_weights
+    _check_tensor(kept, "kept", torch.int32, (seqs, c.heads, budget), dev)
+    _check_tensor(new_lens, "new_lens", torch.int32, (seqs,), dev)
+    _check_tensor(new_weights, "new_weights", torch.float32, (seqs, c.heads, budget), dev)
+    a = HqKvEvictArgs(table.data_ptr(), lens.data_ptr(), weights.data_ptr(), top, seqs, width,
+                      min(top, width * c.page) if max_len is None else max_len, budget, sink, recent, dst_table.data_ptr(),
+                      dst_table.shape[-1], kept.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr())
+    _check(lib().hq_kv_evict(ctypes.byref(c), ctypes.byref(a), _stream_handle(stream)), "hq_kv_evict")
+    return kept, new_lens, new_weights
 
 
 def hq_rate(x, lattice="e8", target_bps=4.0, seed=0, dither=False, step=0.0, rice_k=-1, ws=None, stream=None,

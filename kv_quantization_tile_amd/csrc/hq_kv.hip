@@ -1,0 +1,464 @@
+// hq_kv.hip -- the paged SRFT cache: appending tokens, reading them back, and evicting tokens by
+// accumulated attention weight.  (Attention over the cache: hq_attend.hip.)
+//
+// The cache holds the SRFT codec's codes and scales ("When quantization is free" technical summary,
+// gist.science/ko/paper/2605.05699, section "Methodology": per-channel lambda, 16 groups with binary16
+// scales, signed int4 or int8) in pages of P tokens of one KV head (hq_kv_device.h: Page).
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/hq.h"
+#include "hq_kv_device.h"
+#include "hq_kv_internal.h"
+
+namespace hq_kv {
+
+constexpr int kBlock = 256;
+
+// absmax / L and 1 / d as the flat codec forms them (hq_srft.hip), equal to the correctly rounded
+// quotients.
+template <int L>
+__device__ __forceinline__ float div_l(float a) {
+  constexpr float c = 1.0f / (float)L;
+  const float q0 = a * c;
+  return __builtin_fmaf(__builtin_fmaf(-q0, (float)L, a), c, q0);
+}
+__device__ __forceinline__ float recip_f16_value(float d) {
+  const float y0 = __builtin_amdgcn_rcpf(d);
+  return __builtin_fmaf(__builtin_fmaf(-d, y0, 1.0f), y0, y0);
+}
+
+struct AppendArgs {
+  uint8_t* cache;
+  const void *k, *v;
+  const int64_t* slots;
+  uint64_t tokens;
+  int64_t kt, kh, vt, vh;  // strides in values
+  uint32_t heads, pages, page_log2;
+  int f32, vec;
+};
+
+// One vector per 16 lanes; the four rows of a wavefront take four consecutive tokens of one head and
+// side (K or V), so that the V pieces (4 bytes every 16) of neighbouring tokens meet in one line.
+// About 330 vector instructions a wavefront-step against 234 MB for a prompt of 32768 tokens and 8 heads.
+template <int BITS>
+__global__ __launch_bounds__(kBlock) void append_kernel(AppendArgs a, Tables K) {
+  const uint32_t lane = threadIdx.x & 63u, l = lane & 15u, row = lane >> 4;
+  const uint64_t items = ((a.tokens + 3) / 4) * a.heads * 2;
+  const uint64_t item = (uint64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
+  if (item >= items) return;
+  const uint32_t side = (uint32_t)(item & 1u);
+  const uint64_t rest = item >> 1;
+  const uint32_t head = (uint32_t)(rest % a.heads);
+  const uint64_t tok = (rest / a.heads) * 4 + row;
+  const bool have = tok < a.tokens;
+  const int64_t slot = have ? a.slots[tok] : -1;
+  const uint32_t P = 1u << a.page_log2;
+  const bool live = slot >= 0 && slot < ((int64_t)a.pages << a.page_log2);
+  const LaneForward f = lane_forward(K, l);
+  const uint32_t kappa = rev4(l);
+  float m[8];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    m[2 * r] = side ? K.v[2 * (kappa + 16 * r)] : K.k[2 * (kappa + 16 * r)];
+    m[2 * r + 1] = side ? K.v[2 * (kappa + 16 * r) + 1] : K.k[2 * (kappa + 16 * r) + 1];
+  }
+  float x[8], y[8];
+  const int64_t off = side ? (int64_t)tok * a.vt + (int64_t)head * a.vh : (int64_t)tok * a.kt + (int64_t)head * a.kh;
+  const void* src = side ? a.v : a.k;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+  if (live) {
+    if (a.f32) {
+      const float* p = static_cast<const float*>(src) + off + 8 * l;
+      if (a.vec) {
+        const float4 u0 = reinterpret_cast<const float4*>(p)[0], u1 = reinterpret_cast<const float4*>(p)[1];
+        x[0] = u0.x; x[1] = u0.y; x[2] = u0.z; x[3] = u0.w;
+        x[4] = u1.x; x[5] = u1.y; x[6] = u1.z; x[7] = u1.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = p[i];
+      }
+    } else {
+      const uint16_t* p = static_cast<const uint16_t*>(src) + off + 8 * l;
+      uint32_t w[4];
+      if (a.vec) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    }
+  }
+  forward_row(x, y, m, l, f);
+
+  // Group kappa / 4 + 4 r lies in the four lanes that share kappa / 4: l, l ^ 4, l ^ 8, l ^ 12.
+  constexpr int L = BITS == 4 ? 7 : 127;
+  bool bad = false;
+  float delta[4];
+  uint32_t hb[4], word[4], word1[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    bad |= !__builtin_isfinite(y[2 * r]) || !__builtin_isfinite(y[2 * r + 1]);
+    float g = fmaxf(fabsf(y[2 * r]), fabsf(y[2 * r + 1]));
+    g = fmaxf(g, lane_xor<8>(g));
+    g = fmaxf(g, lane_xor<4>(g));
+    const _Float16 h = (_Float16)fminf(div_l<L>(g), 65504.0f);
+    delta[r] = (float)h;
+    hb[r] = (uint32_t)__builtin_bit_cast(uint16_t, h);
+  }
+  const uint64_t votes = __builtin_amdgcn_ballot_w64(bad);
+  bad = ((votes >> (lane & 48u)) & 0xFFFFu) != 0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float inv = delta[r] > 0.0f ? recip_f16_value(delta[r]) : 0.0f;
+    const int32_t q0 = (int32_t)__builtin_amdgcn_fmed3f(__builtin_rintf(y[2 * r] * inv), (float)-L, (float)L);
+    const int32_t q1 = (int32_t)__builtin_amdgcn_fmed3f(__builtin_rintf(y[2 * r + 1] * inv), (float)-L, (float)L);
+    const uint32_t j = kappa & 3u;  // the lane's pair of the group's 8 codes
+    if (BITS == 4) {
+      word[r] = (((uint32_t)q0 & 15u) | (((uint32_t)q1 & 15u) << 4)) << (8u * j);
+      word1[r] = 0;
+    } else {
+      const uint32_t two = (((uint32_t)q0 & 255u) | (((uint32_t)q1 & 255u) << 8)) << (16u * (j & 1u));
+      word[r] = j < 2u ? two : 0u;
+      word1[r] = j < 2u ? 0u : two;
+    }
+    word[r] |= lane_xor_u<8>(word[r]);
+    word[r] |= lane_xor_u<4>(word[r]);
+    if (BITS == 8) {
+      word1[r] |= lane_xor_u<8>(word1[r]);
+      word1[r] |= lane_xor_u<4>(word1[r]);
+    }
+  }
+  if (!live) return;
+  // each of the four lanes stores one of the four groups: r = kappa mod 4
+  const uint32_t r = kappa & 3u, g = (kappa >> 2) + 4u * r;
+  uint32_t w0 = r == 0 ? word[0] : r == 1 ? word[1] : r == 2 ? word[2] : word[3];
+  uint32_t w1 = r == 0 ? word1[0] : r == 1 ? word1[1] : r == 2 ? word1[2] : word1[3];
+  uint32_t h = r == 0 ? hb[0] : r == 1 ? hb[1] : r == 2 ? hb[2] : hb[3];
+  if (bad) {  // zero codes, NaN scales
+    w0 = w1 = 0u;
+    h = 0x7E00u;
+  }
+  const uint32_t t = (uint32_t)slot & (P - 1u);
+  uint8_t* page = a.cache + ((uint64_t)(slot >> a.page_log2) * a.heads + head) * ((uint64_t)P * Page<BITS>::kToken);
+  uint8_t* cdst = page + (side ? Page<BITS>::v_code(P, t, g) : Page<BITS>::k_code(P, t) + g * BITS);
+  if (BITS == 4) *reinterpret_cast<uint32_t*>(cdst) = w0;
+  else *reinterpret_cast<uint2*>(cdst) = make_uint2(w0, w1);
+  *reinterpret_cast<uint16_t*>(page + (side ? Page<BITS>::v_scale(P, t, g) : Page<BITS>::k_scale(P, t) + 2u * g)) = (uint16_t)h;
+}
+
+struct ReadArgs {
+  const uint8_t* cache;
+  const int64_t* slots;
+  uint64_t tokens;
+  void *k, *v;
+  uint32_t heads, pages, page_log2;
+  int f32, sides;  // bit 0 K, bit 1 V
+};
+
+template <int BITS>
+__global__ __launch_bounds__(kBlock) void read_kernel(ReadArgs a, Tables K) {
+  const uint32_t lane = threadIdx.x & 63u, l = lane & 15u, row = lane >> 4;
+  const uint32_t ns = a.sides == 3 ? 2u : 1u;
+  const uint64_t items = ((a.tokens + 3) / 4) * a.heads * ns;
+  const uint64_t item = (uint64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
+  if (item >= items) return;
+  const uint32_t side = ns == 2u ? (uint32_t)(item & 1u) : (uint32_t)a.sides >> 1;
+  const uint64_t rest = ns == 2u ? item >> 1 : item;
+  const uint32_t head = (uint32_t)(rest % a.heads);
+  const uint64_t tok = (rest / a.heads) * 4 + row;
+  const bool have = tok < a.tokens;
+  const int64_t slot = have ? a.slots[tok] : -1;
+  const bool live = slot >= 0 && slot < ((int64_t)a.pages << a.page_log2);
+  const uint32_t P = 1u << a.page_log2;
+  float y[8], x[8];
+  uint32_t w0 = 0, w1 = 0, hb = 0;
+  if (live) {
+    const uint32_t t = (uint32_t)slot & (P - 1u);
+    const uint8_t* page = a.cache + ((uint64_t)(slot >> a.page_log2) * a.heads + head) * ((uint64_t)P * Page<BITS>::kToken);
+    const uint8_t* c = page + (side ? Page<BITS>::v_code(P, t, l) : Page<BITS>::k_code(P, t) + l * BITS);
+    if (BITS == 4) {
+      w0 = *reinterpret_cast<const uint32_t*>(c);
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(c);
+      w0 = u.x;
+      w1 = u.y;
+    }
+    hb = *reinterpret_cast<const uint16_t*>(page + (side ? Page<BITS>::v_scale(P, t, l) : Page<BITS>::k_scale(P, t) + 2u * l));
+  }
+  const float delta = (float)__builtin_bit_cast(_Float16, (uint16_t)hb);
+  const LaneInverse f = lane_inverse(K, l);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int32_t q = BITS == 4 ? __builtin_amdgcn_sbfe(w0, 4 * i, 4) : __builtin_amdgcn_sbfe(i < 4 ? w0 : w1, 8 * (i & 3), 8);
+    y[i] = ((float)q * delta) * (side ? K.v[8 * l + i] : K.k[8 * l + i]);
+  }
+  inverse_row(y, x, l, f);
+  if (!have) return;
+  const uint64_t at = (tok * a.heads + head) * kD;
+  void* out = side ? a.v : a.k;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {  // each store instruction covers 64 (128) consecutive bytes a row
+    const uint64_t i = at + 2u * inverse_n(l, e);
+    if (a.f32) *reinterpret_cast<float2*>(static_cast<float*>(out) + i) = make_float2(x[2 * e], x[2 * e + 1]);
+    else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + i) = bf16_pair(x[2 * e], x[2 * e + 1]);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Eviction.  Of a (sequence, head)'s n tokens m = min(n, budget) stay: the first `sink`, the last
+// `recent`, and those of most weight among the others, ties to the lowest index.
+struct EvictArgs {
+  uint8_t* cache;
+  const int32_t *table, *lens, *dst;
+  const float* weights;
+  uint64_t wstride;
+  int32_t *kept, *new_lens;
+  float* new_weights;
+  uint32_t seqs, heads, pages, page_log2, width, dst_width, max_len, budget, sink, recent;
+};
+
+// Order-preserving key of a weight: larger weight, larger key; -0 counts as 0, NaN below everything.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  const uint32_t b = __float_as_uint(w + 0.0f);
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0u;
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ uint32_t clamp_len(int32_t n, uint32_t most) { return n < 0 ? 0u : (uint32_t)n < most ? (uint32_t)n : most; }
+
+// One workgroup per (sequence, head): the key of the last token that stays by four counting passes of
+// 8 bits each (most significant first), then one ordered pass that numbers the tokens that stay.
+constexpr int kSelect = 1024;
+__global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t s_prefix, s_left, part[2][kSelect / 64];
+  const uint32_t b = blockIdx.x / a.heads, h = blockIdx.x % a.heads, tid = threadIdx.x;
+  const uint32_t width_tokens = a.width << a.page_log2;
+  const uint32_t n = clamp_len(a.lens[b], a.max_len < width_tokens ? a.max_len : width_tokens);
+  const uint32_t m = n < a.budget ? n : a.budget;
+  const float* w = a.weights + ((uint64_t)b * a.heads + h) * a.wstride;
+  const uint32_t lo = a.sink < n ? a.sink : n, hi = n - (a.recent < n ? a.recent : n) > lo ? n - (a.recent < n ? a.recent : n) : lo;
+  uint32_t want = m - (lo + (n - hi));  // of the middle [lo, hi)
+  if (n <= a.budget) want = hi - lo;
+  if (tid == 0 && h == 0) a.new_lens[b] = (int32_t)m;
+  uint32_t prefix = 0, left = want;  // key bits found so far; how many of the equal ones still to take
+  if (want < hi - lo && want > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (tid < 256) hist[tid] = 0;
+      __syncthreads();
+      const uint32_t above = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+      for (uint32_t t = lo + tid; t < hi; t += kSelect) {
+        const uint32_t key = weight_key(w[t]);
+        if ((key & above) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+      }
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t c = left, d = 255;
+        while (d > 0 && hist[d] < c) c -= hist[d--];
+        s_prefix = prefix | (d << shift);
+        s_left = c;
+      }
+      __syncthreads();
+      prefix = s_prefix;
+      left = s_left;
+      __syncthreads();
+    }
+  }
+  const bool all = want == hi - lo;
+  const uint32_t lane = tid & 63u, wave = tid >> 6;
+  uint32_t kept = 0, eq = 0;
+  int32_t* dst = a.kept + ((uint64_t)b * a.heads + h) * a.budget;
+  float* wd = a.new_weights ? a.new_weights + ((uint64_t)b * a.heads + h) * a.budget : nullptr;
+  for (uint32_t t0 = 0; t0 < n; t0 += kSelect) {
+    const uint32_t t = t0 + tid;
+    bool take = false, tie = false;
+    float wt = 0.0f;
+    if (t < n) {
+      wt = w[t];
+      const bool fixed = t < lo || t >= hi;
+      const uint32_t key = weight_key(wt);
+      take = fixed || all || (want > 0 && key > prefix);
+      tie = !fixed && !all && want > 0 && key == prefix;
+    }
+    // ties before this token: exclusive count over the workgroup
+    const uint64_t vt = __builtin_amdgcn_ballot_w64(tie);
+    if (lane == 0) part[0][wave] = (uint32_t)__builtin_popcountll(vt);
+    __syncthreads();
+    uint32_t before = eq, total = 0;
+    for (uint32_t i = 0; i < kSelect / 64; ++i) {
+      if (i < wave) before += part[0][i];
+      total += part[0][i];
+    }
+    before += (uint32_t)__builtin_popcountll(vt & ((1ull << lane) - 1ull));
+    eq += total;
+    take = take || (tie && before < left);
+    const uint64_t vk = __builtin_amdgcn_ballot_w64(take);
+    if (lane == 0) part[1][wave] = (uint32_t)__builtin_popcountll(vk);
+    __syncthreads();
+    uint32_t at = kept, sum = 0;
+    for (uint32_t i = 0; i < kSelect / 64; ++i) {
+      if (i < wave) at += part[1][i];
+      sum += part[1][i];
+    }
+    at += (uint32_t)__builtin_popcountll(vk & ((1ull << lane) - 1ull));
+    kept += sum;
+    if (take && at < a.budget) {
+      dst[at] = (int32_t)t;
+      if (wd) wd[at] = wt;
+    }
+  }
+  for (uint32_t j = m + tid; j < a.budget; j += kSelect) {
+    dst[j] = -1;
+    if (wd) wd[j] = 0.0f;
+  }
+}
+
+// Moves the tokens that stay, 16 lanes a token: lane g carries group g's codes and scales of K and V.
+template <int BITS>
+__global__ __launch_bounds__(kBlock) void evict_move_kernel(EvictArgs a) {
+  const uint32_t lane = threadIdx.x & 15u;
+  const uint64_t item = (uint64_t)blockIdx.x * (kBlock / 16) + (threadIdx.x >> 4);
+  if (item >= (uint64_t)a.seqs * a.heads * a.budget) return;
+  const uint32_t j = (uint32_t)(item % a.budget), bh = (uint32_t)(item / a.budget), b = bh / a.heads, h = bh % a.heads;
+  const int32_t src = a.kept[item];
+  if (src < 0) return;
+  const uint32_t P = 1u << a.page_log2, so = (uint32_t)src & (P - 1u), to = j & (P - 1u);
+  const int32_t sp = a.table[(uint64_t)b * a.width + ((uint32_t)src >> a.page_log2)];
+  const int32_t dp = a.dst[(uint64_t)b * a.dst_width + (j >> a.page_log2)];
+  if (sp < 0 || (uint32_t)sp >= a.pages || dp < 0 || (uint32_t)dp >= a.pages) return;
+  const uint64_t size = (uint64_t)P * Page<BITS>::kToken;
+  const uint8_t* s = a.cache + ((uint64_t)sp * a.heads + h) * size;
+  uint8_t* d = a.cache + ((uint64_t)dp * a.heads + h) * size;
+  typedef uint32_t piece __attribute__((ext_vector_type(BITS / 4)));
+  *reinterpret_cast<piece*>(d + Page<BITS>::k_code(P, to) + lane * BITS) = *reinterpret_cast<const piece*>(s + Page<BITS>::k_code(P, so) + lane * BITS);
+  *reinterpret_cast<piece*>(d + Page<BITS>::v_code(P, to, lane)) = *reinterpret_cast<const piece*>(s + Page<BITS>::v_code(P, so, lane));
+  *reinterpret_cast<uint16_t*>(d + Page<BITS>::k_scale(P, to) + 2u * lane) = *reinterpret_cast<const uint16_t*>(s + Page<BITS>::k_scale(P, so) + 2u * lane);
+  *reinterpret_cast<uint16_t*>(d + Page<BITS>::v_scale(P, to, lane)) = *reinterpret_cast<const uint16_t*>(s + Page<BITS>::v_scale(P, so, lane));
+}
+
+}  // namespace hq_kv
+
+using namespace hq_kv;
+
+static uint32_t log2_of(uint32_t v) { return 31u - (uint32_t)__builtin_clz(v); }
+
+extern "C" {
+
+int hq_kv_append(const hq_kv_cache* cache, const void* k, const void* v, int32_t dtype, uint64_t tokens,
+                 const int64_t strides[4], const int64_t* slots, hq_stream_t stream) {
+  if (int rc = check_cache(cache)) return rc;
+  if ((dtype != HQ_F32 && dtype != HQ_BF16) || !strides || tokens > (1ull << 31)) return HQ_ERR_INVALID_ARG;
+  if (tokens && (!k || !v || !slots || ((uintptr_t)slots & 7u))) return HQ_ERR_INVALID_ARG;
+  const uint32_t size = dtype == HQ_F32 ? 4u : 2u;
+  if (((uintptr_t)k | (uintptr_t)v) & (size - 1u)) return HQ_ERR_INVALID_ARG;
+  AppendArgs a;
+  Tables T;
+  if (!make_tables(*cache, true, &T)) return HQ_ERR_INVALID_ARG;
+  if (tokens == 0 || cache->pages == 0) return HQ_OK;
+  a.cache = static_cast<uint8_t*>(cache->data);
+  a.k = k;
+  a.v = v;
+  a.slots = slots;
+  a.tokens = tokens;
+  a.kt = strides[0];
+  a.kh = strides[1];
+  a.vt = strides[2];
+  a.vh = strides[3];
+  a.heads = cache->heads;
+  a.pages = cache->pages;
+  a.page_log2 = log2_of(cache->page);
+  a.f32 = dtype == HQ_F32;
+  // 16-byte loads where every row starts on 16 bytes, single values otherwise
+  const int64_t per = 16 / size;
+  a.vec = !(((uintptr_t)k | (uintptr_t)v) & 15u) && !(a.kt % per) && !(a.kh % per) && !(a.vt % per) && !(a.vh % per);
+  const uint64_t items = ((tokens + 3) / 4) * cache->heads * 2;
+  const uint64_t grid = (items + kBlock / 64 - 1) / (kBlock / 64);
+  if (grid > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (cache->bits == 4) hipLaunchKernelGGL(append_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
+  else hipLaunchKernelGGL(append_kernel<8>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
+  return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
+}
+
+int hq_kv_read(const hq_kv_cache* cache, const int64_t* slots, uint64_t tokens, void* k, void* v, int32_t out_dtype,
+               hq_stream_t stream) {
+  if (int rc = check_cache(cache)) return rc;
+  if ((out_dtype != HQ_F32 && out_dtype != HQ_BF16) || tokens > (1ull << 31)) return HQ_ERR_INVALID_ARG;
+  if (tokens && ((!k && !v) || !slots || ((uintptr_t)slots & 7u))) return HQ_ERR_INVALID_ARG;
+  if (((uintptr_t)k | (uintptr_t)v) & 15u) return HQ_ERR_INVALID_ARG;
+  Tables T;
+  if (!make_tables(*cache, false, &T)) return HQ_ERR_INVALID_ARG;
+  if (tokens == 0) return HQ_OK;
+  ReadArgs a;
+  a.cache = static_cast<const uint8_t*>(cache->data);
+  a.slots = slots;
+  a.tokens = tokens;
+  a.k = k;
+  a.v = v;
+  a.heads = cache->heads;
+  a.pages = cache->pages;
+  a.page_log2 = log2_of(cache->page);
+  a.f32 = out_dtype == HQ_F32;
+  a.sides = (k ? 1 : 0) | (v ? 2 : 0);
+  const uint64_t items = ((tokens + 3) / 4) * cache->heads * (a.sides == 3 ? 2 : 1);
+  const uint64_t grid = (items + kBlock / 64 - 1) / (kBlock / 64);
+  if (grid > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (cache->bits == 4) hipLaunchKernelGGL(read_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
+  else hipLaunchKernelGGL(read_kernel<8>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
+  return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
+}
+
+int hq_kv_evict(const hq_kv_cache* cache, const hq_kv_evict_args* e, hq_stream_t stream) {
+  if (int rc = check_cache(cache)) return rc;
+  if (!e || e->max_len > 0x7FFFFFFFu || e->budget > 0x7FFFFFFFu) return HQ_ERR_INVALID_ARG;
+  if ((uint64_t)e->sink + e->recent > e->budget) return HQ_ERR_INVALID_ARG;
+  if ((uint64_t)e->table_width * cache->page > 0x7FFFFFFFull || (uint64_t)e->dst_width * cache->page < e->budget) return HQ_ERR_INVALID_ARG;
+  if (e->weights_stride < e->max_len) return HQ_ERR_INVALID_ARG;
+  if ((uint64_t)e->seqs * cache->heads > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  if (e->seqs == 0) return HQ_OK;
+  if (!e->lens || !e->new_lens || (e->max_len && (!e->weights || !e->table)) || (e->budget && (!e->kept || !e->dst_table))) return HQ_ERR_INVALID_ARG;
+  if (((uintptr_t)e->lens | (uintptr_t)e->new_lens | (uintptr_t)e->weights | (uintptr_t)e->table | (uintptr_t)e->kept |
+       (uintptr_t)e->dst_table | (uintptr_t)e->new_weights) & 3u)
+    return HQ_ERR_INVALID_ARG;
+  EvictArgs a;
+  a.cache = static_cast<uint8_t*>(cache->data);
+  a.table = e->table;
+  a.lens = e->lens;
+  a.dst = e->dst_table;
+  a.weights = e->weights;
+  a.wstride = e->weights_stride;
+  a.kept = e->kept;
+  a.new_lens = e->new_lens;
+  a.new_weights = e->new_weights;
+  a.seqs = e->seqs;
+  a.heads = cache->heads;
+  a.pages = cache->pages;
+  a.page_log2 = log2_of(cache->page);
+  a.width = e->table_width;
+  a.dst_width = e->dst_width;
+  a.max_len = e->max_len;
+  a.budget = e->budget;
+  a.sink = e->sink;
+  a.recent = e->recent;
+  const uint64_t moves = (uint64_t)e->seqs * cache->heads * e->budget, grid = (moves + kBlock / 16 - 1) / (kBlock / 16);
+  if (grid > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  hipLaunchKernelGGL(evict_select_kernel, dim3(e->seqs * cache->heads), dim3(kSelect), 0, st, a);
+  if (grid) {
+    if (cache->bits == 4) hipLaunchKernelGGL(evict_move_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a);
+    else hipLaunchKernelGGL(evict_move_kernel<8>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a);
+  }
+  return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
+}
+
+}  // extern "C"
