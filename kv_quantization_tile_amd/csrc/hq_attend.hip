@@ -33,6 +33,7 @@ namespace hq_kv {
 
 constexpr int kAttBlock = 256;
 constexpr int kAttWaves = 4;
+constexpr int kPad = kD + 4;         // row of a tile in LDS, in floats
 constexpr float kPScaleLog2 = 8.0f;  // P is stored as p 2^8
 constexpr float kSlack = 6.0f;       // the reference may lag the maximum by this much (log2)
 
@@ -45,15 +46,17 @@ struct AttendArgs {
   uint64_t wstride, total_q;
   int64_t qt, qh;  // strides of q in values
   uint32_t heads, group, q_heads, pages, page_log2, width, seqs, max_q, max_len;
-  uint32_t tiles, splits, chunk, window;
+  uint32_t tile_rows, tiles, splits, chunk, window;
+  uint32_t wrows, wpad;  // stored scores: rows of an item, tokens a row
   int causal, q_f32, out_f32, vec;
   float scale_log2, cap_in, cap_out;  // scores in log2 units; s = cap_out tanh(cap_in s) when cap_in > 0
-  // workspace
-  _Float16 *qhi, *qlo;  // [seqs heads tiles][16][128]
-  float* qf;            // [..][16] factor of a row's products
-  float* po;            // [..][splits][16][128]
-  float* pml;           // [..][splits][16][2]
-  float* lse;           // [..][16]
+  // workspace; an item is a (sequence, head, tile of tile_rows rows)
+  _Float16 *qhi, *qlo;  // [items][tile_rows][128]
+  float* qf;            // [items][tile_rows] factor of a row's products
+  float* po;            // [items][splits][tile_rows][128]
+  float* pml;           // [items][splits][tile_rows][2]
+  float* lse;           // [items][tile_rows]
+  float* scores;        // [items][wrows][wpad]
 };
 
 struct Seq {
@@ -87,19 +90,28 @@ __device__ __forceinline__ void visible(const AttendArgs& a, const Seq& s, int32
   *lo = l > h ? h : (int32_t)l;
   *hi = h;
 }
-// Tokens a tile's rows see, as one range.
-__device__ __forceinline__ void tile_range(const AttendArgs& a, const Seq& s, uint32_t tile, int32_t* lo, int32_t* hi) {
-  const uint32_t rows = (uint32_t)s.m * a.group, r0 = tile * 16u;
+// Tokens that some row of [r0, r0 + count) sees, as one range.
+__device__ __forceinline__ void rows_range(const AttendArgs& a, const Seq& s, uint32_t r0, uint32_t count, int32_t* lo, int32_t* hi) {
+  const uint32_t rows = (uint32_t)s.m * a.group;
   if (r0 >= rows) {
     *lo = *hi = 0;
     return;
   }
-  const uint32_t r1 = r0 + 15u < rows ? r0 + 15u : rows - 1u;
+  const uint32_t r1 = r0 + count < rows ? r0 + count - 1u : rows - 1u;
   int32_t l0, h0, l1, h1;
   visible(a, s, (int32_t)(r0 / a.group), &l0, &h0);
   visible(a, s, (int32_t)(r1 / a.group), &l1, &h1);
   *lo = l0;
   *hi = h1;
+}
+
+// Tokens that every row of [r0, r0 + count) sees; none if some of the rows do not exist.
+__device__ __forceinline__ void rows_common(const AttendArgs& a, const Seq& s, uint32_t r0, uint32_t count, int32_t* lo, int32_t* hi) {
+  *lo = *hi = 0;
+  if (r0 + count > (uint32_t)s.m * a.group) return;
+  int32_t x;
+  visible(a, s, (int32_t)((r0 + count - 1u) / a.group), lo, &x);
+  visible(a, s, (int32_t)(r0 / a.group), &x, hi);
 }
 
 __device__ __forceinline__ float swap16_max(float x) {
@@ -207,31 +219,70 @@ __device__ __forceinline__ void load_values(const uint8_t* page, uint32_t P, uin
   s.vs[1] = u.y;
 }
 
-// Raw products of 16 tokens with the tile's rows: lane (n, b) gets row n, tokens 4b..4b+3.
+// A lane's keys as operands: hi[j] is group 4b + j, lo[j] what rounding it left.
 template <int BITS, bool PREC>
-__device__ __forceinline__ f32x4 scores16(const Share<BITS>& s, const f16x8 qh[4], const f16x8 ql[4]) {
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+__device__ __forceinline__ void key_operands(const Share<BITS>& s, f16x8 hi[4], f16x8 lo[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     f16x2 c[4];
     code_pairs<BITS>(s.k + j * (BITS / 4), c);
-    const uint32_t sc = s.ks[j >> 1];
-    const _Float16 d = (j & 1) ? h2(sc)[1] : h2(sc)[0];
+    const _Float16 d = h2(s.ks[j >> 1])[j & 1];
     const f16x2 dd = {d, d};
-    U32x4 hi, lo;
+    U32x4 h, l;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f16x2 p = c[i] * dd;
-      hi.v[i] = u2(p);
-      if (PREC) lo.v[i] = u2(__builtin_elementwise_fma(c[i], dd, -p));
+      h.v[i] = u2(p);
+      if (PREC) l.v[i] = u2(__builtin_elementwise_fma(c[i], dd, -p));
     }
+    hi[j] = frag(h);
+    if (PREC) lo[j] = frag(l);
+  }
+}
+
+__device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+// Raw products of 16 tokens with 16 rows: lane (n, b) gets row n, tokens 4b..4b+3.
+template <bool PREC>
+__device__ __forceinline__ f32x4 scores16(const f16x8 kh[4], const f16x8 kl[4], const f16x8 qh[4], const f16x8 ql[4]) {
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
     if (PREC) {
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(frag(lo), qh[j], acc, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(frag(hi), ql[j], acc, 0, 0, 0);
+      acc = mfma(kl[j], qh[j], acc);
+      acc = mfma(kh[j], ql[j], acc);
     }
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(frag(hi), qh[j], acc, 0, 0, 0);
+    acc = mfma(kh[j], qh[j], acc);
   }
   return acc;
+}
+
+// A lane's values as two of the four registers of the operand of 32 tokens: out[i][w], i the
+// coordinate within the lane's group, w the pair of tokens.
+template <int BITS>
+__device__ __forceinline__ void value_operands(const Share<BITS>& s, uint32_t out[8][2]) {
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    f16x2 c[8];
+    token_pairs<BITS>(s.v + (2 * w) * (BITS / 4), s.v + (2 * w + 1) * (BITS / 4), c);
+    const f16x2 d = h2(s.vs[w]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i][w] = u2(c[i] * d);
+  }
+}
+
+// Which of the lane's four value scales are NaN or infinite (bit r: token 4b + r).
+__device__ __forceinline__ uint32_t bad_scales(const uint32_t vs[2]) {
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= ((vs[i >> 1] >> (16 * (i & 1))) & 0x7C00u) == 0x7C00u ? 1u << i : 0u;
+  return bad;
+}
+// Zeroes the scales of the tokens in `mask`.
+__device__ __forceinline__ void drop_scales(uint32_t vs[2], uint32_t mask) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (mask & (1u << i)) vs[i >> 1] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
 }
 
 // tanh from the exponential: 1 - 2 / (e^2x + 1) away from zero, the odd series below 2^-3 in magnitude
@@ -246,30 +297,35 @@ __device__ __forceinline__ float tanh32(float x) {
 
 __device__ __forceinline__ float capped(const AttendArgs& a, float s) { return a.cap_in > 0.0f ? a.cap_out * tanh32(s * a.cap_in) : s; }
 
+// LDS written by some lanes of a wavefront is read by others of the same one.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---------------------------------------------------------------------------------------------
-// The queries' rows, transformed: two binary16 parts and a factor each, in the operand's order.
+// One query row, by the caller's 16 lanes: transformed, scaled by a power of two, in two binary16
+// parts in the operand's order, to hi[128] (and lo[128] unless null).  Returns the factor that turns the
+// row's products into scores.
 template <int BITS>
-__global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Tables K) {
-  const uint32_t lane = threadIdx.x & 63u, l = lane & 15u;
-  const uint64_t rowid = (uint64_t)blockIdx.x * (kAttBlock / 16) + (threadIdx.x >> 4);  // item * 16 + row
-  const uint64_t item = rowid >> 4;
-  if (item >= (uint64_t)a.seqs * a.heads * a.tiles) return;
-  const uint32_t tile = (uint32_t)(item % a.tiles), h = (uint32_t)(item / a.tiles % a.heads), b = (uint32_t)(item / a.tiles / a.heads);
-  const Seq s = seq_of(a, b);
-  const uint32_t r = tile * 16u + (uint32_t)(rowid & 15u);
-  const bool have = r < (uint32_t)s.m * a.group;
-  if (tile * 16u >= (uint32_t)s.m * a.group) return;
-  const LaneForward f = lane_forward(K, l);
+__device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K, const Seq& s, uint32_t h, uint32_t r, uint32_t l,
+                                            const LaneForward& f, _Float16* hi, _Float16* lo) {
   const uint32_t kappa = rev4(l);
   float m[8], x[8], y[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    m[2 * i] = K.k[2 * (kappa + 16 * i)];
-    m[2 * i + 1] = K.k[2 * (kappa + 16 * i) + 1];
+    const uint32_t c = 2 * (kappa + 16 * i);
+    m[2 * i] = packing(c) * a.scale_log2;
+    m[2 * i + 1] = packing(c + 1) * a.scale_log2;
+    if (K.scaled) {
+      m[2 * i] *= K.k[c];
+      m[2 * i + 1] *= K.k[c + 1];
+    }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-  if (have) {
+  if (r < (uint32_t)s.m * a.group) {
     const int64_t at = (s.q0 + r / a.group) * a.qt + (int64_t)(h * a.group + r % a.group) * a.qh + 8 * l;
     if (a.q_f32) {
       const float* p = static_cast<const float*>(a.q) + at;
@@ -300,8 +356,7 @@ __global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Ta
   top = fmaxf(top, lane_xor<2>(top));
   top = fmaxf(top, lane_xor<1>(top));
   int e = 0;
-  if (top > 0.0f && __builtin_isfinite(top)) e = 14 - (__builtin_amdgcn_frexp_expf(top) - 1);
-  _Float16 *hi = a.qhi + rowid * kD, *lo = a.qlo + rowid * kD;
+  if (top > 0.0f && __builtin_isfinite(top)) e = 15 - __builtin_amdgcn_frexp_expf(top);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t g = (kappa >> 2) + 4u * (i >> 1), c = 2u * (kappa & 3u) + (i & 1);
@@ -309,108 +364,166 @@ __global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Ta
     const float v = __builtin_ldexpf(y[i], e);
     const _Float16 vh = (_Float16)v;
     hi[at] = vh;
-    lo[at] = (_Float16)(v - (float)vh);
+    if (lo) lo[at] = (_Float16)(v - (float)vh);
   }
-  if (l == 0) a.qf[rowid] = __builtin_ldexpf(a.scale_log2 * unit<BITS>(), -e);
+  return __builtin_ldexpf(unit<BITS>(), -e);
+}
+
+// Turns a row's sum_t p_t code Delta (the lane's group, y[8], over unit) back and stores the row.
+template <int BITS>
+__device__ __forceinline__ void store_row(const AttendArgs& a, const Tables& K, const Seq& s, uint32_t h, uint32_t r, uint32_t l,
+                                          const LaneInverse& f, float y[8], float sum) {
+  const float inv = sum == 0.0f ? 0.0f : unit<BITS>() / sum;  // a row that sees nothing is 0
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y[i] *= inv;
+    if (K.scaled) y[i] *= K.v[8 * l + i];
+  }
+  inverse_row(y, x, l, f);
+  if (r >= (uint32_t)s.m * a.group) return;
+  const uint64_t at = ((uint64_t)(s.q0 + r / a.group) * a.q_heads + h * a.group + r % a.group) * kD;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint64_t i = at + 2u * inverse_n(l, e);
+    if (a.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(a.out) + i) = make_float2(x[2 * e], x[2 * e + 1]);
+    else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + i) = bf16_pair(x[2 * e], x[2 * e + 1]);
+  }
+}
+
+struct Item {
+  uint32_t tile, h, b;
+};
+__device__ __forceinline__ Item item_of(const AttendArgs& a, uint32_t item) {
+  Item i;
+  i.tile = item % a.tiles;
+  item /= a.tiles;
+  i.h = item % a.heads;
+  i.b = item / a.heads;
+  return i;
+}
+
+// The page of token tt (-1: absent, or past `end`), the same in every lane.
+__device__ __forceinline__ int32_t page_of(const AttendArgs& a, uint32_t b, int32_t tt, int32_t end) {
+  int32_t p = -1;
+  if (tt < end) p = a.table[(uint64_t)b * a.width + ((uint32_t)tt >> a.page_log2)];
+  p = __builtin_amdgcn_readfirstlane(p);
+  return (uint32_t)p < a.pages ? p : -1;
 }
 
 // ---------------------------------------------------------------------------------------------
-// One (sequence, head, row tile, split): the wavefronts take 32 tokens in turn.
+// Up to 16 rows a (sequence, head): the single-token step.  A workgroup takes one split of the tokens; its
+// four wavefronts take 32 tokens in turn, the next 32 already on their way, and join at the end.  The
+// cache's bytes bound it; its rows are a fraction of the products' 16 columns, which costs nothing here.
 template <int BITS, bool PREC>
-__global__ __launch_bounds__(kAttBlock) void attend_kernel(AttendArgs a) {
-  __shared__ float s_o[16][kD + 4];
-  __shared__ float s_m[kAttWaves][16], s_l[kAttWaves][16];
+__global__ __launch_bounds__(kAttBlock) void attend_few_kernel(AttendArgs a, Tables K) {
+  __shared__ __align__(16) float s_o[kAttWaves][16][kPad];
+  __shared__ __align__(16) _Float16 s_q[PREC ? 2 : 1][16][kD + 8];
+  __shared__ float s_f[16], s_m[kAttWaves][16], s_l[kAttWaves][16];
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, n = lane & 15u, b4 = lane >> 4;
-  const uint32_t split = blockIdx.x % a.splits;
-  const uint64_t item = blockIdx.x / a.splits;
-  const uint32_t tile = (uint32_t)(item % a.tiles), h = (uint32_t)(item / a.tiles % a.heads), b = (uint32_t)(item / a.tiles / a.heads);
-  const Seq s = seq_of(a, b);
+  const uint32_t split = blockIdx.x % a.splits, item = blockIdx.x / a.splits;
+  const Item it = item_of(a, item);
+  const Seq s = seq_of(a, it.b);
+  const uint32_t rows = (uint32_t)s.m * a.group;
   int32_t lo, hi;
-  tile_range(a, s, tile, &lo, &hi);
+  rows_range(a, s, 0, 16, &lo, &hi);
   int32_t t0 = (int32_t)(split * a.chunk), t1 = t0 + (int32_t)a.chunk;
   t0 = t0 > (lo & ~15) ? t0 : lo & ~15;
   t1 = t1 < hi ? t1 : hi;
-  if (t0 >= t1) return;  // the same for the whole workgroup
+  if (a.pages == 0) t1 = t0;
+  if (t0 >= t1 && a.splits > 1) return;  // the same for the whole workgroup
   const uint32_t P = 1u << a.page_log2;
   const uint64_t page_size = (uint64_t)P * Page<BITS>::kToken;
 
-  f16x8 qh[4], ql[4];
-  {
-    const uint64_t row = item * 16 + n;
+  int32_t pg[2], pn[2];
+  Share<BITS> cur[2], nxt[2];
+  auto load = [&](int32_t t, const int32_t page[2], Share<BITS> sh[2]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      qh[j] = *reinterpret_cast<const f16x8*>(a.qhi + row * kD + 8 * (4 * b4 + j));
-      if (PREC) ql[j] = *reinterpret_cast<const f16x8*>(a.qlo + row * kD + 8 * (4 * b4 + j));
+    for (int u = 0; u < 2; ++u) {  // an absent page's place is taken by page 0, masked below
+      const uint8_t* p = a.cache + ((uint64_t)(page[u] < 0 ? 0 : page[u]) * a.heads + it.h) * page_size;
+      load_keys<BITS>(p, P, (uint32_t)(t + 16 * u) & (P - 1u), lane, sh[u]);
+      load_values<BITS>(p, P, (uint32_t)(t + 16 * u) & (P - 1u), lane, sh[u]);
     }
-  }
-  const float qf = a.qf[item * 16 + n];
-  int32_t row_lo = 0, row_hi = 0;
-  if (tile * 16u + n < (uint32_t)s.m * a.group) visible(a, s, (int32_t)((tile * 16u + n) / a.group), &row_lo, &row_hi);
-  // the tokens every row of the tile sees: no masks there
-  const bool whole_tile = tile * 16u + 15u < (uint32_t)s.m * a.group;
-  int32_t all_lo = 0, all_hi = 0;
-  if (whole_tile) {
-    int32_t x;
-    visible(a, s, (int32_t)((tile * 16u + 15u) / a.group), &all_lo, &x);
-    visible(a, s, (int32_t)((tile * 16u) / a.group), &x, &all_hi);
-  }
+  };
+  int32_t t = t0 + 32 * (int32_t)wave;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) pg[u] = page_of(a, it.b, t + 16 * u, t1);
+  if (t < t1) load(t, pg, cur);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) pn[u] = page_of(a, it.b, t + 32 * kAttWaves + 16 * u, t1);
 
-  float m = -1.0e30f, sum = 0.0f;
+  {  // the rows: four to a wavefront, 16 lanes each
+    const uint32_t r = threadIdx.x >> 4;
+    float f = 0.0f;
+    if ((r & ~3u) < rows) f = rotate_row<BITS>(a, K, s, it.h, r, n, lane_forward(K, n), s_q[0][r], PREC ? s_q[PREC ? 1 : 0][r] : nullptr);
+    else
+      for (int i = 0; i < 8; ++i) {
+        s_q[0][r][8 * n + i] = (_Float16)0.0f;
+        if (PREC) s_q[PREC ? 1 : 0][r][8 * n + i] = (_Float16)0.0f;
+      }
+    if (n == 0) s_f[r] = f;
+  }
+  __syncthreads();
+  f16x8 qh[4], ql[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    qh[j] = *reinterpret_cast<const f16x8*>(&s_q[0][n][8 * (4 * b4 + j)]);
+    if (PREC) ql[j] = *reinterpret_cast<const f16x8*>(&s_q[PREC ? 1 : 0][n][8 * (4 * b4 + j)]);
+  }
+  const float qf = s_f[n];
+  int32_t row_lo = 0, row_hi = 0, all_lo = hi, all_hi = lo;
+  if (n < rows) visible(a, s, (int32_t)(n / a.group), &row_lo, &row_hi);
+  // the tokens every existing row sees need no mask (rows past the last are products with zero)
+  if (rows) rows_common(a, s, 0, rows, &all_lo, &all_hi);
+
+  float m = -1.0e30f, sum = 0.0f, poison = 0.0f;
   f32x4 o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-  for (int32_t t = t0 + 32 * (int32_t)wave; t < t1; t += 32 * kAttWaves) {
-    Share<BITS> sh[2];
-    bool there[2];
+  for (; t < t1; t += 32 * kAttWaves) {
+    if (t + 32 * kAttWaves < t1) load(t + 32 * kAttWaves, pn, nxt);
+    const bool there[2] = {pg[0] >= 0, pg[1] >= 0};
+    const int32_t ahead = t + 64 * kAttWaves;
+    int32_t pa[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int32_t tt = t + 16 * u;
-      int32_t page = -1;
-      if (tt < t1) page = a.table[(uint64_t)b * a.width + ((uint32_t)tt >> a.page_log2)];
-      page = __builtin_amdgcn_readfirstlane(page);
-      there[u] = page >= 0 && (uint32_t)page < a.pages;
-      if (there[u]) {
-        const uint8_t* p = a.cache + ((uint64_t)page * a.heads + h) * page_size;
-        load_keys<BITS>(p, P, (uint32_t)tt & (P - 1u), lane, sh[u]);
-        load_values<BITS>(p, P, (uint32_t)tt & (P - 1u), lane, sh[u]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < BITS; ++i) sh[u].k[i] = sh[u].v[i] = 0u;
-        sh[u].ks[0] = sh[u].ks[1] = sh[u].vs[0] = sh[u].vs[1] = 0u;
-      }
-    }
+    for (int u = 0; u < 2; ++u) pa[u] = page_of(a, it.b, ahead + 16 * u, t1);
     float sc[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const f32x4 r = scores16<BITS, PREC>(sh[u], qh, ql);
+      f16x8 kh[4], kl[4];
+      key_operands<BITS, PREC>(cur[u], kh, kl);
+      const f32x4 r = scores16<PREC>(kh, kl, qh, ql);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[4 * u + i] = capped(a, r[i] * qf);
+      for (int i = 0; i < 4; ++i) sc[4 * u + i] = r[i] * qf;
     }
-    const bool plain = there[0] && there[1] && t >= all_lo && t + 32 <= all_hi;
-    if (!plain) {
+    if (a.cap_in > 0.0f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sc[i] = capped(a, sc[i]);
+    }
+    if (!(there[0] && there[1] && t >= all_lo && t + 32 <= all_hi && t + 32 <= t1)) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int32_t tok = t + 16 * (i >> 2) + 4 * (int32_t)b4 + (i & 3);
         if (!there[i >> 2] || tok < row_lo || tok >= row_hi || tok >= t1) sc[i] = -__builtin_inff();
         // a token that no row sees may hold anything
-        if (!there[i >> 2] || tok < lo || tok >= t1) sh[i >> 2].vs[(i >> 1) & 1] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+        if (!there[i >> 2] || tok < lo || tok >= t1) drop_scales(cur[i >> 2].vs, 1u << (i & 3));
       }
     }
-    // A value vector with NaN scales makes the rows that see it NaN, and no other (0 NaN in the product
-    // would reach every row): its scale becomes 0 and its scores NaN.
+    if (a.scores && n < rows) {
+      float* d = a.scores + ((uint64_t)item * a.wrows + n) * a.wpad + (uint32_t)t + 4u * b4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = sh[i >> 1].vs[i & 1];
-      if ((w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u) {
-        if ((w & 0x7C00u) == 0x7C00u) {
-          if (sc[2 * i] != -__builtin_inff()) sc[2 * i] = __builtin_nanf("");
-          sh[i >> 1].vs[i & 1] &= 0xFFFF0000u;
-        }
-        if ((w & 0x7C000000u) == 0x7C000000u) {
-          if (sc[2 * i + 1] != -__builtin_inff()) sc[2 * i + 1] = __builtin_nanf("");
-          sh[i >> 1].vs[i & 1] &= 0x0000FFFFu;
-        }
-      }
+      for (int u = 0; u < 2; ++u)
+        if (t + 16 * u < t1) *reinterpret_cast<f32x4*>(d + 16 * u) = (f32x4){sc[4 * u], sc[4 * u + 1], sc[4 * u + 2], sc[4 * u + 3]};
+    }
+    // A value vector with NaN scales makes the rows that see it NaN and no other (0 NaN in the product
+    // would reach every row): its scales count as 0, and the rows are poisoned.
+    const uint32_t bad = bad_scales(cur[0].vs) | bad_scales(cur[1].vs) << 4;
+    if (__builtin_amdgcn_ballot_w64(bad != 0)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((bad >> i) & 1u && sc[i] != -__builtin_inff()) poison = __builtin_nanf("");
+      drop_scales(cur[0].vs, bad & 15u);
+      drop_scales(cur[1].vs, bad >> 4);
     }
     float top = sc[0];
 #pragma unroll
@@ -423,30 +536,33 @@ __global__ __launch_bounds__(kAttBlock) void attend_kernel(AttendArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] *= f;
     }
+    const float base = m - kPScaleLog2;
     U32x4 pf;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float p0 = __builtin_amdgcn_exp2f(sc[2 * i] - m + kPScaleLog2), p1 = __builtin_amdgcn_exp2f(sc[2 * i + 1] - m + kPScaleLog2);
+      const float p0 = __builtin_amdgcn_exp2f(sc[2 * i] - base), p1 = __builtin_amdgcn_exp2f(sc[2 * i + 1] - base);
       sum += p0 + p1;
       pf.v[i] = u2((f16x2){(_Float16)p0, (_Float16)p1});
     }
-    U32x4 vf[8];
+    uint32_t v0[8][2], v1[8][2];
+    value_operands<BITS>(cur[0], v0);
+    value_operands<BITS>(cur[1], v1);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int i = 0; i < 8; ++i) {
+      const U32x4 v = {{v0[i][0], v0[i][1], v1[i][0], v1[i][1]}};
+      o[i] = mfma(frag(v), frag(pf), o[i]);
+    }
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        f16x2 c[8];
-        token_pairs<BITS>(sh[u].v + (2 * w) * (BITS / 4), sh[u].v + (2 * w + 1) * (BITS / 4), c);
-        const f16x2 d = h2(sh[u].vs[w]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) vf[i].v[2 * u + w] = u2(c[i] * d);
-      }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(frag(vf[i]), frag(pf), o[i], 0, 0, 0);
+    for (int u = 0; u < 2; ++u) {
+      cur[u] = nxt[u];
+      pg[u] = pn[u];
+      pn[u] = pa[u];
+    }
   }
 
   // the wavefronts' parts, joined in order
   sum = blocks_sum(sum);
+  poison = blocks_sum(poison);
   if (b4 == 0) {
     s_m[wave][n] = m;
     s_l[wave][n] = sum;
@@ -456,114 +572,409 @@ __global__ __launch_bounds__(kAttBlock) void attend_kernel(AttendArgs a) {
 #pragma unroll
   for (int w = 1; w < kAttWaves; ++w) mm = fmaxf(mm, s_m[w][n]);
   const float f = __builtin_amdgcn_exp2f(m - mm);
-  for (uint32_t w = 0; w < kAttWaves; ++w) {
-    if (w == wave) {
+  if (n < rows) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float& d = s_o[n][8 * (4 * b4 + r) + i];
-          d = w ? d + o[i][r] * f : o[i][r] * f;
-        }
-    }
-    __syncthreads();
+      for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<f32x4*>(&s_o[wave][n][8 * (4 * b4 + r) + i]) =
+            (f32x4){o[i][r] * f + poison, o[i + 1][r] * f + poison, o[i + 2][r] * f + poison, o[i + 3][r] * f + poison};
   }
-  const uint64_t part = item * a.splits + split;
-  for (uint32_t i = threadIdx.x; i < 16u * kD / 4u; i += kAttBlock) {
-    const uint32_t row = i >> 5, c = 4u * (i & 31u);
-    *reinterpret_cast<f32x4*>(a.po + (part * 16 + row) * kD + c) = *reinterpret_cast<const f32x4*>(&s_o[row][c]);
+  __syncthreads();
+  const uint32_t r = threadIdx.x >> 4;
+  if (r >= rows) return;
+  float total = 0.0f, mr = s_m[0][r], y[8];
+#pragma unroll
+  for (int w = 1; w < kAttWaves; ++w) mr = fmaxf(mr, s_m[w][r]);
+#pragma unroll
+  for (int w = 0; w < kAttWaves; ++w) total += s_l[w][r] * __builtin_amdgcn_exp2f(s_m[w][r] - mr);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = s_o[0][r][8 * n + i];
+#pragma unroll
+  for (int w = 1; w < kAttWaves; ++w)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] += s_o[w][r][8 * n + i];
+  if (a.splits == 1) {
+    if (n == 0) a.lse[item * 16u + r] = mr + __builtin_amdgcn_logf(total) - kPScaleLog2;
+    store_row<BITS>(a, K, s, it.h, r, n, lane_inverse(K, n), y, total);
+    return;
   }
-  if (threadIdx.x < 16) {
-    float l = 0.0f;
-    for (int w = 0; w < kAttWaves; ++w) l += s_l[w][n] * __builtin_amdgcn_exp2f(s_m[w][n] - mm);
-    a.pml[(part * 16 + n) * 2] = mm;
-    a.pml[(part * 16 + n) * 2 + 1] = l;
-  }
+  const uint64_t p = ((uint64_t)item * a.splits + split) * 16u + r;
+  *reinterpret_cast<f32x4*>(a.po + p * kD + 8 * n) = (f32x4){y[0], y[1], y[2], y[3]};
+  *reinterpret_cast<f32x4*>(a.po + p * kD + 8 * n + 4) = (f32x4){y[4], y[5], y[6], y[7]};
+  if (n == 0) *reinterpret_cast<f32x2*>(a.pml + p * 2) = (f32x2){mr, total};
 }
 
-// Joins a row's splits, turns it back and stores it: 16 lanes a row.
+// Joins a row's splits, turns it back and stores it: one workgroup a row, its 16 groups of 16 lanes take the
+// splits in turn.
 template <int BITS>
-__global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables K) {
-  const uint32_t l = threadIdx.x & 15u;
-  const uint64_t rowid = (uint64_t)blockIdx.x * (kAttBlock / 16) + (threadIdx.x >> 4);
-  const uint64_t item = rowid >> 4;
-  if (item >= (uint64_t)a.seqs * a.heads * a.tiles) return;
-  const uint32_t tile = (uint32_t)(item % a.tiles), h = (uint32_t)(item / a.tiles % a.heads), b = (uint32_t)(item / a.tiles / a.heads);
-  const Seq s = seq_of(a, b);
-  const uint32_t r = tile * 16u + (uint32_t)(rowid & 15u);
-  if (tile * 16u >= (uint32_t)s.m * a.group) return;
+__global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables K, uint32_t rows_per_item) {
+  __shared__ float s_y[16][kD + 4], s_m[16], s_l[16];
+  const uint32_t l = threadIdx.x & 15u, g = threadIdx.x >> 4;
+  const uint32_t item = blockIdx.x / rows_per_item, row = blockIdx.x % rows_per_item;
+  const Item it = item_of(a, item);
+  const Seq s = seq_of(a, it.b);
+  const uint32_t r = it.tile * a.tile_rows + row;
+  if (r >= (uint32_t)s.m * a.group) return;
   int32_t lo, hi;
-  tile_range(a, s, tile, &lo, &hi);
+  rows_range(a, s, it.tile * a.tile_rows, a.tile_rows, &lo, &hi);
+  if (a.pages == 0) hi = lo;
   const uint32_t s0 = hi > lo ? (uint32_t)lo / a.chunk : 0u, s1 = hi > lo ? ((uint32_t)hi + a.chunk - 1u) / a.chunk : 0u;
-  float m = -1.0e30f;
-  for (uint32_t i = s0; i < s1; ++i) m = fmaxf(m, a.pml[((item * a.splits + i) * 16 + (rowid & 15u)) * 2]);
-  float sum = 0.0f, y[8], x[8];
+  float m = -1.0e30f, sum = 0.0f, y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-  for (uint32_t i = s0; i < s1; ++i) {
-    const uint64_t p = (item * a.splits + i) * 16 + (rowid & 15u);
-    const float f = __builtin_amdgcn_exp2f(a.pml[p * 2] - m);
-    sum += a.pml[p * 2 + 1] * f;
+  for (uint32_t i = s0 + g; i < s1; i += 16) {
+    const uint64_t p = ((uint64_t)item * a.splits + i) * a.tile_rows + row;
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(a.pml + p * 2);
     const f32x4 u0 = *reinterpret_cast<const f32x4*>(a.po + p * kD + 8 * l), u1 = *reinterpret_cast<const f32x4*>(a.po + p * kD + 8 * l + 4);
+    const float mn = fmaxf(m, ml[0]), f0 = __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(ml[0] - mn);
+    m = mn;
+    sum = sum * f0 + ml[1] * f1;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      y[c] += u0[c] * f;
-      y[4 + c] += u1[c] * f;
+      y[c] = y[c] * f0 + u0[c] * f1;
+      y[4 + c] = y[4 + c] * f0 + u1[c] * f1;
     }
   }
-  if (l == 0) a.lse[rowid] = m + __builtin_amdgcn_logf(sum) - kPScaleLog2;
-  const float inv = sum == 0.0f ? 0.0f : unit<BITS>() / sum;  // a row that sees nothing is 0
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = (y[i] * inv) * K.v[8 * l + i];
-  const LaneInverse f = lane_inverse(K, l);
-  inverse_row(y, x, l, f);
-  if (r >= (uint32_t)s.m * a.group) return;
-  const uint64_t at = ((uint64_t)(s.q0 + r / a.group) * a.q_heads + h * a.group + r % a.group) * kD;
+  for (int i = 0; i < 8; ++i) s_y[g][8 * l + i] = y[i];
+  if (l == 0) {
+    s_m[g] = m;
+    s_l[g] = sum;
+  }
+  __syncthreads();
+  if (g) return;
+  m = s_m[0];
+  for (int i = 1; i < 16; ++i) m = fmaxf(m, s_m[i]);
+  sum = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint64_t i = at + 2u * inverse_n(l, e);
-    if (a.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(a.out) + i) = make_float2(x[2 * e], x[2 * e + 1]);
-    else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + i) = bf16_pair(x[2 * e], x[2 * e + 1]);
+  for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+  for (int i = 0; i < 16; ++i) {
+    const float f = __builtin_amdgcn_exp2f(s_m[i] - m);
+    sum += s_l[i] * f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) y[c] += s_y[i][8 * l + c] * f;
+  }
+  if (l == 0) a.lse[(uint64_t)item * a.tile_rows + row] = m + __builtin_amdgcn_logf(sum) - kPScaleLog2;
+  store_row<BITS>(a, K, s, it.h, r, l, lane_inverse(K, l), y, sum);
+}
+
+// Accumulated weights of up to 16 rows, from the stored scores: a thread owns a token.
+__global__ __launch_bounds__(kAttBlock) void weights_few_kernel(AttendArgs a, uint32_t blocks) {
+  const uint32_t bh = blockIdx.x / blocks, b = bh / a.heads;
+  const Seq s = seq_of(a, b);
+  const uint32_t rows = (uint32_t)s.m * a.group;
+  const int32_t t = (int32_t)((blockIdx.x % blocks) * kAttBlock + threadIdx.x);
+  int32_t lo, hi;
+  rows_range(a, s, 0, 16, &lo, &hi);
+  if (a.pages == 0 || t < (lo & ~15) || t >= hi) return;
+  float w = 0.0f;
+  for (uint32_t r = 0; r < rows; ++r) {
+    const float sc = a.scores[((uint64_t)bh * a.wrows + r) * a.wpad + (uint32_t)t];
+    if (sc != -__builtin_inff()) w += __builtin_amdgcn_exp2f(sc - a.lse[(uint64_t)bh * 16u + r]);
+  }
+  a.weights[(uint64_t)bh * a.wstride + (uint32_t)t] += w;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Many rows: the queries' rows transformed once, to the workspace.
+template <int BITS>
+__global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Tables K, int parts) {
+  __shared__ __align__(16) _Float16 s_q[2][16][kD + 8];
+  const uint32_t l = threadIdx.x & 15u, g = threadIdx.x >> 4, per = a.tile_rows / 16u;
+  const uint32_t item = blockIdx.x / per, row = (blockIdx.x % per) * 16u + g;
+  const Item it = item_of(a, item);
+  const Seq s = seq_of(a, it.b);
+  if (it.tile * a.tile_rows + (row & ~15u) >= (uint32_t)s.m * a.group) return;
+  const float f = rotate_row<BITS>(a, K, s, it.h, it.tile * a.tile_rows + row, l, lane_forward(K, l), s_q[0][g], parts == 2 ? s_q[1][g] : nullptr);
+  const uint64_t at = (uint64_t)item * a.tile_rows + row;
+  if (l == 0) a.qf[at] = f;
+  // a row is written and read by the same wavefront
+  wave_sync();
+  *reinterpret_cast<f16x8*>(a.qhi + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[0][g][8 * l]);
+  if (parts == 2) *reinterpret_cast<f16x8*>(a.qlo + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[1][g][8 * l]);
+}
+
+// Many rows: a workgroup takes 64 R rows of a (sequence, head) and one split of the tokens; each wavefront
+// owns 16 R rows.  64 tokens at a time are made operands once, 16 by each wavefront, into LDS in the
+// order the products read them (lane after lane, 16 bytes each: no bank conflict), while the previous 64
+// are multiplied; the next ones' codes are in flight meanwhile.  At R = 4 each operand read from LDS feeds
+// four products, so LDS (128 bytes a clock) is half busy when the matrix cores are full.
+template <int BITS, bool PREC, int R>
+__global__ __launch_bounds__(kAttBlock, R == 4 ? 1 : 2) void attend_many_kernel(AttendArgs a, Tables K) {
+  constexpr int kK = PREC ? 2 : 1;
+  struct Stage {
+    f16x8 k[kK][4][4][64];  // [part][16 tokens][step][lane]
+    f16x8 v[2][8][64];      // [32 tokens][coordinate][lane]
+  };
+  union Lds {
+    Stage st[2];
+    float o[kAttWaves][16][kPad];
+  };
+  extern __shared__ __align__(16) uint8_t raw[];
+  Lds& sm = *reinterpret_cast<Lds*>(raw);
+  __shared__ uint32_t s_bad[2][4];  // bits 0..15: tokens with NaN value scales; bit 16: absent
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, n = lane & 15u, b4 = lane >> 4;
+  // the last tiles see the most tokens under the causal mask: they go first
+  const uint32_t split = blockIdx.x % a.splits, item = gridDim.x / a.splits - 1u - blockIdx.x / a.splits;
+  const uint32_t sh_i = item % (a.seqs * a.heads);
+  const Item it = {item / (a.seqs * a.heads), sh_i % a.heads, sh_i / a.heads};
+  const uint64_t slot = ((uint64_t)it.b * a.heads + it.h) * a.tiles + it.tile;  // the item's place in the workspace
+  const Seq s = seq_of(a, it.b);
+  const uint32_t rows = (uint32_t)s.m * a.group, r0 = it.tile * a.tile_rows, w0 = r0 + wave * 16u * R;
+  if (r0 >= rows) return;
+  int32_t lo, hi, wlo, whi, all_lo, all_hi;
+  rows_range(a, s, r0, a.tile_rows, &lo, &hi);
+  rows_range(a, s, w0, 16u * R, &wlo, &whi);
+  rows_common(a, s, w0, 16u * R, &all_lo, &all_hi);
+  int32_t t0 = (int32_t)(split * a.chunk), t1 = t0 + (int32_t)a.chunk;
+  t0 = t0 > (lo & ~15) ? t0 : lo & ~15;
+  t1 = t1 < hi ? t1 : hi;
+  if (a.pages == 0) t1 = t0;
+  if (t0 >= t1 && a.splits > 1) return;
+  const uint32_t P = 1u << a.page_log2;
+  const uint64_t page_size = (uint64_t)P * Page<BITS>::kToken;
+
+  Share<BITS> sh;
+  auto load = [&](int32_t t, int32_t page) __attribute__((always_inline)) {
+    const uint8_t* p = a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + it.h) * page_size;
+    load_keys<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
+    load_values<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
+  };
+  // this wavefront's 16 of the 64 tokens at t, as operands
+  auto stage = [&](Stage& d, uint32_t* flags, int32_t t, int32_t page) __attribute__((always_inline)) {
+    f16x8 kh[4], kl[4];
+    key_operands<BITS, PREC>(sh, kh, kl);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      d.k[0][wave][j][lane] = kh[j];
+      if (PREC) d.k[kK - 1][wave][j][lane] = kl[j];
+    }
+    if (page < 0 || t < lo || t + 16 > t1) {  // a token that no row sees may hold anything
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int32_t tok = t + 4 * (int32_t)b4 + i;
+        if (page < 0 || tok < lo || tok >= t1) drop_scales(sh.vs, 1u << i);
+      }
+    }
+    uint32_t word = page < 0 ? 0x10000u : 0u;
+    const uint32_t bad = bad_scales(sh.vs);
+    if (__builtin_amdgcn_ballot_w64(bad != 0)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t votes = __builtin_amdgcn_ballot_w64((bad >> i) & 1u);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) word |= (votes >> (16 * q)) & 0xFFFFu ? 1u << (4 * q + i) : 0u;
+      }
+      drop_scales(sh.vs, bad);
+    }
+    if (lane == 0) flags[wave] = word;
+    uint32_t v[8][2];
+    value_operands<BITS>(sh, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      reinterpret_cast<uint2*>(&d.v[wave >> 1][i][lane])[wave & 1u] = make_uint2(v[i][0], v[i][1]);
+  };
+  int32_t t = t0, page = page_of(a, it.b, t + 16 * (int32_t)wave, t1);
+  if (t < t1) load(t + 16 * (int32_t)wave, page);
+  int32_t next = page_of(a, it.b, t + 64 + 16 * (int32_t)wave, t1);
+
+  f16x8 qh[R][4], ql[R][4];
+  float qf[R], m[R], sum[R], poison[R];
+  int32_t row_lo[R], row_hi[R];
+  f32x4 o[R][8];
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const uint64_t row = slot * a.tile_rows + wave * 16u * R + 16u * q + n;
+    const bool have = w0 + 16u * q < rows;  // 16 rows are transformed together, the last ones as zeros
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      qh[q][j] = ql[q][j] = (f16x8)(_Float16)0.0f;
+      if (have) qh[q][j] = *reinterpret_cast<const f16x8*>(a.qhi + row * kD + 8 * (4 * b4 + j));
+      if (PREC && have) ql[q][j] = *reinterpret_cast<const f16x8*>(a.qlo + row * kD + 8 * (4 * b4 + j));
+    }
+    qf[q] = have ? a.qf[row] : 0.0f;
+    m[q] = -1.0e30f;
+    sum[q] = poison[q] = 0.0f;
+    row_lo[q] = row_hi[q] = 0;
+    if (w0 + 16u * q + n < rows) visible(a, s, (int32_t)((w0 + 16u * q + n) / a.group), &row_lo[q], &row_hi[q]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[q][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  if (t < t1) stage(sm.st[0], s_bad[0], t + 16 * (int32_t)wave, page);
+  __syncthreads();
+  for (uint32_t buf = 0; t < t1; t += 64, buf ^= 1u) {
+    const bool more = t + 64 < t1;
+    if (more) {
+      page = next;
+      load(t + 64 + 16 * (int32_t)wave, page);
+      next = page_of(a, it.b, t + 128 + 16 * (int32_t)wave, t1);
+    }
+    if (t < whi && t + 64 > wlo) {
+      const Stage& d = sm.st[buf];
+      f32x4 sc[R][4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) sc[q][u] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f16x8 kh = d.k[0][u][j][lane];
+          if (PREC) {
+            const f16x8 kl = d.k[kK - 1][u][j][lane];
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+              sc[q][u] = mfma(kl, qh[q][j], sc[q][u]);
+              sc[q][u] = mfma(kh, ql[q][j], sc[q][u]);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < R; ++q) sc[q][u] = mfma(kh, qh[q][j], sc[q][u]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < R; ++q)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sc[q][u] *= qf[q];
+      if (a.cap_in > 0.0f) {
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[q][u][i] = capped(a, sc[q][u][i]);
+      }
+      const uint32_t fl[4] = {s_bad[buf][0], s_bad[buf][1], s_bad[buf][2], s_bad[buf][3]};
+      const bool flagged = __builtin_amdgcn_readfirstlane(fl[0] | fl[1] | fl[2] | fl[3]) != 0;
+      if (flagged || t < all_lo || t + 64 > all_hi || t + 64 > t1) {
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int32_t tok = t + 16 * u + 4 * (int32_t)b4 + i;
+              if ((fl[u] & 0x10000u) || tok < row_lo[q] || tok >= row_hi[q] || tok >= t1) sc[q][u][i] = -__builtin_inff();
+              else if ((fl[u] >> (4 * b4 + i)) & 1u) poison[q] = __builtin_nanf("");
+            }
+      }
+      float top[R];
+      bool rise = false;
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        top[q] = sc[q][0][0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top[q] = fmaxf(top[q], sc[q][i >> 2][i & 3]);
+        rise |= top[q] > m[q] + kSlack;
+      }
+      if (__builtin_amdgcn_ballot_w64(rise)) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          const float mn = fmaxf(m[q], blocks_max(top[q]));
+          const float f = __builtin_amdgcn_exp2f(m[q] - mn);
+          m[q] = mn;
+          sum[q] *= f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[q][i] *= f;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        f16x8 pf[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          const float base = m[q] - kPScaleLog2;
+          U32x4 p;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int u = 2 * w + (i >> 1), c = 2 * (i & 1);
+            const float p0 = __builtin_amdgcn_exp2f(sc[q][u][c] - base), p1 = __builtin_amdgcn_exp2f(sc[q][u][c + 1] - base);
+            sum[q] += p0 + p1;
+            p.v[i] = u2((f16x2){(_Float16)p0, (_Float16)p1});
+          }
+          pf[q] = frag(p);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const f16x8 v = d.v[w][i][lane];
+#pragma unroll
+          for (int q = 0; q < R; ++q) o[q][i] = mfma(v, pf[q], o[q][i]);
+        }
+      }
+    }
+    if (more) stage(sm.st[buf ^ 1u], s_bad[buf ^ 1u], t + 64 + 16 * (int32_t)wave, page);
+    __syncthreads();
+  }
+
+  // each wavefront's rows, 16 at a time, through its part of LDS: a row's values to 16 lanes
+  const LaneInverse inv = lane_inverse(K, n);
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const float total = blocks_sum(sum[q]), bad = blocks_sum(poison[q]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<f32x4*>(&sm.o[wave][n][8 * (4 * b4 + r) + i]) =
+            (f32x4){o[q][i][r] + bad, o[q][i + 1][r] + bad, o[q][i + 2][r] + bad, o[q][i + 3][r] + bad};
+    const uint32_t first = wave * 16u * R + 16u * q;
+    const uint64_t row = slot * a.tile_rows + first;
+    if (a.splits == 1) {
+      if (b4 == 0) a.lse[row + n] = m[q] + __builtin_amdgcn_logf(total) - kPScaleLog2;
+    } else if (b4 == 0) {
+      *reinterpret_cast<f32x2*>(a.pml + (((slot * a.splits + split) * a.tile_rows) + first + n) * 2) = (f32x2){m[q], total};
+    }
+    wave_sync();
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint32_t r = 4u * k + b4;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = sm.o[wave][r][8 * n + i];
+      const float tr = row_get_any(total, r);
+      if (a.splits == 1) {
+        if (w0 + 16u * q + 4u * k < rows) store_row<BITS>(a, K, s, it.h, w0 + 16u * q + r, n, inv, y, tr);
+      } else {
+        float* d = a.po + ((slot * a.splits + split) * a.tile_rows + first + r) * kD + 8 * n;
+        *reinterpret_cast<f32x4*>(d) = (f32x4){y[0], y[1], y[2], y[3]};
+        *reinterpret_cast<f32x4*>(d + 4) = (f32x4){y[4], y[5], y[6], y[7]};
+      }
+    }
+    wave_sync();
   }
 }
 
-// Accumulated weights: a wavefront owns 32 tokens of a (sequence, head), forms their scores with every
-// row again and adds the sum of exp(s - lse) over the rows, in a fixed order.
+// Accumulated weights of many rows: a wavefront owns 64 tokens of a (sequence, head), keeps their keys as
+// operands, forms their scores with every row again and adds the sum of exp(s - lse) over the rows, in a
+// fixed order.
 template <int BITS>
-__global__ __launch_bounds__(kAttBlock) void weights_kernel(AttendArgs a, uint32_t blocks) {
+__global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a, uint32_t blocks) {
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, n = lane & 15u, b4 = lane >> 4;
   const uint32_t bh = blockIdx.x / blocks, h = bh % a.heads, b = bh / a.heads;
   const Seq s = seq_of(a, b);
-  const int32_t t = (int32_t)((blockIdx.x % blocks) * 32u * kAttWaves + 32u * wave);
-  if (t >= s.n) return;
+  const int32_t t = (int32_t)((blockIdx.x % blocks) * 64u * kAttWaves + 64u * wave);
+  const uint32_t rows = (uint32_t)s.m * a.group;
+  if (t >= s.n || a.pages == 0) return;
   const uint32_t P = 1u << a.page_log2;
   const uint64_t page_size = (uint64_t)P * Page<BITS>::kToken;
-  Share<BITS> sh[2];
-  bool there[2];
+  f16x8 kh[4][4], kl[4][4];
+  bool there[4];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int32_t tt = t + 16 * u;
-    int32_t page = -1;
-    if (tt < s.n) page = a.table[(uint64_t)b * a.width + ((uint32_t)tt >> a.page_log2)];
-    page = __builtin_amdgcn_readfirstlane(page);
-    there[u] = page >= 0 && (uint32_t)page < a.pages;
-    if (there[u]) {
-      load_keys<BITS>(a.cache + ((uint64_t)page * a.heads + h) * page_size, P, (uint32_t)tt & (P - 1u), lane, sh[u]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < BITS; ++i) sh[u].k[i] = 0u;
-      sh[u].ks[0] = sh[u].ks[1] = 0u;
-    }
+  for (int u = 0; u < 4; ++u) {
+    const int32_t page = page_of(a, b, t + 16 * u, s.n);
+    there[u] = page >= 0;
+    Share<BITS> sh;
+    load_keys<BITS>(a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + h) * page_size, P, (uint32_t)(t + 16 * u) & (P - 1u), lane, sh);
+    key_operands<BITS, true>(sh, kh[u], kl[u]);
   }
-  float acc[8];
+  float acc[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-  const uint32_t rows = (uint32_t)s.m * a.group;
-  for (uint32_t tile = 0; tile * 16u < rows; ++tile) {
-    int32_t lo, hi;
-    tile_range(a, s, tile, &lo, &hi);
-    if (t >= hi || t + 32 <= lo) continue;
-    const uint64_t item = ((uint64_t)b * a.heads + h) * a.tiles + tile, row = item * 16 + n;
+  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+  for (uint32_t r0 = 0; r0 < rows; r0 += 16) {
+    int32_t lo, hi, all_lo, all_hi;
+    rows_range(a, s, r0, 16, &lo, &hi);
+    if (t >= hi || t + 64 <= lo) continue;
+    rows_common(a, s, r0, 16, &all_lo, &all_hi);
+    const uint64_t row = (uint64_t)bh * a.tiles * a.tile_rows + r0 + n;
     f16x8 qh[4], ql[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -572,27 +983,28 @@ __global__ __launch_bounds__(kAttBlock) void weights_kernel(AttendArgs a, uint32
     }
     const float qf = a.qf[row], lse = a.lse[row];
     int32_t row_lo = 0, row_hi = 0;
-    if (tile * 16u + n < rows) visible(a, s, (int32_t)((tile * 16u + n) / a.group), &row_lo, &row_hi);
+    if (r0 + n < rows) visible(a, s, (int32_t)((r0 + n) / a.group), &row_lo, &row_hi);
+    const bool whole = t >= all_lo && t + 64 <= all_hi;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const f32x4 r = scores16<BITS, true>(sh[u], qh, ql);
+    for (int u = 0; u < 4; ++u) {
+      const f32x4 r = scores16<true>(kh[u], kl[u], qh, ql);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int32_t tok = t + 16 * u + 4 * (int32_t)b4 + i;
         const float p = __builtin_amdgcn_exp2f(capped(a, r[i] * qf) - lse);
-        acc[4 * u + i] += there[u] && tok >= row_lo && tok < row_hi ? p : 0.0f;
+        acc[4 * u + i] += there[u] && (whole || (tok >= row_lo && tok < row_hi)) ? p : 0.0f;
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 16; ++i) {
     float x = acc[i];
     x += lane_xor<1>(x);
     x += lane_xor<2>(x);
     x += lane_xor<4>(x);
     x += lane_xor<8>(x);
     const int32_t tok = t + 16 * (i >> 2) + 4 * (int32_t)b4 + (i & 3);
-    if (n == 0 && tok < s.n) a.weights[((uint64_t)b * a.heads + h) * a.wstride + (uint32_t)tok] += x;
+    if (n == 0 && tok < s.n) a.weights[(uint64_t)bh * a.wstride + (uint32_t)tok] += x;
   }
 }
 
@@ -604,21 +1016,26 @@ namespace {
 
 uint64_t align256(uint64_t v) { return (v + 255u) & ~(uint64_t)255u; }
 
-// How a call is cut: row tiles, splits of the longest sequence, and the workspace they take.
+// How a call is cut: rows a tile, row tiles, splits of the longest sequence, and the workspace they take.
 struct Plan {
   uint64_t items;
-  uint32_t tiles, splits, chunk;
-  uint64_t qhi, qlo, qf, po, pml, lse, bytes;
+  uint32_t tile_rows, tiles, splits, chunk, wrows, wpad;
+  uint64_t qhi, qlo, qf, po, pml, lse, scores, bytes;
 };
 
 Plan plan_of(const hq_kv_cache& c, const hq_kv_attend_args& g) {
   Plan p;
-  const uint32_t group = g.q_heads / c.heads;
-  p.tiles = (uint32_t)(((uint64_t)g.max_q * group + 15) / 16);
+  const uint32_t rows = g.max_q * (g.q_heads / c.heads);
+  // up to 16 rows: one tile, split over many workgroups; beyond, 64 rows a workgroup, and 256 where that
+  // still leaves no workgroup mostly idle
+  p.tile_rows = rows <= 16 ? 16 : rows <= 128 ? 64 : g.weights ? 128 : 256;
+  p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   p.items = (uint64_t)g.seqs * c.heads * p.tiles;
-  // enough workgroups for four a CU, no less than 256 tokens each
-  const uint64_t want = 1024, most = (g.max_len + 255) / 256;
-  uint64_t splits = p.items ? (want + p.items - 1) / p.items : 1;
+  const bool few = rows <= 16;
+  // enough workgroups to fill the chip (256 CUs; single tokens: several a CU, so that ragged lengths even
+  // out), each with enough tokens to be worth its start and its part of the join
+  const uint64_t want = few ? 2048 : 512, least = few ? 256 : 512;
+  uint64_t splits = p.items ? (want + p.items - 1) / p.items : 1, most = (g.max_len + least - 1) / least;
   if (splits > most) splits = most;
   if (splits < 1) splits = 1;
   uint64_t chunk = (g.max_len + splits - 1) / splits;
@@ -627,27 +1044,69 @@ Plan plan_of(const hq_kv_cache& c, const hq_kv_attend_args& g) {
   p.chunk = (uint32_t)chunk;
   p.splits = (uint32_t)((g.max_len + chunk - 1) / chunk);
   if (p.splits == 0) p.splits = 1;
+  p.wrows = few && g.weights ? rows : 0;
+  p.wpad = (g.max_len + 31u) / 16u * 16u;  // whole blocks of 16 from any block's start
   uint64_t at = 0;
   auto take = [&](uint64_t n) {
     const uint64_t here = at;
     at = align256(at + n);
     return here;
   };
-  p.qhi = take(p.items * 16 * kD * 2);
-  p.qlo = take(p.items * 16 * kD * 2);
-  p.qf = take(p.items * 16 * 4);
-  p.lse = take(p.items * 16 * 4);
-  p.pml = take(p.items * p.splits * 16 * 8);
-  p.po = take(p.items * p.splits * 16 * kD * 4);
+  const uint64_t r = p.items * p.tile_rows, parts = p.splits > 1 ? r * p.splits : 0;
+  p.lse = take(r * 4);
+  p.qf = take(few ? 0 : r * 4);
+  p.qhi = take(few ? 0 : r * kD * 2);
+  p.qlo = take(few || !g.weights ? 0 : r * kD * 2);
+  p.pml = take(parts * 8);
+  p.po = take(parts * kD * 4);
+  p.scores = take(p.items * p.wrows * (uint64_t)p.wpad * 4);
   p.bytes = at;
   return p;
+}
+
+template <int BITS, bool PREC, int R>
+hipError_t launch_many(const AttendArgs& a, const Tables& T, uint32_t grid, hipStream_t st) {
+  const size_t stage = (PREC ? 2 : 1) * 16384 + 16384, lds = 2 * stage;
+  static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_many_kernel<BITS, PREC, R>),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (set != hipSuccess) return set;
+  hipLaunchKernelGGL((attend_many_kernel<BITS, PREC, R>), dim3(grid), dim3(kAttBlock), lds, st, a, T);
+  return hipSuccess;
+}
+
+template <int BITS>
+hipError_t launch_attend(const AttendArgs& a, const Tables& T, uint32_t items, hipStream_t st) {
+  const dim3 block(kAttBlock);
+  const bool prec = a.weights != nullptr;
+  const uint32_t grid = items * a.splits, rows = a.max_q * a.group;
+  if (a.tile_rows == 16) {
+    if (prec) hipLaunchKernelGGL((attend_few_kernel<BITS, true>), dim3(grid), block, 0, st, a, T);
+    else hipLaunchKernelGGL((attend_few_kernel<BITS, false>), dim3(grid), block, 0, st, a, T);
+  } else {
+    hipLaunchKernelGGL((rotate_rows_kernel<BITS>), dim3(items * (a.tile_rows / 16)), block, 0, st, a, T, prec ? 2 : 1);
+    hipError_t e;
+    if (a.tile_rows == 64) e = prec ? launch_many<BITS, true, 1>(a, T, grid, st) : launch_many<BITS, false, 1>(a, T, grid, st);
+    else e = prec ? launch_many<BITS, true, 2>(a, T, grid, st) : launch_many<BITS, false, 4>(a, T, grid, st);
+    if (e != hipSuccess) return e;
+  }
+  if (a.splits > 1) {
+    const uint32_t per = rows < a.tile_rows ? rows : a.tile_rows;
+    hipLaunchKernelGGL((combine_kernel<BITS>), dim3(items * per), block, 0, st, a, T, per);
+  }
+  if (prec && a.max_len) {
+    const uint32_t step = a.tile_rows == 16 ? kAttBlock : 64u * kAttWaves, blocks = (a.max_len + step - 1) / step;
+    const dim3 wg(a.seqs * a.heads * blocks);
+    if (a.tile_rows == 16) hipLaunchKernelGGL(weights_few_kernel, wg, block, 0, st, a, blocks);
+    else hipLaunchKernelGGL((weights_many_kernel<BITS>), wg, block, 0, st, a, blocks);
+  }
+  return hipGetLastError();
 }
 
 int check_attend(const hq_kv_cache* cache, const hq_kv_attend_args* g) {
   if (int rc = check_cache(cache)) return rc;
   if (!g || g->q_heads == 0 || g->q_heads % cache->heads || g->q_heads > 65535u * 16u) return HQ_ERR_INVALID_ARG;
   if (g->max_len > 0x7FFFFFFFu || (uint64_t)g->table_width * cache->page > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
-  if (g->total_q > (1ull << 31) || (uint64_t)g->max_q * (g->q_heads / cache->heads) > 0x7FFFFFF0ull) return HQ_ERR_INVALID_ARG;
+  if (g->total_q > (1ull << 31) || (uint64_t)g->max_q * (g->q_heads / cache->heads) > 0x7FFFFF00ull) return HQ_ERR_INVALID_ARG;
   if (!g->q_start && g->seqs && g->total_q % g->seqs) return HQ_ERR_INVALID_ARG;
   return HQ_OK;
 }
@@ -672,8 +1131,6 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   if (g.weights && g.weights_stride < g.max_len) return HQ_ERR_INVALID_ARG;
   Tables T;
   if (!make_tables(*cache, false, &T)) return HQ_ERR_INVALID_ARG;
-  // forward multipliers of the queries: the orthogonal packing's factor times the keys' lambda
-  for (int c = 0; c < kD; ++c) T.k[c] *= c < 2 ? (float)(1.0 / std::sqrt(128.0)) : 0.0625f;
   if (g.total_q == 0 || g.seqs == 0 || g.max_q == 0) return HQ_OK;
   if (!g.q || !g.out || !g.lens || (g.max_len && g.table_width && !g.table)) return HQ_ERR_INVALID_ARG;
   const uint32_t size = g.q_dtype == HQ_F32 ? 4u : 2u;
@@ -681,7 +1138,8 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   if (((uintptr_t)g.lens | (uintptr_t)g.table | (uintptr_t)g.q_start | (uintptr_t)g.weights) & 3u) return HQ_ERR_INVALID_ARG;
   const Plan p = plan_of(*cache, g);
   if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < p.bytes) return HQ_ERR_INVALID_ARG;
-  if (p.items * p.splits > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  if (p.items * p.splits > 0x7FFFFFFFull || p.items * p.tile_rows > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  if ((uint64_t)g.seqs * cache->heads * ((g.max_len + 255u) / 256u) > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
   AttendArgs a;
   a.cache = static_cast<const uint8_t*>(cache->data);
   a.q = g.q;
@@ -703,7 +1161,10 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   a.seqs = g.seqs;
   a.max_q = g.max_q;
   a.max_len = g.max_len;
+  a.tile_rows = p.tile_rows;
   a.tiles = p.tiles;
+  a.wrows = p.wrows;
+  a.wpad = p.wpad;
   a.splits = p.splits;
   a.chunk = p.chunk;
   a.window = g.window;
@@ -721,26 +1182,11 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   a.qf = reinterpret_cast<float*>(w + p.qf);
   a.lse = reinterpret_cast<float*>(w + p.lse);
   a.pml = reinterpret_cast<float*>(w + p.pml);
+  a.scores = p.wrows ? reinterpret_cast<float*>(w + p.scores) : nullptr;
   a.po = reinterpret_cast<float*>(w + p.po);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const dim3 rows((uint32_t)p.items), grid((uint32_t)(p.items * p.splits)), block(kAttBlock);
-  const bool prec = g.weights != nullptr;
-  if (cache->bits == 4) hipLaunchKernelGGL(rotate_rows_kernel<4>, rows, block, 0, st, a, T);
-  else hipLaunchKernelGGL(rotate_rows_kernel<8>, rows, block, 0, st, a, T);
-  if (cache->bits == 4 && prec) hipLaunchKernelGGL((attend_kernel<4, true>), grid, block, 0, st, a);
-  else if (cache->bits == 4) hipLaunchKernelGGL((attend_kernel<4, false>), grid, block, 0, st, a);
-  else if (prec) hipLaunchKernelGGL((attend_kernel<8, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((attend_kernel<8, false>), grid, block, 0, st, a);
-  if (cache->bits == 4) hipLaunchKernelGGL(combine_kernel<4>, rows, block, 0, st, a, T);
-  else hipLaunchKernelGGL(combine_kernel<8>, rows, block, 0, st, a, T);
-  if (prec && g.max_len) {
-    const uint32_t blocks = (g.max_len + 32u * kAttWaves - 1) / (32u * kAttWaves);
-    const uint64_t wg = (uint64_t)g.seqs * cache->heads * blocks;
-    if (wg > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
-    if (cache->bits == 4) hipLaunchKernelGGL(weights_kernel<4>, dim3((uint32_t)wg), block, 0, st, a, blocks);
-    else hipLaunchKernelGGL(weights_kernel<8>, dim3((uint32_t)wg), block, 0, st, a, blocks);
-  }
-  return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
+  const hipError_t e = cache->bits == 4 ? launch_attend<4>(a, T, (uint32_t)p.items, st) : launch_attend<8>(a, T, (uint32_t)p.items, st);
+  return e == hipSuccess ? HQ_OK : HQ_ERR_HIP;
 }
 
 }  // extern "C"

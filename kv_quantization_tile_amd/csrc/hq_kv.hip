@@ -61,8 +61,13 @@ __global__ __launch_bounds__(kBlock) void append_kernel(AppendArgs a, Tables K) 
   float m[8];
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    m[2 * r] = side ? K.v[2 * (kappa + 16 * r)] : K.k[2 * (kappa + 16 * r)];
-    m[2 * r + 1] = side ? K.v[2 * (kappa + 16 * r) + 1] : K.k[2 * (kappa + 16 * r) + 1];
+    const uint32_t c = 2 * (kappa + 16 * r);
+    m[2 * r] = packing(c);
+    m[2 * r + 1] = packing(c + 1);
+    if (K.scaled) {
+      m[2 * r] *= side ? K.v[c] : K.k[c];
+      m[2 * r + 1] *= side ? K.v[c + 1] : K.k[c + 1];
+    }
   }
   float x[8], y[8];
   const int64_t off = side ? (int64_t)tok * a.vt + (int64_t)head * a.vh : (int64_t)tok * a.kt + (int64_t)head * a.kh;
@@ -199,7 +204,8 @@ __global__ __launch_bounds__(kBlock) void read_kernel(ReadArgs a, Tables K) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int32_t q = BITS == 4 ? __builtin_amdgcn_sbfe(w0, 4 * i, 4) : __builtin_amdgcn_sbfe(i < 4 ? w0 : w1, 8 * (i & 3), 8);
-    y[i] = ((float)q * delta) * (side ? K.v[8 * l + i] : K.k[8 * l + i]);
+    y[i] = (float)q * delta;
+    if (K.scaled) y[i] *= side ? K.v[8 * l + i] : K.k[8 * l + i];
   }
   inverse_row(y, x, l, f);
   if (!have) return;

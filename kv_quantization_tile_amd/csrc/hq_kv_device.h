@@ -18,7 +18,6 @@
 #include <stdint.h>
 
 #include "hq_device.h"
-#include "hq_srft_tables.h"
 
 namespace hq_kv {
 
@@ -30,12 +29,45 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// Tables of one call: twiddles, per-coordinate multipliers of K and V, the sign diagonal's bits.
+// What a call's transform depends on: the sign diagonal's bits and, unless all ones, the multipliers of K's
+// and V's coordinates.
 struct Tables {
-  float w64c[32], w64s[32], w128c[64], w128s[64];
-  float k[kD], v[kD];
   uint32_t sign[4];
+  int scaled;         // whether k and v hold anything but ones
+  float k[kD], v[kD];
 };
+
+// cos and sin of 2 pi k / n, k < n / 2, rounded to binary32 from binary64 values in the first octant and
+// continued by symmetry: the values of the flat codec's tables (hq_srft.hip), in device memory because a
+// lane picks its own 20.  The octant's cos and sin are Taylor sums, whose remainder below 2^-60 no binary32
+// rounding here sees.
+struct Twiddles {
+  float c64[32], s64[32], c128[64], s128[64];
+};
+constexpr double taylor(double x, bool sine) {
+  double term = sine ? x : 1.0, sum = 0.0;
+  for (int i = sine ? 1 : 0; i < 24; i += 2) {
+    sum += term;
+    term *= -x * x / ((i + 1.0) * (i + 2.0));
+  }
+  return sum;
+}
+constexpr void twiddle(int n, int k, float& c, float& s) {
+  const double two_pi = 6.283185307179586476925286766559;
+  const int quarter = n / 4, quad = k / quarter, r = k % quarter;
+  const bool low = 2 * r <= quarter;
+  const double a = two_pi * (low ? r : quarter - r) / n;
+  const float c0 = (float)taylor(a, !low), s0 = (float)taylor(a, low);
+  c = quad == 0 ? c0 : 0.0f - s0;
+  s = quad == 0 ? s0 : c0;
+}
+constexpr Twiddles make_twiddles() {
+  Twiddles t{};
+  for (int k = 0; k < 32; ++k) twiddle(64, k, t.c64[k], t.s64[k]);
+  for (int k = 0; k < 64; ++k) twiddle(128, k, t.c128[k], t.s128[k]);
+  return t;
+}
+static __device__ const Twiddles kTwiddles = make_twiddles();
 
 // ---- pages -----------------------------------------------------------------------------------
 // A page of P tokens of one head: K codes [P][16][E], K scales [P][16], V codes [P/4][16][4][E],
@@ -83,6 +115,11 @@ __device__ __forceinline__ float row_get(float x, uint32_t src) {
   return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute((int)(lane << 2), __builtin_bit_cast(int, x)));
 }
 
+// Value of x in lane `src` of the wavefront's first 16 lanes.
+__device__ __forceinline__ float row_get_any(float x, uint32_t src) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute((int)(src << 2), __builtin_bit_cast(int, x)));
+}
+
 // ---- the FFT -----------------------------------------------------------------------------------
 // Twiddles of a lane's passes 1..5 (1 where the pass does not multiply the lane's points).
 struct LaneTwiddles {
@@ -90,15 +127,15 @@ struct LaneTwiddles {
 };
 
 template <bool INV>
-__device__ __forceinline__ LaneTwiddles lane_twiddles(const Tables& K, uint32_t l) {
+__device__ __forceinline__ LaneTwiddles lane_twiddles(uint32_t l) {
   LaneTwiddles t;
   const uint32_t kappa = rev4(l);
   const uint32_t idx[5] = {(l & 4u) ? (kappa & 1u) * 16u : 0u, (l & 2u) ? (kappa & 3u) * 8u : 0u,
                            (l & 1u) ? (kappa & 7u) * 4u : 0u, kappa * 2u, kappa};
 #pragma unroll
   for (int i = 0; i < 5; ++i) {
-    t.c[i] = K.w64c[idx[i]];
-    t.s[i] = INV ? K.w64s[idx[i]] : -K.w64s[idx[i]];
+    t.c[i] = kTwiddles.c64[idx[i]];
+    t.s[i] = INV ? kTwiddles.s64[idx[i]] : -kTwiddles.s64[idx[i]];
   }
   return t;
 }
@@ -149,15 +186,22 @@ struct LaneForward {
   float c[4], e[4];  // W_128^k of the lane's four k
   uint32_t flip[4];  // sign bits of the lane's values, two a word (bits 31 and 15)
 };
+__device__ __forceinline__ uint32_t sign_word(const Tables& K, uint32_t i) {
+  const uint32_t lo = (i & 1u) ? K.sign[1] : K.sign[0], hi = (i & 1u) ? K.sign[3] : K.sign[2];
+  return (i & 2u) ? hi : lo;
+}
+// The orthogonal packing's factor of coordinate c.
+__device__ __forceinline__ float packing(uint32_t c) { return c < 2u ? 0.08838834764831845f : 0.0625f; }
+
 __device__ __forceinline__ LaneForward lane_forward(const Tables& K, uint32_t l) {
   LaneForward f;
-  f.t = lane_twiddles<false>(K, l);
+  f.t = lane_twiddles<false>(l);
   const uint32_t kappa = rev4(l);
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    f.c[r] = K.w128c[kappa + 16 * r];
-    f.e[r] = -K.w128s[kappa + 16 * r];
-    const uint32_t b = K.sign[l >> 2] >> ((8u * l + 2u * (uint32_t)r) & 31u);
+    f.c[r] = kTwiddles.c128[kappa + 16 * r];
+    f.e[r] = -kTwiddles.s128[kappa + 16 * r];
+    const uint32_t b = sign_word(K, l >> 2) >> ((8u * l + 2u * (uint32_t)r) & 31u);
     f.flip[r] = ((b & 1u) << 15) | ((b & 2u) << 30);
   }
   return f;
@@ -207,12 +251,12 @@ __device__ __forceinline__ uint32_t inverse_n(uint32_t l, int e) { return rev4(l
 
 __device__ __forceinline__ LaneInverse lane_inverse(const Tables& K, uint32_t l) {
   LaneInverse f;
-  f.t = lane_twiddles<true>(K, l);
+  f.t = lane_twiddles<true>(l);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    f.c[e] = K.w128c[4 * l + e];
-    f.s[e] = K.w128s[4 * l + e];
-    const uint32_t n = inverse_n(l, e), b = K.sign[n >> 4] >> ((2u * n) & 31u);
+    f.c[e] = kTwiddles.c128[4 * l + e];
+    f.s[e] = kTwiddles.s128[4 * l + e];
+    const uint32_t n = inverse_n(l, e), b = sign_word(K, n >> 4) >> ((2u * n) & 31u);
     f.flip[e] = ((b & 1u) << 15) | ((b & 2u) << 30);
   }
   return f;

@@ -3,6 +3,8 @@
 
 #include <stdint.h>
 
+#include <cmath>
+
 #include "../../include/hq.h"
 #include "hq_kv_device.h"
 
@@ -18,13 +20,6 @@ inline int check_cache(const hq_kv_cache* c) {
   if (c->heads == 0 || c->heads > 65535u || c->pages > 0x7FFFFFFFu) return HQ_ERR_INVALID_ARG;
   if (c->pages && (!c->data || ((uintptr_t)c->data & 15u))) return HQ_ERR_INVALID_ARG;
   return HQ_OK;
-}
-
-inline bool multipliers(const float* lambda, bool encode, float out[kD]) {
-  hq_srft::Consts K;
-  if (!hq_srft::make_consts(lambda, &K)) return false;
-  for (int i = 0; i < kD; ++i) out[i] = encode ? K.m[i] : K.lam[i];
-  return true;
 }
 
 // The sign diagonal's 128 bits (Philox4x32-10, key = seed, counter 0), as the codecs draw them.
@@ -43,15 +38,20 @@ inline void sign_words(uint64_t seed, uint32_t w[4]) {
   for (int i = 0; i < 4; ++i) w[i] = c[i];
 }
 
-// False if a lambda is not finite and positive.
+// False if a lambda is not finite and positive.  Encoding multiplies by binary32 1 / lambda (then by the
+// packing's factor, as hq_srft_encode does), decoding by lambda.
 inline bool make_tables(const hq_kv_cache& c, bool encode, Tables* T) {
-  const hq_srft::Consts& w = hq_srft::twiddles();
-  memcpy(T->w64c, w.w64c, sizeof(T->w64c));
-  memcpy(T->w64s, w.w64s, sizeof(T->w64s));
-  memcpy(T->w128c, w.w128c, sizeof(T->w128c));
-  memcpy(T->w128s, w.w128s, sizeof(T->w128s));
   sign_words(c.seed, T->sign);
-  return multipliers(c.lambda_k, encode, T->k) && multipliers(c.lambda_v, encode, T->v);
+  T->scaled = c.lambda_k || c.lambda_v;
+  if (!T->scaled) return true;
+  for (int i = 0; i < kD; ++i) {
+    const float k = c.lambda_k ? c.lambda_k[i] : 1.0f, v = c.lambda_v ? c.lambda_v[i] : 1.0f;
+    if (!(k > 0.0f) || !(v > 0.0f) || !std::isfinite(k) || !std::isfinite(v)) return false;
+    const volatile float rk = 1.0f / k, rv = 1.0f / v;
+    T->k[i] = encode ? rk : k;
+    T->v[i] = encode ? rv : v;
+  }
+  return true;
 }
 
 }  // namespace hq_kv

@@ -24,7 +24,8 @@
 //   - decode: y_c = (q Delta) lambda_c, then the transpose: Zt_0 = ((y_0 + y_1) + i (y_0 - y_1))
 //     sqrt(2), Zt_k = (Y_k + conj Y_{64-k}) + i W^-k (Y_k - conj Y_{64-k}), z = inverse FFT_64(Zt),
 //     x = s (z / 16), exact zeros as +0.
-// The twiddles and multipliers (hq_srft_tables.h) travel in the kernel argument.
+// Twiddles are binary32 roundings of binary64 cos and sin over the first octant, the rest of the
+// circle by exact symmetry; they travel in the kernel argument with the multipliers.
 // Products by the exact twiddles 1 and -+i are not formed; that changes at most the sign of a zero
 // result, which no code and no nonzero output depends on.  The quotients absmax / L and 1 / Delta are
 // formed by FMA schemes equal to the correctly rounded quotient (div_l, recip_f16_value).
@@ -38,14 +39,60 @@
 
 #include "../../include/hq.h"
 #include "hq_device.h"
-#include "hq_srft_tables.h"
 
 namespace hq_srft {
 
+constexpr int kD = 128;        // values per vector
+constexpr int kN = 64;         // complex FFT length
+constexpr int kGroups = 16;    // scale groups per vector
 constexpr int kBlock = 256;    // one vector per thread
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+struct Consts {
+  float w64c[32], w64s[32];    // cos, sin of 2 pi k / 64
+  float w128c[64], w128s[64];  // cos, sin of 2 pi k / 128
+  float m[kD];                 // encode multipliers sigma_c / lambda_c
+  float lam[kD];               // decode multipliers lambda_c
+};
+
+// ---------------------------------------------------------------------------------------------
+// Host: the constant tables.
+
+static void twiddle(uint32_t n, uint32_t k, float* c, float* s) {
+  const double two_pi = 6.283185307179586476925286766559;
+  const uint32_t quarter = n / 4, quad = (k % n) / quarter, r = (k % n) % quarter;
+  float c0, s0;
+  if (2 * r <= quarter) {
+    c0 = (float)std::cos(two_pi * (double)r / (double)n);
+    s0 = (float)std::sin(two_pi * (double)r / (double)n);
+  } else {
+    c0 = (float)std::sin(two_pi * (double)(quarter - r) / (double)n);
+    s0 = (float)std::cos(two_pi * (double)(quarter - r) / (double)n);
+  }
+  switch (quad) {
+    case 0: *c = c0; *s = s0; break;
+    case 1: *c = 0.0f - s0; *s = c0; break;
+    case 2: *c = 0.0f - c0; *s = 0.0f - s0; break;
+    default: *c = s0; *s = 0.0f - c0; break;
+  }
+}
+
+// Fills the tables; false if a lambda is not finite and positive.
+static bool make_consts(const float* lambda, Consts* K) {
+  for (uint32_t k = 0; k < 32; ++k) twiddle(64, k, &K->w64c[k], &K->w64s[k]);
+  for (uint32_t k = 0; k < 64; ++k) twiddle(128, k, &K->w128c[k], &K->w128s[k]);
+  const float s0 = (float)(1.0 / std::sqrt(128.0));
+  for (int c = 0; c < kD; ++c) {
+    const float l = lambda ? lambda[c] : 1.0f;
+    if (!(l > 0.0f) || !std::isfinite(l)) return false;
+    const volatile float r = 1.0f / l;  // binary32 quotient, then one rounded product
+    K->m[c] = (c < 2 ? s0 : 0.0625f) * r;
+    K->lam[c] = l;
+  }
+  return true;
+}
 
 // ---------------------------------------------------------------------------------------------
 // Device.
