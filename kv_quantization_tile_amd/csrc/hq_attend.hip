@@ -226,7 +226,7 @@ __device__ __forceinline__ void key_operands(const Share<BITS>& s, f16x8 hi[4], 
   for (int j = 0; j < 4; ++j) {
     f16x2 c[4];
     code_pairs<BITS>(s.k + j * (BITS / 4), c);
-    const _Float16 d = h2(s.ks[j >> 1])[j & 1];
+    const _Float16 d = __builtin_bit_cast(_Float16, (uint16_t)(s.ks[j >> 1] >> (16 * (j & 1))));
     const f16x2 dd = {d, d};
     U32x4 h, l;
 #pragma unroll
@@ -271,6 +271,10 @@ __device__ __forceinline__ void value_operands(const Share<BITS>& s, uint32_t ou
   }
 }
 
+// Whether one of four binary16 scales is NaN or infinite: an exponent of all ones carries into the sign's place.
+__device__ __forceinline__ bool any_bad(const uint32_t vs[2]) {
+  return ((((vs[0] & 0x7C007C00u) + 0x04000400u) | ((vs[1] & 0x7C007C00u) + 0x04000400u)) & 0x80008000u) != 0u;
+}
 // Which of the lane's four value scales are NaN or infinite (bit r: token 4b + r).
 __device__ __forceinline__ uint32_t bad_scales(const uint32_t vs[2]) {
   uint32_t bad = 0;
@@ -290,12 +294,18 @@ __device__ __forceinline__ void drop_scales(uint32_t vs[2], uint32_t mask) {
 __device__ __forceinline__ float tanh32(float x) {
   const float a = fabsf(x), x2 = x * x;
   const float e = __builtin_amdgcn_exp2f(fminf(a, 20.0f) * 2.885390081777927f);
-  const float big = 1.0f - 2.0f / (e + 1.0f);
+  const float big = __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f);
   const float small = __builtin_fmaf(x2, __builtin_fmaf(x2, __builtin_fmaf(x2, -17.0f / 315.0f, 2.0f / 15.0f), -1.0f / 3.0f), 1.0f) * a;
   return __builtin_copysignf(a < 0.125f ? small : big, x);
 }
 
-__device__ __forceinline__ float capped(const AttendArgs& a, float s) { return a.cap_in > 0.0f ? a.cap_out * tanh32(s * a.cap_in) : s; }
+template <int N>
+__device__ __forceinline__ void cap_scores(const AttendArgs& a, float* s) {
+  if (a.cap_in > 0.0f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = a.cap_out * tanh32(s[i] * a.cap_in);
+  }
+}
 
 // LDS written by some lanes of a wavefront is read by others of the same one.
 __device__ __forceinline__ void wave_sync() {
@@ -416,11 +426,11 @@ __device__ __forceinline__ int32_t page_of(const AttendArgs& a, uint32_t b, int3
 // four wavefronts take 32 tokens in turn, the next 32 already on their way, and join at the end.  The
 // cache's bytes bound it; its rows are a fraction of the products' 16 columns, which costs nothing here.
 template <int BITS, bool PREC>
-__global__ __launch_bounds__(kAttBlock) void attend_few_kernel(AttendArgs a, Tables K) {
+__global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kernel(AttendArgs a, Tables K) {
   __shared__ __align__(16) float s_o[kAttWaves][16][kPad];
   __shared__ __align__(16) _Float16 s_q[PREC ? 2 : 1][16][kD + 8];
   __shared__ float s_f[16], s_m[kAttWaves][16], s_l[kAttWaves][16];
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, n = lane & 15u, b4 = lane >> 4;
+  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
   const uint32_t split = blockIdx.x % a.splits, item = blockIdx.x / a.splits;
   const Item it = item_of(a, item);
   const Seq s = seq_of(a, it.b);
@@ -435,22 +445,21 @@ __global__ __launch_bounds__(kAttBlock) void attend_few_kernel(AttendArgs a, Tab
   const uint32_t P = 1u << a.page_log2;
   const uint64_t page_size = (uint64_t)P * Page<BITS>::kToken;
 
-  int32_t pg[2], pn[2];
   Share<BITS> cur[2], nxt[2];
-  auto load = [&](int32_t t, const int32_t page[2], Share<BITS> sh[2]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {  // an absent page's place is taken by page 0, masked below
-      const uint8_t* p = a.cache + ((uint64_t)(page[u] < 0 ? 0 : page[u]) * a.heads + it.h) * page_size;
-      load_keys<BITS>(p, P, (uint32_t)(t + 16 * u) & (P - 1u), lane, sh[u]);
-      load_values<BITS>(p, P, (uint32_t)(t + 16 * u) & (P - 1u), lane, sh[u]);
-    }
+  auto load = [&](int32_t t, int32_t page, Share<BITS>& sh) __attribute__((always_inline)) {
+    // an absent page's place is taken by page 0, masked below
+    const uint8_t* p = a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + it.h) * page_size;
+    load_keys<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
+    load_values<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
   };
+  constexpr int32_t kStep = 32 * kAttWaves;
   int32_t t = t0 + 32 * (int32_t)wave;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) pg[u] = page_of(a, it.b, t + 16 * u, t1);
-  if (t < t1) load(t, pg, cur);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) pn[u] = page_of(a, it.b, t + 32 * kAttWaves + 16 * u, t1);
+  int32_t pg0 = page_of(a, it.b, t, t1), pg1 = page_of(a, it.b, t + 16, t1);
+  if (t < t1) {
+    load(t, pg0, cur[0]);
+    load(t + 16, pg1, cur[1]);
+  }
+  int32_t pn0 = page_of(a, it.b, t + kStep, t1), pn1 = page_of(a, it.b, t + kStep + 16, t1);
 
   {  // the rows: four to a wavefront, 16 lanes each
     const uint32_t r = threadIdx.x >> 4;
@@ -480,13 +489,16 @@ __global__ __launch_bounds__(kAttBlock) void attend_few_kernel(AttendArgs a, Tab
   f32x4 o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-  for (; t < t1; t += 32 * kAttWaves) {
-    if (t + 32 * kAttWaves < t1) load(t + 32 * kAttWaves, pn, nxt);
-    const bool there[2] = {pg[0] >= 0, pg[1] >= 0};
-    const int32_t ahead = t + 64 * kAttWaves;
-    int32_t pa[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) pa[u] = page_of(a, it.b, ahead + 16 * u, t1);
+  for (; t < t1; t += kStep) {
+    if (t + kStep < t1) {
+      load(t + kStep, pn0, nxt[0]);
+      load(t + kStep + 16, pn1, nxt[1]);
+    }
+    const bool there[2] = {pg0 >= 0, pg1 >= 0};
+    pg0 = pn0;
+    pg1 = pn1;
+    pn0 = page_of(a, it.b, t + 2 * kStep, t1);
+    pn1 = page_of(a, it.b, t + 2 * kStep + 16, t1);
     float sc[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -496,10 +508,7 @@ __global__ __launch_bounds__(kAttBlock) void attend_few_kernel(AttendArgs a, Tab
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[4 * u + i] = r[i] * qf;
     }
-    if (a.cap_in > 0.0f) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sc[i] = capped(a, sc[i]);
-    }
+    cap_scores<8>(a, sc);
     if (!(there[0] && there[1] && t >= all_lo && t + 32 <= all_hi && t + 32 <= t1)) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -517,8 +526,8 @@ __global__ __launch_bounds__(kAttBlock) void attend_few_kernel(AttendArgs a, Tab
     }
     // A value vector with NaN scales makes the rows that see it NaN and no other (0 NaN in the product
     // would reach every row): its scales count as 0, and the rows are poisoned.
-    const uint32_t bad = bad_scales(cur[0].vs) | bad_scales(cur[1].vs) << 4;
-    if (__builtin_amdgcn_ballot_w64(bad != 0)) {
+    if (__builtin_amdgcn_ballot_w64(any_bad(cur[0].vs) || any_bad(cur[1].vs))) {
+      const uint32_t bad = bad_scales(cur[0].vs) | bad_scales(cur[1].vs) << 4;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if ((bad >> i) & 1u && sc[i] != -__builtin_inff()) poison = __builtin_nanf("");
@@ -552,12 +561,8 @@ __global__ __launch_bounds__(kAttBlock) void attend_few_kernel(AttendArgs a, Tab
       const U32x4 v = {{v0[i][0], v0[i][1], v1[i][0], v1[i][1]}};
       o[i] = mfma(frag(v), frag(pf), o[i]);
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      cur[u] = nxt[u];
-      pg[u] = pn[u];
-      pn[u] = pa[u];
-    }
+    cur[0] = nxt[0];
+    cur[1] = nxt[1];
   }
 
   // the wavefronts' parts, joined in order
@@ -695,31 +700,34 @@ __global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Ta
   if (parts == 2) *reinterpret_cast<f16x8*>(a.qlo + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[1][g][8 * l]);
 }
 
-// Many rows: a workgroup takes 64 R rows of a (sequence, head) and one split of the tokens; each wavefront
-// owns 16 R rows.  64 tokens at a time are made operands once, 16 by each wavefront, into LDS in the
-// order the products read them (lane after lane, 16 bytes each: no bank conflict), while the previous 64
-// are multiplied; the next ones' codes are in flight meanwhile.  At R = 4 each operand read from LDS feeds
-// four products, so LDS (128 bytes a clock) is half busy when the matrix cores are full.
+// Many rows: a workgroup of 8 wavefronts takes 128 R rows of a (sequence, head) and one split of the tokens;
+// each wavefront owns 16 R rows.  128 tokens at a time are made operands once, 16 by each wavefront, into
+// LDS in the order the products read them (lane after lane, 16 bytes each: no bank conflict); the next
+// ones' codes are in flight meanwhile.  Two wavefronts a SIMD, so that one's softmax runs beside the
+// other's products; R = 2 is what 256 registers hold (at R = 4 and one wavefront a SIMD nothing overlapped:
+// 1.2 ms for a prompt of 8192 tokens).  Two stages of LDS, one with the keys in two parts (160 KB hold no more).
+constexpr int kManyWaves = 8, kManyBlock = 64 * kManyWaves;
+template <bool PREC>
+struct Stage {
+  f16x8 k[PREC ? 2 : 1][8][4][64];  // [part][16 tokens][step][lane]
+  f16x8 v[4][8][64];                // [32 tokens][coordinate][lane]
+};
+template <bool PREC>
+constexpr size_t many_lds() { return sizeof(Stage<PREC>) * (PREC ? 1 : 2); }
+
 template <int BITS, bool PREC, int R>
-__global__ __launch_bounds__(kAttBlock, R == 4 ? 1 : 2) void attend_many_kernel(AttendArgs a, Tables K) {
-  constexpr int kK = PREC ? 2 : 1;
-  struct Stage {
-    f16x8 k[kK][4][4][64];  // [part][16 tokens][step][lane]
-    f16x8 v[2][8][64];      // [32 tokens][coordinate][lane]
-  };
-  union Lds {
-    Stage st[2];
-    float o[kAttWaves][16][kPad];
-  };
+__global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a, Tables K) {
+  constexpr int32_t kTok = 16 * kManyWaves;
   extern __shared__ __align__(16) uint8_t raw[];
-  Lds& sm = *reinterpret_cast<Lds*>(raw);
-  __shared__ uint32_t s_bad[2][4];  // bits 0..15: tokens with NaN value scales; bit 16: absent
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, n = lane & 15u, b4 = lane >> 4;
+  Stage<PREC>* st = reinterpret_cast<Stage<PREC>*>(raw);
+  float(*s_o)[16][kPad] = reinterpret_cast<float(*)[16][kPad]>(raw);  // [wavefront], after the last product
+  __shared__ uint32_t s_flags[PREC ? 1 : 2][kManyWaves];  // bits 0..15: tokens with NaN value scales; bit 16: absent
+  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
   // the last tiles see the most tokens under the causal mask: they go first
   const uint32_t split = blockIdx.x % a.splits, item = gridDim.x / a.splits - 1u - blockIdx.x / a.splits;
-  const uint32_t sh_i = item % (a.seqs * a.heads);
-  const Item it = {item / (a.seqs * a.heads), sh_i % a.heads, sh_i / a.heads};
-  const uint64_t slot = ((uint64_t)it.b * a.heads + it.h) * a.tiles + it.tile;  // the item's place in the workspace
+  const uint32_t bh = item % (a.seqs * a.heads);
+  const Item it = {item / (a.seqs * a.heads), bh % a.heads, bh / a.heads};
+  const uint64_t slot = (uint64_t)bh * a.tiles + it.tile;  // the item's place in the workspace
   const Seq s = seq_of(a, it.b);
   const uint32_t rows = (uint32_t)s.m * a.group, r0 = it.tile * a.tile_rows, w0 = r0 + wave * 16u * R;
   if (r0 >= rows) return;
@@ -741,14 +749,14 @@ __global__ __launch_bounds__(kAttBlock, R == 4 ? 1 : 2) void attend_many_kernel(
     load_keys<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
     load_values<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
   };
-  // this wavefront's 16 of the 64 tokens at t, as operands
-  auto stage = [&](Stage& d, uint32_t* flags, int32_t t, int32_t page) __attribute__((always_inline)) {
+  // this wavefront's 16 tokens at t, as operands
+  auto stage = [&](Stage<PREC>& d, uint32_t* flags, int32_t t, int32_t page) __attribute__((always_inline)) {
     f16x8 kh[4], kl[4];
     key_operands<BITS, PREC>(sh, kh, kl);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       d.k[0][wave][j][lane] = kh[j];
-      if (PREC) d.k[kK - 1][wave][j][lane] = kl[j];
+      if (PREC) d.k[PREC ? 1 : 0][wave][j][lane] = kl[j];
     }
     if (page < 0 || t < lo || t + 16 > t1) {  // a token that no row sees may hold anything
 #pragma unroll
@@ -758,15 +766,17 @@ __global__ __launch_bounds__(kAttBlock, R == 4 ? 1 : 2) void attend_many_kernel(
       }
     }
     uint32_t word = page < 0 ? 0x10000u : 0u;
-    const uint32_t bad = bad_scales(sh.vs);
-    if (__builtin_amdgcn_ballot_w64(bad != 0)) {
+    if (__builtin_amdgcn_ballot_w64(any_bad(sh.vs))) {
+      const uint32_t bad = bad_scales(sh.vs);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint64_t votes = __builtin_amdgcn_ballot_w64((bad >> i) & 1u);
 #pragma unroll
         for (int q = 0; q < 4; ++q) word |= (votes >> (16 * q)) & 0xFFFFu ? 1u << (4 * q + i) : 0u;
       }
-      drop_scales(sh.vs, bad);
+      // a value vector with one NaN scale is NaN as a whole: its rows are poisoned, its scales count as 0
+      uint32_t mine = (word >> (4 * b4)) & 15u;
+      drop_scales(sh.vs, mine);
     }
     if (lane == 0) flags[wave] = word;
     uint32_t v[8][2];
@@ -775,14 +785,16 @@ __global__ __launch_bounds__(kAttBlock, R == 4 ? 1 : 2) void attend_many_kernel(
     for (int i = 0; i < 8; ++i)
       reinterpret_cast<uint2*>(&d.v[wave >> 1][i][lane])[wave & 1u] = make_uint2(v[i][0], v[i][1]);
   };
-  int32_t t = t0, page = page_of(a, it.b, t + 16 * (int32_t)wave, t1);
-  if (t < t1) load(t + 16 * (int32_t)wave, page);
-  int32_t next = page_of(a, it.b, t + 64 + 16 * (int32_t)wave, t1);
+  const int32_t mine = 16 * (int32_t)wave;
+  int32_t t = t0, page = page_of(a, it.b, t + mine, t1);
+  if (t < t1) load(t + mine, page);
+  int32_t next = page_of(a, it.b, t + kTok + mine, t1);
 
+  const bool cap = a.cap_in > 0.0f;
   f16x8 qh[R][4], ql[R][4];
-  float qf[R], m[R], sum[R], poison[R];
+  float qf[R], eff[R], m[R], sum[R], poison[R];
   int32_t row_lo[R], row_hi[R];
-  f32x4 o[R][8];
+  f32x4 o[R][8], ones[R];
 #pragma unroll
   for (int q = 0; q < R; ++q) {
     const uint64_t row = slot * a.tile_rows + wave * 16u * R + 16u * q + n;
@@ -793,35 +805,47 @@ __global__ __launch_bounds__(kAttBlock, R == 4 ? 1 : 2) void attend_many_kernel(
       if (have) qh[q][j] = *reinterpret_cast<const f16x8*>(a.qhi + row * kD + 8 * (4 * b4 + j));
       if (PREC && have) ql[q][j] = *reinterpret_cast<const f16x8*>(a.qlo + row * kD + 8 * (4 * b4 + j));
     }
-    qf[q] = have ? a.qf[row] : 0.0f;
+    qf[q] = have ? a.qf[row] : 1.0f;
+    eff[q] = cap ? 1.0f : qf[q];  // scores are eff sc: the product with qf waits for the exponent's fma
     m[q] = -1.0e30f;
     sum[q] = poison[q] = 0.0f;
     row_lo[q] = row_hi[q] = 0;
     if (w0 + 16u * q + n < rows) visible(a, s, (int32_t)((w0 + 16u * q + n) / a.group), &row_lo[q], &row_hi[q]);
+    ones[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[q][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
   }
-  if (t < t1) stage(sm.st[0], s_bad[0], t + 16 * (int32_t)wave, page);
-  __syncthreads();
-  for (uint32_t buf = 0; t < t1; t += 64, buf ^= 1u) {
-    const bool more = t + 64 < t1;
+  uint32_t buf = 0;
+  if (!PREC && t < t1) {
+    stage(st[0], s_flags[0], t + mine, page);
+    __syncthreads();
+  }
+  for (; t < t1; t += kTok) {
+    const bool more = t + kTok < t1;
+    if (PREC) {
+      stage(st[0], s_flags[0], t + mine, page);
+      __syncthreads();
+    }
     if (more) {
       page = next;
-      load(t + 64 + 16 * (int32_t)wave, page);
-      next = page_of(a, it.b, t + 128 + 16 * (int32_t)wave, t1);
+      load(t + kTok + mine, page);
+      next = page_of(a, it.b, t + 2 * kTok + mine, t1);
     }
-    if (t < whi && t + 64 > wlo) {
-      const Stage& d = sm.st[buf];
-      f32x4 sc[R][4];
+    const Stage<PREC>& d = st[buf];
+#pragma unroll 2
+    for (int w = 0; w < kTok / 32; ++w) {
+      const int32_t tw = t + 32 * w;
+      if (tw >= whi || tw + 32 <= wlo || tw >= t1) continue;
+      f32x4 sc[R][2];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int q = 0; q < R; ++q) sc[q][u] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const f16x8 kh = d.k[0][u][j][lane];
+          const f16x8 kh = d.k[0][2 * w + u][j][lane];
           if (PREC) {
-            const f16x8 kl = d.k[kK - 1][u][j][lane];
+            const f16x8 kl = d.k[PREC ? 1 : 0][2 * w + u][j][lane];
 #pragma unroll
             for (int q = 0; q < R; ++q) {
               sc[q][u] = mfma(kl, qh[q][j], sc[q][u]);
@@ -832,30 +856,26 @@ __global__ __launch_bounds__(kAttBlock, R == 4 ? 1 : 2) void attend_many_kernel(
           for (int q = 0; q < R; ++q) sc[q][u] = mfma(kh, qh[q][j], sc[q][u]);
         }
       }
-#pragma unroll
-      for (int q = 0; q < R; ++q)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) sc[q][u] *= qf[q];
-      if (a.cap_in > 0.0f) {
+      if (cap) {
 #pragma unroll
         for (int q = 0; q < R; ++q)
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sc[q][u][i] = capped(a, sc[q][u][i]);
+            for (int i = 0; i < 4; ++i) sc[q][u][i] = a.cap_out * tanh32(sc[q][u][i] * qf[q] * a.cap_in);
       }
-      const uint32_t fl[4] = {s_bad[buf][0], s_bad[buf][1], s_bad[buf][2], s_bad[buf][3]};
-      const bool flagged = __builtin_amdgcn_readfirstlane(fl[0] | fl[1] | fl[2] | fl[3]) != 0;
-      if (flagged || t < all_lo || t + 64 > all_hi || t + 64 > t1) {
+      const uint32_t fl0 = s_flags[buf][2 * w], fl1 = s_flags[buf][2 * w + 1];
+      if (__builtin_amdgcn_readfirstlane(fl0 | fl1) || tw < all_lo || tw + 32 > all_hi || tw + 32 > t1) {
 #pragma unroll
         for (int q = 0; q < R; ++q)
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int32_t tok = t + 16 * u + 4 * (int32_t)b4 + i;
-              if ((fl[u] & 0x10000u) || tok < row_lo[q] || tok >= row_hi[q] || tok >= t1) sc[q][u][i] = -__builtin_inff();
-              else if ((fl[u] >> (4 * b4 + i)) & 1u) poison[q] = __builtin_nanf("");
+              const int32_t tok = tw + 16 * u + 4 * (int32_t)b4 + i;
+              const uint32_t fl = u ? fl1 : fl0;
+              if ((fl & 0x10000u) || tok < row_lo[q] || tok >= row_hi[q] || tok >= t1) sc[q][u][i] = -__builtin_inff();
+              else if ((fl >> (4 * b4 + i)) & 1u) poison[q] = __builtin_nanf("");
             }
       }
       float top[R];
@@ -864,7 +884,8 @@ __global__ __launch_bounds__(kAttBlock, R == 4 ? 1 : 2) void attend_many_kernel(
       for (int q = 0; q < R; ++q) {
         top[q] = sc[q][0][0];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) top[q] = fmaxf(top[q], sc[q][i >> 2][i & 3]);
+        for (int i = 1; i < 8; ++i) top[q] = fmaxf(top[q], sc[q][i >> 2][i & 3]);
+        top[q] *= eff[q];
         rise |= top[q] > m[q] + kSlack;
       }
       if (__builtin_amdgcn_ballot_w64(rise)) {
@@ -874,35 +895,39 @@ __global__ __launch_bounds__(kAttBlock, R == 4 ? 1 : 2) void attend_many_kernel(
           const float f = __builtin_amdgcn_exp2f(m[q] - mn);
           m[q] = mn;
           sum[q] *= f;
+          ones[q] *= f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[q][i] *= f;
         }
       }
+      f16x8 pf[R];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        f16x8 pf[R];
+      for (int q = 0; q < R; ++q) {
+        const float base = kPScaleLog2 - m[q];
+        U32x4 p;
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-          const float base = m[q] - kPScaleLog2;
-          U32x4 p;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int u = 2 * w + (i >> 1), c = 2 * (i & 1);
-            const float p0 = __builtin_amdgcn_exp2f(sc[q][u][c] - base), p1 = __builtin_amdgcn_exp2f(sc[q][u][c + 1] - base);
-            sum[q] += p0 + p1;
-            p.v[i] = u2((f16x2){(_Float16)p0, (_Float16)p1});
-          }
-          pf[q] = frag(p);
+        for (int i = 0; i < 4; ++i) {
+          const int u = i >> 1, c = 2 * (i & 1);
+          const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][u][c], eff[q], base));
+          const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][u][c + 1], eff[q], base));
+          if (PREC) sum[q] += p0 + p1;
+          p.v[i] = u2((f16x2){(_Float16)p0, (_Float16)p1});
         }
+        pf[q] = frag(p);
+        // the sum of the rounded P, the one the output is weighted with, is one more product
+        if (!PREC) ones[q] = mfma((f16x8)(_Float16)1.0f, pf[q], ones[q]);
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const f16x8 v = d.v[w][i][lane];
+      for (int i = 0; i < 8; ++i) {
+        const f16x8 v = d.v[w][i][lane];
 #pragma unroll
-          for (int q = 0; q < R; ++q) o[q][i] = mfma(v, pf[q], o[q][i]);
-        }
+        for (int q = 0; q < R; ++q) o[q][i] = mfma(v, pf[q], o[q][i]);
       }
     }
-    if (more) stage(sm.st[buf ^ 1u], s_bad[buf ^ 1u], t + 64 + 16 * (int32_t)wave, page);
+    if (!PREC && more) {
+      buf ^= 1u;
+      stage(st[buf], s_flags[buf], t + kTok + mine, page);
+    }
     __syncthreads();
   }
 
@@ -910,29 +935,30 @@ __global__ __launch_bounds__(kAttBlock, R == 4 ? 1 : 2) void attend_many_kernel(
   const LaneInverse inv = lane_inverse(K, n);
 #pragma unroll
   for (int q = 0; q < R; ++q) {
-    const float total = blocks_sum(sum[q]), bad = blocks_sum(poison[q]);
+    const float total = PREC ? blocks_sum(sum[q]) : ones[q][0], bad = blocks_sum(poison[q]);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int i = 0; i < 8; i += 4)
-        *reinterpret_cast<f32x4*>(&sm.o[wave][n][8 * (4 * b4 + r) + i]) =
+        *reinterpret_cast<f32x4*>(&s_o[wave][n][8 * (4 * b4 + r) + i]) =
             (f32x4){o[q][i][r] + bad, o[q][i + 1][r] + bad, o[q][i + 2][r] + bad, o[q][i + 3][r] + bad};
     const uint32_t first = wave * 16u * R + 16u * q;
     const uint64_t row = slot * a.tile_rows + first;
-    if (a.splits == 1) {
-      if (b4 == 0) a.lse[row + n] = m[q] + __builtin_amdgcn_logf(total) - kPScaleLog2;
-    } else if (b4 == 0) {
-      *reinterpret_cast<f32x2*>(a.pml + (((slot * a.splits + split) * a.tile_rows) + first + n) * 2) = (f32x2){m[q], total};
+    if (b4 == 0) {
+      if (a.splits == 1) a.lse[row + n] = m[q] + __builtin_amdgcn_logf(total) - kPScaleLog2;
+      else *reinterpret_cast<f32x2*>(a.pml + (((slot * a.splits + split) * a.tile_rows) + first + n) * 2) = (f32x2){m[q], total};
     }
     wave_sync();
+#pragma unroll 1
     for (uint32_t k = 0; k < 4; ++k) {
       const uint32_t r = 4u * k + b4;
+      if (w0 + 16u * q + 4u * k >= rows) break;
       float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = sm.o[wave][r][8 * n + i];
+      for (int i = 0; i < 8; ++i) y[i] = s_o[wave][r][8 * n + i];
       const float tr = row_get_any(total, r);
       if (a.splits == 1) {
-        if (w0 + 16u * q + 4u * k < rows) store_row<BITS>(a, K, s, it.h, w0 + 16u * q + r, n, inv, y, tr);
+        store_row<BITS>(a, K, s, it.h, w0 + 16u * q + r, n, inv, y, tr);
       } else {
         float* d = a.po + ((slot * a.splits + split) * a.tile_rows + first + r) * kD + 8 * n;
         *reinterpret_cast<f32x4*>(d) = (f32x4){y[0], y[1], y[2], y[3]};
@@ -948,7 +974,7 @@ __global__ __launch_bounds__(kAttBlock, R == 4 ? 1 : 2) void attend_many_kernel(
 // fixed order.
 template <int BITS>
 __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a, uint32_t blocks) {
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, n = lane & 15u, b4 = lane >> 4;
+  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
   const uint32_t bh = blockIdx.x / blocks, h = bh % a.heads, b = bh / a.heads;
   const Seq s = seq_of(a, b);
   const int32_t t = (int32_t)((blockIdx.x % blocks) * 64u * kAttWaves + 64u * wave);
@@ -988,10 +1014,14 @@ __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const f32x4 r = scores16<true>(kh[u], kl[u], qh, ql);
+      float sc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[i] = r[i] * qf;
+      cap_scores<4>(a, sc);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int32_t tok = t + 16 * u + 4 * (int32_t)b4 + i;
-        const float p = __builtin_amdgcn_exp2f(capped(a, r[i] * qf) - lse);
+        const float p = __builtin_amdgcn_exp2f(sc[i] - lse);
         acc[4 * u + i] += there[u] && (whole || (tok >= row_lo && tok < row_hi)) ? p : 0.0f;
       }
     }
@@ -1026,9 +1056,9 @@ struct Plan {
 Plan plan_of(const hq_kv_cache& c, const hq_kv_attend_args& g) {
   Plan p;
   const uint32_t rows = g.max_q * (g.q_heads / c.heads);
-  // up to 16 rows: one tile, split over many workgroups; beyond, 64 rows a workgroup, and 256 where that
-  // still leaves no workgroup mostly idle
-  p.tile_rows = rows <= 16 ? 16 : rows <= 128 ? 64 : g.weights ? 128 : 256;
+  // up to 16 rows: one tile, split over many workgroups; beyond, 16 rows a wavefront while that covers them,
+  // then 32
+  p.tile_rows = rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
   p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   p.items = (uint64_t)g.seqs * c.heads * p.tiles;
   const bool few = rows <= 16;
@@ -1066,11 +1096,11 @@ Plan plan_of(const hq_kv_cache& c, const hq_kv_attend_args& g) {
 
 template <int BITS, bool PREC, int R>
 hipError_t launch_many(const AttendArgs& a, const Tables& T, uint32_t grid, hipStream_t st) {
-  const size_t stage = (PREC ? 2 : 1) * 16384 + 16384, lds = 2 * stage;
+  // more dynamic LDS than the default limit: asked for once per kernel (the attribute holds for every device)
   static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_many_kernel<BITS, PREC, R>),
-                                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)many_lds<PREC>());
   if (set != hipSuccess) return set;
-  hipLaunchKernelGGL((attend_many_kernel<BITS, PREC, R>), dim3(grid), dim3(kAttBlock), lds, st, a, T);
+  hipLaunchKernelGGL((attend_many_kernel<BITS, PREC, R>), dim3(grid), dim3(kManyBlock), many_lds<PREC>(), st, a, T);
   return hipSuccess;
 }
 
@@ -1085,8 +1115,8 @@ hipError_t launch_attend(const AttendArgs& a, const Tables& T, uint32_t items, h
   } else {
     hipLaunchKernelGGL((rotate_rows_kernel<BITS>), dim3(items * (a.tile_rows / 16)), block, 0, st, a, T, prec ? 2 : 1);
     hipError_t e;
-    if (a.tile_rows == 64) e = prec ? launch_many<BITS, true, 1>(a, T, grid, st) : launch_many<BITS, false, 1>(a, T, grid, st);
-    else e = prec ? launch_many<BITS, true, 2>(a, T, grid, st) : launch_many<BITS, false, 4>(a, T, grid, st);
+    if (a.tile_rows == 128) e = prec ? launch_many<BITS, true, 1>(a, T, grid, st) : launch_many<BITS, false, 1>(a, T, grid, st);
+    else e = prec ? launch_many<BITS, true, 2>(a, T, grid, st) : launch_many<BITS, false, 2>(a, T, grid, st);
     if (e != hipSuccess) return e;
   }
   if (a.splits > 1) {
