@@ -367,14 +367,16 @@ int hq_kv_attend_workspace_size(const hq_kv_cache *cache, const hq_kv_attend_arg
 
 /* HQ_ERR_INVALID_ARG: null or misaligned pointers, sizes outside their ranges, q_heads not a multiple of
  * heads, q_start == NULL with total_q not a multiple of seqs, a scale or softcap that is not finite, a
- * negative softcap, weights_stride < max_len, or a workspace that is too small. */
+ * negative softcap, weights_stride < max_len, max_len over 2^30, a launch of 2^32 threads or more, or a
+ * workspace that is too small.  Rows of `out` that no sequence's queries name are not written. */
 int hq_kv_attend(const hq_kv_cache *cache, const hq_kv_attend_args *args, void *workspace,
                  size_t workspace_bytes, hq_stream_t stream);
 
 /* Eviction by accumulated weight.  Of each (sequence, head)'s n tokens, m = min(n, budget) stay: the first
  * `sink`, the last `recent`, and of the others those of most weight (ties to the lowest index; NaN counts
  * least).  They move, in order, to tokens 0..m-1 of the pages of dst_table, which must not be pages that
- * any table of the call reads; slots past m are not written. */
+ * any table of the call reads; slots past m are not written, and a token of an absent page that stays (as
+ * one of the first or last, or within the budget) leaves its slot as it was. */
 typedef struct {
   const int32_t *table;      /* DEVICE, [seqs][table_width]                                */
   const int32_t *lens;       /* DEVICE, [seqs]                                             */

@@ -406,6 +406,21 @@ def _check_tensor(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
+def _size(v, name: str) -> int:
+    if not 0 <= int(v) <= 0xFFFFFFFF:
+        raise ValueError(f"{name} must be a 32-bit size, not {v}")
+    return int(v)
+
+
+def _empty(shape, dtype, device, stream):
+    """A buffer of the call's own, from the pool of the stream the call runs on."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check_rows(t, name, heads, device):
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128 or (t.stride(2) != 1 and t.numel()) or t.device != device:
         raise ValueError(f"{name} must be [tokens][{heads}][128] on {device}, its last dimension contiguous")
@@ -436,8 +451,8 @@ def hq_kv_read(cache, slots, bits: int = 4, seed: int = 0, lam_k=None, lam_v=Non
     c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
     _check_tensor(slots, "slots", torch.int64, (slots.numel(),), cache.device)
     shape, dt = (slots.numel(), c.heads, 128), out_dtype or torch.bfloat16
-    k = torch.empty(shape, dtype=dt, device=cache.device) if k is None else k
-    v = torch.empty(shape, dtype=dt, device=cache.device) if v is None else v
+    k = _empty(shape, dt, cache.device, stream) if k is None else k
+    v = _empty(shape, dt, cache.device, stream) if v is None else v
     _check_tensor(k, "k", dt, shape, cache.device)
     _check_tensor(v, "v", dt, shape, cache.device)
     _check(lib().hq_kv_read(ctypes.byref(c), slots.data_ptr(), slots.numel(), k.data_ptr(), v.data_ptr(), _dtype_code(k),
@@ -452,7 +467,7 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
 
     table int32 [seqs][width], lens int32 [seqs] (tokens cached, the queries' own among them); q_start int32
     [seqs + 1] offsets of each sequence's queries (None: as many each); max_q, max_len bounds on a sequence's
-    queries and tokens (None: all queries, the table's width).  weights float32 [seqs][heads][>= max_len] gets each
+    queries and tokens (None: all queries, what the table's width or the weights hold).  weights float32 [seqs][heads][>= max_len] gets each
     token's softmax weights added.  Returns out ([queries][q heads][128], bf16 unless given)."""
     torch = _torch()
     c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
@@ -468,10 +483,8 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
         _check_tensor(q_start, "q_start", torch.int32, (seqs + 1,), dev)
     if max_q is None:
         max_q = total if q_start is not None else total // max(seqs, 1)
-    if max_len is None:
-        max_len = width * c.page
     if out is None:
-        out = torch.empty((total, heads, 128), dtype=torch.bfloat16, device=dev)
+        out = _empty((total, heads, 128), torch.bfloat16, dev, stream)
     _check_tensor(out, "out", out.dtype, (total, heads, 128), dev)
     stride = 0
     if weights is not None:
@@ -479,14 +492,16 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
             raise ValueError("weights must be [seqs][heads][tokens]")
         stride = weights.shape[2]
         _check_tensor(weights, "weights", torch.float32, (seqs, c.heads, stride), dev)
+    if max_len is None:
+        max_len = width * c.page if weights is None else min(stride, width * c.page)
     a = HqKvAttendArgs(q.data_ptr(), out.data_ptr(), _dtype_code(q), _dtype_code(out), q.stride(0), q.stride(1), total, heads, seqs,
-                       max_q, max_len, q_start.data_ptr() if q_start is not None else None, table.data_ptr(), width,
-                       lens.data_ptr(), 128 ** -0.5 if scale is None else scale, softcap, 1 if causal else 0, window,
+                       _size(max_q, "max_q"), _size(max_len, "max_len"), q_start.data_ptr() if q_start is not None else None, table.data_ptr(), width,
+                       lens.data_ptr(), 128 ** -0.5 if scale is None else scale, softcap, 1 if causal else 0, _size(window, "window"),
                        weights.data_ptr() if weights is not None else None, stride)
     L, need = lib(), ctypes.c_size_t(0)
     if ws is None:
         _check(L.hq_kv_attend_workspace_size(ctypes.byref(c), ctypes.byref(a), ctypes.byref(need)), "hq_kv_attend")
-        ws = torch.empty(max(need.value, 256), dtype=torch.uint8, device=dev)
+        ws = _empty(max(need.value, 256), torch.uint8, dev, stream)
     elif not (ws.is_contiguous() and ws.device == dev and ws.dtype == torch.uint8):
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
     _check(L.hq_kv_attend(ctypes.byref(c), ctypes.byref(a), ws.data_ptr(), ws.numel(), _stream_handle(stream)), "hq_kv_attend")
@@ -506,16 +521,18 @@ def hq_kv_evict(cache, table, lens, weights, budget: int, sink: int, recent: int
     _check_tensor(table, "table", torch.int32, (seqs, width), dev)
     _check_tensor(weights, "weights", torch.float32, (seqs, c.heads, top), dev)
     _check_tensor(dst_table, "dst_table", torch.int32, (seqs, dst_table.shape[-1]), dev)
-    if min(budget, sink, recent) < 0:
-        raise ValueError("budget, sink and recent are not negative")
-    kept = torch.empty((seqs, c.heads, budget), dtype=torch.int32, device=dev) if kept is None else kept
-    new_lens = torch.empty(seqs, dtype=torch.int32, device=dev) if new_lens is None else new_lens
-    new_weights = torch.empty((seqs, c.heads, budget), dtype=torch.float32, device=dev) if new_weights is None else new_weights
+    budget, sink, recent = _size(budget, "budget"), _size(sink, "sink"), _size(recent, "recent")
+    if budget > dst_table.shape[-1] * c.page:
+        raise ValueError("budget is more than dst_table's pages hold")
+    max_len = min(top, width * c.page) if max_len is None else _size(max_len, "max_len")
+    kept = _empty((seqs, c.heads, budget), torch.int32, dev, stream) if kept is None else kept
+    new_lens = _empty((seqs,), torch.int32, dev, stream) if new_lens is None else new_lens
+    new_weights = _empty((seqs, c.heads, budget), torch.float32, dev, stream) if new_weights is None else new_weights
     _check_tensor(kept, "kept", torch.int32, (seqs, c.heads, budget), dev)
     _check_tensor(new_lens, "new_lens", torch.int32, (seqs,), dev)
     _check_tensor(new_weights, "new_weights", torch.float32, (seqs, c.heads, budget), dev)
     a = HqKvEvictArgs(table.data_ptr(), lens.data_ptr(), weights.data_ptr(), top, seqs, width,
-                      min(top, width * c.page) if max_len is None else max_len, budget, sink, recent, dst_table.data_ptr(),
+                      max_len, budget, sink, recent, dst_table.data_ptr(),
                       dst_table.shape[-1], kept.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr())
     _check(lib().hq_kv_evict(ctypes.byref(c), ctypes.byref(a), _stream_handle(stream)), "hq_kv_evict")
     return kept, new_lens, new_weights

@@ -289,11 +289,12 @@ __device__ __forceinline__ void drop_scales(uint32_t vs[2], uint32_t mask) {
     if (mask & (1u << i)) vs[i >> 1] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
 }
 
-// tanh from the exponential: 1 - 2 / (e^2x + 1) away from zero, the odd series below 2^-3 in magnitude
-// (next term 17 x^7 / 315 < 3 10^-8 x), so that small scores keep their relative precision.
+// tanh from the exponential: 1 - 2 / (e^2x + 1) away from zero, the odd series to x^7 below 2^-3 in
+// magnitude (the next term, 62 x^9 / 2835, is below 2^-29 of x), so that small scores keep their relative
+// precision.  NaN stays NaN (a key whose scales are NaN).
 __device__ __forceinline__ float tanh32(float x) {
   const float a = fabsf(x), x2 = x * x;
-  const float e = __builtin_amdgcn_exp2f(fminf(a, 20.0f) * 2.885390081777927f);
+  const float e = __builtin_amdgcn_exp2f((a > 20.0f ? 20.0f : a) * 2.885390081777927f);
   const float big = __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f);
   const float small = __builtin_fmaf(x2, __builtin_fmaf(x2, __builtin_fmaf(x2, -17.0f / 315.0f, 2.0f / 15.0f), -1.0f / 3.0f), 1.0f) * a;
   return __builtin_copysignf(a < 0.125f ? small : big, x);
@@ -367,6 +368,7 @@ __device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K
   top = fmaxf(top, lane_xor<1>(top));
   int e = 0;
   if (top > 0.0f && __builtin_isfinite(top)) e = 15 - __builtin_amdgcn_frexp_expf(top);
+  e = e < 120 ? e : 120;  // the factor unit 2^-e stays normal: a masked score (-inf times it) is never NaN
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t g = (kappa >> 2) + 4u * (i >> 1), c = 2u * (kappa & 3u) + (i & 1);
@@ -1135,8 +1137,10 @@ hipError_t launch_attend(const AttendArgs& a, const Tables& T, uint32_t items, h
 int check_attend(const hq_kv_cache* cache, const hq_kv_attend_args* g) {
   if (int rc = check_cache(cache)) return rc;
   if (!g || g->q_heads == 0 || g->q_heads % cache->heads || g->q_heads > 65535u * 16u) return HQ_ERR_INVALID_ARG;
-  if (g->max_len > 0x7FFFFFFFu || (uint64_t)g->table_width * cache->page > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  // token indices and the ends of chunks and steps past them are 32-bit
+  if (g->max_len > kMaxTokens || (uint64_t)g->table_width * cache->page > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
   if (g->total_q > (1ull << 31) || (uint64_t)g->max_q * (g->q_heads / cache->heads) > 0x7FFFFF00ull) return HQ_ERR_INVALID_ARG;
+  if ((uint64_t)g->seqs * cache->heads > kMaxThreads / kAttBlock) return HQ_ERR_INVALID_ARG;
   if (!g->q_start && g->seqs && g->total_q % g->seqs) return HQ_ERR_INVALID_ARG;
   return HQ_OK;
 }
@@ -1168,8 +1172,10 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   if (((uintptr_t)g.lens | (uintptr_t)g.table | (uintptr_t)g.q_start | (uintptr_t)g.weights) & 3u) return HQ_ERR_INVALID_ARG;
   const Plan p = plan_of(*cache, g);
   if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < p.bytes) return HQ_ERR_INVALID_ARG;
-  if (p.items * p.splits > 0x7FFFFFFFull || p.items * p.tile_rows > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
-  if ((uint64_t)g.seqs * cache->heads * ((g.max_len + 255u) / 256u) > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  // every launch below 2^32 threads: workgroups of 256 and 512, a row's 16 lanes, a row's join
+  if (p.items * p.splits > kMaxThreads / kManyBlock || p.items * p.tile_rows > kMaxThreads / 16) return HQ_ERR_INVALID_ARG;
+  if (p.splits > 1 && p.items * p.tile_rows > kMaxThreads / kAttBlock) return HQ_ERR_INVALID_ARG;
+  if ((uint64_t)g.seqs * cache->heads * ((g.max_len + 255u) / 256u) > kMaxThreads / kAttBlock) return HQ_ERR_INVALID_ARG;
   AttendArgs a;
   a.cache = static_cast<const uint8_t*>(cache->data);
   a.q = g.q;

@@ -241,114 +241,203 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 __device__ __forceinline__ uint32_t clamp_len(int32_t n, uint32_t most) { return n < 0 ? 0u : (uint32_t)n < most ? (uint32_t)n : most; }
 
-// One workgroup per (sequence, head): the key of the last token that stays by four counting passes of
-// 8 bits each (most significant first), then one ordered pass that numbers the tokens that stay.
-constexpr int kSelect = 1024;
+// One workgroup per (sequence, head): the key of the last token that stays by three counting passes of 11, 11
+// and 10 bits (most significant first), then one ordered pass that numbers the tokens that stay.  A wavefront
+// owns a run of tokens, PER of them a lane in registers (one read of the weights, for up to 1024 PER tokens), so the ordered pass needs the counts of the wavefronts before it and no exchange within.  With
+// PER == 0 the weights are read again in each pass.
+constexpr int kSelect = 1024, kSelectWaves = kSelect / 64, kHeld = 32, kBins = 2048;
+
+template <int PER>
 __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_prefix, s_left, part[2][kSelect / 64];
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t s_prefix, s_left, s_wave[kSelectWaves], s_tie[kSelectWaves];
   const uint32_t b = blockIdx.x / a.heads, h = blockIdx.x % a.heads, tid = threadIdx.x;
+  const uint32_t lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t width_tokens = a.width << a.page_log2;
   const uint32_t n = clamp_len(a.lens[b], a.max_len < width_tokens ? a.max_len : width_tokens);
   const uint32_t m = n < a.budget ? n : a.budget;
   const float* w = a.weights + ((uint64_t)b * a.heads + h) * a.wstride;
-  const uint32_t lo = a.sink < n ? a.sink : n, hi = n - (a.recent < n ? a.recent : n) > lo ? n - (a.recent < n ? a.recent : n) : lo;
-  uint32_t want = m - (lo + (n - hi));  // of the middle [lo, hi)
-  if (n <= a.budget) want = hi - lo;
+  const uint32_t lo = a.sink < n ? a.sink : n, rest = n - (a.recent < n ? a.recent : n), hi = rest > lo ? rest : lo;
+  const uint32_t want = n <= a.budget ? hi - lo : m - (lo + (n - hi));  // of the middle [lo, hi)
+  const bool all = want == hi - lo;
+  // the wavefront's run of tokens: `steps` times 64 from `first`
+  const uint32_t steps = (n + kSelect - 1) / kSelect, first = wave * steps * 64u + lane;
+  float held[PER ? PER : 1];
+  if (PER) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      held[PER ? i : 0] = 0.0f;
+      if ((uint32_t)i < steps && first + 64u * i < n) held[PER ? i : 0] = w[first + 64u * i];
+    }
+  }
+  auto each = [&](auto&& body) __attribute__((always_inline)) {
+    if (PER) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if ((uint32_t)i < steps) body(first + 64u * i, held[PER ? i : 0]);
+    } else {
+      for (uint32_t i = 0; i < steps; ++i) body(first + 64u * i, first + 64u * i < n ? w[first + 64u * i] : 0.0f);
+    }
+  };
   if (tid == 0 && h == 0) a.new_lens[b] = (int32_t)m;
+
   uint32_t prefix = 0, left = want;  // key bits found so far; how many of the equal ones still to take
-  if (want < hi - lo && want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+  if (!all && want > 0) {
+    hist[2 * tid] = hist[2 * tid + 1] = 0;
+    __syncthreads();
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t above = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u, mask = pass == 2 ? 1023u : 2047u;
+      each([&](uint32_t t, float wt) {
+        const uint32_t key = weight_key(wt), bin = (key >> shift) & mask;
+        const bool in = t >= lo && t < hi && (key & above) == prefix;
+        const uint64_t votes = __builtin_amdgcn_ballot_w64(in);
+        if (!votes) return;
+        // the first lane's bin is counted with one addition, so that many equal keys do not queue up
+        const uint32_t lead = (uint32_t)__builtin_ctzll(votes), common = __builtin_amdgcn_readlane(bin, lead);
+        const bool same = in && bin == common;
+        const uint32_t count = (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(same));
+        if (in && (!same || lane == lead)) atomicAdd(&hist[bin], same ? count : 1u);
+      });
       __syncthreads();
-      const uint32_t above = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      for (uint32_t t = lo + tid; t < hi; t += kSelect) {
-        const uint32_t key = weight_key(w[t]);
-        if ((key & above) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+      // tokens in this thread's two bins and all above them
+      const uint32_t c1 = hist[2 * tid + 1], c0 = hist[2 * tid];
+      hist[2 * tid] = hist[2 * tid + 1] = 0;
+      uint32_t sum = c0 + c1;
+#pragma unroll
+      for (uint32_t d = 1; d < 64; d <<= 1) {
+        const uint32_t up = (uint32_t)__builtin_amdgcn_ds_bpermute((int)(((lane + d) & 63u) << 2), (int)sum);
+        if (lane + d < 64u) sum += up;
       }
+      if (lane == 0) s_wave[wave] = sum;
       __syncthreads();
-      if (tid == 0) {
-        uint32_t c = left, d = 255;
-        while (d > 0 && hist[d] < c) c -= hist[d--];
-        s_prefix = prefix | (d << shift);
-        s_left = c;
+      for (uint32_t i = wave + 1; i < kSelectWaves; ++i) sum += s_wave[i];
+      const uint32_t before = sum - c0 - c1;  // in the bins above
+      if (before < left && left <= sum) {     // one thread
+        const bool upper = left <= before + c1;
+        s_prefix = prefix | (2 * tid + (upper ? 1u : 0u)) << shift;
+        s_left = upper ? left - before : left - before - c1;
       }
       __syncthreads();
       prefix = s_prefix;
       left = s_left;
-      __syncthreads();
     }
   }
-  const bool all = want == hi - lo;
-  const uint32_t lane = tid & 63u, wave = tid >> 6;
-  uint32_t kept = 0, eq = 0;
+
+  auto state = [&](uint32_t t, float wt, bool* take, bool* tie) __attribute__((always_inline)) {
+    const uint32_t key = weight_key(wt);
+    const bool in = t < n, fixed = t < lo || t >= hi;
+    *take = in && (fixed || all || (want > 0 && key > prefix));
+    *tie = in && !fixed && !all && want > 0 && key == prefix;
+  };
+  uint32_t sure = 0, ties = 0;
+  each([&](uint32_t t, float wt) {
+    bool take, tie;
+    state(t, wt, &take, &tie);
+    sure += (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(take));
+    ties += (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(tie));
+  });
+  __syncthreads();
+  if (lane == 0) {
+    s_wave[wave] = sure;
+    s_tie[wave] = ties;
+  }
+  __syncthreads();
+  uint32_t kept = 0, eq = 0;  // tokens that stay, and ties, of the wavefronts before
+  for (uint32_t i = 0; i < wave; ++i) {
+    const uint32_t room = left > eq ? left - eq : 0u, tie = s_tie[i];
+    kept += s_wave[i] + (tie < room ? tie : room);
+    eq += tie;
+  }
   int32_t* dst = a.kept + ((uint64_t)b * a.heads + h) * a.budget;
   float* wd = a.new_weights ? a.new_weights + ((uint64_t)b * a.heads + h) * a.budget : nullptr;
-  for (uint32_t t0 = 0; t0 < n; t0 += kSelect) {
-    const uint32_t t = t0 + tid;
-    bool take = false, tie = false;
-    float wt = 0.0f;
-    if (t < n) {
-      wt = w[t];
-      const bool fixed = t < lo || t >= hi;
-      const uint32_t key = weight_key(wt);
-      take = fixed || all || (want > 0 && key > prefix);
-      tie = !fixed && !all && want > 0 && key == prefix;
-    }
-    // ties before this token: exclusive count over the workgroup
+  const uint64_t below = (1ull << lane) - 1ull;
+  each([&](uint32_t t, float wt) {
+    bool take, tie;
+    state(t, wt, &take, &tie);
     const uint64_t vt = __builtin_amdgcn_ballot_w64(tie);
-    if (lane == 0) part[0][wave] = (uint32_t)__builtin_popcountll(vt);
-    __syncthreads();
-    uint32_t before = eq, total = 0;
-    for (uint32_t i = 0; i < kSelect / 64; ++i) {
-      if (i < wave) before += part[0][i];
-      total += part[0][i];
-    }
-    before += (uint32_t)__builtin_popcountll(vt & ((1ull << lane) - 1ull));
-    eq += total;
-    take = take || (tie && before < left);
+    take = take || (tie && eq + (uint32_t)__builtin_popcountll(vt & below) < left);
+    eq += (uint32_t)__builtin_popcountll(vt);
     const uint64_t vk = __builtin_amdgcn_ballot_w64(take);
-    if (lane == 0) part[1][wave] = (uint32_t)__builtin_popcountll(vk);
-    __syncthreads();
-    uint32_t at = kept, sum = 0;
-    for (uint32_t i = 0; i < kSelect / 64; ++i) {
-      if (i < wave) at += part[1][i];
-      sum += part[1][i];
-    }
-    at += (uint32_t)__builtin_popcountll(vk & ((1ull << lane) - 1ull));
-    kept += sum;
+    const uint32_t at = kept + (uint32_t)__builtin_popcountll(vk & below);
+    kept += (uint32_t)__builtin_popcountll(vk);
     if (take && at < a.budget) {
       dst[at] = (int32_t)t;
       if (wd) wd[at] = wt;
     }
-  }
+  });
   for (uint32_t j = m + tid; j < a.budget; j += kSelect) {
     dst[j] = -1;
     if (wd) wd[j] = 0.0f;
   }
 }
 
-// Moves the tokens that stay, 16 lanes a token: lane g carries group g's codes and scales of K and V.
+// Moves the tokens that stay: 16 lanes take four consecutive destination tokens, which are one block of V, so
+// that a lane stores its group's codes and scales of all four at once.  Values lie by blocks of four tokens,
+// so where a quarter of the tokens stay nearly all of V is read; that traffic bounds the kernel.
 template <int BITS>
-__global__ __launch_bounds__(kBlock) void evict_move_kernel(EvictArgs a) {
-  const uint32_t lane = threadIdx.x & 15u;
-  const uint64_t item = (uint64_t)blockIdx.x * (kBlock / 16) + (threadIdx.x >> 4);
-  if (item >= (uint64_t)a.seqs * a.heads * a.budget) return;
-  const uint32_t j = (uint32_t)(item % a.budget), bh = (uint32_t)(item / a.budget), b = bh / a.heads, h = bh % a.heads;
-  const int32_t src = a.kept[item];
-  if (src < 0) return;
-  const uint32_t P = 1u << a.page_log2, so = (uint32_t)src & (P - 1u), to = j & (P - 1u);
-  const int32_t sp = a.table[(uint64_t)b * a.width + ((uint32_t)src >> a.page_log2)];
+__global__ __launch_bounds__(kBlock) void evict_move_kernel(EvictArgs a, uint32_t blocks) {
+  const uint32_t l = threadIdx.x & 15u, bh = blockIdx.x / blocks, b = bh / a.heads, h = bh % a.heads;
+  const uint32_t j = ((blockIdx.x % blocks) * (kBlock / 16) + (threadIdx.x >> 4)) * 4u;
+  if (j >= a.budget) return;
+  const int32_t* kept = a.kept + (uint64_t)bh * a.budget;
+  const uint32_t P = 1u << a.page_log2, to = j & (P - 1u);
   const int32_t dp = a.dst[(uint64_t)b * a.dst_width + (j >> a.page_log2)];
-  if (sp < 0 || (uint32_t)sp >= a.pages || dp < 0 || (uint32_t)dp >= a.pages) return;
+  if ((uint32_t)dp >= a.pages) return;
   const uint64_t size = (uint64_t)P * Page<BITS>::kToken;
-  const uint8_t* s = a.cache + ((uint64_t)sp * a.heads + h) * size;
   uint8_t* d = a.cache + ((uint64_t)dp * a.heads + h) * size;
+  int32_t src[4];
+  const uint8_t* page[4];
+  bool whole = true;
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i) {
+    src[i] = j + i < a.budget ? kept[j + i] : -1;
+    const int32_t sp = src[i] >= 0 ? a.table[(uint64_t)b * a.width + ((uint32_t)src[i] >> a.page_log2)] : -1;
+    if ((uint32_t)sp >= a.pages) src[i] = -1;
+    page[i] = a.cache + ((uint64_t)(src[i] < 0 ? 0 : sp) * a.heads + h) * size;
+    whole &= src[i] >= 0;
+  }
   typedef uint32_t piece __attribute__((ext_vector_type(BITS / 4)));
-  *reinterpret_cast<piece*>(d + Page<BITS>::k_code(P, to) + lane * BITS) = *reinterpret_cast<const piece*>(s + Page<BITS>::k_code(P, so) + lane * BITS);
-  *reinterpret_cast<piece*>(d + Page<BITS>::v_code(P, to, lane)) = *reinterpret_cast<const piece*>(s + Page<BITS>::v_code(P, so, lane));
-  *reinterpret_cast<uint16_t*>(d + Page<BITS>::k_scale(P, to) + 2u * lane) = *reinterpret_cast<const uint16_t*>(s + Page<BITS>::k_scale(P, so) + 2u * lane);
-  *reinterpret_cast<uint16_t*>(d + Page<BITS>::v_scale(P, to, lane)) = *reinterpret_cast<const uint16_t*>(s + Page<BITS>::v_scale(P, so, lane));
+  piece v[4];
+  uint32_t s[4];
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i) {
+    const uint32_t so = (uint32_t)(src[i] < 0 ? 0 : src[i]) & (P - 1u);
+    v[i] = *reinterpret_cast<const piece*>(page[i] + Page<BITS>::v_code(P, so, l));
+    s[i] = *reinterpret_cast<const uint16_t*>(page[i] + Page<BITS>::v_scale(P, so, l));
+  }
+  // keys: the lane's quarter of one of the four vectors
+  const uint32_t which = l >> 2, part = l & 3u;
+  const int32_t ks = which == 0 ? src[0] : which == 1 ? src[1] : which == 2 ? src[2] : src[3];
+  const uint8_t* kp = which == 0 ? page[0] : which == 1 ? page[1] : which == 2 ? page[2] : page[3];
+  const uint32_t ko = (uint32_t)(ks < 0 ? 0 : ks) & (P - 1u);
+  const uint4* kc = reinterpret_cast<const uint4*>(kp + Page<BITS>::k_code(P, ko) + part * 4u * BITS);
+  const uint4 k0 = kc[0], k1 = kc[BITS / 8];
+  const uint2 kscale = *reinterpret_cast<const uint2*>(kp + Page<BITS>::k_scale(P, ko) + 8u * part);
+  if (ks >= 0) {
+    uint4* kd = reinterpret_cast<uint4*>(d + Page<BITS>::k_code(P, to + which) + part * 4u * BITS);
+    kd[0] = k0;
+    if (BITS == 8) kd[1] = k1;
+    *reinterpret_cast<uint2*>(d + Page<BITS>::k_scale(P, to + which) + 8u * part) = kscale;
+  }
+  uint8_t *vd = d + Page<BITS>::v_code(P, to, l), *sd = d + Page<BITS>::v_scale(P, to, l);
+  if (whole) {
+    uint32_t w[BITS];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < BITS / 4; ++c) w[i * (BITS / 4) + c] = v[i][c];
+#pragma unroll
+    for (int i = 0; i < BITS / 4; ++i) reinterpret_cast<uint4*>(vd)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    *reinterpret_cast<uint2*>(sd) = make_uint2(s[0] | s[1] << 16, s[2] | s[3] << 16);
+  } else {
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+      if (src[i] >= 0) {
+        reinterpret_cast<piece*>(vd)[i] = v[i];
+        reinterpret_cast<uint16_t*>(sd)[i] = (uint16_t)s[i];
+      }
+  }
 }
 
 }  // namespace hq_kv
@@ -388,7 +477,7 @@ int hq_kv_append(const hq_kv_cache* cache, const void* k, const void* v, int32_t
   a.vec = !(((uintptr_t)k | (uintptr_t)v) & 15u) && !(a.kt % per) && !(a.kh % per) && !(a.vt % per) && !(a.vh % per);
   const uint64_t items = ((tokens + 3) / 4) * cache->heads * 2;
   const uint64_t grid = (items + kBlock / 64 - 1) / (kBlock / 64);
-  if (grid > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  if (grid > kMaxThreads / kBlock) return HQ_ERR_INVALID_ARG;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (cache->bits == 4) hipLaunchKernelGGL(append_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
   else hipLaunchKernelGGL(append_kernel<8>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
@@ -417,7 +506,7 @@ int hq_kv_read(const hq_kv_cache* cache, const int64_t* slots, uint64_t tokens, 
   a.sides = (k ? 1 : 0) | (v ? 2 : 0);
   const uint64_t items = ((tokens + 3) / 4) * cache->heads * (a.sides == 3 ? 2 : 1);
   const uint64_t grid = (items + kBlock / 64 - 1) / (kBlock / 64);
-  if (grid > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  if (grid > kMaxThreads / kBlock) return HQ_ERR_INVALID_ARG;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (cache->bits == 4) hipLaunchKernelGGL(read_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
   else hipLaunchKernelGGL(read_kernel<8>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
@@ -426,11 +515,11 @@ int hq_kv_read(const hq_kv_cache* cache, const int64_t* slots, uint64_t tokens, 
 
 int hq_kv_evict(const hq_kv_cache* cache, const hq_kv_evict_args* e, hq_stream_t stream) {
   if (int rc = check_cache(cache)) return rc;
-  if (!e || e->max_len > 0x7FFFFFFFu || e->budget > 0x7FFFFFFFu) return HQ_ERR_INVALID_ARG;
+  if (!e || e->max_len > kMaxTokens || e->budget > 0x7FFFFFFFu) return HQ_ERR_INVALID_ARG;
   if ((uint64_t)e->sink + e->recent > e->budget) return HQ_ERR_INVALID_ARG;
   if ((uint64_t)e->table_width * cache->page > 0x7FFFFFFFull || (uint64_t)e->dst_width * cache->page < e->budget) return HQ_ERR_INVALID_ARG;
   if (e->weights_stride < e->max_len) return HQ_ERR_INVALID_ARG;
-  if ((uint64_t)e->seqs * cache->heads > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  if ((uint64_t)e->seqs * cache->heads > kMaxThreads / kSelect) return HQ_ERR_INVALID_ARG;
   if (e->seqs == 0) return HQ_OK;
   if (!e->lens || !e->new_lens || (e->max_len && (!e->weights || !e->table)) || (e->budget && (!e->kept || !e->dst_table))) return HQ_ERR_INVALID_ARG;
   if (((uintptr_t)e->lens | (uintptr_t)e->new_lens | (uintptr_t)e->weights | (uintptr_t)e->table | (uintptr_t)e->kept |
@@ -456,13 +545,17 @@ int hq_kv_evict(const hq_kv_cache* cache, const hq_kv_evict_args* e, hq_stream_t
   a.budget = e->budget;
   a.sink = e->sink;
   a.recent = e->recent;
-  const uint64_t moves = (uint64_t)e->seqs * cache->heads * e->budget, grid = (moves + kBlock / 16 - 1) / (kBlock / 16);
-  if (grid > 0x7FFFFFFFull) return HQ_ERR_INVALID_ARG;
+  // 64 destination tokens a workgroup
+  const uint32_t blocks = (e->budget + kBlock / 4 - 1) / (kBlock / 4);
+  const uint64_t grid = (uint64_t)e->seqs * cache->heads * blocks;
+  if (grid > kMaxThreads / kBlock) return HQ_ERR_INVALID_ARG;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  hipLaunchKernelGGL(evict_select_kernel, dim3(e->seqs * cache->heads), dim3(kSelect), 0, st, a);
-  if (grid) {
-    if (cache->bits == 4) hipLaunchKernelGGL(evict_move_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a);
-    else hipLaunchKernelGGL(evict_move_kernel<8>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a);
+  const dim3 select(e->seqs * cache->heads);
+  if (e->max_len <= kSelect * kHeld) hipLaunchKernelGGL(evict_select_kernel<kHeld>, select, dim3(kSelect), 0, st, a);
+  else hipLaunchKernelGGL(evict_select_kernel<0>, select, dim3(kSelect), 0, st, a);
+  if (grid && cache->pages) {
+    if (cache->bits == 4) hipLaunchKernelGGL(evict_move_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, blocks);
+    else hipLaunchKernelGGL(evict_move_kernel<8>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, blocks);
   }
   return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
 }

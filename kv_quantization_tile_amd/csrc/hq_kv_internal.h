@@ -10,7 +10,8 @@
 
 namespace hq_kv {
 
-inline uint32_t page_bytes(const hq_kv_cache& c) { return c.page * 2u * (16u * (uint32_t)c.bits + 32u); }
+constexpr uint64_t kMaxThreads = 0xFFFFFFFFull;  // of one launch
+constexpr uint32_t kMaxTokens = 1u << 30;        // of one sequence
 
 // HQ_OK for a cache the kernels can address.  P a power of two (slots split by shift and mask) and at
 // least 16 (a block of 16 tokens lies in one page).
