@@ -35,27 +35,22 @@ struct AppendArgs {
   const int64_t* slots;
   uint64_t tokens;
   int64_t kt, kh, vt, vh;  // strides in values
-  uint32_t heads, pages, page_log2;
+  uint32_t heads, pages, page_log2, quads;
   int f32, vec;
 };
 
 // One vector per 16 lanes; the four rows of a wavefront take four consecutive tokens of one head and
-// side (K or V), so that the V pieces (4 bytes every 16) of neighbouring tokens meet in one line.
-// About 330 vector instructions a wavefront-step against 234 MB for a prompt of 32768 tokens and 8 heads.
+// side (K or V), so that the V pieces (4 bytes every 16) of neighbouring tokens meet in one line, and `quads`
+// such fours in turn, so that the twiddles are fetched once for all of them.
 template <int BITS>
 __global__ __launch_bounds__(kBlock) void append_kernel(AppendArgs a, Tables K) {
   const uint32_t lane = threadIdx.x & 63u, l = lane & 15u, row = lane >> 4;
-  const uint64_t items = ((a.tokens + 3) / 4) * a.heads * 2;
-  const uint64_t item = (uint64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
-  if (item >= items) return;
-  const uint32_t side = (uint32_t)(item & 1u);
-  const uint64_t rest = item >> 1;
-  const uint32_t head = (uint32_t)(rest % a.heads);
-  const uint64_t tok = (rest / a.heads) * 4 + row;
-  const bool have = tok < a.tokens;
-  const int64_t slot = have ? a.slots[tok] : -1;
+  const uint32_t item = __builtin_amdgcn_readfirstlane(blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6));
+  const uint32_t side = item & 1u, head = (item >> 1) % a.heads;
+  uint64_t tok = (uint64_t)((item >> 1) / a.heads) * a.quads * 4u;
+  if (tok >= a.tokens) return;
+  const uint64_t end = tok + 4u * a.quads < a.tokens ? tok + 4u * a.quads : a.tokens;
   const uint32_t P = 1u << a.page_log2;
-  const bool live = slot >= 0 && slot < ((int64_t)a.pages << a.page_log2);
   const LaneForward f = lane_forward(K, l);
   const uint32_t kappa = rev4(l);
   float m[8];
@@ -69,95 +64,100 @@ __global__ __launch_bounds__(kBlock) void append_kernel(AppendArgs a, Tables K) 
       m[2 * r + 1] *= side ? K.v[c + 1] : K.k[c + 1];
     }
   }
-  float x[8], y[8];
-  const int64_t off = side ? (int64_t)tok * a.vt + (int64_t)head * a.vh : (int64_t)tok * a.kt + (int64_t)head * a.kh;
-  const void* src = side ? a.v : a.k;
+  for (tok += row; tok - row < end; tok += 4) {
+    const int64_t slot = tok < end ? a.slots[tok] : -1;
+    const bool live = slot >= 0 && slot < ((int64_t)a.pages << a.page_log2);
+    float x[8], y[8];
+    const int64_t off = side ? (int64_t)tok * a.vt + (int64_t)head * a.vh : (int64_t)tok * a.kt + (int64_t)head * a.kh;
+    const void* src = side ? a.v : a.k;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-  if (live) {
-    if (a.f32) {
-      const float* p = static_cast<const float*>(src) + off + 8 * l;
-      if (a.vec) {
-        const float4 u0 = reinterpret_cast<const float4*>(p)[0], u1 = reinterpret_cast<const float4*>(p)[1];
-        x[0] = u0.x; x[1] = u0.y; x[2] = u0.z; x[3] = u0.w;
-        x[4] = u1.x; x[5] = u1.y; x[6] = u1.z; x[7] = u1.w;
+    for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    if (live) {
+      if (a.f32) {
+        const float* p = static_cast<const float*>(src) + off + 8 * l;
+        if (a.vec) {
+          const float4 u0 = reinterpret_cast<const float4*>(p)[0], u1 = reinterpret_cast<const float4*>(p)[1];
+          x[0] = u0.x; x[1] = u0.y; x[2] = u0.z; x[3] = u0.w;
+          x[4] = u1.x; x[5] = u1.y; x[6] = u1.z; x[7] = u1.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = p[i];
+        }
       } else {
+        const uint16_t* p = static_cast<const uint16_t*>(src) + off + 8 * l;
+        uint32_t w[4];
+        if (a.vec) {
+          const uint4 u = *reinterpret_cast<const uint4*>(p);
+          w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = p[i];
-      }
-    } else {
-      const uint16_t* p = static_cast<const uint16_t*>(src) + off + 8 * l;
-      uint32_t w[4];
-      if (a.vec) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-      } else {
+          for (int i = 0; i < 4; ++i) w[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = __uint_as_float(w[i] << 16);
+          x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
       }
     }
-  }
-  forward_row(x, y, m, l, f);
+    forward_row(x, y, m, l, f);
 
-  // Group kappa / 4 + 4 r lies in the four lanes that share kappa / 4: l, l ^ 4, l ^ 8, l ^ 12.
-  constexpr int L = BITS == 4 ? 7 : 127;
-  bool bad = false;
-  float delta[4];
-  uint32_t hb[4], word[4], word1[4];
+    // Group kappa / 4 + 4 r lies in the four lanes that share kappa / 4: l, l ^ 4, l ^ 8, l ^ 12.
+    constexpr int L = BITS == 4 ? 7 : 127;
+    bool bad = false;
+    float delta[4];
+    uint32_t hb[4], word[4], word1[4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    bad |= !__builtin_isfinite(y[2 * r]) || !__builtin_isfinite(y[2 * r + 1]);
-    float g = fmaxf(fabsf(y[2 * r]), fabsf(y[2 * r + 1]));
-    g = fmaxf(g, lane_xor<8>(g));
-    g = fmaxf(g, lane_xor<4>(g));
-    const _Float16 h = (_Float16)fminf(div_l<L>(g), 65504.0f);
-    delta[r] = (float)h;
-    hb[r] = (uint32_t)__builtin_bit_cast(uint16_t, h);
-  }
-  const uint64_t votes = __builtin_amdgcn_ballot_w64(bad);
-  bad = ((votes >> (lane & 48u)) & 0xFFFFu) != 0;
+    for (int r = 0; r < 4; ++r) {
+      bad |= !__builtin_isfinite(y[2 * r]) || !__builtin_isfinite(y[2 * r + 1]);
+      float g = fmaxf(fabsf(y[2 * r]), fabsf(y[2 * r + 1]));
+      g = fmaxf(g, lane_xor<8>(g));
+      g = fmaxf(g, lane_xor<4>(g));
+      const _Float16 h = (_Float16)fminf(div_l<L>(g), 65504.0f);
+      delta[r] = (float)h;
+      hb[r] = (uint32_t)__builtin_bit_cast(uint16_t, h);
+    }
+    const uint64_t votes = __builtin_amdgcn_ballot_w64(bad);
+    bad = ((votes >> (lane & 48u)) & 0xFFFFu) != 0;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const float inv = delta[r] > 0.0f ? recip_f16_value(delta[r]) : 0.0f;
-    const int32_t q0 = (int32_t)__builtin_amdgcn_fmed3f(__builtin_rintf(y[2 * r] * inv), (float)-L, (float)L);
-    const int32_t q1 = (int32_t)__builtin_amdgcn_fmed3f(__builtin_rintf(y[2 * r + 1] * inv), (float)-L, (float)L);
-    const uint32_t j = kappa & 3u;  // the lane's pair of the group's 8 codes
-    if (BITS == 4) {
-      word[r] = (((uint32_t)q0 & 15u) | (((uint32_t)q1 & 15u) << 4)) << (8u * j);
-      word1[r] = 0;
-    } else {
-      const uint32_t two = (((uint32_t)q0 & 255u) | (((uint32_t)q1 & 255u) << 8)) << (16u * (j & 1u));
-      word[r] = j < 2u ? two : 0u;
-      word1[r] = j < 2u ? 0u : two;
+    for (int r = 0; r < 4; ++r) {
+      const float inv = delta[r] > 0.0f ? recip_f16_value(delta[r]) : 0.0f;
+      const int32_t q0 = (int32_t)__builtin_amdgcn_fmed3f(__builtin_rintf(y[2 * r] * inv), (float)-L, (float)L);
+      const int32_t q1 = (int32_t)__builtin_amdgcn_fmed3f(__builtin_rintf(y[2 * r + 1] * inv), (float)-L, (float)L);
+      const uint32_t j = kappa & 3u;  // the lane's pair of the group's 8 codes
+      if (BITS == 4) {
+        word[r] = (((uint32_t)q0 & 15u) | (((uint32_t)q1 & 15u) << 4)) << (8u * j);
+        word1[r] = 0;
+      } else {
+        const uint32_t two = (((uint32_t)q0 & 255u) | (((uint32_t)q1 & 255u) << 8)) << (16u * (j & 1u));
+        word[r] = j < 2u ? two : 0u;
+        word1[r] = j < 2u ? 0u : two;
+      }
+      word[r] |= lane_xor_u<8>(word[r]);
+      word[r] |= lane_xor_u<4>(word[r]);
+      if (BITS == 8) {
+        word1[r] |= lane_xor_u<8>(word1[r]);
+        word1[r] |= lane_xor_u<4>(word1[r]);
+      }
     }
-    word[r] |= lane_xor_u<8>(word[r]);
-    word[r] |= lane_xor_u<4>(word[r]);
-    if (BITS == 8) {
-      word1[r] |= lane_xor_u<8>(word1[r]);
-      word1[r] |= lane_xor_u<4>(word1[r]);
+    if (live) {
+      // each of the four lanes stores one of the four groups: r = kappa mod 4
+      const uint32_t r = kappa & 3u, g = (kappa >> 2) + 4u * r;
+      uint32_t w0 = r == 0 ? word[0] : r == 1 ? word[1] : r == 2 ? word[2] : word[3];
+      uint32_t w1 = r == 0 ? word1[0] : r == 1 ? word1[1] : r == 2 ? word1[2] : word1[3];
+      uint32_t h = r == 0 ? hb[0] : r == 1 ? hb[1] : r == 2 ? hb[2] : hb[3];
+      if (bad) {  // zero codes, NaN scales
+        w0 = w1 = 0u;
+        h = 0x7E00u;
+      }
+      const uint32_t t = (uint32_t)slot & (P - 1u);
+      uint8_t* page = a.cache + ((uint64_t)(slot >> a.page_log2) * a.heads + head) * ((uint64_t)P * Page<BITS>::kToken);
+      uint8_t* cdst = page + (side ? Page<BITS>::v_code(P, t, g) : Page<BITS>::k_code(P, t) + g * BITS);
+      if (BITS == 4) *reinterpret_cast<uint32_t*>(cdst) = w0;
+      else *reinterpret_cast<uint2*>(cdst) = make_uint2(w0, w1);
+      *reinterpret_cast<uint16_t*>(page + (side ? Page<BITS>::v_scale(P, t, g) : Page<BITS>::k_scale(P, t) + 2u * g)) = (uint16_t)h;
     }
   }
-  if (!live) return;
-  // each of the four lanes stores one of the four groups: r = kappa mod 4
-  const uint32_t r = kappa & 3u, g = (kappa >> 2) + 4u * r;
-  uint32_t w0 = r == 0 ? word[0] : r == 1 ? word[1] : r == 2 ? word[2] : word[3];
-  uint32_t w1 = r == 0 ? word1[0] : r == 1 ? word1[1] : r == 2 ? word1[2] : word1[3];
-  uint32_t h = r == 0 ? hb[0] : r == 1 ? hb[1] : r == 2 ? hb[2] : hb[3];
-  if (bad) {  // zero codes, NaN scales
-    w0 = w1 = 0u;
-    h = 0x7E00u;
-  }
-  const uint32_t t = (uint32_t)slot & (P - 1u);
-  uint8_t* page = a.cache + ((uint64_t)(slot >> a.page_log2) * a.heads + head) * ((uint64_t)P * Page<BITS>::kToken);
-  uint8_t* cdst = page + (side ? Page<BITS>::v_code(P, t, g) : Page<BITS>::k_code(P, t) + g * BITS);
-  if (BITS == 4) *reinterpret_cast<uint32_t*>(cdst) = w0;
-  else *reinterpret_cast<uint2*>(cdst) = make_uint2(w0, w1);
-  *reinterpret_cast<uint16_t*>(page + (side ? Page<BITS>::v_scale(P, t, g) : Page<BITS>::k_scale(P, t) + 2u * g)) = (uint16_t)h;
 }
 
 struct ReadArgs {
@@ -165,57 +165,58 @@ struct ReadArgs {
   const int64_t* slots;
   uint64_t tokens;
   void *k, *v;
-  uint32_t heads, pages, page_log2;
+  uint32_t heads, pages, page_log2, quads;
   int f32, sides;  // bit 0 K, bit 1 V
 };
 
 template <int BITS>
 __global__ __launch_bounds__(kBlock) void read_kernel(ReadArgs a, Tables K) {
   const uint32_t lane = threadIdx.x & 63u, l = lane & 15u, row = lane >> 4;
-  const uint32_t ns = a.sides == 3 ? 2u : 1u;
-  const uint64_t items = ((a.tokens + 3) / 4) * a.heads * ns;
-  const uint64_t item = (uint64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
-  if (item >= items) return;
-  const uint32_t side = ns == 2u ? (uint32_t)(item & 1u) : (uint32_t)a.sides >> 1;
-  const uint64_t rest = ns == 2u ? item >> 1 : item;
-  const uint32_t head = (uint32_t)(rest % a.heads);
-  const uint64_t tok = (rest / a.heads) * 4 + row;
-  const bool have = tok < a.tokens;
-  const int64_t slot = have ? a.slots[tok] : -1;
-  const bool live = slot >= 0 && slot < ((int64_t)a.pages << a.page_log2);
+  const uint32_t item = __builtin_amdgcn_readfirstlane(blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6));
+  const uint32_t side = a.sides == 3 ? item & 1u : (uint32_t)a.sides >> 1, rest = a.sides == 3 ? item >> 1 : item;
+  const uint32_t head = rest % a.heads;
+  uint64_t tok = (uint64_t)(rest / a.heads) * a.quads * 4u;
+  if (tok >= a.tokens) return;
+  const uint64_t end = tok + 4u * a.quads < a.tokens ? tok + 4u * a.quads : a.tokens;
   const uint32_t P = 1u << a.page_log2;
-  float y[8], x[8];
-  uint32_t w0 = 0, w1 = 0, hb = 0;
-  if (live) {
-    const uint32_t t = (uint32_t)slot & (P - 1u);
-    const uint8_t* page = a.cache + ((uint64_t)(slot >> a.page_log2) * a.heads + head) * ((uint64_t)P * Page<BITS>::kToken);
-    const uint8_t* c = page + (side ? Page<BITS>::v_code(P, t, l) : Page<BITS>::k_code(P, t) + l * BITS);
-    if (BITS == 4) {
-      w0 = *reinterpret_cast<const uint32_t*>(c);
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(c);
-      w0 = u.x;
-      w1 = u.y;
-    }
-    hb = *reinterpret_cast<const uint16_t*>(page + (side ? Page<BITS>::v_scale(P, t, l) : Page<BITS>::k_scale(P, t) + 2u * l));
-  }
-  const float delta = (float)__builtin_bit_cast(_Float16, (uint16_t)hb);
   const LaneInverse f = lane_inverse(K, l);
+  for (tok += row; tok - row < end; tok += 4) {
+    const bool have = tok < end;
+    const int64_t slot = have ? a.slots[tok] : -1;
+    const bool live = slot >= 0 && slot < ((int64_t)a.pages << a.page_log2);
+    float y[8], x[8];
+    uint32_t w0 = 0, w1 = 0, hb = 0;
+    if (live) {
+      const uint32_t t = (uint32_t)slot & (P - 1u);
+      const uint8_t* page = a.cache + ((uint64_t)(slot >> a.page_log2) * a.heads + head) * ((uint64_t)P * Page<BITS>::kToken);
+      const uint8_t* c = page + (side ? Page<BITS>::v_code(P, t, l) : Page<BITS>::k_code(P, t) + l * BITS);
+      if (BITS == 4) {
+        w0 = *reinterpret_cast<const uint32_t*>(c);
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(c);
+        w0 = u.x;
+        w1 = u.y;
+      }
+      hb = *reinterpret_cast<const uint16_t*>(page + (side ? Page<BITS>::v_scale(P, t, l) : Page<BITS>::k_scale(P, t) + 2u * l));
+    }
+    const float delta = (float)__builtin_bit_cast(_Float16, (uint16_t)hb);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int32_t q = BITS == 4 ? __builtin_amdgcn_sbfe(w0, 4 * i, 4) : __builtin_amdgcn_sbfe(i < 4 ? w0 : w1, 8 * (i & 3), 8);
-    y[i] = (float)q * delta;
-    if (K.scaled) y[i] *= side ? K.v[8 * l + i] : K.k[8 * l + i];
-  }
-  inverse_row(y, x, l, f);
-  if (!have) return;
-  const uint64_t at = (tok * a.heads + head) * kD;
-  void* out = side ? a.v : a.k;
+    for (int i = 0; i < 8; ++i) {
+      const int32_t q = BITS == 4 ? __builtin_amdgcn_sbfe(w0, 4 * i, 4) : __builtin_amdgcn_sbfe(i < 4 ? w0 : w1, 8 * (i & 3), 8);
+      y[i] = (float)q * delta;
+      if (K.scaled) y[i] *= side ? K.v[8 * l + i] : K.k[8 * l + i];
+    }
+    inverse_row(y, x, l, f);
+    if (have) {
+      const uint64_t at = (tok * a.heads + head) * kD;
+      void* out = side ? a.v : a.k;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {  // each store instruction covers 64 (128) consecutive bytes a row
-    const uint64_t i = at + 2u * inverse_n(l, e);
-    if (a.f32) *reinterpret_cast<float2*>(static_cast<float*>(out) + i) = make_float2(x[2 * e], x[2 * e + 1]);
-    else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + i) = bf16_pair(x[2 * e], x[2 * e + 1]);
+      for (int e = 0; e < 4; ++e) {  // each store instruction covers 64 (128) consecutive bytes a row
+        const uint64_t i = at + 2u * inverse_n(l, e);
+        if (a.f32) *reinterpret_cast<float2*>(static_cast<float*>(out) + i) = make_float2(x[2 * e], x[2 * e + 1]);
+        else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + i) = bf16_pair(x[2 * e], x[2 * e + 1]);
+      }
+    }
   }
 }
 
@@ -232,25 +233,27 @@ struct EvictArgs {
   uint32_t seqs, heads, pages, page_log2, width, dst_width, max_len, budget, sink, recent;
 };
 
-// Order-preserving key of a weight: larger weight, larger key; -0 counts as 0, NaN below everything.
+// Order-preserving key of a weight: larger weight, larger key; -0 counts as 0, NaN below everything.  Keys of
+// weights lie in [1, 0xFF800000]; 0 is a token past the end, all ones one that stays whatever its weight.
 __device__ __forceinline__ uint32_t weight_key(float w) {
   const uint32_t b = __float_as_uint(w + 0.0f);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0u;
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 1u;
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
 __device__ __forceinline__ uint32_t clamp_len(int32_t n, uint32_t most) { return n < 0 ? 0u : (uint32_t)n < most ? (uint32_t)n : most; }
 
-// One workgroup per (sequence, head): the key of the last token that stays by three counting passes of 11, 11
-// and 10 bits (most significant first), then one ordered pass that numbers the tokens that stay.  A wavefront
-// owns a run of tokens, PER of them a lane in registers (one read of the weights, for up to 1024 PER tokens), so the ordered pass needs the counts of the wavefronts before it and no exchange within.  With
-// PER == 0 the weights are read again in each pass.
+// One workgroup per (sequence, head): the m-th largest key by three counting passes of 11, 11 and 10 bits (most
+// significant first), then one ordered pass that numbers the tokens that stay.  A wavefront owns a run of
+// tokens, PER of them a lane as keys in registers (the weights are read once, for up to 1024 PER tokens), so
+// the ordered pass needs the counts of the wavefronts before it and no exchange within.  With PER == 0 the
+// weights are read again in each pass.  Vector instructions bound it: one compute unit works on a row.
 constexpr int kSelect = 1024, kSelectWaves = kSelect / 64, kHeld = 32, kBins = 2048;
 
 template <int PER>
 __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
-  __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t s_prefix, s_left, s_wave[kSelectWaves], s_tie[kSelectWaves];
+  __shared__ __align__(16) uint32_t hist[kBins], s_wave[kSelectWaves], s_tie[kSelectWaves];
+  __shared__ uint32_t s_prefix, s_left;
   const uint32_t b = blockIdx.x / a.heads, h = blockIdx.x % a.heads, tid = threadIdx.x;
   const uint32_t lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t width_tokens = a.width << a.page_log2;
@@ -258,16 +261,23 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
   const uint32_t m = n < a.budget ? n : a.budget;
   const float* w = a.weights + ((uint64_t)b * a.heads + h) * a.wstride;
   const uint32_t lo = a.sink < n ? a.sink : n, rest = n - (a.recent < n ? a.recent : n), hi = rest > lo ? rest : lo;
-  const uint32_t want = n <= a.budget ? hi - lo : m - (lo + (n - hi));  // of the middle [lo, hi)
-  const bool all = want == hi - lo;
   // the wavefront's run of tokens: `steps` times 64 from `first`
   const uint32_t steps = (n + kSelect - 1) / kSelect, first = wave * steps * 64u + lane;
-  float held[PER ? PER : 1];
+  auto key_at = [&](uint32_t t) __attribute__((always_inline)) {
+    return t >= n ? 0u : t < lo || t >= hi ? 0xFFFFFFFFu : weight_key(w[t]);
+  };
+  uint32_t held[PER ? PER : 1];
   if (PER) {
+    float raw[PER ? PER : 1];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      held[PER ? i : 0] = 0.0f;
-      if ((uint32_t)i < steps && first + 64u * i < n) held[PER ? i : 0] = w[first + 64u * i];
+      raw[PER ? i : 0] = 0.0f;
+      if ((uint32_t)i < steps && first + 64u * i < n) raw[PER ? i : 0] = w[first + 64u * i];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint32_t t = first + 64u * i;
+      held[PER ? i : 0] = t >= n ? 0u : t < lo || t >= hi ? 0xFFFFFFFFu : weight_key(raw[PER ? i : 0]);
     }
   }
   auto each = [&](auto&& body) __attribute__((always_inline)) {
@@ -276,26 +286,28 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
       for (int i = 0; i < PER; ++i)
         if ((uint32_t)i < steps) body(first + 64u * i, held[PER ? i : 0]);
     } else {
-      for (uint32_t i = 0; i < steps; ++i) body(first + 64u * i, first + 64u * i < n ? w[first + 64u * i] : 0.0f);
+      for (uint32_t i = 0; i < steps; ++i) body(first + 64u * i, key_at(first + 64u * i));
     }
   };
   if (tid == 0 && h == 0) a.new_lens[b] = (int32_t)m;
 
-  uint32_t prefix = 0, left = want;  // key bits found so far; how many of the equal ones still to take
-  if (!all && want > 0) {
+  // tokens with keys above `prefix` stay, and of those with it the first `left`
+  uint32_t prefix = m == n ? 0u : 0xFFFFFFFFu, left = 0;
+  if (m > 0 && m < n) {
+    prefix = 0;
+    left = m;
     hist[2 * tid] = hist[2 * tid + 1] = 0;
     __syncthreads();
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t above = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u, mask = pass == 2 ? 1023u : 2047u;
-      each([&](uint32_t t, float wt) {
-        const uint32_t key = weight_key(wt), bin = (key >> shift) & mask;
-        const bool in = t >= lo && t < hi && (key & above) == prefix;
+      each([&](uint32_t, uint32_t key) {
+        const bool in = (key & above) == prefix;
         const uint64_t votes = __builtin_amdgcn_ballot_w64(in);
         if (!votes) return;
         // the first lane's bin is counted with one addition, so that many equal keys do not queue up
-        const uint32_t lead = (uint32_t)__builtin_ctzll(votes), common = __builtin_amdgcn_readlane(bin, lead);
-        const bool same = in && bin == common;
+        const uint32_t bin = (key >> shift) & mask, lead = (uint32_t)__builtin_ctzll(votes);
+        const bool same = in && bin == (uint32_t)__builtin_amdgcn_readlane((int)bin, (int)lead);
         const uint32_t count = (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(same));
         if (in && (!same || lane == lead)) atomicAdd(&hist[bin], same ? count : 1u);
       });
@@ -311,7 +323,8 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
       }
       if (lane == 0) s_wave[wave] = sum;
       __syncthreads();
-      for (uint32_t i = wave + 1; i < kSelectWaves; ++i) sum += s_wave[i];
+#pragma unroll
+      for (uint32_t i = 0; i < kSelectWaves; ++i) sum += i > wave ? s_wave[i] : 0u;
       const uint32_t before = sum - c0 - c1;  // in the bins above
       if (before < left && left <= sum) {     // one thread
         const bool upper = left <= before + c1;
@@ -324,18 +337,10 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
     }
   }
 
-  auto state = [&](uint32_t t, float wt, bool* take, bool* tie) __attribute__((always_inline)) {
-    const uint32_t key = weight_key(wt);
-    const bool in = t < n, fixed = t < lo || t >= hi;
-    *take = in && (fixed || all || (want > 0 && key > prefix));
-    *tie = in && !fixed && !all && want > 0 && key == prefix;
-  };
   uint32_t sure = 0, ties = 0;
-  each([&](uint32_t t, float wt) {
-    bool take, tie;
-    state(t, wt, &take, &tie);
-    sure += (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(take));
-    ties += (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(tie));
+  each([&](uint32_t, uint32_t key) {
+    sure += (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(key > prefix));
+    ties += (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(key == prefix));
   });
   __syncthreads();
   if (lane == 0) {
@@ -344,26 +349,27 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
   }
   __syncthreads();
   uint32_t kept = 0, eq = 0;  // tokens that stay, and ties, of the wavefronts before
-  for (uint32_t i = 0; i < wave; ++i) {
-    const uint32_t room = left > eq ? left - eq : 0u, tie = s_tie[i];
-    kept += s_wave[i] + (tie < room ? tie : room);
+#pragma unroll
+  for (uint32_t i = 0; i < kSelectWaves; ++i) {
+    const uint32_t room = left > eq ? left - eq : 0u, tie = i < wave ? s_tie[i] : 0u;
+    kept += (i < wave ? s_wave[i] : 0u) + (tie < room ? tie : room);
     eq += tie;
   }
   int32_t* dst = a.kept + ((uint64_t)b * a.heads + h) * a.budget;
   float* wd = a.new_weights ? a.new_weights + ((uint64_t)b * a.heads + h) * a.budget : nullptr;
   const uint64_t below = (1ull << lane) - 1ull;
-  each([&](uint32_t t, float wt) {
-    bool take, tie;
-    state(t, wt, &take, &tie);
+  each([&](uint32_t t, uint32_t key) {
+    const bool tie = key == prefix;
     const uint64_t vt = __builtin_amdgcn_ballot_w64(tie);
-    take = take || (tie && eq + (uint32_t)__builtin_popcountll(vt & below) < left);
+    const bool take = key > prefix || (tie && eq + (uint32_t)__builtin_popcountll(vt & below) < left);
     eq += (uint32_t)__builtin_popcountll(vt);
     const uint64_t vk = __builtin_amdgcn_ballot_w64(take);
+    if (!vk) return;
     const uint32_t at = kept + (uint32_t)__builtin_popcountll(vk & below);
     kept += (uint32_t)__builtin_popcountll(vk);
     if (take && at < a.budget) {
       dst[at] = (int32_t)t;
-      if (wd) wd[at] = wt;
+      if (wd) wd[at] = w[t];
     }
   });
   for (uint32_t j = m + tid; j < a.budget; j += kSelect) {
@@ -446,6 +452,16 @@ using namespace hq_kv;
 
 static uint32_t log2_of(uint32_t v) { return 31u - (uint32_t)__builtin_clz(v); }
 
+// Workgroups of append and read, and the fours of tokens a wavefront takes in turn: as many as leave the chip
+// 16384 wavefronts (256 CUs of 4 SIMDs, 16 each), at most 32.
+static uint64_t transform_grid(uint64_t tokens, uint64_t rows, uint32_t* quads) {
+  const uint64_t all = (tokens + 3) / 4;
+  const uint64_t per = all * rows / 16384;
+  *quads = (uint32_t)(per < 1 ? 1 : per > 32 ? 32 : per);
+  const uint64_t items = (all + *quads - 1) / *quads * rows;
+  return (items + kBlock / 64 - 1) / (kBlock / 64);
+}
+
 extern "C" {
 
 int hq_kv_append(const hq_kv_cache* cache, const void* k, const void* v, int32_t dtype, uint64_t tokens,
@@ -475,8 +491,7 @@ int hq_kv_append(const hq_kv_cache* cache, const void* k, const void* v, int32_t
   // 16-byte loads where every row starts on 16 bytes, single values otherwise
   const int64_t per = 16 / size;
   a.vec = !(((uintptr_t)k | (uintptr_t)v) & 15u) && !(a.kt % per) && !(a.kh % per) && !(a.vt % per) && !(a.vh % per);
-  const uint64_t items = ((tokens + 3) / 4) * cache->heads * 2;
-  const uint64_t grid = (items + kBlock / 64 - 1) / (kBlock / 64);
+  const uint64_t grid = transform_grid(tokens, cache->heads * 2, &a.quads);
   if (grid > kMaxThreads / kBlock) return HQ_ERR_INVALID_ARG;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (cache->bits == 4) hipLaunchKernelGGL(append_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
@@ -504,8 +519,7 @@ int hq_kv_read(const hq_kv_cache* cache, const int64_t* slots, uint64_t tokens, 
   a.page_log2 = log2_of(cache->page);
   a.f32 = out_dtype == HQ_F32;
   a.sides = (k ? 1 : 0) | (v ? 2 : 0);
-  const uint64_t items = ((tokens + 3) / 4) * cache->heads * (a.sides == 3 ? 2 : 1);
-  const uint64_t grid = (items + kBlock / 64 - 1) / (kBlock / 64);
+  const uint64_t grid = transform_grid(tokens, cache->heads * (a.sides == 3 ? 2 : 1), &a.quads);
   if (grid > kMaxThreads / kBlock) return HQ_ERR_INVALID_ARG;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (cache->bits == 4) hipLaunchKernelGGL(read_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
