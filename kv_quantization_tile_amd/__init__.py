@@ -387,29 +387,30 @@ def hq_kv_cache(pages: int, heads: int, page: int = 64, bits: int = 4, device="c
 
 def _cache_arg(cache, bits, seed, lam_k, lam_v):
     """The C description of a cache tensor, and what has to outlive the call."""
-    torch = _torch()
-    if not (cache.is_cuda and cache.is_contiguous() and cache.dtype == torch.uint8 and cache.dim() == 3):
+    if cache.dtype != _torch().uint8 or cache.dim() != 3 or not (cache.is_cuda and cache.is_contiguous()):
         raise TypeError("cache must be a contiguous uint8 CUDA tensor [pages][heads][page bytes]")
-    if bits not in (4, 8):
+    if bits != 4 and bits != 8:
         raise ValueError("bits is 4 or 8")
     pages, heads, size = cache.shape
-    page, rest = divmod(size, hq_kv_token_bytes(bits))
+    page, rest = divmod(size, 2 * (16 * bits + 32))
     if rest:
         raise ValueError("the cache's last dimension is not a whole number of tokens at these bits")
+    if lam_k is None and lam_v is None:
+        return HqKvCache(cache.data_ptr(), pages, heads, page, bits, seed, None, None), None
     keep_k, pk = _host_lambda(lam_k)
     keep_v, pv = _host_lambda(lam_v)
     return HqKvCache(cache.data_ptr(), pages, heads, page, bits, seed, pk, pv), (keep_k, keep_v)
 
 
 def _check_tensor(t, name, dtype, shape, device):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
 def _size(v, name: str) -> int:
-    if not 0 <= int(v) <= 0xFFFFFFFF:
+    if not 0 <= v <= 0xFFFFFFFF:
         raise ValueError(f"{name} must be a 32-bit size, not {v}")
-    return int(v)
+    return v
 
 
 def _empty(shape, dtype, device, stream):
@@ -421,25 +422,33 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _check_rows(t, name, heads, device):
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128 or (t.stride(2) != 1 and t.numel()) or t.device != device:
-        raise ValueError(f"{name} must be [tokens][{heads}][128] on {device}, its last dimension contiguous")
+def _stream_on(stream, device):
+    """The handle of `stream`, or of the device's current stream (without the Stream object, which takes 3 us to make)."""
+    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
+def _row_strides(t, name, heads, device):
+    """Token and head strides of t [tokens][heads][128] (heads None: any)."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads) or t.device != device or (strides[2] != 1 and shape[0]):
+        raise ValueError(f"{name} must be [tokens][{heads or 'heads'}][128] on {device}, its last dimension contiguous")
+    return strides
+
+
+_Strides4 = ctypes.c_int64 * 4
 
 
 def hq_kv_append(cache, k, v, slots, bits: int = 4, seed: int = 0, lam_k=None, lam_v=None, stream=None):
     """Encode K and V of new tokens ([tokens][heads][128] bf16 or float32, any token and head strides) into
     their slots (int64 [tokens]: page * P + offset; a slot outside the cache, -1 say, writes nothing)."""
-    torch = _torch()
     c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
-    dev = cache.device
-    _check_rows(k, "k", c.heads, dev)
-    _check_rows(v, "v", c.heads, dev)
-    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+    dev, tokens = cache.device, k.shape[0]
+    ks, vs = _row_strides(k, "k", c.heads, dev), _row_strides(v, "v", c.heads, dev)
+    if k.dtype != v.dtype or v.shape[0] != tokens:
         raise ValueError("k and v must have one type and length")
-    _check_tensor(slots, "slots", torch.int64, (k.shape[0],), dev)
-    strides = (ctypes.c_int64 * 4)(k.stride(0), k.stride(1), v.stride(0), v.stride(1))
-    _check(lib().hq_kv_append(ctypes.byref(c), k.data_ptr(), v.data_ptr(), _dtype_code(k), k.shape[0], strides,
-                              slots.data_ptr(), _stream_handle(stream)), "hq_kv_append")
+    _check_tensor(slots, "slots", _torch().int64, (tokens,), dev)
+    _check(lib().hq_kv_append(ctypes.byref(c), k.data_ptr(), v.data_ptr(), _dtype_code(k), tokens, _Strides4(ks[0], ks[1], vs[0], vs[1]),
+                              slots.data_ptr(), _stream_on(stream, dev)), "hq_kv_append")
     return cache
 
 
@@ -449,14 +458,19 @@ def hq_kv_read(cache, slots, bits: int = 4, seed: int = 0, lam_k=None, lam_v=Non
     outside the cache reads as zeros."""
     torch = _torch()
     c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
-    _check_tensor(slots, "slots", torch.int64, (slots.numel(),), cache.device)
-    shape, dt = (slots.numel(), c.heads, 128), out_dtype or torch.bfloat16
-    k = _empty(shape, dt, cache.device, stream) if k is None else k
-    v = _empty(shape, dt, cache.device, stream) if v is None else v
-    _check_tensor(k, "k", dt, shape, cache.device)
-    _check_tensor(v, "v", dt, shape, cache.device)
-    _check(lib().hq_kv_read(ctypes.byref(c), slots.data_ptr(), slots.numel(), k.data_ptr(), v.data_ptr(), _dtype_code(k),
-                            _stream_handle(stream)), "hq_kv_read")
+    dev, tokens = cache.device, slots.numel()
+    _check_tensor(slots, "slots", torch.int64, (tokens,), dev)
+    shape, dt = (tokens, c.heads, 128), out_dtype or torch.bfloat16
+    if k is None:
+        k = _empty(shape, dt, dev, stream)
+    else:
+        _check_tensor(k, "k", dt, shape, dev)
+    if v is None:
+        v = _empty(shape, dt, dev, stream)
+    else:
+        _check_tensor(v, "v", dt, shape, dev)
+    _check(lib().hq_kv_read(ctypes.byref(c), slots.data_ptr(), tokens, k.data_ptr(), v.data_ptr(), _dtype_code(k),
+                            _stream_on(stream, dev)), "hq_kv_read")
     return k, v
 
 
@@ -467,15 +481,16 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
 
     table int32 [seqs][width], lens int32 [seqs] (tokens cached, the queries' own among them); q_start int32
     [seqs + 1] offsets of each sequence's queries (None: as many each); max_q, max_len bounds on a sequence's
-    queries and tokens (None: all queries, what the table's width or the weights hold).  weights float32 [seqs][heads][>= max_len] gets each
-    token's softmax weights added.  Returns out ([queries][q heads][128], bf16 unless given)."""
+    queries and tokens (None: all queries, what the table's width or the weights hold).  weights float32
+    [seqs][heads][>= max_len] gets each token's softmax weights added.  Returns out ([queries][q heads][128], bf16
+    unless given)."""
     torch = _torch()
     c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
     dev = cache.device
-    if q.dim() != 3 or q.shape[1] == 0 or q.shape[1] % c.heads:
+    strides = _row_strides(q, "q", None, dev)
+    total, heads, _ = q.shape
+    if heads == 0 or heads % c.heads:
         raise ValueError("q must be [queries][q heads][128], q heads a multiple of the cache's heads")
-    _check_rows(q, "q", q.shape[1], dev)
-    total, heads = q.shape[0], q.shape[1]
     seqs, width = lens.numel(), table.shape[-1]
     _check_tensor(lens, "lens", torch.int32, (seqs,), dev)
     _check_tensor(table, "table", torch.int32, (seqs, width), dev)
@@ -485,7 +500,8 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
         max_q = total if q_start is not None else total // max(seqs, 1)
     if out is None:
         out = _empty((total, heads, 128), torch.bfloat16, dev, stream)
-    _check_tensor(out, "out", out.dtype, (total, heads, 128), dev)
+    else:
+        _check_tensor(out, "out", out.dtype, (total, heads, 128), dev)
     stride = 0
     if weights is not None:
         if weights.dim() != 3:
@@ -494,17 +510,18 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
         _check_tensor(weights, "weights", torch.float32, (seqs, c.heads, stride), dev)
     if max_len is None:
         max_len = width * c.page if weights is None else min(stride, width * c.page)
-    a = HqKvAttendArgs(q.data_ptr(), out.data_ptr(), _dtype_code(q), _dtype_code(out), q.stride(0), q.stride(1), total, heads, seqs,
-                       _size(max_q, "max_q"), _size(max_len, "max_len"), q_start.data_ptr() if q_start is not None else None, table.data_ptr(), width,
-                       lens.data_ptr(), 128 ** -0.5 if scale is None else scale, softcap, 1 if causal else 0, _size(window, "window"),
-                       weights.data_ptr() if weights is not None else None, stride)
-    L, need = lib(), ctypes.c_size_t(0)
+    a = HqKvAttendArgs(q.data_ptr(), out.data_ptr(), _dtype_code(q), _dtype_code(out), strides[0], strides[1], total, heads, seqs,
+                       _size(max_q, "max_q"), _size(max_len, "max_len"), q_start.data_ptr() if q_start is not None else None,
+                       table.data_ptr(), width, lens.data_ptr(), 128 ** -0.5 if scale is None else scale, softcap, 1 if causal else 0,
+                       _size(window, "window"), weights.data_ptr() if weights is not None else None, stride)
+    L, cp, ap = lib(), ctypes.byref(c), ctypes.byref(a)
     if ws is None:
-        _check(L.hq_kv_attend_workspace_size(ctypes.byref(c), ctypes.byref(a), ctypes.byref(need)), "hq_kv_attend")
-        ws = _empty(max(need.value, 256), torch.uint8, dev, stream)
+        need = ctypes.c_size_t()
+        _check(L.hq_kv_attend_workspace_size(cp, ap, ctypes.byref(need)), "hq_kv_attend")
+        ws = _empty(need.value, torch.uint8, dev, stream)
     elif not (ws.is_contiguous() and ws.device == dev and ws.dtype == torch.uint8):
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
-    _check(L.hq_kv_attend(ctypes.byref(c), ctypes.byref(a), ws.data_ptr(), ws.numel(), _stream_handle(stream)), "hq_kv_attend")
+    _check(L.hq_kv_attend(cp, ap, ws.data_ptr(), ws.numel(), _stream_on(stream, dev)), "hq_kv_attend")
     return out
 
 
@@ -516,25 +533,31 @@ def hq_kv_evict(cache, table, lens, weights, budget: int, sink: int, recent: int
     new_weights float32 [seqs][heads][budget])."""
     torch = _torch()
     c, _ = _cache_arg(cache, bits, 0, None, None)
-    dev, seqs, width, top = cache.device, lens.numel(), table.shape[-1], weights.shape[-1]
+    dev, heads, seqs, width, dst_width, top = cache.device, c.heads, lens.numel(), table.shape[-1], dst_table.shape[-1], weights.shape[-1]
     _check_tensor(lens, "lens", torch.int32, (seqs,), dev)
     _check_tensor(table, "table", torch.int32, (seqs, width), dev)
-    _check_tensor(weights, "weights", torch.float32, (seqs, c.heads, top), dev)
-    _check_tensor(dst_table, "dst_table", torch.int32, (seqs, dst_table.shape[-1]), dev)
-    budget, sink, recent = _size(budget, "budget"), _size(sink, "sink"), _size(recent, "recent")
-    if budget > dst_table.shape[-1] * c.page:
+    _check_tensor(weights, "weights", torch.float32, (seqs, heads, top), dev)
+    _check_tensor(dst_table, "dst_table", torch.int32, (seqs, dst_width), dev)
+    shape = (seqs, heads, _size(budget, "budget"))
+    if budget > dst_width * c.page:
         raise ValueError("budget is more than dst_table's pages hold")
-    max_len = min(top, width * c.page) if max_len is None else _size(max_len, "max_len")
-    kept = _empty((seqs, c.heads, budget), torch.int32, dev, stream) if kept is None else kept
-    new_lens = _empty((seqs,), torch.int32, dev, stream) if new_lens is None else new_lens
-    new_weights = _empty((seqs, c.heads, budget), torch.float32, dev, stream) if new_weights is None else new_weights
-    _check_tensor(kept, "kept", torch.int32, (seqs, c.heads, budget), dev)
-    _check_tensor(new_lens, "new_lens", torch.int32, (seqs,), dev)
-    _check_tensor(new_weights, "new_weights", torch.float32, (seqs, c.heads, budget), dev)
+    if kept is None:
+        kept = _empty(shape, torch.int32, dev, stream)
+    else:
+        _check_tensor(kept, "kept", torch.int32, shape, dev)
+    if new_lens is None:
+        new_lens = _empty((seqs,), torch.int32, dev, stream)
+    else:
+        _check_tensor(new_lens, "new_lens", torch.int32, (seqs,), dev)
+    if new_weights is None:
+        new_weights = _empty(shape, torch.float32, dev, stream)
+    else:
+        _check_tensor(new_weights, "new_weights", torch.float32, shape, dev)
     a = HqKvEvictArgs(table.data_ptr(), lens.data_ptr(), weights.data_ptr(), top, seqs, width,
-                      max_len, budget, sink, recent, dst_table.data_ptr(),
-                      dst_table.shape[-1], kept.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr())
-    _check(lib().hq_kv_evict(ctypes.byref(c), ctypes.byref(a), _stream_handle(stream)), "hq_kv_evict")
+                      min(top, width * c.page) if max_len is None else _size(max_len, "max_len"), budget, _size(sink, "sink"),
+                      _size(recent, "recent"), dst_table.data_ptr(), dst_width, kept.data_ptr(), new_lens.data_ptr(),
+                      new_weights.data_ptr())
+    _check(lib().hq_kv_evict(ctypes.byref(c), ctypes.byref(a), _stream_on(stream, dev)), "hq_kv_evict")
     return kept, new_lens, new_weights
 
 

@@ -46,6 +46,7 @@ struct AttendArgs {
   uint64_t wstride, total_q;
   int64_t qt, qh;  // strides of q in values
   uint32_t heads, group, q_heads, pages, page_log2, width, seqs, max_q, max_len;
+  uint32_t group_mul, group_shift;  // query_of
   uint32_t tile_rows, tiles, splits, chunk, window;
   uint32_t wrows, wpad;  // stored scores: rows of an item, tokens a row
   int causal, q_f32, out_f32, vec;
@@ -58,6 +59,10 @@ struct AttendArgs {
   float* lse;           // [items][tile_rows]
   float* scores;        // [items][wrows][wpad]
 };
+
+// Query r / group of row r < 2^31: with 2^sh >= group > 2^(sh-1) and M = floor(2^(31+sh) / group) + 1 the product r M
+// exceeds r 2^(31+sh) / group by less than 2^(31+sh) / group, so its quotient by 2^(31+sh) is exact.
+__device__ __forceinline__ uint32_t query_of(const AttendArgs& a, uint32_t r) { return (uint32_t)(((uint64_t)r * a.group_mul) >> a.group_shift); }
 
 struct Seq {
   int64_t q0;
@@ -99,8 +104,8 @@ __device__ __forceinline__ void rows_range(const AttendArgs& a, const Seq& s, ui
   }
   const uint32_t r1 = r0 + count < rows ? r0 + count - 1u : rows - 1u;
   int32_t l0, h0, l1, h1;
-  visible(a, s, (int32_t)(r0 / a.group), &l0, &h0);
-  visible(a, s, (int32_t)(r1 / a.group), &l1, &h1);
+  visible(a, s, (int32_t)query_of(a, r0), &l0, &h0);
+  visible(a, s, (int32_t)query_of(a, r1), &l1, &h1);
   *lo = l0;
   *hi = h1;
 }
@@ -110,8 +115,8 @@ __device__ __forceinline__ void rows_common(const AttendArgs& a, const Seq& s, u
   *lo = *hi = 0;
   if (r0 + count > (uint32_t)s.m * a.group) return;
   int32_t x;
-  visible(a, s, (int32_t)((r0 + count - 1u) / a.group), lo, &x);
-  visible(a, s, (int32_t)(r0 / a.group), &x, hi);
+  visible(a, s, (int32_t)query_of(a, r0 + count - 1u), lo, &x);
+  visible(a, s, (int32_t)query_of(a, r0), &x, hi);
 }
 
 __device__ __forceinline__ float swap16_max(float x) {
@@ -337,7 +342,8 @@ __device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = 0.0f;
   if (r < (uint32_t)s.m * a.group) {
-    const int64_t at = (s.q0 + r / a.group) * a.qt + (int64_t)(h * a.group + r % a.group) * a.qh + 8 * l;
+    const uint32_t i = query_of(a, r);
+    const int64_t at = (s.q0 + i) * a.qt + (int64_t)(h * a.group + r - i * a.group) * a.qh + 8 * l;
     if (a.q_f32) {
       const float* p = static_cast<const float*>(a.q) + at;
 #pragma unroll
@@ -394,7 +400,8 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, const Tables& K, 
   }
   inverse_row(y, x, l, f);
   if (r >= (uint32_t)s.m * a.group) return;
-  const uint64_t at = ((uint64_t)(s.q0 + r / a.group) * a.q_heads + h * a.group + r % a.group) * kD;
+  const uint32_t q = query_of(a, r);
+  const uint64_t at = ((uint64_t)(s.q0 + q) * a.q_heads + h * a.group + r - q * a.group) * kD;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint64_t i = at + 2u * inverse_n(l, e);
@@ -415,13 +422,17 @@ __device__ __forceinline__ Item item_of(const AttendArgs& a, uint32_t item) {
   return i;
 }
 
-// The page of token tt (-1: absent, or past `end`), the same in every lane.
-__device__ __forceinline__ int32_t page_of(const AttendArgs& a, uint32_t b, int32_t tt, int32_t end) {
-  int32_t p = -1;
-  if (tt < end) p = a.table[(uint64_t)b * a.width + ((uint32_t)tt >> a.page_log2)];
-  p = __builtin_amdgcn_readfirstlane(p);
+// The table's entry for token tt (-1 past `end`), the same in every lane; and the page it names (-1: absent).  Two
+// steps, so that a loop can fetch an entry in one turn and first wait for it in the next: memory answers in
+// order, and waiting at once would wait for the codes asked for before it.
+__device__ __forceinline__ int32_t entry_of(const AttendArgs& a, uint32_t b, int32_t tt, int32_t end) {
+  return tt < end ? a.table[(uint64_t)b * a.width + ((uint32_t)tt >> a.page_log2)] : -1;
+}
+__device__ __forceinline__ int32_t page_in(const AttendArgs& a, int32_t entry) {
+  const int32_t p = __builtin_amdgcn_readfirstlane(entry);
   return (uint32_t)p < a.pages ? p : -1;
 }
+__device__ __forceinline__ int32_t page_of(const AttendArgs& a, uint32_t b, int32_t tt, int32_t end) { return page_in(a, entry_of(a, b, tt, end)); }
 
 // ---------------------------------------------------------------------------------------------
 // Up to 16 rows a (sequence, head): the single-token step.  A workgroup takes one split of the tokens; its
@@ -461,7 +472,7 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
     load(t, pg0, cur[0]);
     load(t + 16, pg1, cur[1]);
   }
-  int32_t pn0 = page_of(a, it.b, t + kStep, t1), pn1 = page_of(a, it.b, t + kStep + 16, t1);
+  int32_t en0 = entry_of(a, it.b, t + kStep, t1), en1 = entry_of(a, it.b, t + kStep + 16, t1);
 
   {  // the rows: four to a wavefront, 16 lanes each
     const uint32_t r = threadIdx.x >> 4;
@@ -483,7 +494,7 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
   }
   const float qf = s_f[n];
   int32_t row_lo = 0, row_hi = 0, all_lo = hi, all_hi = lo;
-  if (n < rows) visible(a, s, (int32_t)(n / a.group), &row_lo, &row_hi);
+  if (n < rows) visible(a, s, (int32_t)query_of(a, n), &row_lo, &row_hi);
   // the tokens every existing row sees need no mask (rows past the last are products with zero)
   if (rows) rows_common(a, s, 0, rows, &all_lo, &all_hi);
 
@@ -492,15 +503,15 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
   for (; t < t1; t += kStep) {
-    if (t + kStep < t1) {
-      load(t + kStep, pn0, nxt[0]);
-      load(t + kStep + 16, pn1, nxt[1]);
-    }
     const bool there[2] = {pg0 >= 0, pg1 >= 0};
-    pg0 = pn0;
-    pg1 = pn1;
-    pn0 = page_of(a, it.b, t + 2 * kStep, t1);
-    pn1 = page_of(a, it.b, t + 2 * kStep + 16, t1);
+    pg0 = page_in(a, en0);
+    pg1 = page_in(a, en1);
+    en0 = entry_of(a, it.b, t + 2 * kStep, t1);
+    en1 = entry_of(a, it.b, t + 2 * kStep + 16, t1);
+    if (t + kStep < t1) {
+      load(t + kStep, pg0, nxt[0]);
+      load(t + kStep + 16, pg1, nxt[1]);
+    }
     float sc[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -612,13 +623,15 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
   if (n == 0) *reinterpret_cast<f32x2*>(a.pml + p * 2) = (f32x2){mr, total};
 }
 
-// Joins a row's splits, turns it back and stores it: one workgroup a row, its 16 groups of 16 lanes take the
-// splits in turn.
-template <int BITS>
-__global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables K, uint32_t rows_per_item) {
-  __shared__ float s_y[16][kD + 4], s_m[16], s_l[16];
+// Joins a row's splits, turns it back and stores it.  WIDE: one workgroup a row, its 16 groups of 16 lanes take
+// the splits in turn and join in LDS; otherwise 16 lanes take a row and all its splits.
+template <int BITS, bool WIDE>
+__global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables K, uint32_t rows_per_item, uint32_t all_rows) {
+  __shared__ float s_y[WIDE ? 16 : 1][kD + 4], s_m[16], s_l[16];
   const uint32_t l = threadIdx.x & 15u, g = threadIdx.x >> 4;
-  const uint32_t item = blockIdx.x / rows_per_item, row = blockIdx.x % rows_per_item;
+  const uint32_t index = WIDE ? blockIdx.x : blockIdx.x * 16u + g;
+  if (!WIDE && index >= all_rows) return;
+  const uint32_t item = index / rows_per_item, row = index % rows_per_item;
   const Item it = item_of(a, item);
   const Seq s = seq_of(a, it.b);
   const uint32_t r = it.tile * a.tile_rows + row;
@@ -630,7 +643,7 @@ __global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables
   float m = -1.0e30f, sum = 0.0f, y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-  for (uint32_t i = s0 + g; i < s1; i += 16) {
+  for (uint32_t i = s0 + (WIDE ? g : 0u); i < s1; i += WIDE ? 16u : 1u) {
     const uint64_t p = ((uint64_t)item * a.splits + i) * a.tile_rows + row;
     const f32x2 ml = *reinterpret_cast<const f32x2*>(a.pml + p * 2);
     const f32x4 u0 = *reinterpret_cast<const f32x4*>(a.po + p * kD + 8 * l), u1 = *reinterpret_cast<const f32x4*>(a.po + p * kD + 8 * l + 4);
@@ -643,24 +656,26 @@ __global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables
       y[4 + c] = y[4 + c] * f0 + u1[c] * f1;
     }
   }
+  if (WIDE) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s_y[g][8 * l + i] = y[i];
-  if (l == 0) {
-    s_m[g] = m;
-    s_l[g] = sum;
-  }
-  __syncthreads();
-  if (g) return;
-  m = s_m[0];
-  for (int i = 1; i < 16; ++i) m = fmaxf(m, s_m[i]);
-  sum = 0.0f;
+    for (int i = 0; i < 8; ++i) s_y[WIDE ? g : 0][8 * l + i] = y[i];
+    if (l == 0) {
+      s_m[g] = m;
+      s_l[g] = sum;
+    }
+    __syncthreads();
+    if (g) return;
+    m = s_m[0];
+    for (int i = 1; i < 16; ++i) m = fmaxf(m, s_m[i]);
+    sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-  for (int i = 0; i < 16; ++i) {
-    const float f = __builtin_amdgcn_exp2f(s_m[i] - m);
-    sum += s_l[i] * f;
+    for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+    for (int i = 0; i < 16; ++i) {
+      const float f = __builtin_amdgcn_exp2f(s_m[i] - m);
+      sum += s_l[i] * f;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) y[c] += s_y[i][8 * l + c] * f;
+      for (int c = 0; c < 8; ++c) y[c] += s_y[WIDE ? i : 0][8 * l + c] * f;
+    }
   }
   if (l == 0) a.lse[(uint64_t)item * a.tile_rows + row] = m + __builtin_amdgcn_logf(sum) - kPScaleLog2;
   store_row<BITS>(a, K, s, it.h, r, l, lane_inverse(K, l), y, sum);
@@ -790,7 +805,7 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
   const int32_t mine = 16 * (int32_t)wave;
   int32_t t = t0, page = page_of(a, it.b, t + mine, t1);
   if (t < t1) load(t + mine, page);
-  int32_t next = page_of(a, it.b, t + kTok + mine, t1);
+  int32_t next = entry_of(a, it.b, t + kTok + mine, t1);
 
   const bool cap = a.cap_in > 0.0f;
   f16x8 qh[R][4], ql[R][4];
@@ -812,7 +827,7 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
     m[q] = -1.0e30f;
     sum[q] = poison[q] = 0.0f;
     row_lo[q] = row_hi[q] = 0;
-    if (w0 + 16u * q + n < rows) visible(a, s, (int32_t)((w0 + 16u * q + n) / a.group), &row_lo[q], &row_hi[q]);
+    if (w0 + 16u * q + n < rows) visible(a, s, (int32_t)query_of(a, w0 + 16u * q + n), &row_lo[q], &row_hi[q]);
     ones[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[q][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -829,11 +844,13 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
       __syncthreads();
     }
     if (more) {
-      page = next;
+      page = page_in(a, next);
       load(t + kTok + mine, page);
-      next = page_of(a, it.b, t + 2 * kTok + mine, t1);
+      next = entry_of(a, it.b, t + 2 * kTok + mine, t1);
     }
     const Stage<PREC>& d = st[buf];
+    // blocks of 16 tokens with a flag, asked for once and not between the products
+    const uint32_t flagged = (uint32_t)__builtin_amdgcn_ballot_w64(lane < (uint32_t)kManyWaves && s_flags[buf][lane & (kManyWaves - 1)] != 0u);
 #pragma unroll 2
     for (int w = 0; w < kTok / 32; ++w) {
       const int32_t tw = t + 32 * w;
@@ -866,8 +883,8 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
 #pragma unroll
             for (int i = 0; i < 4; ++i) sc[q][u][i] = a.cap_out * tanh32(sc[q][u][i] * qf[q] * a.cap_in);
       }
-      const uint32_t fl0 = s_flags[buf][2 * w], fl1 = s_flags[buf][2 * w + 1];
-      if (__builtin_amdgcn_readfirstlane(fl0 | fl1) || tw < all_lo || tw + 32 > all_hi || tw + 32 > t1) {
+      if ((flagged >> (2 * w) & 3u) || tw < all_lo || tw + 32 > all_hi || tw + 32 > t1) {
+        const uint32_t fl0 = s_flags[buf][2 * w], fl1 = s_flags[buf][2 * w + 1];
 #pragma unroll
         for (int q = 0; q < R; ++q)
 #pragma unroll
@@ -973,23 +990,32 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
 
 // Accumulated weights of many rows: a wavefront owns 64 tokens of a (sequence, head), keeps their keys as
 // operands, forms their scores with every row again and adds the sum of exp(s - lse) over the rows, in a
-// fixed order.
+// fixed order.  The four wavefronts share each 16 rows' operands through LDS, the next ones' on their way.
 template <int BITS>
 __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a, uint32_t blocks) {
+  __shared__ f16x8 s_q[2][2][4][64];  // [buffer][part][step][lane]
+  __shared__ float s_f[2][16], s_l[2][16];
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
-  const uint32_t bh = blockIdx.x / blocks, h = bh % a.heads, b = bh / a.heads;
+  // consecutive workgroups go to the 8 XCDs in turn: those of one (sequence, head), which read the same rows, meet
+  // in one XCD's L2
+  const uint32_t bh = blockIdx.x / 8u / blocks * 8u + blockIdx.x % 8u, h = bh % a.heads, b = bh / a.heads;
+  if (bh >= a.seqs * a.heads) return;
   const Seq s = seq_of(a, b);
-  const int32_t t = (int32_t)((blockIdx.x % blocks) * 64u * kAttWaves + 64u * wave);
+  const int32_t first = (int32_t)((blockIdx.x / 8u % blocks) * 64u * kAttWaves), t = first + 64 * (int32_t)wave;
   const uint32_t rows = (uint32_t)s.m * a.group;
-  if (t >= s.n || a.pages == 0) return;
+  if (first >= s.n || a.pages == 0) return;
+  // queries [i0, i1) see some of the workgroup's tokens
+  const int64_t back = s.n - s.m, last = (int64_t)first + 64 * kAttWaves - 1;
+  const int64_t i0 = a.causal && first > back ? first - back : 0, i1 = a.window && last + a.window - back < s.m ? last + a.window - back : s.m;
+  if (i0 >= i1) return;
   const uint32_t P = 1u << a.page_log2;
   const uint64_t page_size = (uint64_t)P * Page<BITS>::kToken;
   f16x8 kh[4][4], kl[4][4];
-  bool there[4];
+  uint32_t absent = 0;  // blocks of 16 tokens without a page
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int32_t page = page_of(a, b, t + 16 * u, s.n);
-    there[u] = page >= 0;
+    absent |= page < 0 ? 1u << u : 0u;
     Share<BITS> sh;
     load_keys<BITS>(a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + h) * page_size, P, (uint32_t)(t + 16 * u) & (P - 1u), lane, sh);
     key_operands<BITS, true>(sh, kh[u], kl[u]);
@@ -997,34 +1023,70 @@ __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a
   float acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-  for (uint32_t r0 = 0; r0 < rows; r0 += 16) {
+  // a thread's share of 16 rows: group threadIdx mod 16 of row threadIdx / 16, in both parts
+  const uint64_t base = (uint64_t)bh * a.tiles * a.tile_rows;
+  const uint32_t lr = threadIdx.x >> 4, lg = threadIdx.x & 15u;
+  f16x8 qh, ql;
+  float qf = 0.0f, lse = 0.0f;
+  auto fetch = [&](uint32_t r0) __attribute__((always_inline)) {
+    const uint64_t row = base + r0 + lr;
+    qh = *reinterpret_cast<const f16x8*>(a.qhi + row * kD + 8 * lg);
+    ql = *reinterpret_cast<const f16x8*>(a.qlo + row * kD + 8 * lg);
+    if (lg == 0) {
+      qf = a.qf[row];
+      lse = a.lse[row];
+    }
+  };
+  const uint32_t r1 = (uint32_t)i1 * a.group;
+  uint32_t buf = 0, r0 = (uint32_t)i0 * a.group & ~15u;
+  fetch(r0);
+  for (; r0 < r1; r0 += 16, buf ^= 1u) {
+    s_q[buf][0][lg & 3u][lr + 16u * (lg >> 2)] = qh;
+    s_q[buf][1][lg & 3u][lr + 16u * (lg >> 2)] = ql;
+    if (lg == 0) {
+      s_f[buf][lr] = qf;
+      s_l[buf][lr] = lse;
+    }
+    __syncthreads();
+    if (r0 + 16 < r1) fetch(r0 + 16);
     int32_t lo, hi, all_lo, all_hi;
     rows_range(a, s, r0, 16, &lo, &hi);
     if (t >= hi || t + 64 <= lo) continue;
     rows_common(a, s, r0, 16, &all_lo, &all_hi);
-    const uint64_t row = (uint64_t)bh * a.tiles * a.tile_rows + r0 + n;
-    f16x8 qh[4], ql[4];
+    f16x8 oh[4], ol[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      qh[j] = *reinterpret_cast<const f16x8*>(a.qhi + row * kD + 8 * (4 * b4 + j));
-      ql[j] = *reinterpret_cast<const f16x8*>(a.qlo + row * kD + 8 * (4 * b4 + j));
+      oh[j] = s_q[buf][0][j][lane];
+      ol[j] = s_q[buf][1][j][lane];
     }
-    const float qf = a.qf[row], lse = a.lse[row];
-    int32_t row_lo = 0, row_hi = 0;
-    if (r0 + n < rows) visible(a, s, (int32_t)((r0 + n) / a.group), &row_lo, &row_hi);
-    const bool whole = t >= all_lo && t + 64 <= all_hi;
+    const float f = s_f[buf][n], ls = s_l[buf][n];
+    f32x4 raw[4];
+    float sc[16];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const f32x4 r = scores16<true>(kh[u], kl[u], qh, ql);
-      float sc[4];
+    for (int u = 0; u < 4; ++u) raw[u] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[i] = r[i] * qf;
-      cap_scores<4>(a, sc);
+    for (int j = 0; j < 4; ++j) {  // the four blocks in turn: no product waits for the one before
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int32_t tok = t + 16 * u + 4 * (int32_t)b4 + i;
-        const float p = __builtin_amdgcn_exp2f(sc[i] - lse);
-        acc[4 * u + i] += there[u] && (whole || (tok >= row_lo && tok < row_hi)) ? p : 0.0f;
+      for (int u = 0; u < 4; ++u) raw[u] = mfma(kl[u][j], oh[j], raw[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) raw[u] = mfma(kh[u][j], ol[j], raw[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) raw[u] = mfma(kh[u][j], oh[j], raw[u]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sc[i] = raw[i >> 2][i & 3] * f;
+    cap_scores<16>(a, sc);
+    if (!absent && t >= all_lo && t + 64 <= all_hi) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] += __builtin_amdgcn_exp2f(sc[i] - ls);
+    } else {
+      int32_t row_lo = 0, row_hi = 0;
+      if (r0 + n < rows) visible(a, s, (int32_t)query_of(a, r0 + n), &row_lo, &row_hi);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int32_t tok = t + 16 * (i >> 2) + 4 * (int32_t)b4 + (i & 3);
+        const float p = __builtin_amdgcn_exp2f(sc[i] - ls);
+        acc[i] += bool((tok >= row_lo) & (tok < row_hi) & !((absent >> (i >> 2)) & 1u)) ? p : 0.0f;
       }
     }
   }
@@ -1064,10 +1126,12 @@ Plan plan_of(const hq_kv_cache& c, const hq_kv_attend_args& g) {
   p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   p.items = (uint64_t)g.seqs * c.heads * p.tiles;
   const bool few = rows <= 16;
-  // enough workgroups to fill the chip (256 CUs; single tokens: several a CU, so that ragged lengths even
-  // out), each with enough tokens to be worth its start and its part of the join
-  const uint64_t want = few ? 2048 : 512, least = few ? 256 : 512;
-  uint64_t splits = p.items ? (want + p.items - 1) / p.items : 1, most = (g.max_len + least - 1) / least;
+  // Workgroups to fill 256 CUs and to even out ragged lengths, each with enough tokens to be worth its start
+  // (about 5 us) and its part of the join.  Few rows: 2048 of at least 1024 tokens, or of 512 where that
+  // leaves fewer than 512 (64 sequences of 4001 tokens: 59 us at 1024, 67 at 512; one of 32768: 31 and 30;
+  // one of 301: 14 us whole, 17 in two).  Many rows: 1536 of at least 512, unless the tiles alone are two a CU.
+  const uint64_t want = few ? 2048 : 1536, least = few && p.items * ((g.max_len + 1023) / 1024) >= 512 ? 1024 : 512;
+  uint64_t splits = p.items && (few || p.items < 512) ? (want + p.items - 1) / p.items : 1, most = (g.max_len + least - 1) / least;
   if (splits > most) splits = most;
   if (splits < 1) splits = 1;
   uint64_t chunk = (g.max_len + splits - 1) / splits;
@@ -1123,13 +1187,16 @@ hipError_t launch_attend(const AttendArgs& a, const Tables& T, uint32_t items, h
   }
   if (a.splits > 1) {
     const uint32_t per = rows < a.tile_rows ? rows : a.tile_rows;
-    hipLaunchKernelGGL((combine_kernel<BITS>), dim3(items * per), block, 0, st, a, T, per);
+    // a workgroup a row while those are at most 16 a CU, 16 lanes a row beyond: 64 rows of 12 splits 5 us as one,
+    // 49152 rows of 3 splits 87 us against COMBINE_US us
+    if (items * per <= 4096) hipLaunchKernelGGL((combine_kernel<BITS, true>), dim3(items * per), block, 0, st, a, T, per, items * per);
+    else hipLaunchKernelGGL((combine_kernel<BITS, false>), dim3((items * per + 15) / 16), block, 0, st, a, T, per, items * per);
   }
   if (prec && a.max_len) {
     const uint32_t step = a.tile_rows == 16 ? kAttBlock : 64u * kAttWaves, blocks = (a.max_len + step - 1) / step;
-    const dim3 wg(a.seqs * a.heads * blocks);
-    if (a.tile_rows == 16) hipLaunchKernelGGL(weights_few_kernel, wg, block, 0, st, a, blocks);
-    else hipLaunchKernelGGL((weights_many_kernel<BITS>), wg, block, 0, st, a, blocks);
+    const uint32_t bh = a.seqs * a.heads;
+    if (a.tile_rows == 16) hipLaunchKernelGGL(weights_few_kernel, dim3(bh * blocks), block, 0, st, a, blocks);
+    else hipLaunchKernelGGL((weights_many_kernel<BITS>), dim3((bh + 7u) / 8u * 8u * blocks), block, 0, st, a, blocks);
   }
   return hipGetLastError();
 }
@@ -1175,7 +1242,7 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   // every launch below 2^32 threads: workgroups of 256 and 512, a row's 16 lanes, a row's join
   if (p.items * p.splits > kMaxThreads / kManyBlock || p.items * p.tile_rows > kMaxThreads / 16) return HQ_ERR_INVALID_ARG;
   if (p.splits > 1 && p.items * p.tile_rows > kMaxThreads / kAttBlock) return HQ_ERR_INVALID_ARG;
-  if ((uint64_t)g.seqs * cache->heads * ((g.max_len + 255u) / 256u) > kMaxThreads / kAttBlock) return HQ_ERR_INVALID_ARG;
+  if ((uint64_t)(g.seqs * cache->heads + 7u) * ((g.max_len + 255u) / 256u) > kMaxThreads / kAttBlock) return HQ_ERR_INVALID_ARG;
   AttendArgs a;
   a.cache = static_cast<const uint8_t*>(cache->data);
   a.q = g.q;
@@ -1190,6 +1257,10 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   a.qh = g.q_stride_head;
   a.heads = cache->heads;
   a.group = g.q_heads / cache->heads;
+  uint32_t sh = 0;
+  while ((1u << sh) < a.group) ++sh;
+  a.group_mul = (uint32_t)((1ull << (31u + sh)) / a.group + 1u);
+  a.group_shift = 31u + sh;
   a.q_heads = g.q_heads;
   a.pages = cache->pages;
   a.page_log2 = 31u - (uint32_t)__builtin_clz(cache->page);
