@@ -50,6 +50,7 @@ struct AttendArgs {
   uint32_t tile_rows, tiles, splits, chunk, window;
   uint32_t wrows, wpad;  // stored scores: rows of an item, tokens a row
   int causal, q_f32, out_f32, vec;
+  int light;  // tiles of up to 16 rows are left to the few rows' kernel
   float scale_log2, cap_in, cap_out;  // scores in log2 units; s = cap_out tanh(cap_in s) when cap_in > 0
   // workspace; an item is a (sequence, head, tile of tile_rows rows)
   _Float16 *qhi, *qlo;  // [items][tile_rows][128]
@@ -435,7 +436,9 @@ __device__ __forceinline__ int32_t page_in(const AttendArgs& a, int32_t entry) {
 __device__ __forceinline__ int32_t page_of(const AttendArgs& a, uint32_t b, int32_t tt, int32_t end) { return page_in(a, entry_of(a, b, tt, end)); }
 
 // ---------------------------------------------------------------------------------------------
-// Up to 16 rows a (sequence, head): the single-token step.  A workgroup takes one split of the tokens; its
+// Tiles of up to 16 rows: the single-token step, and the single tokens and last rows of a batch that has longer
+// chunks too (those take the other kernel's whole turn there: 181 us against LIGHT_US us for 4 x 129 and 4 x 1
+// queries).  A workgroup takes one split of the tokens; its
 // four wavefronts take 32 tokens in turn, the next 32 already on their way, and join at the end.  The
 // cache's bytes bound it; its rows are a fraction of the products' 16 columns, which costs nothing here.
 template <int BITS, bool PREC>
@@ -447,9 +450,11 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
   const uint32_t split = blockIdx.x % a.splits, item = blockIdx.x / a.splits;
   const Item it = item_of(a, item);
   const Seq s = seq_of(a, it.b);
-  const uint32_t rows = (uint32_t)s.m * a.group;
+  const uint32_t r0 = it.tile * a.tile_rows, all = (uint32_t)s.m * a.group;
+  if (a.tile_rows != 16 && (r0 >= all || all - r0 > 16u)) return;
+  const uint32_t rows = all - r0;  // of this tile
   int32_t lo, hi;
-  rows_range(a, s, 0, 16, &lo, &hi);
+  rows_range(a, s, r0, 16, &lo, &hi);
   int32_t t0 = (int32_t)(split * a.chunk), t1 = t0 + (int32_t)a.chunk;
   t0 = t0 > (lo & ~15) ? t0 : lo & ~15;
   t1 = t1 < hi ? t1 : hi;
@@ -477,7 +482,7 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
   {  // the rows: four to a wavefront, 16 lanes each
     const uint32_t r = threadIdx.x >> 4;
     float f = 0.0f;
-    if ((r & ~3u) < rows) f = rotate_row<BITS>(a, K, s, it.h, r, n, lane_forward(K, n), s_q[0][r], PREC ? s_q[PREC ? 1 : 0][r] : nullptr);
+    if ((r & ~3u) < rows) f = rotate_row<BITS>(a, K, s, it.h, r0 + r, n, lane_forward(K, n), s_q[0][r], PREC ? s_q[PREC ? 1 : 0][r] : nullptr);
     else
       for (int i = 0; i < 8; ++i) {
         s_q[0][r][8 * n + i] = (_Float16)0.0f;
@@ -494,9 +499,9 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
   }
   const float qf = s_f[n];
   int32_t row_lo = 0, row_hi = 0, all_lo = hi, all_hi = lo;
-  if (n < rows) visible(a, s, (int32_t)query_of(a, n), &row_lo, &row_hi);
+  if (n < rows) visible(a, s, (int32_t)query_of(a, r0 + n), &row_lo, &row_hi);
   // the tokens every existing row sees need no mask (rows past the last are products with zero)
-  if (rows) rows_common(a, s, 0, rows, &all_lo, &all_hi);
+  if (rows) rows_common(a, s, r0, rows, &all_lo, &all_hi);
 
   float m = -1.0e30f, sum = 0.0f, poison = 0.0f;
   f32x4 o[8];
@@ -613,11 +618,11 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] += s_o[w][r][8 * n + i];
   if (a.splits == 1) {
-    if (n == 0) a.lse[item * 16u + r] = mr + __builtin_amdgcn_logf(total) - kPScaleLog2;
-    store_row<BITS>(a, K, s, it.h, r, n, lane_inverse(K, n), y, total);
+    if (n == 0) a.lse[(uint64_t)item * a.tile_rows + r] = mr + __builtin_amdgcn_logf(total) - kPScaleLog2;
+    store_row<BITS>(a, K, s, it.h, r0 + r, n, lane_inverse(K, n), y, total);
     return;
   }
-  const uint64_t p = ((uint64_t)item * a.splits + split) * 16u + r;
+  const uint64_t p = ((uint64_t)item * a.splits + split) * a.tile_rows + r;
   *reinterpret_cast<f32x4*>(a.po + p * kD + 8 * n) = (f32x4){y[0], y[1], y[2], y[3]};
   *reinterpret_cast<f32x4*>(a.po + p * kD + 8 * n + 4) = (f32x4){y[4], y[5], y[6], y[7]};
   if (n == 0) *reinterpret_cast<f32x2*>(a.pml + p * 2) = (f32x2){mr, total};
@@ -747,7 +752,7 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
   const uint64_t slot = (uint64_t)bh * a.tiles + it.tile;  // the item's place in the workspace
   const Seq s = seq_of(a, it.b);
   const uint32_t rows = (uint32_t)s.m * a.group, r0 = it.tile * a.tile_rows, w0 = r0 + wave * 16u * R;
-  if (r0 >= rows) return;
+  if (r0 >= rows || (a.light && rows - r0 <= 16u)) return;
   int32_t lo, hi, wlo, whi, all_lo, all_hi;
   rows_range(a, s, r0, a.tile_rows, &lo, &hi);
   rows_range(a, s, w0, 16u * R, &wlo, &whi);
@@ -1180,6 +1185,10 @@ hipError_t launch_attend(const AttendArgs& a, const Tables& T, uint32_t items, h
     else hipLaunchKernelGGL((attend_few_kernel<BITS, false>), dim3(grid), block, 0, st, a, T);
   } else {
     hipLaunchKernelGGL((rotate_rows_kernel<BITS>), dim3(items * (a.tile_rows / 16)), block, 0, st, a, T, prec ? 2 : 1);
+    if (a.light) {
+      if (prec) hipLaunchKernelGGL((attend_few_kernel<BITS, true>), dim3(grid), block, 0, st, a, T);
+      else hipLaunchKernelGGL((attend_few_kernel<BITS, false>), dim3(grid), block, 0, st, a, T);
+    }
     hipError_t e;
     if (a.tile_rows == 128) e = prec ? launch_many<BITS, true, 1>(a, T, grid, st) : launch_many<BITS, false, 1>(a, T, grid, st);
     else e = prec ? launch_many<BITS, true, 2>(a, T, grid, st) : launch_many<BITS, false, 2>(a, T, grid, st);
@@ -1188,7 +1197,7 @@ hipError_t launch_attend(const AttendArgs& a, const Tables& T, uint32_t items, h
   if (a.splits > 1) {
     const uint32_t per = rows < a.tile_rows ? rows : a.tile_rows;
     // a workgroup a row while those are at most 16 a CU, 16 lanes a row beyond: 64 rows of 12 splits 5 us as one,
-    // 49152 rows of 3 splits 87 us against COMBINE_US us
+    // 49152 rows of 3 splits 87 us against 14 us
     if (items * per <= 4096) hipLaunchKernelGGL((combine_kernel<BITS, true>), dim3(items * per), block, 0, st, a, T, per, items * per);
     else hipLaunchKernelGGL((combine_kernel<BITS, false>), dim3((items * per + 15) / 16), block, 0, st, a, T, per, items * per);
   }
@@ -1275,6 +1284,8 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   a.splits = p.splits;
   a.chunk = p.chunk;
   a.window = g.window;
+  const uint64_t last = g.total_q / g.seqs * a.group % p.tile_rows;  // rows of the last tile of equal sequences
+  a.light = g.q_start ? g.seqs > 1 : last > 0 && last <= 16;
   a.causal = g.causal != 0;
   a.q_f32 = g.q_dtype == HQ_F32;
   a.out_f32 = g.out_dtype == HQ_F32;
