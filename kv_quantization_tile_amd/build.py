@@ -16,7 +16,7 @@ SOURCES = ["hq_kernels.hip", "hq_api.hip", "hq_rotate.hip", "hq_srft.hip", "hq_k
 # exactly once in program order (no contraction into FMA, no fast-math, denormals kept, correctly
 # rounded division and square root), so that the kernels reproduce the CPU oracle bit for bit.
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     "-ffp-contract=off", "-fno-fast-math", "-fno-gpu-flush-denormals-to-zero",
     "-fhip-fp32-correctly-rounded-divide-sqrt",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -38,10 +38,11 @@ def _run(cmd, verbose: bool) -> None:
 
 def build(verbose: bool = False) -> str:
     """Compiles every source (side by side) and links them."""
+    compile_flags = [f for f in FLAGS if f != "-shared"]
     objects = [os.path.join(BUILD, s[:-4] + ".o") for s in SOURCES]
     os.makedirs(BUILD, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as pool:
-        list(pool.map(lambda so: _run(["hipcc", *FLAGS, "-c", os.path.join(CSRC, so[0]), "-o", so[1]], verbose),
+        list(pool.map(lambda so: _run(["hipcc", *compile_flags, "-c", os.path.join(CSRC, so[0]), "-o", so[1]], verbose),
                       zip(SOURCES, objects)))
     _run(["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", *objects, "-o", LIB + ".tmp"], verbose)
     os.replace(LIB + ".tmp", LIB)
