@@ -437,10 +437,13 @@ __device__ __forceinline__ int32_t page_of(const AttendArgs& a, uint32_t b, int3
 
 // ---------------------------------------------------------------------------------------------
 // Tiles of up to 16 rows: the single-token step, and the single tokens and last rows of a batch that has longer
-// chunks too (those take the other kernel's whole turn there: 181 us against LIGHT_US us for 4 x 129 and 4 x 1
-// queries).  A workgroup takes one split of the tokens; its
-// four wavefronts take 32 tokens in turn, the next 32 already on their way, and join at the end.  The
-// cache's bytes bound it; its rows are a fraction of the products' 16 columns, which costs nothing here.
+// chunks too (left to the other kernel they take as long there as 256 rows: 181 us, against 108 and 23 here, for
+// 4 x 129 and 4 x 1 queries).  A workgroup takes one split of the tokens; its four wavefronts take 32 tokens in
+// turn, the next 32 already on their way, and join at the end.  The rows are a fraction of the products' 16
+// columns, which costs nothing here.  The cache's bytes bound it where there are many: 16 sequences of up to
+// 32768 tokens, 535 MB, in 145 us (3.7 TB/s; a sum over 1 GiB reads 3.9, a 2 GiB copy moves 4.9); an extra
+// wavefront a SIMD (128 registers, some spilled) left that at 160 us.  One sequence of 301 tokens takes 9 us:
+// 2 until the codes are asked for, 1.5 for the rows, 4.2 for three turns, 1 for the join.
 template <int BITS, bool PREC>
 __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kernel(AttendArgs a, Tables K) {
   __shared__ __align__(16) float s_o[kAttWaves][16][kPad];
@@ -728,6 +731,11 @@ __global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Ta
 // ones' codes are in flight meanwhile.  Two wavefronts a SIMD, so that one's softmax runs beside the
 // other's products; R = 2 is what 256 registers hold (at R = 4 and one wavefront a SIMD nothing overlapped:
 // 1.2 ms for a prompt of 8192 tokens).  Two stages of LDS, one with the keys in two parts (160 KB hold no more).
+// A prompt of 8192 tokens, 550 GFLOP, takes 700 us (780 TFLOP/s; a 16-bit product of 8192^3 reaches 1050 to 1100).
+// A turn of 128 tokens is 12800 cycles: 4350 of matrix instructions, about 6800 of vector instructions and 4100
+// of LDS a SIMD, in phases that the two wavefronts share (scores 700, softmax 700, output 750, four times; 1750
+// for the operands, 1000 for the loads).  Priorities, an offset between the wavefronts, operands fetched from LDS
+// ahead, and R = 1 with four wavefronts a SIMD changed the 750 us by 3 % at most.
 constexpr int kManyWaves = 8, kManyBlock = 64 * kManyWaves;
 template <bool PREC>
 struct Stage {
@@ -996,6 +1004,8 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
 // Accumulated weights of many rows: a wavefront owns 64 tokens of a (sequence, head), keeps their keys as
 // operands, forms their scores with every row again and adds the sum of exp(s - lse) over the rows, in a
 // fixed order.  The four wavefronts share each 16 rows' operands through LDS, the next ones' on their way.
+// 4 x 129 queries on up to 5003 tokens, 8 heads, 4 a head: 83 us (142 us with a branch a score and each wavefront
+// fetching the rows by itself).  Storing the scores instead, as for few rows, would move 0.6 GB.
 template <int BITS>
 __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a, uint32_t blocks) {
   __shared__ f16x8 s_q[2][2][4][64];  // [buffer][part][step][lane]

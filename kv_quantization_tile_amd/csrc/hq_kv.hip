@@ -41,7 +41,9 @@ struct AppendArgs {
 
 // One vector per 16 lanes; the four rows of a wavefront take four consecutive tokens of one head and
 // side (K or V), so that the V pieces (4 bytes every 16) of neighbouring tokens meet in one line, and `quads`
-// such fours in turn, so that the twiddles are fetched once for all of them.
+// such fours in turn, so that the twiddles are fetched once for all of them.  Vector instructions bound it: 516 a four
+// (a prompt of 32768 tokens, 8 heads: 120 us at 97 % of the issue rate for 235 MB).  A thread a vector needs 2.5
+// times fewer (no exchanges) but 64 vectors to fill a wavefront and 160 registers, and cannot start on a handful.
 template <int BITS>
 __global__ __launch_bounds__(kBlock) void append_kernel(AppendArgs a, Tables K) {
   const uint32_t lane = threadIdx.x & 63u, l = lane & 15u, row = lane >> 4;
@@ -248,7 +250,7 @@ __device__ __forceinline__ uint32_t clamp_len(int32_t n, uint32_t most) { return
 // tokens, PER of them a lane as keys in registers (the weights are read once, for up to 1024 PER tokens), so
 // the ordered pass needs the counts of the wavefronts before it and no exchange within.  With PER == 0 the
 // weights are read again in each pass.  Vector instructions bound it: one compute unit works on a row.
-constexpr int kSelect = 1024, kSelectWaves = kSelect / 64, kHeld = 32, kBins = 2048;
+constexpr int kSelect = 1024, kSelectWaves = kSelect / 64, kHeldFew = 8, kHeld = 32, kBins = 2048;
 
 template <int PER>
 __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
@@ -565,7 +567,10 @@ int hq_kv_evict(const hq_kv_cache* cache, const hq_kv_evict_args* e, hq_stream_t
   if (grid > kMaxThreads / kBlock) return HQ_ERR_INVALID_ARG;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const dim3 select(e->seqs * cache->heads);
-  if (e->max_len <= kSelect * kHeld) hipLaunchKernelGGL(evict_select_kernel<kHeld>, select, dim3(kSelect), 0, st, a);
+  // 8 keys a lane where they hold the tokens: every pass is unrolled over them, and fetching skipped code costs (1040
+  // tokens: 8.6 us against 12.3 with 32 keys a lane).  Keys in LDS: 8.4 us for 1040, but 47 against 34 for 32768.
+  if (e->max_len <= kSelect * kHeldFew) hipLaunchKernelGGL(evict_select_kernel<kHeldFew>, select, dim3(kSelect), 0, st, a);
+  else if (e->max_len <= kSelect * kHeld) hipLaunchKernelGGL(evict_select_kernel<kHeld>, select, dim3(kSelect), 0, st, a);
   else hipLaunchKernelGGL(evict_select_kernel<0>, select, dim3(kSelect), 0, st, a);
   if (grid && cache->pages) {
     if (cache->bits == 4) hipLaunchKernelGGL(evict_move_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, blocks);
