@@ -326,7 +326,7 @@ __device__ __forceinline__ void wave_sync() {
 // parts in the operand's order, to hi[128] (and lo[128] unless null).  Returns the factor that turns the
 // row's products into scores.
 template <int BITS>
-__device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K, const Seq& s, uint32_t h, uint32_t r, uint32_t l,
+__device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K, const float* lam, const Seq& s, uint32_t h, uint32_t r, uint32_t l,
                                             const LaneForward& f, _Float16* hi, _Float16* lo) {
   const uint32_t kappa = rev4(l);
   float m[8], x[8], y[8];
@@ -336,8 +336,8 @@ __device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K
     m[2 * i] = packing(c) * a.scale_log2;
     m[2 * i + 1] = packing(c + 1) * a.scale_log2;
     if (K.scaled) {
-      m[2 * i] *= K.k[c];
-      m[2 * i + 1] *= K.k[c + 1];
+      m[2 * i] *= lam[c];
+      m[2 * i + 1] *= lam[c + 1];
     }
   }
 #pragma unroll
@@ -390,14 +390,14 @@ __device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K
 
 // Turns a row's sum_t p_t code Delta (the lane's group, y[8], over unit) back and stores the row.
 template <int BITS>
-__device__ __forceinline__ void store_row(const AttendArgs& a, const Tables& K, const Seq& s, uint32_t h, uint32_t r, uint32_t l,
+__device__ __forceinline__ void store_row(const AttendArgs& a, const Tables& K, const float* lam, const Seq& s, uint32_t h, uint32_t r, uint32_t l,
                                           const LaneInverse& f, float y[8], float sum) {
   const float inv = sum == 0.0f ? 0.0f : unit<BITS>() / sum;  // a row that sees nothing is 0
   float x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     y[i] *= inv;
-    if (K.scaled) y[i] *= K.v[8 * l + i];
+    if (K.scaled) y[i] *= lam[8 * l + i];
   }
   inverse_row(y, x, l, f);
   if (r >= (uint32_t)s.m * a.group) return;
@@ -448,7 +448,7 @@ template <int BITS, bool PREC>
 __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kernel(AttendArgs a, Tables K) {
   __shared__ __align__(16) float s_o[kAttWaves][16][kPad];
   __shared__ __align__(16) _Float16 s_q[PREC ? 2 : 1][16][kD + 8];
-  __shared__ float s_f[16], s_m[kAttWaves][16], s_l[kAttWaves][16];
+  __shared__ float s_f[16], s_m[kAttWaves][16], s_l[kAttWaves][16], s_lam[2][kD];
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
   const uint32_t split = blockIdx.x % a.splits, item = blockIdx.x / a.splits;
   const Item it = item_of(a, item);
@@ -482,10 +482,11 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
   }
   int32_t en0 = entry_of(a, it.b, t + kStep, t1), en1 = entry_of(a, it.b, t + kStep + 16, t1);
 
+  stage_tables(K, s_lam);
   {  // the rows: four to a wavefront, 16 lanes each
     const uint32_t r = threadIdx.x >> 4;
     float f = 0.0f;
-    if ((r & ~3u) < rows) f = rotate_row<BITS>(a, K, s, it.h, r0 + r, n, lane_forward(K, n), s_q[0][r], PREC ? s_q[PREC ? 1 : 0][r] : nullptr);
+    if ((r & ~3u) < rows) f = rotate_row<BITS>(a, K, s_lam[0], s, it.h, r0 + r, n, lane_forward(K, n), s_q[0][r], PREC ? s_q[PREC ? 1 : 0][r] : nullptr);
     else
       for (int i = 0; i < 8; ++i) {
         s_q[0][r][8 * n + i] = (_Float16)0.0f;
@@ -622,7 +623,7 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
     for (int i = 0; i < 8; ++i) y[i] += s_o[w][r][8 * n + i];
   if (a.splits == 1) {
     if (n == 0) a.lse[(uint64_t)item * a.tile_rows + r] = mr + __builtin_amdgcn_logf(total) - kPScaleLog2;
-    store_row<BITS>(a, K, s, it.h, r0 + r, n, lane_inverse(K, n), y, total);
+    store_row<BITS>(a, K, s_lam[1], s, it.h, r0 + r, n, lane_inverse(K, n), y, total);
     return;
   }
   const uint64_t p = ((uint64_t)item * a.splits + split) * a.tile_rows + r;
@@ -686,7 +687,7 @@ __global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables
     }
   }
   if (l == 0) a.lse[(uint64_t)item * a.tile_rows + row] = m + __builtin_amdgcn_logf(sum) - kPScaleLog2;
-  store_row<BITS>(a, K, s, it.h, r, l, lane_inverse(K, l), y, sum);
+  store_row<BITS>(a, K, K.v, s, it.h, r, l, lane_inverse(K, l), y, sum);
 }
 
 // Accumulated weights of up to 16 rows, from the stored scores: a thread owns a token.
@@ -711,12 +712,14 @@ __global__ __launch_bounds__(kAttBlock) void weights_few_kernel(AttendArgs a, ui
 template <int BITS>
 __global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Tables K, int parts) {
   __shared__ __align__(16) _Float16 s_q[2][16][kD + 8];
+  __shared__ float s_lam[2][kD];
+  stage_tables(K, s_lam);
   const uint32_t l = threadIdx.x & 15u, g = threadIdx.x >> 4, per = a.tile_rows / 16u;
   const uint32_t item = blockIdx.x / per, row = (blockIdx.x % per) * 16u + g;
   const Item it = item_of(a, item);
   const Seq s = seq_of(a, it.b);
   if (it.tile * a.tile_rows + (row & ~15u) >= (uint32_t)s.m * a.group) return;
-  const float f = rotate_row<BITS>(a, K, s, it.h, it.tile * a.tile_rows + row, l, lane_forward(K, l), s_q[0][g], parts == 2 ? s_q[1][g] : nullptr);
+  const float f = rotate_row<BITS>(a, K, s_lam[0], s, it.h, it.tile * a.tile_rows + row, l, lane_forward(K, l), s_q[0][g], parts == 2 ? s_q[1][g] : nullptr);
   const uint64_t at = (uint64_t)item * a.tile_rows + row;
   if (l == 0) a.qf[at] = f;
   // a row is written and read by the same wavefront
@@ -990,7 +993,7 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
       for (int i = 0; i < 8; ++i) y[i] = s_o[wave][r][8 * n + i];
       const float tr = row_get_any(total, r);
       if (a.splits == 1) {
-        store_row<BITS>(a, K, s, it.h, w0 + 16u * q + r, n, inv, y, tr);
+        store_row<BITS>(a, K, K.v, s, it.h, w0 + 16u * q + r, n, inv, y, tr);
       } else {
         float* d = a.po + ((slot * a.splits + split) * a.tile_rows + first + r) * kD + 8 * n;
         *reinterpret_cast<f32x4*>(d) = (f32x4){y[0], y[1], y[2], y[3]};

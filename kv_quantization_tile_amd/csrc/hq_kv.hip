@@ -42,10 +42,12 @@ struct AppendArgs {
 // One vector per 16 lanes; the four rows of a wavefront take four consecutive tokens of one head and
 // side (K or V), so that the V pieces (4 bytes every 16) of neighbouring tokens meet in one line, and `quads`
 // such fours in turn, so that the twiddles are fetched once for all of them.  Vector instructions bound it: 516 a four
-// (a prompt of 32768 tokens, 8 heads: 120 us at 97 % of the issue rate for 235 MB).  A thread a vector needs 2.5
-// times fewer (no exchanges) but 64 vectors to fill a wavefront and 160 registers, and cannot start on a handful.
+// (32768 tokens of 8 heads: 105 to 120 us, 97 % of the issue rate).  Many tokens go to the kernels with a vector a
+// thread, which need 64 vectors a wavefront; a decode step's 4 tokens of 8 heads take 3.6 us here.
 template <int BITS>
 __global__ __launch_bounds__(kBlock) void append_kernel(AppendArgs a, Tables K) {
+  __shared__ float s_mul[2][kD];
+  stage_tables(K, s_mul);
   const uint32_t lane = threadIdx.x & 63u, l = lane & 15u, row = lane >> 4;
   const uint32_t item = __builtin_amdgcn_readfirstlane(blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6));
   const uint32_t side = item & 1u, head = (item >> 1) % a.heads;
@@ -62,8 +64,8 @@ __global__ __launch_bounds__(kBlock) void append_kernel(AppendArgs a, Tables K) 
     m[2 * r] = packing(c);
     m[2 * r + 1] = packing(c + 1);
     if (K.scaled) {
-      m[2 * r] *= side ? K.v[c] : K.k[c];
-      m[2 * r + 1] *= side ? K.v[c + 1] : K.k[c + 1];
+      m[2 * r] *= s_mul[side][c];
+      m[2 * r + 1] *= s_mul[side][c + 1];
     }
   }
   for (tok += row; tok - row < end; tok += 4) {
@@ -173,6 +175,8 @@ struct ReadArgs {
 
 template <int BITS>
 __global__ __launch_bounds__(kBlock) void read_kernel(ReadArgs a, Tables K) {
+  __shared__ float s_mul[2][kD];
+  stage_tables(K, s_mul);
   const uint32_t lane = threadIdx.x & 63u, l = lane & 15u, row = lane >> 4;
   const uint32_t item = __builtin_amdgcn_readfirstlane(blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6));
   const uint32_t side = a.sides == 3 ? item & 1u : (uint32_t)a.sides >> 1, rest = a.sides == 3 ? item >> 1 : item;
@@ -182,6 +186,9 @@ __global__ __launch_bounds__(kBlock) void read_kernel(ReadArgs a, Tables K) {
   const uint64_t end = tok + 4u * a.quads < a.tokens ? tok + 4u * a.quads : a.tokens;
   const uint32_t P = 1u << a.page_log2;
   const LaneInverse f = lane_inverse(K, l);
+  float lam[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) lam[i] = K.scaled ? s_mul[side][8 * l + i] : 1.0f;
   for (tok += row; tok - row < end; tok += 4) {
     const bool have = tok < end;
     const int64_t slot = have ? a.slots[tok] : -1;
@@ -206,7 +213,7 @@ __global__ __launch_bounds__(kBlock) void read_kernel(ReadArgs a, Tables K) {
     for (int i = 0; i < 8; ++i) {
       const int32_t q = BITS == 4 ? __builtin_amdgcn_sbfe(w0, 4 * i, 4) : __builtin_amdgcn_sbfe(i < 4 ? w0 : w1, 8 * (i & 3), 8);
       y[i] = (float)q * delta;
-      if (K.scaled) y[i] *= side ? K.v[8 * l + i] : K.k[8 * l + i];
+      y[i] *= lam[i];
     }
     inverse_row(y, x, l, f);
     if (have) {
@@ -464,6 +471,16 @@ static uint64_t transform_grid(uint64_t tokens, uint64_t rows, uint32_t* quads) 
   return (items + kBlock / 64 - 1) / (kBlock / 64);
 }
 
+// A vector a thread (hq_srft.hip) takes 2.5 times fewer instructions than 16 lanes a vector, once it fills the chip:
+// 32768 tokens of 8 heads append in 74 us against 105 and read in 44 against 67, 8192 in 26 against 33 and 18
+// against 23, 4096 (at 8 bits) in 19 against 20 and 15 against 13.  K and V with lambdas are launches of their
+// own, so that each has to fill it.
+constexpr uint64_t kManyVectors = 1u << 17;  // of a launch
+static bool many_vectors(const hq_kv_cache& c, uint64_t tokens, uint32_t sides) {
+  const uint64_t vectors = tokens * c.heads * (c.lambda_k || c.lambda_v ? 1u : sides);
+  return vectors >= kManyVectors && (tokens + 255) / 256 * c.heads * sides <= kMaxThreads / 256;
+}
+
 extern "C" {
 
 int hq_kv_append(const hq_kv_cache* cache, const void* k, const void* v, int32_t dtype, uint64_t tokens,
@@ -496,6 +513,11 @@ int hq_kv_append(const hq_kv_cache* cache, const void* k, const void* v, int32_t
   const uint64_t grid = transform_grid(tokens, cache->heads * 2, &a.quads);
   if (grid > kMaxThreads / kBlock) return HQ_ERR_INVALID_ARG;
   const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (a.vec && many_vectors(*cache, tokens, 2)) {
+    const ManyAppend many = {a.cache, k, v, slots, tokens, a.kt, a.kh, a.vt, a.vh, a.heads, a.pages, a.page_log2, 0, 0};
+    launch_append_many(*cache, many, a.f32, st);
+    return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
+  }
   if (cache->bits == 4) hipLaunchKernelGGL(append_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
   else hipLaunchKernelGGL(append_kernel<8>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
   return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
@@ -524,6 +546,11 @@ int hq_kv_read(const hq_kv_cache* cache, const int64_t* slots, uint64_t tokens, 
   const uint64_t grid = transform_grid(tokens, cache->heads * (a.sides == 3 ? 2 : 1), &a.quads);
   if (grid > kMaxThreads / kBlock) return HQ_ERR_INVALID_ARG;
   const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (many_vectors(*cache, tokens, a.sides == 3 ? 2 : 1)) {
+    const ManyRead many = {a.cache, slots, tokens, k, v, a.heads, a.pages, a.page_log2, 0, 0};
+    launch_read_many(*cache, many, a.f32, st);
+    return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
+  }
   if (cache->bits == 4) hipLaunchKernelGGL(read_kernel<4>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
   else hipLaunchKernelGGL(read_kernel<8>, dim3((uint32_t)grid), dim3(kBlock), 0, st, a, T);
   return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;

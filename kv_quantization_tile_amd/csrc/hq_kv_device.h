@@ -37,6 +37,14 @@ struct Tables {
   float k[kD], v[kD];
 };
 
+// The multipliers in LDS, when there are any: lanes pick their own, and vector loads from a kernel's arguments are
+// slow enough (9 us over a launch of 16384 wavefronts) to be made once a workgroup of 256.
+__device__ __forceinline__ void stage_tables(const Tables& K, float (*s)[kD]) {
+  if (!K.scaled) return;
+  s[threadIdx.x >> 7][threadIdx.x & 127u] = threadIdx.x < 128u ? K.k[threadIdx.x] : K.v[threadIdx.x - 128u];
+  __syncthreads();
+}
+
 // cos and sin of 2 pi k / n, k < n / 2, rounded to binary32 from binary64 values in the first octant and
 // continued by symmetry: the values of the flat codec's tables (hq_srft.hip), in device memory because a
 // lane picks its own 20.  The octant's cos and sin are Taylor sums, whose remainder below 2^-60 no binary32

@@ -55,4 +55,25 @@ inline bool make_tables(const hq_kv_cache& c, bool encode, Tables* T) {
   return true;
 }
 
+// The paged cache's transforms a vector a thread, for many tokens (hq_srft.hip).
+struct ManyAppend {
+  uint8_t* cache;
+  const void *k, *v;
+  const int64_t* slots;
+  uint64_t tokens;
+  int64_t kt, kh, vt, vh;  // strides in values
+  uint32_t heads, pages, page_log2;
+  uint32_t sides, one;     // workgroups take K and V in turn (2), or the side `one` (1); set by the launch
+};
+struct ManyRead {
+  const uint8_t* cache;
+  const int64_t* slots;
+  uint64_t tokens;
+  void *k, *v;  // one may be null
+  uint32_t heads, pages, page_log2;
+  uint32_t sides, one;
+};
+void launch_append_many(const hq_kv_cache& c, const ManyAppend& a, int f32_in, hipStream_t st);
+void launch_read_many(const hq_kv_cache& c, const ManyRead& a, int f32_out, hipStream_t st);
+
 }  // namespace hq_kv

@@ -39,6 +39,8 @@
 
 #include "../../include/hq.h"
 #include "hq_device.h"
+#include "hq_kv_device.h"
+#include "hq_kv_internal.h"
 
 namespace hq_srft {
 
@@ -163,17 +165,83 @@ __device__ __forceinline__ void sign_words(uint64_t seed, uint32_t w[4]) {
   w[3] = p.w;
 }
 
-template <int BITS>
-__global__ __launch_bounds__(kBlock) void srft_encode_kernel(const void* __restrict__ x, int f32_in, uint64_t nvec,
-                                                             uint64_t seed, Consts K, uint8_t* __restrict__ codes,
-                                                             uint16_t* __restrict__ scales) {
-  const uint64_t v = (uint64_t)blockIdx.x * kBlock + threadIdx.x;
-  if (v >= nvec) return;
+// Where a thread's vector comes from and goes to.  Flat: vector after vector.
+struct FlatEncode {
+  const void* __restrict__ x;
+  uint64_t nvec;
+  uint8_t* __restrict__ codes;
+  uint16_t* __restrict__ scales;
+  __device__ __forceinline__ uint64_t vector() const { return (uint64_t)blockIdx.x * kBlock + threadIdx.x; }
+  __device__ __forceinline__ bool have(uint64_t v) const { return v < nvec; }
+  __device__ __forceinline__ const uint4* bf16_row(uint64_t v) const { return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + v * kD); }
+  __device__ __forceinline__ const uint4* f32_row(uint64_t v) const { return reinterpret_cast<const uint4*>(static_cast<const float*>(x) + v * kD); }
+  template <int BITS>
+  __device__ __forceinline__ void store(uint64_t v, const uint32_t* cw, const uint32_t* sc) const {
+    uint4* cdst = reinterpret_cast<uint4*>(codes + v * (BITS == 4 ? kD / 2 : kD));
+#pragma unroll
+    for (int i = 0; i < (BITS == 4 ? 4 : 8); ++i) cdst[i] = make_uint4(cw[4 * i], cw[4 * i + 1], cw[4 * i + 2], cw[4 * i + 3]);
+    uint4* sdst = reinterpret_cast<uint4*>(scales + v * kGroups);
+    sdst[0] = make_uint4(sc[0], sc[1], sc[2], sc[3]);
+    sdst[1] = make_uint4(sc[4], sc[5], sc[6], sc[7]);
+  }
+};
+
+// Paged: a workgroup takes 256 consecutive tokens of one head, of keys or values (both in turn with sides == 2, else
+// the side `one`); a vector's number is its token.
+struct PagedEncode {
+  hq_kv::ManyAppend a;
+  __device__ __forceinline__ uint32_t side() const { return a.sides == 2u ? blockIdx.x & 1u : a.one; }
+  __device__ __forceinline__ uint32_t row() const { return a.sides == 2u ? blockIdx.x >> 1 : blockIdx.x; }
+  __device__ __forceinline__ uint64_t vector() const { return (uint64_t)(row() / a.heads) * kBlock + threadIdx.x; }
+  __device__ __forceinline__ int64_t slot(uint64_t v) const { return v < a.tokens ? a.slots[v] : -1; }
+  __device__ __forceinline__ bool have(uint64_t v) const {
+    const int64_t s = slot(v);
+    return s >= 0 && s < ((int64_t)a.pages << a.page_log2);
+  }
+  __device__ __forceinline__ int64_t offset(uint64_t v) const {
+    const int64_t h = row() % a.heads;
+    return side() ? (int64_t)v * a.vt + h * a.vh : (int64_t)v * a.kt + h * a.kh;
+  }
+  __device__ __forceinline__ const uint4* bf16_row(uint64_t v) const {
+    return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(side() ? a.v : a.k) + offset(v));
+  }
+  __device__ __forceinline__ const uint4* f32_row(uint64_t v) const {
+    return reinterpret_cast<const uint4*>(static_cast<const float*>(side() ? a.v : a.k) + offset(v));
+  }
+  template <int BITS>
+  __device__ __forceinline__ void store(uint64_t v, const uint32_t* cw, const uint32_t* sc) const {
+    typedef hq_kv::Page<BITS> Page;
+    const int64_t s = slot(v);
+    const uint32_t P = 1u << a.page_log2, t = (uint32_t)s & (P - 1u);
+    uint8_t* page = a.cache + ((uint64_t)(s >> a.page_log2) * a.heads + row() % a.heads) * ((uint64_t)P * Page::kToken);
+    if (side() == 0) {
+      uint4* c = reinterpret_cast<uint4*>(page + Page::k_code(P, t));
+#pragma unroll
+      for (int i = 0; i < BITS; ++i) c[i] = make_uint4(cw[4 * i], cw[4 * i + 1], cw[4 * i + 2], cw[4 * i + 3]);
+      uint4* d = reinterpret_cast<uint4*>(page + Page::k_scale(P, t));
+      d[0] = make_uint4(sc[0], sc[1], sc[2], sc[3]);
+      d[1] = make_uint4(sc[4], sc[5], sc[6], sc[7]);
+    } else {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        uint32_t* c = reinterpret_cast<uint32_t*>(page + Page::v_code(P, t, g));
+#pragma unroll
+        for (int i = 0; i < BITS / 4; ++i) c[i] = cw[g * (BITS / 4) + i];
+        *reinterpret_cast<uint16_t*>(page + Page::v_scale(P, t, g)) = (uint16_t)(sc[g >> 1] >> (16 * (g & 1)));
+      }
+    }
+  }
+};
+
+template <int BITS, class IO>
+__global__ __launch_bounds__(kBlock) void srft_encode_kernel(IO io, int f32_in, uint64_t seed, Consts K) {
+  const uint64_t v = io.vector();
+  if (!io.have(v)) return;
   uint32_t sw[4];
   sign_words(seed, sw);
   float re[kN], im[kN];
   if (!f32_in) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + v * kD);
+    const uint4* src = io.bf16_row(v);
 #pragma unroll
     for (int q4 = 0; q4 < 16; ++q4) {
       const uint4 u = src[q4];
@@ -188,7 +256,7 @@ __global__ __launch_bounds__(kBlock) void srft_encode_kernel(const void* __restr
       }
     }
   } else {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + v * kD);
+    const uint4* src = io.f32_row(v);
 #pragma unroll
     for (int q4 = 0; q4 < 32; ++q4) {
       const uint4 u = src[q4];
@@ -259,39 +327,93 @@ __global__ __launch_bounds__(kBlock) void srft_encode_kernel(const void* __restr
   }
   // a non-finite coordinate: zero codes, NaN scales
   const uint32_t keep = bad ? 0u : 0xFFFFFFFFu;
-  uint4* cdst = reinterpret_cast<uint4*>(codes + v * (BITS == 4 ? kD / 2 : kD));
 #pragma unroll
-  for (int i = 0; i < (BITS == 4 ? 4 : 8); ++i)
-    cdst[i] = make_uint4(cw[4 * i] & keep, cw[4 * i + 1] & keep, cw[4 * i + 2] & keep, cw[4 * i + 3] & keep);
-  uint4* sdst = reinterpret_cast<uint4*>(scales + v * kGroups);
-  const uint32_t nan2 = 0x7E007E00u;
-  sdst[0] = bad ? make_uint4(nan2, nan2, nan2, nan2) : make_uint4(sc[0], sc[1], sc[2], sc[3]);
-  sdst[1] = bad ? make_uint4(nan2, nan2, nan2, nan2) : make_uint4(sc[4], sc[5], sc[6], sc[7]);
+  for (int i = 0; i < (BITS == 4 ? 16 : 32); ++i) cw[i] &= keep;
+#pragma unroll
+  for (int i = 0; i < kGroups / 2; ++i) sc[i] = bad ? 0x7E007E00u : sc[i];
+  io.template store<BITS>(v, cw, sc);
 }
 
-template <int BITS, bool LAM>
-__global__ __launch_bounds__(kBlock) void srft_decode_kernel(const uint8_t* __restrict__ codes,
-                                                             const uint16_t* __restrict__ scales, uint64_t nvec,
-                                                             uint64_t seed, Consts K, void* __restrict__ out,
-                                                             int f32_out) {
-  // every thread stays to the end (the bf16 store goes through LDS with workgroup barriers); a
-  // thread past the last vector decodes the last vector again and stores nothing
-  const uint64_t v = (uint64_t)blockIdx.x * kBlock + threadIdx.x;
-  const uint64_t vl = v < nvec ? v : nvec - 1;
-  constexpr int kWords = BITS == 4 ? 16 : 32;
-  uint32_t cw[kWords];
-  const uint4* csrc = reinterpret_cast<const uint4*>(codes + vl * (BITS == 4 ? kD / 2 : kD));
+struct FlatDecode {
+  const uint8_t* __restrict__ codes;
+  const uint16_t* __restrict__ scales;
+  uint64_t nvec;
+  void* __restrict__ out;
+  __device__ __forceinline__ uint64_t vector() const { return (uint64_t)blockIdx.x * kBlock + threadIdx.x; }
+  __device__ __forceinline__ bool have(uint64_t v) const { return v < nvec; }
+  __device__ __forceinline__ void* base() const { return out; }
+  __device__ __forceinline__ uint64_t row(uint64_t v) const { return v; }
+  template <int BITS>
+  __device__ __forceinline__ void load(uint64_t v, uint32_t* cw, uint32_t* sc) const {
+    const uint64_t vl = v < nvec ? v : nvec - 1;  // a thread past the last vector decodes it again and stores nothing
+    const uint4* csrc = reinterpret_cast<const uint4*>(codes + vl * (BITS == 4 ? kD / 2 : kD));
 #pragma unroll
-  for (int i = 0; i < kWords / 4; ++i) {
-    const uint4 u = csrc[i];
-    cw[4 * i] = u.x;
-    cw[4 * i + 1] = u.y;
-    cw[4 * i + 2] = u.z;
-    cw[4 * i + 3] = u.w;
+    for (int i = 0; i < BITS; ++i) {
+      const uint4 u = csrc[i];
+      cw[4 * i] = u.x;
+      cw[4 * i + 1] = u.y;
+      cw[4 * i + 2] = u.z;
+      cw[4 * i + 3] = u.w;
+    }
+    const uint4* ssrc = reinterpret_cast<const uint4*>(scales + vl * kGroups);
+    const uint4 s0 = ssrc[0], s1 = ssrc[1];
+    sc[0] = s0.x; sc[1] = s0.y; sc[2] = s0.z; sc[3] = s0.w;
+    sc[4] = s1.x; sc[5] = s1.y; sc[6] = s1.z; sc[7] = s1.w;
   }
-  const uint4* ssrc = reinterpret_cast<const uint4*>(scales + vl * kGroups);
-  const uint4 s0 = ssrc[0], s1 = ssrc[1];
-  const uint32_t sc[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+};
+
+// As PagedEncode; a slot outside the cache reads as zeros.
+struct PagedDecode {
+  hq_kv::ManyRead a;
+  __device__ __forceinline__ uint32_t side() const { return a.sides == 2u ? blockIdx.x & 1u : a.one; }
+  __device__ __forceinline__ uint32_t group() const { return a.sides == 2u ? blockIdx.x >> 1 : blockIdx.x; }
+  __device__ __forceinline__ uint64_t vector() const { return (uint64_t)(group() / a.heads) * kBlock + threadIdx.x; }
+  __device__ __forceinline__ bool have(uint64_t v) const { return v < a.tokens; }
+  __device__ __forceinline__ void* base() const { return side() ? a.v : a.k; }
+  __device__ __forceinline__ uint64_t row(uint64_t v) const { return v * a.heads + group() % a.heads; }
+  template <int BITS>
+  __device__ __forceinline__ void load(uint64_t v, uint32_t* cw, uint32_t* sc) const {
+    typedef hq_kv::Page<BITS> Page;
+    const int64_t s = v < a.tokens ? a.slots[v] : -1;
+#pragma unroll
+    for (int i = 0; i < 4 * BITS; ++i) cw[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < kGroups / 2; ++i) sc[i] = 0u;
+    if (s < 0 || s >= ((int64_t)a.pages << a.page_log2)) return;
+    const uint32_t P = 1u << a.page_log2, t = (uint32_t)s & (P - 1u);
+    const uint8_t* page = a.cache + ((uint64_t)(s >> a.page_log2) * a.heads + group() % a.heads) * ((uint64_t)P * Page::kToken);
+    if (side() == 0) {
+      const uint4* c = reinterpret_cast<const uint4*>(page + Page::k_code(P, t));
+#pragma unroll
+      for (int i = 0; i < BITS; ++i) {
+        const uint4 u = c[i];
+        cw[4 * i] = u.x;
+        cw[4 * i + 1] = u.y;
+        cw[4 * i + 2] = u.z;
+        cw[4 * i + 3] = u.w;
+      }
+      const uint4* d = reinterpret_cast<const uint4*>(page + Page::k_scale(P, t));
+      const uint4 s0 = d[0], s1 = d[1];
+      sc[0] = s0.x; sc[1] = s0.y; sc[2] = s0.z; sc[3] = s0.w;
+      sc[4] = s1.x; sc[5] = s1.y; sc[6] = s1.z; sc[7] = s1.w;
+    } else {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const uint32_t* c = reinterpret_cast<const uint32_t*>(page + Page::v_code(P, t, g));
+#pragma unroll
+        for (int i = 0; i < BITS / 4; ++i) cw[g * (BITS / 4) + i] = c[i];
+        sc[g >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(page + Page::v_scale(P, t, g)) << (16 * (g & 1));
+      }
+    }
+  }
+};
+
+template <int BITS, bool LAM, class IO>
+__global__ __launch_bounds__(kBlock) void srft_decode_kernel(IO io, uint64_t seed, Consts K, int f32_out) {
+  // every thread stays to the end (the bf16 store goes through LDS with workgroup barriers)
+  const uint64_t v = io.vector();
+  uint32_t cw[BITS == 4 ? 16 : 32], sc[kGroups / 2];
+  io.template load<BITS>(v, cw, sc);
   // y_c = (q_c Delta_g) lambda_c, formed where the unpack needs it
   auto y = [&](const int c) __attribute__((always_inline)) -> float {
     const int32_t q = BITS == 4 ? __builtin_amdgcn_sbfe(cw[c >> 3], 4 * (c & 7), 4)
@@ -340,8 +462,8 @@ __global__ __launch_bounds__(kBlock) void srft_decode_kernel(const uint8_t* __re
     // instruction writes 8 whole 128-byte lines; row r's 16-byte chunk c sits at slot c ^ (r & 7).
     __shared__ uint4 s_out[kBlock / 64][64 * 8];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const uint64_t wbase = (uint64_t)blockIdx.x * kBlock + (uint64_t)wv * 64;
-    uint4* dst = reinterpret_cast<uint4*>(out);
+    const uint64_t wbase = v - (uint64_t)lane;
+    uint4* dst = static_cast<uint4*>(io.base());
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -354,13 +476,13 @@ __global__ __launch_bounds__(kBlock) void srft_decode_kernel(const uint8_t* __re
       for (int i = 0; i < 8; ++i) {
         const int r = 8 * i + (lane >> 3), c = lane & 7;
         const uint64_t vec = wbase + (uint64_t)r;
-        if (vec < nvec) dst[vec * 16 + 8 * h + c] = s_out[wv][r * 8 + (c ^ (r & 7))];
+        if (io.have(vec)) dst[io.row(vec) * 16 + 8 * h + c] = s_out[wv][r * 8 + (c ^ (r & 7))];
       }
       __syncthreads();
     }
   } else {
-    if (v >= nvec) return;
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + v * kD);
+    if (!io.have(v)) return;
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(io.base()) + io.row(v) * kD);
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       float xo[4];
@@ -378,6 +500,62 @@ __global__ __launch_bounds__(kBlock) void srft_decode_kernel(const uint8_t* __re
 
 }  // namespace hq_srft
 
+// ---------------------------------------------------------------------------------------------
+// The paged cache's launches: one for K and V where they share their multipliers, else one each.
+namespace {
+
+// The tables of both sides; the constant part is computed once a process.
+void paged_consts(const hq_kv_cache& c, hq_srft::Consts K[2]) {
+  static const hq_srft::Consts base = [] {
+    hq_srft::Consts t;
+    (void)hq_srft::make_consts(nullptr, &t);
+    return t;
+  }();
+  const float* lambda[2] = {c.lambda_k, c.lambda_v};
+  for (int i = 0; i < 2; ++i) {
+    K[i] = base;
+    if (!lambda[i]) continue;
+    for (int j = 0; j < hq_srft::kD; ++j) {
+      const volatile float r = 1.0f / lambda[i][j];
+      K[i].m[j] = base.m[j] * r;
+      K[i].lam[j] = lambda[i][j];
+    }
+  }
+}
+
+uint32_t workgroups(uint64_t tokens, uint64_t rows) { return (uint32_t)((tokens + hq_srft::kBlock - 1) / hq_srft::kBlock * rows); }
+
+}  // namespace
+
+void hq_kv::launch_append_many(const hq_kv_cache& c, const hq_kv::ManyAppend& a, int f32_in, hipStream_t st) {
+  hq_srft::Consts K[2];
+  paged_consts(c, K);
+  const auto kernel = c.bits == 4 ? hq_srft::srft_encode_kernel<4, hq_srft::PagedEncode> : hq_srft::srft_encode_kernel<8, hq_srft::PagedEncode>;
+  hq_srft::PagedEncode io = {a};
+  const uint32_t calls = c.lambda_k || c.lambda_v ? 2 : 1;
+  for (uint32_t i = 0; i < calls; ++i) {
+    io.a.sides = 3u - calls;
+    io.a.one = i;
+    hipLaunchKernelGGL(kernel, dim3(workgroups(a.tokens, (uint64_t)a.heads * io.a.sides)), dim3(hq_srft::kBlock), 0, st, io, f32_in, c.seed, K[i]);
+  }
+}
+
+void hq_kv::launch_read_many(const hq_kv_cache& c, const hq_kv::ManyRead& a, int f32_out, hipStream_t st) {
+  hq_srft::Consts K[2];
+  paged_consts(c, K);
+  hq_srft::PagedDecode io = {a};
+  const bool both = a.k && a.v, joint = both && !c.lambda_k && !c.lambda_v;
+  for (uint32_t i = 0; i < (joint ? 1u : 2u); ++i) {
+    if (!joint && !(i ? a.v : a.k)) continue;
+    io.a.sides = joint ? 2u : 1u;
+    io.a.one = i;
+    const bool lam = i ? c.lambda_v : c.lambda_k;
+    const auto kernel = c.bits == 4 ? (lam ? hq_srft::srft_decode_kernel<4, true, hq_srft::PagedDecode> : hq_srft::srft_decode_kernel<4, false, hq_srft::PagedDecode>)
+                                    : (lam ? hq_srft::srft_decode_kernel<8, true, hq_srft::PagedDecode> : hq_srft::srft_decode_kernel<8, false, hq_srft::PagedDecode>);
+    hipLaunchKernelGGL(kernel, dim3(workgroups(a.tokens, (uint64_t)a.heads * io.a.sides)), dim3(hq_srft::kBlock), 0, st, io, c.seed, K[i], f32_out);
+  }
+}
+
 extern "C" {
 
 int hq_srft_encode(const void* x, int32_t dtype, uint64_t n, uint64_t seed, const float* lambda, int32_t bits,
@@ -393,12 +571,10 @@ int hq_srft_encode(const void* x, int32_t dtype, uint64_t n, uint64_t seed, cons
   const dim3 grid((uint32_t)((nvec + hq_srft::kBlock - 1) / hq_srft::kBlock));
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const int f32_in = dtype == HQ_F32;
-  if (bits == 4)
-    hipLaunchKernelGGL(hq_srft::srft_encode_kernel<4>, grid, dim3(hq_srft::kBlock), 0, st, x, f32_in, nvec, seed, K,
-                       static_cast<uint8_t*>(codes), static_cast<uint16_t*>(scales));
-  else
-    hipLaunchKernelGGL(hq_srft::srft_encode_kernel<8>, grid, dim3(hq_srft::kBlock), 0, st, x, f32_in, nvec, seed, K,
-                       static_cast<uint8_t*>(codes), static_cast<uint16_t*>(scales));
+  const hq_srft::FlatEncode io = {x, nvec, static_cast<uint8_t*>(codes), static_cast<uint16_t*>(scales)};
+  const dim3 block(hq_srft::kBlock);
+  if (bits == 4) hipLaunchKernelGGL((hq_srft::srft_encode_kernel<4, hq_srft::FlatEncode>), grid, block, 0, st, io, f32_in, seed, K);
+  else hipLaunchKernelGGL((hq_srft::srft_encode_kernel<8, hq_srft::FlatEncode>), grid, block, 0, st, io, f32_in, seed, K);
   return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
 }
 
@@ -415,17 +591,10 @@ int hq_srft_decode(const void* codes, const void* scales, uint64_t n, uint64_t s
   const dim3 grid((uint32_t)((nvec + hq_srft::kBlock - 1) / hq_srft::kBlock));
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const int f32_out = out_dtype == HQ_F32;
-  const uint8_t* c = static_cast<const uint8_t*>(codes);
-  const uint16_t* sp = static_cast<const uint16_t*>(scales);
-  const dim3 block(hq_srft::kBlock);
-  if (bits == 4 && lambda)
-    hipLaunchKernelGGL((hq_srft::srft_decode_kernel<4, true>), grid, block, 0, st, c, sp, nvec, seed, K, out, f32_out);
-  else if (bits == 4)
-    hipLaunchKernelGGL((hq_srft::srft_decode_kernel<4, false>), grid, block, 0, st, c, sp, nvec, seed, K, out, f32_out);
-  else if (lambda)
-    hipLaunchKernelGGL((hq_srft::srft_decode_kernel<8, true>), grid, block, 0, st, c, sp, nvec, seed, K, out, f32_out);
-  else
-    hipLaunchKernelGGL((hq_srft::srft_decode_kernel<8, false>), grid, block, 0, st, c, sp, nvec, seed, K, out, f32_out);
+  const hq_srft::FlatDecode io = {static_cast<const uint8_t*>(codes), static_cast<const uint16_t*>(scales), nvec, out};
+  const auto kernel = bits == 4 ? (lambda ? hq_srft::srft_decode_kernel<4, true, hq_srft::FlatDecode> : hq_srft::srft_decode_kernel<4, false, hq_srft::FlatDecode>)
+                                : (lambda ? hq_srft::srft_decode_kernel<8, true, hq_srft::FlatDecode> : hq_srft::srft_decode_kernel<8, false, hq_srft::FlatDecode>);
+  hipLaunchKernelGGL(kernel, grid, dim3(hq_srft::kBlock), 0, st, io, seed, K, f32_out);
   return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
 }
 

@@ -242,3 +242,41 @@ def test_append_into_a_synthetic_layer_equals_flat_codec(orc):
         flat = codes.swapaxes(0, 1).reshape(8 * 4096, 64)
         assert np.array_equal(flat, c.cpu().numpy())
         assert np.array_equal(scales.view(np.uint16).swapaxes(0, 1).reshape(-1, 16), s.cpu().numpy().view(np.uint16))
+
+
+@pytest.mark.parametrize("bits,page,heads,tokens,dtype,lam", [
+    (4, 64, 8, 8203, "bf16", (False, False)),
+    (8, 16, 4, 32801, "f32", (True, True)),
+    (4, 256, 8, 16387, "bf16", (True, False)),
+    (8, 32, 16, 8199, "bf16", (False, True)),
+    (4, 16, 1, 65537, "f32", (False, False)),
+])
+def test_many_tokens_equal_few_at_a_time(bits, page, heads, tokens, dtype, lam):
+    """Enough vectors for a thread to take one each: the bytes and values of calls too small for that, which are tested
+    against the oracle; vectors that are not finite, and slots outside the cache, among them."""
+    say(f"case: {tokens} tokens in one call and in many, {heads} heads, page {page}, {bits} bits, {dtype}, lambda {lam}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(tokens)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    row = torch.randn(tokens, 3 * heads * 128, generator=g, device="cuda").to(dt)
+    k, v = row[:, heads * 128:2 * heads * 128].unflatten(1, (heads, 128)), row[:, 2 * heads * 128:].unflatten(1, (heads, 128))
+    k[17, 0, 5], v[tokens - 1, heads - 1, 127], k[300] = float("nan"), float("inf"), 0
+    r = np.random.default_rng(tokens)
+    fmt = dict(bits=bits, seed=13, lam_k=r.uniform(0.5, 2.0, 128).astype(np.float32) if lam[0] else None,
+               lam_v=r.uniform(0.5, 2.0, 128).astype(np.float32) if lam[1] else None)
+    pages = -(-tokens // page) + 2
+    slots = torch.from_numpy(slots_of(tokens, pages, page, tokens, True)).cuda()
+    one, many = (torch.full((pages, heads, page * hq.hq_kv_token_bytes(bits)), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(2))
+    hq.hq_kv_append(one, k, v, slots, **fmt)
+    step = 1000
+    vectors = heads * (1 if lam[0] or lam[1] else 2)  # of a launch and token
+    assert step * vectors < 1 << 17 <= tokens * vectors
+    for i in range(0, tokens, step):
+        hq.hq_kv_append(many, k[i:i + step], v[i:i + step], slots[i:i + step], **fmt)
+    assert torch.equal(one, many)
+    for od in (torch.bfloat16, torch.float32):
+        whole = hq.hq_kv_read(one, slots, out_dtype=od, **fmt)
+        for i in range(0, tokens, step):
+            part = hq.hq_kv_read(one, slots[i:i + step], out_dtype=od, **fmt)
+            for a, b in zip(whole, part):
+                assert np.array_equal(host(a[i:i + step]), host(b))
