@@ -122,6 +122,10 @@ CASES = {
     "everything_many": dict(lens=[90, 200], q_lens=[90, 35], heads=1, group=2, causal=False),
     "window_without_causal": dict(lens=[90, 200], q_lens=[40, 35], heads=1, group=2, causal=False, window=20),
     "many_queries_than_tokens": dict(lens=[7, 0, 64], q_lens=[20, 18, 64], heads=1, group=2),
+    # tiles of up to 16 rows beside full ones: single tokens, and what is left of 256 or 128 rows
+    "mixed": dict(lens=[300, 77, 150, 400], q_lens=[130, 1, 8, 129], heads=1, group=2, page=32, lam=True),
+    "mixed_window_cap": dict(lens=[200, 33, 180], q_lens=[66, 2, 65], heads=2, group=2, window=50, softcap=25.0, bits=8),
+    "mixed_splits": dict(lens=[1400, 900], q_lens=[44, 1], heads=1, group=3, page=256),
     "negative_scale": dict(lens=[70, 64], q_lens=[1, 1], scale=-0.11),
     "zero_scale": dict(lens=[70, 64], q_lens=[20, 1], scale=0.0),
 }
@@ -236,6 +240,16 @@ def test_query_offsets(orc):
     c.lens = [-3, 64, 64]
     out = c.run(max_len=64)
     assert not out[:2].any() and torch.equal(out[2:], short[2:])
+
+
+def test_equal_sequences_without_offsets(orc):
+    """Without q_start the last tile of each sequence may be a light one: the same rows as with offsets."""
+    say("case: attend equal sequences, light last tiles")
+    for m, group in ((130, 2), (44, 3), (86, 3)):
+        c = Case(orc, [300, 260], [m, m], heads=1, group=group)
+        w = [torch.zeros(2, 1, 300, device="cuda") for _ in range(2)]
+        assert torch.equal(c.run(q_start=None, max_q=None), c.run())
+        assert torch.equal(c.run(q_start=None, weights=w[0]), c.run(weights=w[1])) and torch.equal(*w)
 
 
 def test_no_pages_and_empty_calls():
