@@ -708,24 +708,33 @@ __global__ __launch_bounds__(kAttBlock) void weights_few_kernel(AttendArgs a, ui
 }
 
 // ---------------------------------------------------------------------------------------------
-// Many rows: the queries' rows transformed once, to the workspace.
+// Many rows: the queries' rows transformed once, to the workspace.  A workgroup takes `span` rows, 16 at a time: 64 where
+// that leaves four workgroups a CU, so that the twiddles are fetched once for four (262144 rows: 45 us, 53 us with
+// 16; a mixed batch of 2080 rows in 192 tiles: 13 us, 11.5 us with 16).
 template <int BITS>
-__global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Tables K, int parts) {
+__global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Tables K, int parts, uint32_t span) {
   __shared__ __align__(16) _Float16 s_q[2][16][kD + 8];
   __shared__ float s_lam[2][kD];
   stage_tables(K, s_lam);
-  const uint32_t l = threadIdx.x & 15u, g = threadIdx.x >> 4, per = a.tile_rows / 16u;
-  const uint32_t item = blockIdx.x / per, row = (blockIdx.x % per) * 16u + g;
+  const uint32_t l = threadIdx.x & 15u, g = threadIdx.x >> 4, per = a.tile_rows / span;
+  const uint32_t item = blockIdx.x / per, first = (blockIdx.x % per) * span;
   const Item it = item_of(a, item);
   const Seq s = seq_of(a, it.b);
-  if (it.tile * a.tile_rows + (row & ~15u) >= (uint32_t)s.m * a.group) return;
-  const float f = rotate_row<BITS>(a, K, s_lam[0], s, it.h, it.tile * a.tile_rows + row, l, lane_forward(K, l), s_q[0][g], parts == 2 ? s_q[1][g] : nullptr);
-  const uint64_t at = (uint64_t)item * a.tile_rows + row;
-  if (l == 0) a.qf[at] = f;
-  // a row is written and read by the same wavefront
-  wave_sync();
-  *reinterpret_cast<f16x8*>(a.qhi + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[0][g][8 * l]);
-  if (parts == 2) *reinterpret_cast<f16x8*>(a.qlo + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[1][g][8 * l]);
+  const uint32_t rows = (uint32_t)s.m * a.group, r0 = it.tile * a.tile_rows;
+  if (r0 + first >= rows) return;
+  const LaneForward forward = lane_forward(K, l);
+#pragma unroll 1
+  for (uint32_t k = first; k < first + span && r0 + k < rows; k += 16u) {
+    const uint32_t row = k + g;
+    const float f = rotate_row<BITS>(a, K, s_lam[0], s, it.h, r0 + row, l, forward, s_q[0][g], parts == 2 ? s_q[1][g] : nullptr);
+    const uint64_t at = (uint64_t)item * a.tile_rows + row;
+    if (l == 0) a.qf[at] = f;
+    // a row is written and read by the same wavefront
+    wave_sync();
+    *reinterpret_cast<f16x8*>(a.qhi + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[0][g][8 * l]);
+    if (parts == 2) *reinterpret_cast<f16x8*>(a.qlo + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[1][g][8 * l]);
+    wave_sync();
+  }
 }
 
 // Many rows: a workgroup of 8 wavefronts takes 128 R rows of a (sequence, head) and one split of the tokens;
@@ -734,11 +743,14 @@ __global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Ta
 // ones' codes are in flight meanwhile.  Two wavefronts a SIMD, so that one's softmax runs beside the
 // other's products; R = 2 is what 256 registers hold (at R = 4 and one wavefront a SIMD nothing overlapped:
 // 1.2 ms for a prompt of 8192 tokens).  Two stages of LDS, one with the keys in two parts (160 KB hold no more).
-// A prompt of 8192 tokens, 550 GFLOP, takes 700 us (780 TFLOP/s; a 16-bit product of 8192^3 reaches 1050 to 1100).
-// A turn of 128 tokens is 12800 cycles: 4350 of matrix instructions, about 6800 of vector instructions and 4100
+// A prompt of 8192 tokens, 550 GFLOP, takes 645 to 715 us (770 to 850 TFLOP/s, less the longer the card
+// has been at it; a 16-bit product of 8192^3 reaches 1050 to 1100).
+// A turn of 128 tokens was 12800 cycles: 4350 of matrix instructions, about 6800 of vector instructions and 4100
 // of LDS a SIMD, in phases that the two wavefronts share (scores 700, softmax 700, output 750, four times; 1750
-// for the operands, 1000 for the loads).  Priorities, an offset between the wavefronts, operands fetched from LDS
-// ahead, and R = 1 with four wavefronts a SIMD changed the 750 us by 3 % at most.
+// for the operands, 1000 for the loads).  Where every row sees every token of a turn, a step's scores are now under
+// way during the softmax of the one before (732 us to 689 for the call, in turn).  Priorities, an offset between the wavefronts,
+// operands fetched from LDS ahead, those of the next turn made between the products, and R = 1 with four wavefronts
+// a SIMD changed the rest by 3 % at most.
 constexpr int kManyWaves = 8, kManyBlock = 64 * kManyWaves;
 template <bool PREC>
 struct Stage {
@@ -848,6 +860,19 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[q][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
   }
+  // a new reference for the rows' exponentials
+  auto raise = [&](const float* top) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const float mn = fmaxf(m[q], blocks_max(top[q]));
+      const float f = __builtin_amdgcn_exp2f(m[q] - mn);
+      m[q] = mn;
+      sum[q] *= f;
+      ones[q] *= f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[q][i] *= f;
+    }
+  };
   uint32_t buf = 0;
   if (!PREC && t < t1) {
     stage(st[0], s_flags[0], t + mine, page);
@@ -867,8 +892,67 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
     const Stage<PREC>& d = st[buf];
     // blocks of 16 tokens with a flag, asked for once and not between the products
     const uint32_t flagged = (uint32_t)__builtin_amdgcn_ballot_w64(lane < (uint32_t)kManyWaves && s_flags[buf][lane & (kManyWaves - 1)] != 0u);
+    bool whole = false;
+    if constexpr (!PREC) {
+      if (!cap && !flagged && t >= all_lo && t + kTok <= all_hi && t + kTok <= t1) {
+        // every row sees every token: each step's scores are under way during the softmax of the one before
+        f32x4 sc[2][R][2];
+        auto products = [&](int w, f32x4 (*x)[2]) __attribute__((always_inline)) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int q = 0; q < R; ++q) x[q][u] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const f16x8 kh = d.k[0][2 * w + u][j][lane];
+#pragma unroll
+              for (int q = 0; q < R; ++q) x[q][u] = mfma(kh, qh[q][j], x[q][u]);
+            }
+          }
+        };
+        products(0, sc[0]);
+#pragma unroll
+        for (int w = 0; w < kTok / 32; ++w) {
+          f32x4(*x)[2] = sc[w & 1];
+          float top[R];
+          bool rise = false;
+#pragma unroll
+          for (int q = 0; q < R; ++q) {
+            top[q] = x[q][0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) top[q] = fmaxf(top[q], x[q][i >> 2][i & 3]);
+            top[q] *= eff[q];
+            rise |= top[q] > m[q] + kSlack;
+          }
+          if (__builtin_amdgcn_ballot_w64(rise)) raise(top);
+          if (w + 1 < kTok / 32) products(w + 1, sc[(w + 1) & 1]);
+          f16x8 pf[R];
+#pragma unroll
+          for (int q = 0; q < R; ++q) {
+            const float base = kPScaleLog2 - m[q];
+            U32x4 p;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int u = i >> 1, c = 2 * (i & 1);
+              const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[q][u][c], eff[q], base));
+              const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[q][u][c + 1], eff[q], base));
+              p.v[i] = u2((f16x2){(_Float16)p0, (_Float16)p1});
+            }
+            pf[q] = frag(p);
+            ones[q] = mfma((f16x8)(_Float16)1.0f, pf[q], ones[q]);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const f16x8 v = d.v[w][i][lane];
+#pragma unroll
+            for (int q = 0; q < R; ++q) o[q][i] = mfma(v, pf[q], o[q][i]);
+          }
+        }
+        whole = true;
+      }
+    }
 #pragma unroll 2
-    for (int w = 0; w < kTok / 32; ++w) {
+    for (int w = whole ? kTok / 32 : 0; w < kTok / 32; ++w) {
       const int32_t tw = t + 32 * w;
       if (tw >= whi || tw + 32 <= wlo || tw >= t1) continue;
       f32x4 sc[R][2];
@@ -923,18 +1007,7 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
         top[q] *= eff[q];
         rise |= top[q] > m[q] + kSlack;
       }
-      if (__builtin_amdgcn_ballot_w64(rise)) {
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-          const float mn = fmaxf(m[q], blocks_max(top[q]));
-          const float f = __builtin_amdgcn_exp2f(m[q] - mn);
-          m[q] = mn;
-          sum[q] *= f;
-          ones[q] *= f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[q][i] *= f;
-        }
-      }
+      if (__builtin_amdgcn_ballot_w64(rise)) raise(top);
       f16x8 pf[R];
 #pragma unroll
       for (int q = 0; q < R; ++q) {
@@ -1197,7 +1270,8 @@ hipError_t launch_attend(const AttendArgs& a, const Tables& T, uint32_t items, h
     if (prec) hipLaunchKernelGGL((attend_few_kernel<BITS, true>), dim3(grid), block, 0, st, a, T);
     else hipLaunchKernelGGL((attend_few_kernel<BITS, false>), dim3(grid), block, 0, st, a, T);
   } else {
-    hipLaunchKernelGGL((rotate_rows_kernel<BITS>), dim3(items * (a.tile_rows / 16)), block, 0, st, a, T, prec ? 2 : 1);
+    const uint32_t span = items * (a.tile_rows / 64) >= 1024 ? 64 : 16;
+    hipLaunchKernelGGL((rotate_rows_kernel<BITS>), dim3(items * (a.tile_rows / span)), block, 0, st, a, T, prec ? 2 : 1, span);
     if (a.light) {
       if (prec) hipLaunchKernelGGL((attend_few_kernel<BITS, true>), dim3(grid), block, 0, st, a, T);
       else hipLaunchKernelGGL((attend_few_kernel<BITS, false>), dim3(grid), block, 0, st, a, T);
