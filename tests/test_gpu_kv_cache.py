@@ -150,6 +150,8 @@ def evict_case(seed, seqs, heads, top, page, bits, kind):
     (4, 16, 1, [50, 3], 64, 4, 4, "ties"),            # nothing to evict
     (4, 16, 2, [20, 5], 0, 0, 0, "plain"),            # nothing stays
     (4, 128, 2, [20000], 7777, 4, 1000, "ties"),
+    (4, 256, 1, [40000, 7], 3000, 4, 100, "odd"),     # more tokens than keys are held
+    (8, 64, 1, [33000], 32900, 1, 1, "equal"),
 ])
 def test_evict_exact(bits, page, heads, lens, budget, sink, recent, kind):
     say(f"case: evict {lens} to {budget} (sink {sink}, recent {recent}), page {page}, {bits} bits, weights {kind}")
