@@ -347,7 +347,7 @@ typedef struct {
   uint64_t total_q;
   uint32_t q_heads;         /* a multiple of the cache's heads                                             */
   uint32_t seqs;
-  uint32_t max_q;           /* most queries of a sequence; further ones are not computed                    */
+  uint32_t max_q;           /* most queries of a sequence; further ones count in m but are not computed     */
   uint32_t max_len;         /* most tokens of a sequence; a larger length counts as this                    */
   const int32_t *q_start;   /* DEVICE, seqs + 1 query offsets; NULL: total_q / seqs queries each            */
   const int32_t *table;     /* DEVICE, [seqs][table_width]                                                  */

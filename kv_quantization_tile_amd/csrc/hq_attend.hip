@@ -67,28 +67,30 @@ __device__ __forceinline__ uint32_t query_of(const AttendArgs& a, uint32_t r) { 
 
 struct Seq {
   int64_t q0;
-  int32_t m, n;  // queries, cached tokens
+  int32_t m, n;  // queries that are computed (the first max_q), cached tokens
+  int32_t back;  // position of query 0: the tokens less all the sequence's queries, computed or not
 };
 __device__ __forceinline__ Seq seq_of(const AttendArgs& a, uint32_t b) {
   Seq s;
+  int64_t all;
   if (a.q_start) {
     const int64_t x = a.q_start[b], y = a.q_start[b + 1], top = (int64_t)a.total_q;
     s.q0 = x < 0 ? 0 : x > top ? top : x;
-    const int64_t e = y < s.q0 ? s.q0 : y > top ? top : y;
-    s.m = (int32_t)(e - s.q0 < (int64_t)a.max_q ? e - s.q0 : (int64_t)a.max_q);
+    all = y < s.q0 ? 0 : (y > top ? top : y) - s.q0;
   } else {
-    const int64_t per = (int64_t)(a.total_q / a.seqs);
-    s.q0 = per * b;
-    s.m = (int32_t)(per < (int64_t)a.max_q ? per : (int64_t)a.max_q);
+    all = (int64_t)(a.total_q / a.seqs);
+    s.q0 = all * b;
   }
+  s.m = (int32_t)(all < (int64_t)a.max_q ? all : (int64_t)a.max_q);
   const uint64_t held = (uint64_t)a.width << a.page_log2, most = held < a.max_len ? held : a.max_len;
   const int32_t n = a.lens[b];
   s.n = n < 0 ? 0 : (uint64_t)n < most ? n : (int32_t)most;
+  s.back = (int32_t)(s.n - all);
   return s;
 }
 // Visible tokens [lo, hi) of query i of a sequence.
 __device__ __forceinline__ void visible(const AttendArgs& a, const Seq& s, int32_t i, int32_t* lo, int32_t* hi) {
-  const int32_t pos = s.n - s.m + i;
+  const int32_t pos = s.back + i;
   int32_t h = a.causal ? (pos + 1 < s.n ? pos + 1 : s.n) : s.n;
   if (h < 0) h = 0;
   int64_t l = a.window ? (int64_t)pos + 1 - (int64_t)a.window : 0;
@@ -1096,7 +1098,7 @@ __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a
   const uint32_t rows = (uint32_t)s.m * a.group;
   if (first >= s.n || a.pages == 0) return;
   // queries [i0, i1) see some of the workgroup's tokens
-  const int64_t back = s.n - s.m, last = (int64_t)first + 64 * kAttWaves - 1;
+  const int64_t back = s.back, last = (int64_t)first + 64 * kAttWaves - 1;
   const int64_t i0 = a.causal && first > back ? first - back : 0, i1 = a.window && last + a.window - back < s.m ? last + a.window - back : s.m;
   if (i0 >= i1) return;
   const uint32_t P = 1u << a.page_log2;
