@@ -336,9 +336,12 @@ int hq_kv_read(const hq_kv_cache *cache, const int64_t *slots, uint64_t tokens, 
  * n - m + i of its n = lens[b] cached tokens (its own token is cached first); it sees tokens up to its
  * position (all tokens when causal == 0), and with window > 0 only the last `window` of those up to its
  * position.  Scores are scale q.k, then softcap tanh(score / softcap) when softcap > 0; a row that sees
- * nothing gives 0.  Query head j reads KV head j / (q_heads / heads).  Products and softmax statistics
- * are binary32 sums of binary16 products (relative error about 2^-11 of a value; about 2^-20 of a score
- * when weights are asked for). */
+ * nothing gives 0.  Query head j reads KV head j / (q_heads / heads).  Transformed queries, keys, values
+ * and softmax weights enter the products as binary16, each off by at most 2^-11 of itself whatever its
+ * size (next to a scale of 2^13, at 8 bits 2^9, or more, scales of the same 16 tokens are off by up to
+ * 2^-18); sums, maxima and softmax statistics are binary32.  With weights asked for, queries and keys
+ * enter in two parts, and a score is off by about 2^-20 of scale sum |q_c k_c|; out then differs from a
+ * call without weights by that much. */
 typedef struct {
   const void *q;            /* DEVICE, value c of head j of query i at q[i stride_token + j stride_head + c] */
   void *out;                /* DEVICE, [total_q][q_heads][128], 16-byte aligned                              */

@@ -12,12 +12,14 @@
 // over 32 tokens, with V's blocks of four tokens laid out to match, so nothing crosses lanes between
 // the two products.  Lane (n, b) of O^t holds row n, groups 4b..4b+3.
 //
-// Codes become binary16 in two steps: or-ing a code's offset bits into the mantissa of 128.0 (4 bits;
-// 8.0 for 8) gives 128 + (c + 8) / 8 exactly, subtracting 129 gives c / 8 (c / 128), and the product
-// with Delta is rounded once to binary16 (2^-11 of the value; it cannot overflow, |c / 8| < 1).
+// Codes become binary16 in two steps: or-ing a code's offset bits into the mantissa of 1024.0 gives
+// 1024 + c + 8 (c + 128) exactly, subtracting 1032 (1152) gives c, and the product with Delta is rounded once
+// to binary16.  Delta and so c Delta are whole multiples of 2^-24, binary16's smallest step: the rounding is
+// at most 2^-11 of the value however small the vector.  A step with a scale so large that c Delta would overflow
+// takes its scales times 2^-7 (shrink) and undoes that in the scores and in P.
 // Rows of Q are scaled by a power of two so that their largest coordinate lies in [2^14, 2^15).
 // With accumulated weights asked for, scores are needed to binary32: Q and the keys go in two parts
-// (hi = rounded product, lo = fma(code, Delta, -hi), exact down to 2^-25), three products instead of one.
+// (hi = rounded product, lo = fma(code, Delta, -hi), exact), three products instead of one.
 // Scores, maxima, sums and outputs are binary32; P is binary16, scaled by 2^8 against a running
 // reference at most 2^6 below the maximum (so P <= 2^14, and terms down to 2^-22 of it stay normal).
 #include <hip/hip_runtime.h>
@@ -141,35 +143,31 @@ __device__ __forceinline__ float blocks_sum(float x) {
 __device__ __forceinline__ f16x2 h2(uint32_t u) { return __builtin_bit_cast(f16x2, u); }
 __device__ __forceinline__ uint32_t u2(f16x2 h) { return __builtin_bit_cast(uint32_t, h); }
 
-constexpr float kUnit4 = 8.0f, kUnit8 = 128.0f;  // a dequantised value is code Delta / unit
-template <int BITS>
-constexpr float unit() { return BITS == 4 ? kUnit4 : kUnit8; }
-
 struct U32x4 {
   uint32_t v[4];
 };
 __device__ __forceinline__ f16x8 frag(const U32x4& u) { return __builtin_bit_cast(f16x8, u); }
 
-// 8 codes (one group of one token) -> 4 registers of value pairs code / unit, exact.  Pair order:
+// 8 codes (one group of one token) -> 4 registers of code pairs, exact.  Pair order:
 // 4 bits (c_i, c_{i+4}), 8 bits (c_2i, c_2i+1).
 template <int BITS>
 __device__ __forceinline__ void code_pairs(const uint32_t* w, f16x2 out[4]) {
   if (BITS == 4) {
     const uint32_t u = w[0] ^ 0x88888888u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = h2(((u >> (4 * i)) & 0x000F000Fu) | 0x58005800u) - (f16x2){(_Float16)129.0f, (_Float16)129.0f};
+    for (int i = 0; i < 4; ++i) out[i] = h2(((u >> (4 * i)) & 0x000F000Fu) | 0x64006400u) - (f16x2){(_Float16)1032.0f, (_Float16)1032.0f};
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t u = w[i >> 1] ^ 0x80808080u;
-      // bytes: code, 0x48, code, 0x48
-      const uint32_t p = __builtin_amdgcn_perm(u, 0x48484848u, (i & 1) ? 0x00070006u : 0x00050004u);
-      out[i] = h2(p) - (f16x2){(_Float16)9.0f, (_Float16)9.0f};
+      // bytes: code, 0x64, code, 0x64
+      const uint32_t p = __builtin_amdgcn_perm(u, 0x64646464u, (i & 1) ? 0x00070006u : 0x00050004u);
+      out[i] = h2(p) - (f16x2){(_Float16)1152.0f, (_Float16)1152.0f};
     }
   }
 }
 
-// The same for tokens a and b: out[i] = (code_i of a, code_i of b) / unit, i = 0..7.
+// The same for tokens a and b: out[i] = (code_i of a, code_i of b), i = 0..7.
 template <int BITS>
 __device__ __forceinline__ void token_pairs(const uint32_t* a, const uint32_t* b, f16x2 out[8]) {
   if (BITS == 4) {
@@ -177,7 +175,7 @@ __device__ __forceinline__ void token_pairs(const uint32_t* a, const uint32_t* b
     const uint32_t hi = __builtin_amdgcn_perm(b[0], a[0], 0x07060302u) ^ 0x88888888u;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      out[i] = h2((((i < 4 ? lo : hi) >> (4 * (i & 3))) & 0x000F000Fu) | 0x58005800u) - (f16x2){(_Float16)129.0f, (_Float16)129.0f};
+      out[i] = h2((((i < 4 ? lo : hi) >> (4 * (i & 3))) & 0x000F000Fu) | 0x64006400u) - (f16x2){(_Float16)1032.0f, (_Float16)1032.0f};
   } else {
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -185,8 +183,8 @@ __device__ __forceinline__ void token_pairs(const uint32_t* a, const uint32_t* b
       const uint32_t q = __builtin_amdgcn_perm(b[w], a[w], 0x07030602u) ^ 0x80808080u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t r = __builtin_amdgcn_perm(i < 2 ? p : q, 0x48484848u, (i & 1) ? 0x00070006u : 0x00050004u);
-        out[4 * w + i] = h2(r) - (f16x2){(_Float16)9.0f, (_Float16)9.0f};
+        const uint32_t r = __builtin_amdgcn_perm(i < 2 ? p : q, 0x64646464u, (i & 1) ? 0x00070006u : 0x00050004u);
+        out[4 * w + i] = h2(r) - (f16x2){(_Float16)1152.0f, (_Float16)1152.0f};
       }
     }
   }
@@ -279,10 +277,33 @@ __device__ __forceinline__ void value_operands(const Share<BITS>& s, uint32_t ou
   }
 }
 
-// Whether one of four binary16 scales is NaN or infinite: an exponent of all ones carries into the sign's place.
-__device__ __forceinline__ bool any_bad(const uint32_t vs[2]) {
-  return ((((vs[0] & 0x7C007C00u) + 0x04000400u) | ((vs[1] & 0x7C007C00u) + 0x04000400u)) & 0x80008000u) != 0u;
+// Scales from here on are large: 2^13 (2^9 at 8 bits), below which 7 (127) of them stay under binary16's 65504.
+template <int BITS>
+constexpr uint32_t kLargeScale = BITS == 4 ? 0x7000u : 0x6000u;
+
+// The largest bits of pairs of scales, and whether one of a pair is out of the ordinary: large, infinite or NaN (no
+// scale has a sign).
+__device__ __forceinline__ u16x2 most(uint32_t a, uint32_t b) { return __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)); }
+template <int BITS>
+__device__ __forceinline__ bool odd_scales(u16x2 m) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(m, (u16x2)(uint16_t)(kLargeScale<BITS> - 1u))) != 0u;
 }
+// Takes the scales times 2^-7 if one of the wavefront's is large (and finite): what is made of them is then 2^-7 of what it
+// stands for.  A scale in the same 16 tokens as a large one is then off by up to 2^-18, at most 2^-27 of the large one.
+template <int BITS>
+__device__ __forceinline__ bool shrink(uint32_t s[2]) {
+  bool large = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = (s[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
+    large |= h >= kLargeScale<BITS> && h < 0x7C00u;
+  }
+  if (!__builtin_amdgcn_ballot_w64(large)) return false;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) s[i] = u2(h2(s[i]) * (f16x2){(_Float16)0x1p-7f, (_Float16)0x1p-7f});
+  return true;
+}
+constexpr float kShrunk = 128.0f;
 // Which of the lane's four value scales are NaN or infinite (bit r: token 4b + r).
 __device__ __forceinline__ uint32_t bad_scales(const uint32_t vs[2]) {
   uint32_t bad = 0;
@@ -377,7 +398,7 @@ __device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K
   top = fmaxf(top, lane_xor<1>(top));
   int e = 0;
   if (top > 0.0f && __builtin_isfinite(top)) e = 15 - __builtin_amdgcn_frexp_expf(top);
-  e = e < 120 ? e : 120;  // the factor unit 2^-e stays normal: a masked score (-inf times it) is never NaN
+  e = e < 120 ? e : 120;  // the factor 2^-e stays normal: a masked score (-inf times it) is never NaN
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t g = (kappa >> 2) + 4u * (i >> 1), c = 2u * (kappa & 3u) + (i & 1);
@@ -387,14 +408,14 @@ __device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K
     hi[at] = vh;
     if (lo) lo[at] = (_Float16)(v - (float)vh);
   }
-  return __builtin_ldexpf(unit<BITS>(), -e);
+  return __builtin_ldexpf(1.0f, -e);
 }
 
-// Turns a row's sum_t p_t code Delta (the lane's group, y[8], over unit) back and stores the row.
+// Turns a row's sum_t p_t code Delta (the lane's group, y[8]) back and stores the row.
 template <int BITS>
 __device__ __forceinline__ void store_row(const AttendArgs& a, const Tables& K, const float* lam, const Seq& s, uint32_t h, uint32_t r, uint32_t l,
                                           const LaneInverse& f, float y[8], float sum) {
-  const float inv = sum == 0.0f ? 0.0f : unit<BITS>() / sum;  // a row that sees nothing is 0
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row that sees nothing is 0
   float x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -523,14 +544,24 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
       load(t + kStep, pg0, nxt[0]);
       load(t + kStep + 16, pg1, nxt[1]);
     }
+    uint32_t large = 0;  // bit u: shrunk keys, bit 2 + u: shrunk values
     float sc[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      if (__builtin_amdgcn_ballot_w64(odd_scales<BITS>(most(cur[u].ks[0], cur[u].ks[1])))) {
+        const int32_t tok = t + 16 * u + (int32_t)n;
+        if (!there[u] || tok < lo || tok >= t1) cur[u].ks[0] = cur[u].ks[1] = 0u;  // a token that no row sees may hold anything
+        if (shrink<BITS>(cur[u].ks)) large |= 1u << u;
+      }
       f16x8 kh[4], kl[4];
       key_operands<BITS, PREC>(cur[u], kh, kl);
       const f32x4 r = scores16<PREC>(kh, kl, qh, ql);
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[4 * u + i] = r[i] * qf;
+    }
+    if (large & 3u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sc[i] *= (large >> (i >> 2)) & 1u ? kShrunk : 1.0f;
     }
     cap_scores<8>(a, sc);
     if (!(there[0] && there[1] && t >= all_lo && t + 32 <= all_hi && t + 32 <= t1)) {
@@ -538,8 +569,6 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
       for (int i = 0; i < 8; ++i) {
         const int32_t tok = t + 16 * (i >> 2) + 4 * (int32_t)b4 + (i & 3);
         if (!there[i >> 2] || tok < row_lo || tok >= row_hi || tok >= t1) sc[i] = -__builtin_inff();
-        // a token that no row sees may hold anything
-        if (!there[i >> 2] || tok < lo || tok >= t1) drop_scales(cur[i >> 2].vs, 1u << (i & 3));
       }
     }
     if (a.scores && n < rows) {
@@ -550,18 +579,26 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
     }
     // A value vector with NaN scales makes the rows that see it NaN and no other (0 NaN in the product
     // would reach every row): its scales count as 0, and the rows are poisoned.
-    if (__builtin_amdgcn_ballot_w64(any_bad(cur[0].vs) || any_bad(cur[1].vs))) {
-      const uint32_t bad = bad_scales(cur[0].vs) | bad_scales(cur[1].vs) << 4;
+    if (__builtin_amdgcn_ballot_w64(odd_scales<BITS>(__builtin_elementwise_max(most(cur[0].vs[0], cur[0].vs[1]), most(cur[1].vs[0], cur[1].vs[1]))))) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if ((bad >> i) & 1u && sc[i] != -__builtin_inff()) poison = __builtin_nanf("");
-      drop_scales(cur[0].vs, bad & 15u);
-      drop_scales(cur[1].vs, bad >> 4);
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t bad = bad_scales(cur[u].vs);
+        uint32_t drop = bad;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t tok = t + 16 * u + 4 * (int32_t)b4 + i;
+          if (!there[u] || tok < lo || tok >= t1) drop |= 1u << i;  // as with the keys
+          if ((bad >> i) & 1u && sc[4 * u + i] != -__builtin_inff()) poison = __builtin_nanf("");
+        }
+        drop_scales(cur[u].vs, drop);
+        if (shrink<BITS>(cur[u].vs)) large |= 4u << u;
+      }
     }
     float top = sc[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[i]);
-    if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+    // with shrunk values, P goes up to 2^15 against the maximum itself
+    if (large >= 4u || __builtin_amdgcn_ballot_w64(top > m + kSlack)) {
       const float mn = fmaxf(m, blocks_max(top));
       const float f = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
@@ -576,6 +613,11 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
       const float p0 = __builtin_amdgcn_exp2f(sc[2 * i] - base), p1 = __builtin_amdgcn_exp2f(sc[2 * i + 1] - base);
       sum += p0 + p1;
       pf.v[i] = u2((f16x2){(_Float16)p0, (_Float16)p1});
+    }
+    if (large >= 4u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((large >> (2 + (i >> 1))) & 1u) pf.v[i] = u2(h2(pf.v[i]) * (f16x2){(_Float16)kShrunk, (_Float16)kShrunk});
     }
     uint32_t v0[8][2], v1[8][2];
     value_operands<BITS>(cur[0], v0);
@@ -768,7 +810,7 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
   extern __shared__ __align__(16) uint8_t raw[];
   Stage<PREC>* st = reinterpret_cast<Stage<PREC>*>(raw);
   float(*s_o)[16][kPad] = reinterpret_cast<float(*)[16][kPad]>(raw);  // [wavefront], after the last product
-  __shared__ uint32_t s_flags[PREC ? 1 : 2][kManyWaves];  // bits 0..15: tokens with NaN value scales; bit 16: absent
+  __shared__ uint32_t s_flags[PREC ? 1 : 2][kManyWaves];  // bits 0..15: tokens with NaN value scales; 16: absent; 17, 18: shrunk keys, values
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
   // the last tiles see the most tokens under the causal mask: they go first
   const uint32_t split = blockIdx.x % a.splits, item = gridDim.x / a.splits - 1u - blockIdx.x / a.splits;
@@ -798,6 +840,12 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
   };
   // this wavefront's 16 tokens at t, as operands
   auto stage = [&](Stage<PREC>& d, uint32_t* flags, int32_t t, int32_t page) __attribute__((always_inline)) {
+    uint32_t word = page < 0 ? 0x10000u : 0u;
+    if (__builtin_amdgcn_ballot_w64(odd_scales<BITS>(most(sh.ks[0], sh.ks[1])))) {
+      const int32_t tok = t + (int32_t)n;
+      if (page < 0 || tok < lo || tok >= t1) sh.ks[0] = sh.ks[1] = 0u;  // a token that no row sees may hold anything
+      if (shrink<BITS>(sh.ks)) word |= 0x20000u;
+    }
     f16x8 kh[4], kl[4];
     key_operands<BITS, PREC>(sh, kh, kl);
 #pragma unroll
@@ -805,15 +853,12 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
       d.k[0][wave][j][lane] = kh[j];
       if (PREC) d.k[PREC ? 1 : 0][wave][j][lane] = kl[j];
     }
-    if (page < 0 || t < lo || t + 16 > t1) {  // a token that no row sees may hold anything
+    if (__builtin_amdgcn_ballot_w64(odd_scales<BITS>(most(sh.vs[0], sh.vs[1])))) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int32_t tok = t + 4 * (int32_t)b4 + i;
         if (page < 0 || tok < lo || tok >= t1) drop_scales(sh.vs, 1u << i);
       }
-    }
-    uint32_t word = page < 0 ? 0x10000u : 0u;
-    if (__builtin_amdgcn_ballot_w64(any_bad(sh.vs))) {
       const uint32_t bad = bad_scales(sh.vs);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -822,8 +867,8 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
         for (int q = 0; q < 4; ++q) word |= (votes >> (16 * q)) & 0xFFFFu ? 1u << (4 * q + i) : 0u;
       }
       // a value vector with one NaN scale is NaN as a whole: its rows are poisoned, its scales count as 0
-      uint32_t mine = (word >> (4 * b4)) & 15u;
-      drop_scales(sh.vs, mine);
+      drop_scales(sh.vs, (word >> (4 * b4)) & 15u);
+      if (shrink<BITS>(sh.vs)) word |= 0x40000u;
     }
     if (lane == 0) flags[wave] = word;
     uint32_t v[8][2];
@@ -977,7 +1022,17 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
           for (int q = 0; q < R; ++q) sc[q][u] = mfma(kh, qh[q][j], sc[q][u]);
         }
       }
+      auto unshrink = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float k = s_flags[buf][2 * w + u] & 0x20000u ? kShrunk : 1.0f;
+#pragma unroll
+          for (int q = 0; q < R; ++q) sc[q][u] *= k;
+        }
+      };
+      uint32_t large = 0;  // blocks of shrunk values
       if (cap) {
+        if (flagged >> (2 * w) & 3u) unshrink();
 #pragma unroll
         for (int q = 0; q < R; ++q)
 #pragma unroll
@@ -987,6 +1042,8 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
       }
       if ((flagged >> (2 * w) & 3u) || tw < all_lo || tw + 32 > all_hi || tw + 32 > t1) {
         const uint32_t fl0 = s_flags[buf][2 * w], fl1 = s_flags[buf][2 * w + 1];
+        large = (uint32_t)__builtin_amdgcn_readfirstlane((int)((fl0 >> 18 & 1u) | (fl1 >> 18 & 1u) << 1));
+        if (!cap) unshrink();
 #pragma unroll
         for (int q = 0; q < R; ++q)
 #pragma unroll
@@ -1009,7 +1066,8 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
         top[q] *= eff[q];
         rise |= top[q] > m[q] + kSlack;
       }
-      if (__builtin_amdgcn_ballot_w64(rise)) raise(top);
+      // with shrunk values, P goes up to 2^15 against the maximum itself
+      if (large || __builtin_amdgcn_ballot_w64(rise)) raise(top);
       f16x8 pf[R];
 #pragma unroll
       for (int q = 0; q < R; ++q) {
@@ -1026,6 +1084,12 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
         pf[q] = frag(p);
         // the sum of the rounded P, the one the output is weighted with, is one more product
         if (!PREC) ones[q] = mfma((f16x8)(_Float16)1.0f, pf[q], ones[q]);
+      }
+      if (large) {
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pf[q][i] *= (large >> (i >> 2)) & 1u ? (_Float16)kShrunk : (_Float16)1.0f;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -1105,12 +1169,18 @@ __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a
   const uint64_t page_size = (uint64_t)P * Page<BITS>::kToken;
   f16x8 kh[4][4], kl[4][4];
   uint32_t absent = 0;  // blocks of 16 tokens without a page
+  float factor[4];      // undoes a block's shrunk keys
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int32_t page = page_of(a, b, t + 16 * u, s.n);
     absent |= page < 0 ? 1u << u : 0u;
+    factor[u] = 1.0f;
     Share<BITS> sh;
     load_keys<BITS>(a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + h) * page_size, P, (uint32_t)(t + 16 * u) & (P - 1u), lane, sh);
+    if (__builtin_amdgcn_ballot_w64(odd_scales<BITS>(most(sh.ks[0], sh.ks[1])))) {
+      if (page < 0 || t + 16 * u + (int32_t)n >= s.n) sh.ks[0] = sh.ks[1] = 0u;
+      if (shrink<BITS>(sh.ks)) factor[u] = kShrunk;
+    }
     key_operands<BITS, true>(sh, kh[u], kl[u]);
   }
   float acc[16];
@@ -1167,7 +1237,7 @@ __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a
       for (int u = 0; u < 4; ++u) raw[u] = mfma(kh[u][j], oh[j], raw[u]);
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sc[i] = raw[i >> 2][i & 3] * f;
+    for (int i = 0; i < 16; ++i) sc[i] = raw[i >> 2][i & 3] * (f * factor[i >> 2]);
     cap_scores<16>(a, sc);
     if (!absent && t >= all_lo && t + 64 <= all_hi) {
 #pragma unroll

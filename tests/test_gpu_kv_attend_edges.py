@@ -1,4 +1,5 @@
-"""GPU: attention over the paged SRFT cache at the edges of what a call may ask: fewer queries computed than a sequence has.
+"""GPU: attention over the paged SRFT cache at the edges of what a call may ask: fewer queries computed than a sequence has,
+small and large cached values.
 
 Bounds are kv_reference.attend's; cases are those of test_gpu_kv_attend."""
 import numpy as np
@@ -54,3 +55,66 @@ def test_fewer_queries_than_a_sequence_has(orc, lens, q_lens, group, max_q, kw):
     got = host(w).astype(np.float64)
     top = ww.shape[2]
     assert (np.abs(got[..., :top] - ww) <= wtol + 2.0 ** -23 * ww).all() and not got[..., top:].any()
+
+
+class Scaled(Case):
+    """A case whose keys and values are taken times `k` and `v` (numbers, or one per slot), with the scores' scale undoing
+    the largest of `k`."""
+
+    def __init__(self, orc, *a, k, v, **kw):
+        super().__init__(orc, *a, **kw)
+        slots = torch.arange(self.cache.shape[0] * kw.get("page", 16), device="cuda")
+        old = hq.hq_kv_read(self.cache, slots, out_dtype=torch.float32, **self.fmt)
+        new = [x * dev(np.full(slots.shape, f, np.float32))[:, None, None] for x, f in zip(old, (k, v))]
+        hq.hq_kv_append(self.cache, *new, slots, **self.fmt)
+        self.scale = float(128 ** -0.5 / np.max(k))
+
+
+SHAPES = {"single": dict(lens=[300, 77], q_lens=[1, 1], group=4), "many": dict(lens=[150, 200], q_lens=[40, 33], group=2),
+          "tile_256": dict(lens=[300, 40], q_lens=[130, 1], heads=1, group=2, page=32)}
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("size", [1e-1, 1e-2, 1e-3, 1e-4, 1e-5])
+def test_small_values(orc, size, bits, shape):
+    """Operands are off by half a step of binary16 however small the cached vectors are: the bounds are those of unit ones."""
+    say(f"case: attend over values of {size}, {bits} bits, {shape}")
+    Scaled(orc, bits=bits, k=size, v=size, **SHAPES[shape]).check()
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("which", ["keys", "values", "both", "some"])
+def test_large_values(orc, which, bits, shape):
+    """Scales up to the largest there are (65504), everywhere or at one token in ten: nothing overflows, bounds as ever."""
+    say(f"case: attend over large {which}, {bits} bits, {shape}")
+    page = SHAPES[shape].get("page", 16)
+    slots = (sum(-(-n // page) for n in SHAPES[shape]["lens"]) + 2) * page
+    g = np.random.default_rng(5)
+    some = [np.where(g.random(slots) < 0.1, 1e7, 1.0) for _ in range(2)]
+    k, v = {"keys": (1e7, 1), "values": (1, 1e7), "both": (1e7, 1e7), "some": some}[which]
+    c = Scaled(orc, bits=bits, k=k, v=v, **SHAPES[shape])
+    _, ks, _, vs = ref.parts(host(c.cache), bits)
+    assert max(ks.max(), vs.max()) == 65504
+    c.check()
+    c.kw["softcap"] = 20.0
+    c.check()
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_large_scales_past_a_length(orc, shape):
+    """What lies past a length in its last page, the largest scales there are, leaves small values before it as exact."""
+    say(f"case: attend beside stale large scales, {shape}")
+    c = Scaled(orc, bits=8, k=1e-4, v=1e-4, **SHAPES[shape])
+    w = [torch.zeros(len(c.lens), c.cache.shape[1], max(c.lens), device="cuda") for _ in range(2)]
+    want = c.run(), c.run(weights=w[0])
+    stale = host(c.cache)
+    _, ks, vc, vs = ref.parts(stale, 8)
+    page = ks.shape[2]
+    for b, n in enumerate(c.lens):
+        for t in range(n, -(-n // page) * page):
+            pg = c.table[b, t // page]
+            ks.view(np.uint16)[pg, :, t % page] = vs.view(np.uint16)[pg, :, t % page // 4, :, t % page % 4] = 0x7BFF
+    c.cache = dev(stale)
+    assert torch.equal(c.run(), want[0]) and torch.equal(c.run(weights=w[1]), want[1]) and torch.equal(*w)
