@@ -352,7 +352,8 @@ typedef struct {
   uint32_t seqs;
   uint32_t max_q;           /* most queries of a sequence; further ones count in m but are not computed     */
   uint32_t max_len;         /* most tokens of a sequence; a larger length counts as this                    */
-  const int32_t *q_start;   /* DEVICE, seqs + 1 query offsets; NULL: total_q / seqs queries each            */
+  const int32_t *q_start;   /* DEVICE, seqs + 1 query offsets that do not decrease (cut to [0, total_q]);
+                               NULL: total_q / seqs queries each                                            */
   const int32_t *table;     /* DEVICE, [seqs][table_width]                                                  */
   uint32_t table_width;
   const int32_t *lens;      /* DEVICE, [seqs]; a negative length counts as 0                                */
@@ -364,14 +365,16 @@ typedef struct {
   uint64_t weights_stride;  /* at least max_len                                                             */
 } hq_kv_attend_args;
 
-/* Workspace bytes of hq_kv_attend for these sizes (host only; pointers are not read).  The workspace
- * needs no initialisation, is 256-byte aligned, and serves one call in flight. */
+/* Workspace bytes of hq_kv_attend for these sizes (host only; pointers are not read; the errors are
+ * hq_kv_attend's).  About 264 bytes a row of total_q x q_heads (520 with weights; none where no sequence
+ * has more than 16 rows a KV head), and up to 300 MB for the outputs of split tiles.  The workspace needs no
+ * initialisation, is 256-byte aligned, and serves one call in flight. */
 int hq_kv_attend_workspace_size(const hq_kv_cache *cache, const hq_kv_attend_args *args, size_t *bytes);
 
 /* HQ_ERR_INVALID_ARG: null or misaligned pointers, sizes outside their ranges, q_heads not a multiple of
  * heads, q_start == NULL with total_q not a multiple of seqs, a scale or softcap that is not finite, a
- * negative softcap, weights_stride < max_len, max_len over 2^30, a launch of 2^32 threads or more, or a
- * workspace that is too small.  Rows of `out` that no sequence's queries name are not written. */
+ * negative softcap, weights_stride < max_len, max_len over 2^30, a launch of 2^32 threads or more (2^28
+ * rows of queries and heads), or a workspace that is too small.  Rows of `out` that no sequence's queries name are not written. */
 int hq_kv_attend(const hq_kv_cache *cache, const hq_kv_attend_args *args, void *workspace,
                  size_t workspace_bytes, hq_stream_t stream);
 

@@ -49,18 +49,23 @@ struct AttendArgs {
   int64_t qt, qh;  // strides of q in values
   uint32_t heads, group, q_heads, pages, page_log2, width, seqs, max_q, max_len;
   uint32_t group_mul, group_shift;  // query_of
-  uint32_t tile_rows, tiles, splits, chunk, window;
-  uint32_t wrows, wpad;  // stored scores: rows of an item, tokens a row
+  // rows of a head: `rows` = total_q group of them, a sequence's from q0 group on, cut into tiles of tile_rows
+  uint32_t rows, tile_rows, window;
+  uint32_t lsplits, lchunk;     // splits of a light tile (of up to 16 rows, a sequence's last), tokens of each
+  uint32_t bound, parts, most;  // full tiles of a head, at most; split tiles there is room for; splits of a full tile, at most
+  uint32_t wrows, wpad;  // stored scores: rows of a (sequence, head), tokens a row
   int causal, q_f32, out_f32, vec;
-  int light;  // tiles of up to 16 rows are left to the few rows' kernel
+  int light;  // light tiles are left to the few rows' kernel
   float scale_log2, cap_in, cap_out;  // scores in log2 units; s = cap_out tanh(cap_in s) when cap_in > 0
-  // workspace; an item is a (sequence, head, tile of tile_rows rows)
-  _Float16 *qhi, *qlo;  // [items][tile_rows][128]
-  float* qf;            // [items][tile_rows] factor of a row's products
-  float* po;            // [items][splits][tile_rows][128]
-  float* pml;           // [items][splits][tile_rows][2]
-  float* lse;           // [items][tile_rows]
-  float* scores;        // [items][wrows][wpad]
+  // workspace
+  uint32_t* plan;       // full tiles of a head, their splits, tokens of each, sequences with a full tile (plan_tiles)
+  uint32_t* first;      // [seqs + 1] full tiles before a sequence
+  _Float16 *qhi, *qlo;  // [heads][rows][128]
+  float* qf;            // [heads][rows] factor of a row's products
+  float* lse;           // [heads][rows]
+  float *po, *pml;      // [full tiles][heads][splits][tile_rows], 128 and 2 values
+  float *lpo, *lpml;    // [seqs][heads][lsplits][16], the same of light tiles
+  float* scores;        // [seqs][heads][wrows][wpad]
 };
 
 // Query r / group of row r < 2^31: with 2^sh >= group > 2^(sh-1) and M = floor(2^(31+sh) / group) + 1 the product r M
@@ -345,11 +350,11 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // ---------------------------------------------------------------------------------------------
-// One query row, by the caller's 16 lanes: transformed, scaled by a power of two, in two binary16
-// parts in the operand's order, to hi[128] (and lo[128] unless null).  Returns the factor that turns the
+// Row `r` of head h (zeros unless `have`), by the caller's 16 lanes: transformed, scaled by a power of two, in two
+// binary16 parts in the operand's order, to hi[128] (and lo[128] unless null).  Returns the factor that turns the
 // row's products into scores.
 template <int BITS>
-__device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K, const float* lam, const Seq& s, uint32_t h, uint32_t r, uint32_t l,
+__device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K, const float* lam, uint32_t h, uint32_t r, bool have, uint32_t l,
                                             const LaneForward& f, _Float16* hi, _Float16* lo) {
   const uint32_t kappa = rev4(l);
   float m[8], x[8], y[8];
@@ -365,9 +370,9 @@ __device__ __forceinline__ float rotate_row(const AttendArgs& a, const Tables& K
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-  if (r < (uint32_t)s.m * a.group) {
+  if (have) {
     const uint32_t i = query_of(a, r);
-    const int64_t at = (s.q0 + i) * a.qt + (int64_t)(h * a.group + r - i * a.group) * a.qh + 8 * l;
+    const int64_t at = (int64_t)i * a.qt + (int64_t)(h * a.group + r - i * a.group) * a.qh + 8 * l;
     if (a.q_f32) {
       const float* p = static_cast<const float*>(a.q) + at;
 #pragma unroll
@@ -434,16 +439,29 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, const Tables& K, 
   }
 }
 
-struct Item {
-  uint32_t tile, h, b;
-};
-__device__ __forceinline__ Item item_of(const AttendArgs& a, uint32_t item) {
-  Item i;
-  i.tile = item % a.tiles;
-  item /= a.tiles;
-  i.h = item % a.heads;
-  i.b = item / a.heads;
-  return i;
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
+
+// Where row r of a sequence lies among its head's, in [heads][rows].
+__device__ __forceinline__ uint64_t row_at(const AttendArgs& a, const Seq& s, uint32_t h, uint32_t r) {
+  return (uint64_t)h * a.rows + (uint64_t)s.q0 * a.group + r;
+}
+// The last tile of a sequence: its first row.
+__device__ __forceinline__ uint32_t last_tile(const AttendArgs& a, const Seq& s) {
+  const uint32_t rows = (uint32_t)s.m * a.group;
+  return rows ? (rows - 1u) / a.tile_rows * a.tile_rows : 0u;
+}
+
+// The sequence of full tile f: the last whose tiles begin at or before it.  A wavefront looks at 64 places at a time.
+__device__ __forceinline__ uint32_t seq_with(const AttendArgs& a, uint32_t f) {
+  uint32_t b = 0, count = a.seqs;
+  while (count > 1u) {
+    const uint32_t step = (count + 63u) / 64u, i = (threadIdx.x & 63u) * step;
+    const bool here = i < count && a.first[b + i] <= f;
+    const uint32_t skip = ((uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(here)) - 1u) * step;
+    b += skip;
+    count = count - skip < step ? count - skip : step;
+  }
+  return b;
 }
 
 // The table's entry for token tt (-1 past `end`), the same in every lane; and the page it names (-1: absent).  Two
@@ -473,43 +491,41 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
   __shared__ __align__(16) _Float16 s_q[PREC ? 2 : 1][16][kD + 8];
   __shared__ float s_f[16], s_m[kAttWaves][16], s_l[kAttWaves][16], s_lam[2][kD];
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
-  const uint32_t split = blockIdx.x % a.splits, item = blockIdx.x / a.splits;
-  const Item it = item_of(a, item);
-  const Seq s = seq_of(a, it.b);
-  const uint32_t r0 = it.tile * a.tile_rows, all = (uint32_t)s.m * a.group;
-  if (a.tile_rows != 16 && (r0 >= all || all - r0 > 16u)) return;
-  const uint32_t rows = all - r0;  // of this tile
+  const uint32_t split = blockIdx.x % a.lsplits, item = blockIdx.x / a.lsplits, h = item % a.heads, b = item / a.heads;
+  const Seq s = seq_of(a, b);
+  const uint32_t r0 = last_tile(a, s), rows = (uint32_t)s.m * a.group - r0;  // of this tile
+  if (rows == 0 || rows > 16u) return;
   int32_t lo, hi;
   rows_range(a, s, r0, 16, &lo, &hi);
-  int32_t t0 = (int32_t)(split * a.chunk), t1 = t0 + (int32_t)a.chunk;
+  int32_t t0 = (int32_t)(split * a.lchunk), t1 = t0 + (int32_t)a.lchunk;
   t0 = t0 > (lo & ~15) ? t0 : lo & ~15;
   t1 = t1 < hi ? t1 : hi;
   if (a.pages == 0) t1 = t0;
-  if (t0 >= t1 && a.splits > 1) return;  // the same for the whole workgroup
+  if (t0 >= t1 && a.lsplits > 1) return;  // the same for the whole workgroup
   const uint32_t P = 1u << a.page_log2;
   const uint64_t page_size = (uint64_t)P * Page<BITS>::kToken;
 
   Share<BITS> cur[2], nxt[2];
   auto load = [&](int32_t t, int32_t page, Share<BITS>& sh) __attribute__((always_inline)) {
     // an absent page's place is taken by page 0, masked below
-    const uint8_t* p = a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + it.h) * page_size;
+    const uint8_t* p = a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + h) * page_size;
     load_keys<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
     load_values<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
   };
   constexpr int32_t kStep = 32 * kAttWaves;
   int32_t t = t0 + 32 * (int32_t)wave;
-  int32_t pg0 = page_of(a, it.b, t, t1), pg1 = page_of(a, it.b, t + 16, t1);
+  int32_t pg0 = page_of(a, b, t, t1), pg1 = page_of(a, b, t + 16, t1);
   if (t < t1) {
     load(t, pg0, cur[0]);
     load(t + 16, pg1, cur[1]);
   }
-  int32_t en0 = entry_of(a, it.b, t + kStep, t1), en1 = entry_of(a, it.b, t + kStep + 16, t1);
+  int32_t en0 = entry_of(a, b, t + kStep, t1), en1 = entry_of(a, b, t + kStep + 16, t1);
 
   stage_tables(K, s_lam);
   {  // the rows: four to a wavefront, 16 lanes each
     const uint32_t r = threadIdx.x >> 4;
     float f = 0.0f;
-    if ((r & ~3u) < rows) f = rotate_row<BITS>(a, K, s_lam[0], s, it.h, r0 + r, n, lane_forward(K, n), s_q[0][r], PREC ? s_q[PREC ? 1 : 0][r] : nullptr);
+    if ((r & ~3u) < rows) f = rotate_row<BITS>(a, K, s_lam[0], h, (uint32_t)s.q0 * a.group + r0 + r, r < rows, n, lane_forward(K, n), s_q[0][r], PREC ? s_q[PREC ? 1 : 0][r] : nullptr);
     else
       for (int i = 0; i < 8; ++i) {
         s_q[0][r][8 * n + i] = (_Float16)0.0f;
@@ -538,8 +554,8 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
     const bool there[2] = {pg0 >= 0, pg1 >= 0};
     pg0 = page_in(a, en0);
     pg1 = page_in(a, en1);
-    en0 = entry_of(a, it.b, t + 2 * kStep, t1);
-    en1 = entry_of(a, it.b, t + 2 * kStep + 16, t1);
+    en0 = entry_of(a, b, t + 2 * kStep, t1);
+    en1 = entry_of(a, b, t + 2 * kStep + 16, t1);
     if (t + kStep < t1) {
       load(t + kStep, pg0, nxt[0]);
       load(t + kStep + 16, pg1, nxt[1]);
@@ -665,41 +681,51 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
   for (int w = 1; w < kAttWaves; ++w)
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] += s_o[w][r][8 * n + i];
-  if (a.splits == 1) {
-    if (n == 0) a.lse[(uint64_t)item * a.tile_rows + r] = mr + __builtin_amdgcn_logf(total) - kPScaleLog2;
-    store_row<BITS>(a, K, s_lam[1], s, it.h, r0 + r, n, lane_inverse(K, n), y, total);
+  if (a.lsplits == 1) {
+    if (n == 0) a.lse[row_at(a, s, h, r0 + r)] = mr + __builtin_amdgcn_logf(total) - kPScaleLog2;
+    store_row<BITS>(a, K, s_lam[1], s, h, r0 + r, n, lane_inverse(K, n), y, total);
     return;
   }
-  const uint64_t p = ((uint64_t)item * a.splits + split) * a.tile_rows + r;
-  *reinterpret_cast<f32x4*>(a.po + p * kD + 8 * n) = (f32x4){y[0], y[1], y[2], y[3]};
-  *reinterpret_cast<f32x4*>(a.po + p * kD + 8 * n + 4) = (f32x4){y[4], y[5], y[6], y[7]};
-  if (n == 0) *reinterpret_cast<f32x2*>(a.pml + p * 2) = (f32x2){mr, total};
+  const uint64_t p = ((uint64_t)item * a.lsplits + split) * 16u + r;
+  *reinterpret_cast<f32x4*>(a.lpo + p * kD + 8 * n) = (f32x4){y[0], y[1], y[2], y[3]};
+  *reinterpret_cast<f32x4*>(a.lpo + p * kD + 8 * n + 4) = (f32x4){y[4], y[5], y[6], y[7]};
+  if (n == 0) *reinterpret_cast<f32x2*>(a.lpml + p * 2) = (f32x2){mr, total};
 }
 
 // Joins a row's splits, turns it back and stores it.  WIDE: one workgroup a row, its 16 groups of 16 lanes take
-// the splits in turn and join in LDS; otherwise 16 lanes take a row and all its splits.
-template <int BITS, bool WIDE>
-__global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables K, uint32_t rows_per_item, uint32_t all_rows) {
+// the splits in turn and join in LDS; otherwise 16 lanes take a row and all its splits.  LIGHT: the rows of light tiles,
+// else of full ones.
+template <int BITS, bool WIDE, bool LIGHT>
+__global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables K, uint32_t rows_per_tile, uint32_t all_rows) {
   __shared__ float s_y[WIDE ? 16 : 1][kD + 4], s_m[16], s_l[16];
   const uint32_t l = threadIdx.x & 15u, g = threadIdx.x >> 4;
   const uint32_t index = WIDE ? blockIdx.x : blockIdx.x * 16u + g;
-  if (!WIDE && index >= all_rows) return;
-  const uint32_t item = index / rows_per_item, row = index % rows_per_item;
-  const Item it = item_of(a, item);
-  const Seq s = seq_of(a, it.b);
-  const uint32_t r = it.tile * a.tile_rows + row;
-  if (r >= (uint32_t)s.m * a.group) return;
+  const uint32_t tile_rows = LIGHT ? 16u : a.tile_rows, splits = LIGHT ? a.lsplits : a.plan[1], chunk = LIGHT ? a.lchunk : a.plan[2];
+  const float *po = LIGHT ? a.lpo : a.po, *pml = LIGHT ? a.lpml : a.pml;
+  if (index >= all_rows) return;  // no part of a workgroup unless WIDE or LIGHT: tiles have 16 rows or a multiple
+  const uint32_t item = index / rows_per_tile, row = index % rows_per_tile, h = item % a.heads;
+  uint32_t b = item / a.heads, r0;
+  if (!LIGHT) {
+    if (splits == 1 || item >= a.plan[0] * a.heads) return;
+    const uint32_t f = b;
+    b = seq_with(a, f);
+    r0 = (f - a.first[b]) * tile_rows;
+  }
+  const Seq s = seq_of(a, b);
+  if (LIGHT) r0 = last_tile(a, s);
+  const uint32_t r = r0 + row, rows = (uint32_t)s.m * a.group;
+  if (r >= rows || (LIGHT && rows - r0 > 16u)) return;
   int32_t lo, hi;
-  rows_range(a, s, it.tile * a.tile_rows, a.tile_rows, &lo, &hi);
+  rows_range(a, s, r0, tile_rows, &lo, &hi);
   if (a.pages == 0) hi = lo;
-  const uint32_t s0 = hi > lo ? (uint32_t)lo / a.chunk : 0u, s1 = hi > lo ? ((uint32_t)hi + a.chunk - 1u) / a.chunk : 0u;
+  const uint32_t s0 = hi > lo ? (uint32_t)lo / chunk : 0u, s1 = hi > lo ? ((uint32_t)hi + chunk - 1u) / chunk : 0u;
   float m = -1.0e30f, sum = 0.0f, y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = 0.0f;
   for (uint32_t i = s0 + (WIDE ? g : 0u); i < s1; i += WIDE ? 16u : 1u) {
-    const uint64_t p = ((uint64_t)item * a.splits + i) * a.tile_rows + row;
-    const f32x2 ml = *reinterpret_cast<const f32x2*>(a.pml + p * 2);
-    const f32x4 u0 = *reinterpret_cast<const f32x4*>(a.po + p * kD + 8 * l), u1 = *reinterpret_cast<const f32x4*>(a.po + p * kD + 8 * l + 4);
+    const uint64_t p = ((uint64_t)item * splits + i) * tile_rows + row;
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(pml + p * 2);
+    const f32x4 u0 = *reinterpret_cast<const f32x4*>(po + p * kD + 8 * l), u1 = *reinterpret_cast<const f32x4*>(po + p * kD + 8 * l + 4);
     const float mn = fmaxf(m, ml[0]), f0 = __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(ml[0] - mn);
     m = mn;
     sum = sum * f0 + ml[1] * f1;
@@ -730,8 +756,8 @@ __global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables
       for (int c = 0; c < 8; ++c) y[c] += s_y[WIDE ? i : 0][8 * l + c] * f;
     }
   }
-  if (l == 0) a.lse[(uint64_t)item * a.tile_rows + row] = m + __builtin_amdgcn_logf(sum) - kPScaleLog2;
-  store_row<BITS>(a, K, K.v, s, it.h, r, l, lane_inverse(K, l), y, sum);
+  if (l == 0) a.lse[row_at(a, s, h, r)] = m + __builtin_amdgcn_logf(sum) - kPScaleLog2;
+  store_row<BITS>(a, K, K.v, s, h, r, l, lane_inverse(K, l), y, sum);
 }
 
 // Accumulated weights of up to 16 rows, from the stored scores: a thread owns a token.
@@ -746,37 +772,89 @@ __global__ __launch_bounds__(kAttBlock) void weights_few_kernel(AttendArgs a, ui
   float w = 0.0f;
   for (uint32_t r = 0; r < rows; ++r) {
     const float sc = a.scores[((uint64_t)bh * a.wrows + r) * a.wpad + (uint32_t)t];
-    if (sc != -__builtin_inff()) w += __builtin_amdgcn_exp2f(sc - a.lse[(uint64_t)bh * 16u + r]);
+    if (sc != -__builtin_inff()) w += __builtin_amdgcn_exp2f(sc - a.lse[row_at(a, s, bh % a.heads, r)]);
   }
   a.weights[(uint64_t)bh * a.wstride + (uint32_t)t] += w;
 }
 
 // ---------------------------------------------------------------------------------------------
-// Many rows: the queries' rows transformed once, to the workspace.  A workgroup takes `span` rows, 16 at a time: 64 where
-// that leaves four workgroups a CU, so that the twiddles are fetched once for four (262144 rows: 45 us, 53 us with
-// 16; a mixed batch of 2080 rows in 192 tiles: 13 us, 11.5 us with 16).
+// Many rows: which tiles there are, by one workgroup.  A sequence's tiles of tile_rows rows are full but for a light last
+// one; `first` counts them sequence after sequence, and the splits are what leaves `parts` of them in all.
+__device__ void plan_tiles(const AttendArgs& a) {
+  __shared__ uint32_t s_tiles[kAttWaves], s_seqs[kAttWaves];
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  uint32_t total = 0, some = 0;
+  for (uint32_t b0 = 0; b0 < a.seqs; b0 += kAttBlock) {
+    const uint32_t b = b0 + threadIdx.x;
+    uint32_t count = 0;
+    if (b < a.seqs) {
+      const uint32_t rows = (uint32_t)seq_of(a, b).m * a.group;
+      count = rows / a.tile_rows + (rows % a.tile_rows > (a.light ? 16u : 0u) ? 1u : 0u);
+    }
+    uint32_t sum = count;  // of this lane and those before it
+#pragma unroll
+    for (uint32_t d = 1; d < 64; d <<= 1) {
+      const uint32_t down = (uint32_t)__builtin_amdgcn_ds_bpermute((int)(((lane - d) & 63u) << 2), (int)sum);
+      if (lane >= d) sum += down;
+    }
+    if (lane == 63) s_tiles[wave] = sum;
+    const uint64_t votes = __builtin_amdgcn_ballot_w64(count > 0);
+    if (lane == 0) s_seqs[wave] = (uint32_t)__builtin_popcountll(votes);
+    __syncthreads();
+    uint32_t before = total, all = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kAttWaves; ++i) {
+      before += i < wave ? s_tiles[i] : 0u;
+      all += s_tiles[i];
+      some += s_seqs[i];
+    }
+    // no more than there is room for, whatever the offsets say
+    before += sum - count;
+    if (b < a.seqs) a.first[b] = before < a.bound ? before : a.bound;
+    total = total + all < a.bound ? total + all : a.bound;
+    __syncthreads();
+  }
+  if (threadIdx.x) return;
+  a.first[a.seqs] = total;
+  uint32_t splits = total ? a.parts / (total * a.heads) : 1u;
+  splits = splits < a.most ? splits : a.most;
+  if (splits < 1u) splits = 1u;
+  uint32_t chunk = ((a.max_len + splits - 1u) / splits + 127u) / 128u * 128u;
+  if (chunk == 0) chunk = 128u;
+  splits = (a.max_len + chunk - 1u) / chunk;
+  a.plan[0] = total;
+  a.plan[1] = splits ? splits : 1u;
+  a.plan[2] = chunk;
+  a.plan[3] = some;
+}
+
+// Many rows: the queries' rows transformed once, to the workspace; the first workgroup counts the tiles.  A workgroup
+// takes `span` rows of a head, 16 at a time: 64 where that leaves four workgroups a CU, so that the twiddles are fetched
+// once for four (262144 rows: 45 us, 53 us with 16; 16640 rows: 12 us with 64, 11.5 us with 16).
 template <int BITS>
 __global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Tables K, int parts, uint32_t span) {
   __shared__ __align__(16) _Float16 s_q[2][16][kD + 8];
   __shared__ float s_lam[2][kD];
+  if (blockIdx.x == 0) {
+    plan_tiles(a);
+    return;
+  }
   stage_tables(K, s_lam);
-  const uint32_t l = threadIdx.x & 15u, g = threadIdx.x >> 4, per = a.tile_rows / span;
-  const uint32_t item = blockIdx.x / per, first = (blockIdx.x % per) * span;
-  const Item it = item_of(a, item);
-  const Seq s = seq_of(a, it.b);
-  const uint32_t rows = (uint32_t)s.m * a.group, r0 = it.tile * a.tile_rows;
-  if (r0 + first >= rows) return;
+  const uint32_t l = threadIdx.x & 15u, g = threadIdx.x >> 4, per = (a.rows + span - 1u) / span;
+  const uint32_t h = (blockIdx.x - 1u) / per, begin = (blockIdx.x - 1u) % per * span;
   const LaneForward forward = lane_forward(K, l);
 #pragma unroll 1
-  for (uint32_t k = first; k < first + span && r0 + k < rows; k += 16u) {
+  for (uint32_t k = begin; k < begin + span && k < a.rows; k += 16u) {
     const uint32_t row = k + g;
-    const float f = rotate_row<BITS>(a, K, s_lam[0], s, it.h, r0 + row, l, forward, s_q[0][g], parts == 2 ? s_q[1][g] : nullptr);
-    const uint64_t at = (uint64_t)item * a.tile_rows + row;
-    if (l == 0) a.qf[at] = f;
+    const float f = rotate_row<BITS>(a, K, s_lam[0], h, row, row < a.rows, l, forward, s_q[0][g], parts == 2 ? s_q[1][g] : nullptr);
+    const uint64_t at = (uint64_t)h * a.rows + row;
     // a row is written and read by the same wavefront
     wave_sync();
-    *reinterpret_cast<f16x8*>(a.qhi + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[0][g][8 * l]);
-    if (parts == 2) *reinterpret_cast<f16x8*>(a.qlo + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[1][g][8 * l]);
+    if (row < a.rows) {
+      if (l == 0) a.qf[at] = f;
+      *reinterpret_cast<f16x8*>(a.qhi + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[0][g][8 * l]);
+      if (parts == 2) *reinterpret_cast<f16x8*>(a.qlo + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[1][g][8 * l]);
+    }
     wave_sync();
   }
 }
@@ -812,29 +890,44 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
   float(*s_o)[16][kPad] = reinterpret_cast<float(*)[16][kPad]>(raw);  // [wavefront], after the last product
   __shared__ uint32_t s_flags[PREC ? 1 : 2][kManyWaves];  // bits 0..15: tokens with NaN value scales; 16: absent; 17, 18: shrunk keys, values
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
-  // the last tiles see the most tokens under the causal mask: they go first
-  const uint32_t split = blockIdx.x % a.splits, item = gridDim.x / a.splits - 1u - blockIdx.x / a.splits;
-  const uint32_t bh = item % (a.seqs * a.heads);
-  const Item it = {item / (a.seqs * a.heads), bh % a.heads, bh / a.heads};
-  const uint64_t slot = (uint64_t)bh * a.tiles + it.tile;  // the item's place in the workspace
-  const Seq s = seq_of(a, it.b);
-  const uint32_t rows = (uint32_t)s.m * a.group, r0 = it.tile * a.tile_rows, w0 = r0 + wave * 16u * R;
-  if (r0 >= rows || (a.light && rows - r0 <= 16u)) return;
+  const uint32_t tiles = uniform(a.plan[0]), splits = uniform(a.plan[1]), chunk = uniform(a.plan[2]), items = tiles * a.heads;
+  if (blockIdx.x >= items * splits) return;
+  // The last tiles see the most tokens under the causal mask: they go first, those of all sequences in turn (of
+  // sequences with as many tiles each, all the last ones, then all the ones before).  The head changes fastest, so that
+  // with 8 heads an XCD reads one head's cache.
+  const uint32_t split = blockIdx.x % splits, order = items - 1u - blockIdx.x / splits, h = order % a.heads, seqs = uniform(a.plan[3]);
+  uint32_t f = order / a.heads;
+  if (f < tiles / seqs * seqs) f = f % seqs * (tiles / seqs) + f / seqs;
+  const uint32_t b = seq_with(a, f);
+  const Seq s = seq_of(a, b);
+  const uint32_t rows = (uint32_t)s.m * a.group, r0 = (f - a.first[b]) * a.tile_rows, w0 = r0 + wave * 16u * R;
+  if (r0 >= rows) return;
   int32_t lo, hi, wlo, whi, all_lo, all_hi;
   rows_range(a, s, r0, a.tile_rows, &lo, &hi);
   rows_range(a, s, w0, 16u * R, &wlo, &whi);
   rows_common(a, s, w0, 16u * R, &all_lo, &all_hi);
-  int32_t t0 = (int32_t)(split * a.chunk), t1 = t0 + (int32_t)a.chunk;
+  int32_t t0 = (int32_t)(split * chunk), t1 = t0 + (int32_t)chunk;
   t0 = t0 > (lo & ~15) ? t0 : lo & ~15;
   t1 = t1 < hi ? t1 : hi;
   if (a.pages == 0) t1 = t0;
-  if (t0 >= t1 && a.splits > 1) return;
+  if (t0 >= t1 && splits > 1) return;
+  // what the end of the kernel needs, out of the scalar registers meanwhile (a prompt of 8192 tokens: 680 us, 708 with
+  // these spilled)
+  __shared__ uint32_t s_keep[6];
+  if (threadIdx.x == 0) {
+    s_keep[0] = (uint32_t)s.q0;
+    s_keep[1] = (uint32_t)s.m;
+    s_keep[2] = h;
+    s_keep[3] = r0;
+    s_keep[4] = splits;
+    s_keep[5] = ((f * a.heads + h) * splits + split) * a.tile_rows;  // the tile's rows among the split outputs
+  }
   const uint32_t P = 1u << a.page_log2;
   const uint64_t page_size = (uint64_t)P * Page<BITS>::kToken;
 
   Share<BITS> sh;
   auto load = [&](int32_t t, int32_t page) __attribute__((always_inline)) {
-    const uint8_t* p = a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + it.h) * page_size;
+    const uint8_t* p = a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + h) * page_size;
     load_keys<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
     load_values<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
   };
@@ -878,9 +971,9 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
       reinterpret_cast<uint2*>(&d.v[wave >> 1][i][lane])[wave & 1u] = make_uint2(v[i][0], v[i][1]);
   };
   const int32_t mine = 16 * (int32_t)wave;
-  int32_t t = t0, page = page_of(a, it.b, t + mine, t1);
+  int32_t t = t0, page = page_of(a, b, t + mine, t1);
   if (t < t1) load(t + mine, page);
-  int32_t next = entry_of(a, it.b, t + kTok + mine, t1);
+  int32_t next = entry_of(a, b, t + kTok + mine, t1);
 
   const bool cap = a.cap_in > 0.0f;
   f16x8 qh[R][4], ql[R][4];
@@ -889,8 +982,8 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
   f32x4 o[R][8], ones[R];
 #pragma unroll
   for (int q = 0; q < R; ++q) {
-    const uint64_t row = slot * a.tile_rows + wave * 16u * R + 16u * q + n;
-    const bool have = w0 + 16u * q < rows;  // 16 rows are transformed together, the last ones as zeros
+    const uint64_t row = row_at(a, s, h, w0 + 16u * q + n);
+    const bool have = w0 + 16u * q < rows;  // the last 16 may have rows of the next sequence among them: they see nothing
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       qh[q][j] = ql[q][j] = (f16x8)(_Float16)0.0f;
@@ -934,7 +1027,7 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
     if (more) {
       page = page_in(a, next);
       load(t + kTok + mine, page);
-      next = entry_of(a, it.b, t + 2 * kTok + mine, t1);
+      next = entry_of(a, b, t + 2 * kTok + mine, t1);
     }
     const Stage<PREC>& d = st[buf];
     // blocks of 16 tokens with a flag, asked for once and not between the products
@@ -1106,6 +1199,11 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
   }
 
   // each wavefront's rows, 16 at a time, through its part of LDS: a row's values to 16 lanes
+  __syncthreads();
+  const Seq es = {(int64_t)uniform(s_keep[0]), (int32_t)uniform(s_keep[1]), 0, 0};
+  const uint32_t eh = uniform(s_keep[2]), erows = (uint32_t)es.m * a.group, ew = uniform(s_keep[3]) + wave * 16u * R;
+  const bool whole_tile = uniform(s_keep[4]) == 1u;
+  const uint32_t first_part = uniform(s_keep[5]) + wave * 16u * R;
   const LaneInverse inv = lane_inverse(K, n);
 #pragma unroll
   for (int q = 0; q < R; ++q) {
@@ -1116,25 +1214,24 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
       for (int i = 0; i < 8; i += 4)
         *reinterpret_cast<f32x4*>(&s_o[wave][n][8 * (4 * b4 + r) + i]) =
             (f32x4){o[q][i][r] + bad, o[q][i + 1][r] + bad, o[q][i + 2][r] + bad, o[q][i + 3][r] + bad};
-    const uint32_t first = wave * 16u * R + 16u * q;
-    const uint64_t row = slot * a.tile_rows + first;
-    if (b4 == 0) {
-      if (a.splits == 1) a.lse[row + n] = m[q] + __builtin_amdgcn_logf(total) - kPScaleLog2;
-      else *reinterpret_cast<f32x2*>(a.pml + (((slot * a.splits + split) * a.tile_rows) + first + n) * 2) = (f32x2){m[q], total};
+    const uint32_t part = first_part + 16u * q;
+    if (b4 == 0 && ew + 16u * q + n < erows) {
+      if (whole_tile) a.lse[row_at(a, es, eh, ew + 16u * q + n)] = m[q] + __builtin_amdgcn_logf(total) - kPScaleLog2;
+      else *reinterpret_cast<f32x2*>(a.pml + (uint64_t)(part + n) * 2) = (f32x2){m[q], total};
     }
     wave_sync();
 #pragma unroll 1
     for (uint32_t k = 0; k < 4; ++k) {
       const uint32_t r = 4u * k + b4;
-      if (w0 + 16u * q + 4u * k >= rows) break;
+      if (ew + 16u * q + 4u * k >= erows) break;
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = s_o[wave][r][8 * n + i];
       const float tr = row_get_any(total, r);
-      if (a.splits == 1) {
-        store_row<BITS>(a, K, K.v, s, it.h, w0 + 16u * q + r, n, inv, y, tr);
+      if (whole_tile) {
+        store_row<BITS>(a, K, K.v, es, eh, ew + 16u * q + r, n, inv, y, tr);
       } else {
-        float* d = a.po + ((slot * a.splits + split) * a.tile_rows + first + r) * kD + 8 * n;
+        float* d = a.po + (uint64_t)(part + r) * kD + 8 * n;
         *reinterpret_cast<f32x4*>(d) = (f32x4){y[0], y[1], y[2], y[3]};
         *reinterpret_cast<f32x4*>(d + 4) = (f32x4){y[4], y[5], y[6], y[7]};
       }
@@ -1187,7 +1284,7 @@ __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
   // a thread's share of 16 rows: group threadIdx mod 16 of row threadIdx / 16, in both parts
-  const uint64_t base = (uint64_t)bh * a.tiles * a.tile_rows;
+  const uint64_t base = row_at(a, s, h, 0);
   const uint32_t lr = threadIdx.x >> 4, lg = threadIdx.x & 15u;
   f16x8 qh, ql;
   float qf = 0.0f, lse = 0.0f;
@@ -1273,37 +1370,66 @@ namespace {
 
 uint64_t align256(uint64_t v) { return (v + 255u) & ~(uint64_t)255u; }
 
-// How a call is cut: rows a tile, row tiles, splits of the longest sequence, and the workspace they take.
+// How a call is cut, and the workspace it takes.
 struct Plan {
-  uint64_t items;
-  uint32_t tile_rows, tiles, splits, chunk, wrows, wpad;
-  uint64_t qhi, qlo, qf, po, pml, lse, scores, bytes;
+  uint32_t max_q, rows, tile_rows, bound, most, parts, grid, lsplits, lchunk, wrows, wpad;
+  bool few, light;
+  uint64_t plan, first, qhi, qlo, qf, lse, pml, po, lpml, lpo, scores, bytes;
 };
 
-Plan plan_of(const hq_kv_cache& c, const hq_kv_attend_args& g) {
+// HQ_OK, or an error for a call that the launches cannot take.
+int plan_of(const hq_kv_cache& c, const hq_kv_attend_args& g, Plan* out) {
   Plan p;
-  const uint32_t rows = g.max_q * (g.q_heads / c.heads);
+  const uint32_t group = g.q_heads / c.heads;
+  const uint64_t each = g.q_start || g.seqs == 0 ? g.total_q : g.total_q / g.seqs, sh = (uint64_t)g.seqs * c.heads;
+  p.max_q = (uint32_t)(each < g.max_q ? each : g.max_q);
+  // rows of a sequence, at most, and of a head
+  const uint64_t rows = (uint64_t)p.max_q * group, all = g.total_q * group;
+  if (all > 0x7FFFFF00ull || all * c.heads > kMaxThreads / 16) return HQ_ERR_INVALID_ARG;
+  p.rows = (uint32_t)all;
+  p.few = rows <= 16;
   // up to 16 rows: one tile, split over many workgroups; beyond, 16 rows a wavefront while that covers them,
   // then 32
-  p.tile_rows = rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
-  p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
-  p.items = (uint64_t)g.seqs * c.heads * p.tiles;
-  const bool few = rows <= 16;
-  // Workgroups to fill 256 CUs and to even out ragged lengths, each with enough tokens to be worth its start
-  // (about 5 us) and its part of the join.  Few rows: 2048 of at least 1024 tokens, or of 512 where that
+  p.tile_rows = p.few ? 16 : rows <= 128 ? 128 : 256;
+  const uint64_t last = rows % p.tile_rows;  // of equal sequences
+  p.light = !p.few && (g.q_start ? g.seqs > 1 : last > 0 && last <= 16);
+  // Light tiles (all tiles of few rows): workgroups to fill 256 CUs and to even out ragged lengths, each with enough
+  // tokens to be worth its start (about 5 us) and its part of the join: 2048 of at least 1024 tokens, or of 512 where that
   // leaves fewer than 512 (64 sequences of 4001 tokens: 59 us at 1024, 67 at 512; one of 32768: 31 and 30;
-  // one of 301: 14 us whole, 17 in two).  Many rows: 1536 of at least 512, unless the tiles alone are two a CU.
-  const uint64_t want = few ? 2048 : 1536, least = few && p.items * ((g.max_len + 1023) / 1024) >= 512 ? 1024 : 512;
-  uint64_t splits = p.items && (few || p.items < 512) ? (want + p.items - 1) / p.items : 1, most = (g.max_len + least - 1) / least;
-  if (splits > most) splits = most;
-  if (splits < 1) splits = 1;
-  uint64_t chunk = (g.max_len + splits - 1) / splits;
-  chunk = (chunk + 127) / 128 * 128;
-  if (chunk == 0) chunk = 128;
-  p.chunk = (uint32_t)chunk;
-  p.splits = (uint32_t)((g.max_len + chunk - 1) / chunk);
-  if (p.splits == 0) p.splits = 1;
-  p.wrows = few && g.weights ? rows : 0;
+  // one of 301: 14 us whole, 17 in two).
+  auto cut = [&](uint64_t splits, uint64_t least, uint32_t* chunk) {
+    const uint64_t most = (g.max_len + least - 1) / least;
+    if (splits > most) splits = most;
+    if (splits < 1) splits = 1;
+    *chunk = (uint32_t)(((g.max_len + splits - 1) / splits + 127) / 128 * 128);
+    if (*chunk == 0) *chunk = 128;
+    const uint32_t n = (g.max_len + *chunk - 1) / *chunk;
+    return n ? n : 1u;
+  };
+  p.lsplits = p.few || p.light ? cut(sh ? (2048 + sh - 1) / sh : 1, sh * ((g.max_len + 1023) / 1024) >= 512 ? 1024 : 512, &p.lchunk) : 1;
+  // Full tiles of a head: what the rows fill, and each sequence's last if it is not light.  Their number is known on the
+  // device (plan_tiles), which splits them over what workgroups and split outputs there are: 1536 of at least 512 tokens,
+  // unless the tiles are two a CU as they stand.  Where half of them or more may not exist, because many sequences share few
+  // rows, 512 of 256 rows or 1024 of 128: two rounds of the chip or more, and 68 MB.
+  const uint64_t odd = p.light ? all / 17 : all, tiles = (rows + p.tile_rows - 1) / p.tile_rows;
+  uint64_t bound = all / p.tile_rows + (odd < g.seqs ? odd : g.seqs), parts = 0;
+  if (tiles * g.seqs < bound) bound = tiles * g.seqs;
+  if (p.few) bound = 0;
+  const uint64_t items = bound * c.heads, filled = (all + p.tile_rows - 1) / p.tile_rows * c.heads;
+  p.most = (g.max_len + 511) / 512;
+  if (p.most > 1 && items) {
+    if (2 * filled <= items) parts = filled < 512 ? 512 * 256 / p.tile_rows : 0;
+    else if (items < 512) parts = items * ((1536 + items - 1) / items);
+    if (parts > items * p.most) parts = items * p.most;
+  }
+  const uint64_t grid = items > parts ? items : parts;
+  if (grid > kMaxThreads / kManyBlock || sh * p.lsplits > kMaxThreads / kAttBlock) return HQ_ERR_INVALID_ARG;
+  // the weights: a thread a token
+  if (g.weights && (sh + 7) * ((g.max_len + 255u) / 256u) > kMaxThreads / kAttBlock) return HQ_ERR_INVALID_ARG;
+  p.bound = (uint32_t)bound;
+  p.parts = (uint32_t)parts;
+  p.grid = (uint32_t)grid;
+  p.wrows = p.few && g.weights ? (uint32_t)rows : 0;
   p.wpad = (g.max_len + 31u) / 16u * 16u;  // whole blocks of 16 from any block's start
   uint64_t at = 0;
   auto take = [&](uint64_t n) {
@@ -1311,16 +1437,22 @@ Plan plan_of(const hq_kv_cache& c, const hq_kv_attend_args& g) {
     at = align256(at + n);
     return here;
   };
-  const uint64_t r = p.items * p.tile_rows, parts = p.splits > 1 ? r * p.splits : 0;
+  // 16 rows are read together from any row on
+  const uint64_t r = all * c.heads + 16, split = parts * p.tile_rows, lsplit = p.lsplits > 1 ? sh * p.lsplits * 16 : 0;
+  p.plan = take(p.few ? 0 : 16);
+  p.first = take(p.few ? 0 : ((uint64_t)g.seqs + 1) * 4);
   p.lse = take(r * 4);
-  p.qf = take(few ? 0 : r * 4);
-  p.qhi = take(few ? 0 : r * kD * 2);
-  p.qlo = take(few || !g.weights ? 0 : r * kD * 2);
-  p.pml = take(parts * 8);
-  p.po = take(parts * kD * 4);
-  p.scores = take(p.items * p.wrows * (uint64_t)p.wpad * 4);
+  p.qf = take(p.few ? 0 : r * 4);
+  p.qhi = take(p.few ? 0 : r * kD * 2);
+  p.qlo = take(p.few || !g.weights ? 0 : r * kD * 2);
+  p.pml = take(split * 8);
+  p.po = take(split * kD * 4);
+  p.lpml = take(lsplit * 8);
+  p.lpo = take(lsplit * kD * 4);
+  p.scores = take(p.wrows * sh * p.wpad * 4);
   p.bytes = at;
-  return p;
+  *out = p;
+  return HQ_OK;
 }
 
 template <int BITS, bool PREC, int R>
@@ -1333,38 +1465,42 @@ hipError_t launch_many(const AttendArgs& a, const Tables& T, uint32_t grid, hipS
   return hipSuccess;
 }
 
+// The join of split tiles.  A workgroup a row while those are at most 16 a CU, 16 lanes a row beyond: 64 rows of 12 splits
+// 5 us as one, 49152 rows of 3 splits 87 us against 14 us.
+template <int BITS, bool LIGHT>
+void launch_combine(const AttendArgs& a, const Tables& T, uint32_t tiles, uint32_t per, hipStream_t st) {
+  const dim3 block(kAttBlock);
+  if ((uint64_t)tiles * per <= 4096) hipLaunchKernelGGL((combine_kernel<BITS, true, LIGHT>), dim3(tiles * per), block, 0, st, a, T, per, tiles * per);
+  else hipLaunchKernelGGL((combine_kernel<BITS, false, LIGHT>), dim3((tiles * per + 15) / 16), block, 0, st, a, T, per, tiles * per);
+}
+
 template <int BITS>
-hipError_t launch_attend(const AttendArgs& a, const Tables& T, uint32_t items, hipStream_t st) {
+hipError_t launch_attend(const AttendArgs& a, const Tables& T, const Plan& p, hipStream_t st) {
   const dim3 block(kAttBlock);
   const bool prec = a.weights != nullptr;
-  const uint32_t grid = items * a.splits, rows = a.max_q * a.group;
-  if (a.tile_rows == 16) {
-    if (prec) hipLaunchKernelGGL((attend_few_kernel<BITS, true>), dim3(grid), block, 0, st, a, T);
-    else hipLaunchKernelGGL((attend_few_kernel<BITS, false>), dim3(grid), block, 0, st, a, T);
-  } else {
-    const uint32_t span = items * (a.tile_rows / 64) >= 1024 ? 64 : 16;
-    hipLaunchKernelGGL((rotate_rows_kernel<BITS>), dim3(items * (a.tile_rows / span)), block, 0, st, a, T, prec ? 2 : 1, span);
-    if (a.light) {
-      if (prec) hipLaunchKernelGGL((attend_few_kernel<BITS, true>), dim3(grid), block, 0, st, a, T);
-      else hipLaunchKernelGGL((attend_few_kernel<BITS, false>), dim3(grid), block, 0, st, a, T);
-    }
-    hipError_t e;
-    if (a.tile_rows == 128) e = prec ? launch_many<BITS, true, 1>(a, T, grid, st) : launch_many<BITS, false, 1>(a, T, grid, st);
-    else e = prec ? launch_many<BITS, true, 2>(a, T, grid, st) : launch_many<BITS, false, 2>(a, T, grid, st);
-    if (e != hipSuccess) return e;
+  const uint32_t sh = a.seqs * a.heads, rows = a.max_q * a.group;
+  if (!p.few) {
+    const uint32_t span = (uint64_t)a.rows * a.heads / 64 >= 1024 ? 64 : 16;
+    hipLaunchKernelGGL((rotate_rows_kernel<BITS>), dim3((a.rows + span - 1) / span * a.heads + 1), block, 0, st, a, T, prec ? 2 : 1, span);
   }
-  if (a.splits > 1) {
-    const uint32_t per = rows < a.tile_rows ? rows : a.tile_rows;
-    // a workgroup a row while those are at most 16 a CU, 16 lanes a row beyond: 64 rows of 12 splits 5 us as one,
-    // 49152 rows of 3 splits 87 us against 14 us
-    if (items * per <= 4096) hipLaunchKernelGGL((combine_kernel<BITS, true>), dim3(items * per), block, 0, st, a, T, per, items * per);
-    else hipLaunchKernelGGL((combine_kernel<BITS, false>), dim3((items * per + 15) / 16), block, 0, st, a, T, per, items * per);
+  if (p.few || p.light) {
+    const dim3 grid(sh * a.lsplits);
+    if (prec) hipLaunchKernelGGL((attend_few_kernel<BITS, true>), grid, block, 0, st, a, T);
+    else hipLaunchKernelGGL((attend_few_kernel<BITS, false>), grid, block, 0, st, a, T);
+    if (a.lsplits > 1) launch_combine<BITS, true>(a, T, sh, rows < 16 ? rows : 16, st);
+  }
+  if (p.grid) {
+    const hipError_t e = a.tile_rows == 128 ? prec ? launch_many<BITS, true, 1>(a, T, p.grid, st) : launch_many<BITS, false, 1>(a, T, p.grid, st)
+                                            : prec ? launch_many<BITS, true, 2>(a, T, p.grid, st) : launch_many<BITS, false, 2>(a, T, p.grid, st);
+    if (e != hipSuccess) return e;
+    // of split tiles there are half as many as parts
+    const uint32_t items = a.bound * a.heads, per = rows < a.tile_rows ? (rows + 15) / 16 * 16 : a.tile_rows;
+    if (a.parts) launch_combine<BITS, false>(a, T, items < a.parts / 2 ? items : a.parts / 2, per, st);
   }
   if (prec && a.max_len) {
-    const uint32_t step = a.tile_rows == 16 ? kAttBlock : 64u * kAttWaves, blocks = (a.max_len + step - 1) / step;
-    const uint32_t bh = a.seqs * a.heads;
-    if (a.tile_rows == 16) hipLaunchKernelGGL(weights_few_kernel, dim3(bh * blocks), block, 0, st, a, blocks);
-    else hipLaunchKernelGGL((weights_many_kernel<BITS>), dim3((bh + 7u) / 8u * 8u * blocks), block, 0, st, a, blocks);
+    const uint32_t blocks = (a.max_len + 255u) / 256u;  // of 256 tokens
+    if (p.few) hipLaunchKernelGGL(weights_few_kernel, dim3(sh * blocks), block, 0, st, a, blocks);
+    else hipLaunchKernelGGL((weights_many_kernel<BITS>), dim3((sh + 7u) / 8u * 8u * blocks), block, 0, st, a, blocks);
   }
   return hipGetLastError();
 }
@@ -1387,7 +1523,9 @@ extern "C" {
 int hq_kv_attend_workspace_size(const hq_kv_cache* cache, const hq_kv_attend_args* args, size_t* bytes) {
   if (!bytes) return HQ_ERR_INVALID_ARG;
   if (int rc = check_attend(cache, args)) return rc;
-  *bytes = plan_of(*cache, *args).bytes;
+  Plan p;
+  if (int rc = plan_of(*cache, *args, &p)) return rc;
+  *bytes = p.bytes;
   return HQ_OK;
 }
 
@@ -1405,12 +1543,9 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   const uint32_t size = g.q_dtype == HQ_F32 ? 4u : 2u;
   if (((uintptr_t)g.q & (size - 1u)) || ((uintptr_t)g.out & 15u)) return HQ_ERR_INVALID_ARG;
   if (((uintptr_t)g.lens | (uintptr_t)g.table | (uintptr_t)g.q_start | (uintptr_t)g.weights) & 3u) return HQ_ERR_INVALID_ARG;
-  const Plan p = plan_of(*cache, g);
+  Plan p;
+  if (int rc = plan_of(*cache, g, &p)) return rc;
   if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < p.bytes) return HQ_ERR_INVALID_ARG;
-  // every launch below 2^32 threads: workgroups of 256 and 512, a row's 16 lanes, a row's join
-  if (p.items * p.splits > kMaxThreads / kManyBlock || p.items * p.tile_rows > kMaxThreads / 16) return HQ_ERR_INVALID_ARG;
-  if (p.splits > 1 && p.items * p.tile_rows > kMaxThreads / kAttBlock) return HQ_ERR_INVALID_ARG;
-  if ((uint64_t)(g.seqs * cache->heads + 7u) * ((g.max_len + 255u) / 256u) > kMaxThreads / kAttBlock) return HQ_ERR_INVALID_ARG;
   AttendArgs a;
   a.cache = static_cast<const uint8_t*>(cache->data);
   a.q = g.q;
@@ -1434,17 +1569,19 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   a.page_log2 = 31u - (uint32_t)__builtin_clz(cache->page);
   a.width = g.table_width;
   a.seqs = g.seqs;
-  a.max_q = g.max_q;
+  a.max_q = p.max_q;
+  a.rows = p.rows;
   a.max_len = g.max_len;
   a.tile_rows = p.tile_rows;
-  a.tiles = p.tiles;
+  a.bound = p.bound;
+  a.parts = p.parts;
+  a.most = p.most;
+  a.lsplits = p.lsplits;
+  a.lchunk = p.lchunk;
+  a.light = p.light;
   a.wrows = p.wrows;
   a.wpad = p.wpad;
-  a.splits = p.splits;
-  a.chunk = p.chunk;
   a.window = g.window;
-  const uint64_t last = g.total_q / g.seqs * a.group % p.tile_rows;  // rows of the last tile of equal sequences
-  a.light = g.q_start ? g.seqs > 1 : last > 0 && last <= 16;
   a.causal = g.causal != 0;
   a.q_f32 = g.q_dtype == HQ_F32;
   a.out_f32 = g.out_dtype == HQ_F32;
@@ -1454,6 +1591,8 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   a.cap_in = g.softcap > 0.0f ? (float)(1.0 / (g.softcap * log2e)) : 0.0f;
   a.cap_out = (float)(g.softcap * log2e);
   char* w = static_cast<char*>(workspace);
+  a.plan = reinterpret_cast<uint32_t*>(w + p.plan);
+  a.first = reinterpret_cast<uint32_t*>(w + p.first);
   a.qhi = reinterpret_cast<_Float16*>(w + p.qhi);
   a.qlo = reinterpret_cast<_Float16*>(w + p.qlo);
   a.qf = reinterpret_cast<float*>(w + p.qf);
@@ -1461,8 +1600,10 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   a.pml = reinterpret_cast<float*>(w + p.pml);
   a.scores = p.wrows ? reinterpret_cast<float*>(w + p.scores) : nullptr;
   a.po = reinterpret_cast<float*>(w + p.po);
+  a.lpml = reinterpret_cast<float*>(w + p.lpml);
+  a.lpo = reinterpret_cast<float*>(w + p.lpo);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const hipError_t e = cache->bits == 4 ? launch_attend<4>(a, T, (uint32_t)p.items, st) : launch_attend<8>(a, T, (uint32_t)p.items, st);
+  const hipError_t e = cache->bits == 4 ? launch_attend<4>(a, T, p, st) : launch_attend<8>(a, T, p, st);
   return e == hipSuccess ? HQ_OK : HQ_ERR_HIP;
 }
 

@@ -1,5 +1,5 @@
 """GPU: attention over the paged SRFT cache at the edges of what a call may ask: fewer queries computed than a sequence has,
-small and large cached values.
+small and large cached values, batches that are mostly single tokens.
 
 Bounds are kv_reference.attend's; cases are those of test_gpu_kv_attend."""
 import numpy as np
@@ -118,3 +118,61 @@ def test_large_scales_past_a_length(orc, shape):
             ks.view(np.uint16)[pg, :, t % page] = vs.view(np.uint16)[pg, :, t % page // 4, :, t % page % 4] = 0x7BFF
     c.cache = dev(stale)
     assert torch.equal(c.run(), want[0]) and torch.equal(c.run(weights=w[1]), want[1]) and torch.equal(*w)
+
+
+def mixture(seed, seqs, long):
+    """Lengths and query counts of a continuous batch: mostly single tokens, some sequences idle, a few chunks."""
+    g = np.random.default_rng(seed)
+    m = g.choice([0, 1, 1, 1, 1, 5, 17, 40], seqs)
+    m[g.integers(seqs)] = long
+    lens = m + g.integers(0, 200, seqs)
+    lens[g.integers(seqs)] = 1400
+    return lens.tolist(), m.tolist()
+
+
+@pytest.mark.parametrize("seed,seqs,long,kw", [
+    (1, 9, 150, dict(heads=2, group=2)),
+    (2, 70, 90, dict(heads=1, group=4, page=64)),       # more sequences than a wavefront looks at together
+    (3, 130, 33, dict(heads=1, group=1, bits=8, page=32)),
+    (4, 12, 300, dict(heads=1, group=3, window=70)),
+    (5, 5, 140, dict(heads=3, group=2, softcap=20.0, lam=True)),
+    (6, 300, 70, dict(heads=1, group=2, causal=False, page=128)),
+])
+def test_continuous_batches(orc, seed, seqs, long, kw):
+    say(f"case: attend a continuous batch of {seqs} sequences, a chunk of {long}, {kw}")
+    lens, m = mixture(seed, seqs, long)
+    c = Case(orc, lens, m, **kw)
+    c.check()
+    bounded = c.run()
+    # without bounds on queries or lengths: another cut of the same work
+    want, tol, _, _ = c.want()
+    within(host(c.run(max_q=None, max_len=None)), want, tol)
+    within(host(bounded), want, tol)
+
+
+def test_many_sequences_beside_a_chunk_of_32768():
+    """Each sequence's rows are those of the sequence alone, bit for bit (lengths of one split)."""
+    say("case: attend 255 single tokens and a chunk of 32768 queries, 8 heads")
+    seqs, heads, group, page, chunk = 256, 8, 4, 64, 32768
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    lens = torch.randint(1, 400, (seqs,), generator=g, device="cuda").to(torch.int32)
+    lens[77] = 410
+    used = [-(-n // page) for n in lens.tolist()]
+    cache = hq.hq_kv_cache(sum(used), heads, page)
+    slots = torch.arange(sum(used) * page, device="cuda")
+    k, v = (torch.randn(slots.numel(), heads, 128, generator=g, device="cuda") for _ in range(2))
+    hq.hq_kv_append(cache, k, v, slots)
+    first = np.concatenate([[0], np.cumsum(used)[:-1]])
+    table = dev((first[:, None] + np.arange(max(used))).astype(np.int32))
+    m = np.ones(seqs, np.int64)
+    m[77] = chunk
+    start = np.concatenate([[0], np.cumsum(m)]).astype(np.int32)
+    q = torch.randn(int(start[-1]), heads * group, 128, generator=g, device="cuda").bfloat16()
+    for max_q in (chunk, None):
+        out = hq.hq_kv_attend(cache, q, table, lens, q_start=dev(start), max_q=max_q, max_len=410)
+        a, b = int(start[77]), int(start[78])
+        assert torch.equal(out[a:b], hq.hq_kv_attend(cache, q[a:b], table[77:78], lens[77:78], max_len=410))
+        assert not out[a:b - 410].any() and bool(out[b - 410:b].any(-1).all())
+        alone = hq.hq_kv_attend(cache, torch.cat([q[:a], q[b:]]), torch.cat([table[:77], table[78:]]), torch.cat([lens[:77], lens[78:]]), max_len=410)
+        assert torch.equal(torch.cat([out[:a], out[b:]]), alone)
