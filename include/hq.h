@@ -310,7 +310,7 @@ int hq_srft_decode(const void *codes, const void *scales, uint64_t n, uint64_t s
  * lambda (lambda_k for keys, lambda_v for values; HOST, 128 binary32 values or NULL for ones).
  * A slot is page * P + offset.  Token t of sequence b is slot offset t mod P of page
  * table[b * table_width + t / P]; a table entry outside [0, pages) is an absent page, whose tokens take
- * no part.  All calls below are asynchronous on `stream`, allocate nothing and may be captured. */
+ * no part, and so does a token whose K scales are -0 (hq_kv_append writes none; hq_kv_evict does).  All calls below are asynchronous on `stream`, allocate nothing and may be captured. */
 typedef struct {
   void *data;
   uint32_t pages, heads, page;
@@ -381,8 +381,8 @@ int hq_kv_attend(const hq_kv_cache *cache, const hq_kv_attend_args *args, void *
 /* Eviction by accumulated weight.  Of each (sequence, head)'s n tokens, m = min(n, budget) stay: the first
  * `sink`, the last `recent`, and of the others those of most weight (ties to the lowest index; NaN counts
  * least).  They move, in order, to tokens 0..m-1 of the pages of dst_table, which must not be pages that
- * any table of the call reads; slots past m are not written, and a token of an absent page that stays (as
- * one of the first or last, or within the budget) leaves its slot as it was. */
+ * any table of the call reads; slots past m are not written.  A token of an absent page that stays (as
+ * one of the first or last, or within the budget) becomes one that takes no part: zeros, its K scales -0. */
 typedef struct {
   const int32_t *table;      /* DEVICE, [seqs][table_width]                                */
   const int32_t *lens;       /* DEVICE, [seqs]                                             */

@@ -286,8 +286,8 @@ __device__ __forceinline__ void value_operands(const Share<BITS>& s, uint32_t ou
 template <int BITS>
 constexpr uint32_t kLargeScale = BITS == 4 ? 0x7000u : 0x6000u;
 
-// The largest bits of pairs of scales, and whether one of a pair is out of the ordinary: large, infinite or NaN (no
-// scale has a sign).
+// The largest bits of pairs of scales, and whether one of a pair is out of the ordinary: large, infinite, NaN, or with the
+// sign that marks the key of a token that takes no part.
 __device__ __forceinline__ u16x2 most(uint32_t a, uint32_t b) { return __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)); }
 template <int BITS>
 __device__ __forceinline__ bool odd_scales(u16x2 m) {
@@ -309,6 +309,8 @@ __device__ __forceinline__ bool shrink(uint32_t s[2]) {
   return true;
 }
 constexpr float kShrunk = 128.0f;
+// Which of 16 tokens (bit 0: the first) have keys that take no part.
+__device__ __forceinline__ uint32_t gone_keys(const uint32_t ks[2]) { return (uint32_t)__builtin_amdgcn_ballot_w64((ks[0] & 0x8000u) != 0u) & 0xFFFFu; }
 // Which of the lane's four value scales are NaN or infinite (bit r: token 4b + r).
 __device__ __forceinline__ uint32_t bad_scales(const uint32_t vs[2]) {
   uint32_t bad = 0;
@@ -448,7 +450,7 @@ __device__ __forceinline__ uint64_t row_at(const AttendArgs& a, const Seq& s, ui
 // The last tile of a sequence: its first row.
 __device__ __forceinline__ uint32_t last_tile(const AttendArgs& a, const Seq& s) {
   const uint32_t rows = (uint32_t)s.m * a.group;
-  return rows ? (rows - 1u) / a.tile_rows * a.tile_rows : 0u;
+  return rows ? (rows - 1u) & ~(a.tile_rows - 1u) : 0u;  // a power of two
 }
 
 // The sequence of full tile f: the last whose tiles begin at or before it.  A wavefront looks at 64 places at a time.
@@ -560,13 +562,14 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
       load(t + kStep, pg0, nxt[0]);
       load(t + kStep + 16, pg1, nxt[1]);
     }
-    uint32_t large = 0;  // bit u: shrunk keys, bit 2 + u: shrunk values
+    uint32_t large = 0, gone = 0;  // bit u: shrunk keys, bit 2 + u: shrunk values; tokens that take no part
     float sc[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (__builtin_amdgcn_ballot_w64(odd_scales<BITS>(most(cur[u].ks[0], cur[u].ks[1])))) {
         const int32_t tok = t + 16 * u + (int32_t)n;
         if (!there[u] || tok < lo || tok >= t1) cur[u].ks[0] = cur[u].ks[1] = 0u;  // a token that no row sees may hold anything
+        gone |= gone_keys(cur[u].ks) << (16 * u);
         if (shrink<BITS>(cur[u].ks)) large |= 1u << u;
       }
       f16x8 kh[4], kl[4];
@@ -580,6 +583,11 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
       for (int i = 0; i < 8; ++i) sc[i] *= (large >> (i >> 2)) & 1u ? kShrunk : 1.0f;
     }
     cap_scores<8>(a, sc);
+    if (gone) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((gone >> (4u * b4) >> (16 * (i >> 2) + (i & 3))) & 1u) sc[i] = -__builtin_inff();
+    }
     if (!(there[0] && there[1] && t >= all_lo && t + 32 <= all_hi && t + 32 <= t1)) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -888,7 +896,8 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
   extern __shared__ __align__(16) uint8_t raw[];
   Stage<PREC>* st = reinterpret_cast<Stage<PREC>*>(raw);
   float(*s_o)[16][kPad] = reinterpret_cast<float(*)[16][kPad]>(raw);  // [wavefront], after the last product
-  __shared__ uint32_t s_flags[PREC ? 1 : 2][kManyWaves];  // bits 0..15: tokens with NaN value scales; 16: absent; 17, 18: shrunk keys, values
+  // bits 0..15: tokens with NaN value scales, 16..31: tokens that take no part; bits 0 and 1: shrunk keys, values
+  __shared__ uint2 s_flags[PREC ? 1 : 2][kManyWaves];
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
   const uint32_t tiles = uniform(a.plan[0]), splits = uniform(a.plan[1]), chunk = uniform(a.plan[2]), items = tiles * a.heads;
   if (blockIdx.x >= items * splits) return;
@@ -932,12 +941,13 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
     load_values<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
   };
   // this wavefront's 16 tokens at t, as operands
-  auto stage = [&](Stage<PREC>& d, uint32_t* flags, int32_t t, int32_t page) __attribute__((always_inline)) {
-    uint32_t word = page < 0 ? 0x10000u : 0u;
+  auto stage = [&](Stage<PREC>& d, uint2* flags, int32_t t, int32_t page) __attribute__((always_inline)) {
+    uint32_t word = page < 0 ? 0xFFFF0000u : 0u, large = 0;
     if (__builtin_amdgcn_ballot_w64(odd_scales<BITS>(most(sh.ks[0], sh.ks[1])))) {
       const int32_t tok = t + (int32_t)n;
       if (page < 0 || tok < lo || tok >= t1) sh.ks[0] = sh.ks[1] = 0u;  // a token that no row sees may hold anything
-      if (shrink<BITS>(sh.ks)) word |= 0x20000u;
+      word |= gone_keys(sh.ks) << 16;
+      if (shrink<BITS>(sh.ks)) large |= 1u;
     }
     f16x8 kh[4], kl[4];
     key_operands<BITS, PREC>(sh, kh, kl);
@@ -961,9 +971,9 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
       }
       // a value vector with one NaN scale is NaN as a whole: its rows are poisoned, its scales count as 0
       drop_scales(sh.vs, (word >> (4 * b4)) & 15u);
-      if (shrink<BITS>(sh.vs)) word |= 0x40000u;
+      if (shrink<BITS>(sh.vs)) large |= 2u;
     }
-    if (lane == 0) flags[wave] = word;
+    if (lane == 0) flags[wave] = make_uint2(word, large);
     uint32_t v[8][2];
     value_operands<BITS>(sh, v);
 #pragma unroll
@@ -1031,7 +1041,8 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
     }
     const Stage<PREC>& d = st[buf];
     // blocks of 16 tokens with a flag, asked for once and not between the products
-    const uint32_t flagged = (uint32_t)__builtin_amdgcn_ballot_w64(lane < (uint32_t)kManyWaves && s_flags[buf][lane & (kManyWaves - 1)] != 0u);
+    const uint2 flags = s_flags[buf][lane & (kManyWaves - 1)];
+    const uint32_t flagged = (uint32_t)__builtin_amdgcn_ballot_w64(lane < (uint32_t)kManyWaves && (flags.x | flags.y) != 0u);
     bool whole = false;
     if constexpr (!PREC) {
       if (!cap && !flagged && t >= all_lo && t + kTok <= all_hi && t + kTok <= t1) {
@@ -1118,7 +1129,7 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
       auto unshrink = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float k = s_flags[buf][2 * w + u] & 0x20000u ? kShrunk : 1.0f;
+          const float k = s_flags[buf][2 * w + u].y & 1u ? kShrunk : 1.0f;
 #pragma unroll
           for (int q = 0; q < R; ++q) sc[q][u] *= k;
         }
@@ -1134,8 +1145,8 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
             for (int i = 0; i < 4; ++i) sc[q][u][i] = a.cap_out * tanh32(sc[q][u][i] * qf[q] * a.cap_in);
       }
       if ((flagged >> (2 * w) & 3u) || tw < all_lo || tw + 32 > all_hi || tw + 32 > t1) {
-        const uint32_t fl0 = s_flags[buf][2 * w], fl1 = s_flags[buf][2 * w + 1];
-        large = (uint32_t)__builtin_amdgcn_readfirstlane((int)((fl0 >> 18 & 1u) | (fl1 >> 18 & 1u) << 1));
+        const uint2 f0 = s_flags[buf][2 * w], f1 = s_flags[buf][2 * w + 1];
+        large = uniform(f0.y >> 1 | (f1.y & 2u));
         if (!cap) unshrink();
 #pragma unroll
         for (int q = 0; q < R; ++q)
@@ -1144,9 +1155,9 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int32_t tok = tw + 16 * u + 4 * (int32_t)b4 + i;
-              const uint32_t fl = u ? fl1 : fl0;
+              const uint32_t fl = (u ? f1.x : f0.x) >> (4 * b4 + i);
               if ((fl & 0x10000u) || tok < row_lo[q] || tok >= row_hi[q] || tok >= t1) sc[q][u][i] = -__builtin_inff();
-              else if ((fl >> (4 * b4 + i)) & 1u) poison[q] = __builtin_nanf("");
+              else if (fl & 1u) poison[q] = __builtin_nanf("");
             }
       }
       float top[R];
@@ -1265,19 +1276,22 @@ __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a
   const uint32_t P = 1u << a.page_log2;
   const uint64_t page_size = (uint64_t)P * Page<BITS>::kToken;
   f16x8 kh[4][4], kl[4][4];
-  uint32_t absent = 0;  // blocks of 16 tokens without a page
-  float factor[4];      // undoes a block's shrunk keys
+  uint32_t hidden = 0, some = 0;  // of the lane's 16 tokens, those that take no part; whether any of the 64 does not
+  float factor[4];                // undoes a block's shrunk keys
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int32_t page = page_of(a, b, t + 16 * u, s.n);
-    absent |= page < 0 ? 1u << u : 0u;
+    uint32_t gone = page < 0 ? 0xFFFFu : 0u;
     factor[u] = 1.0f;
     Share<BITS> sh;
     load_keys<BITS>(a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + h) * page_size, P, (uint32_t)(t + 16 * u) & (P - 1u), lane, sh);
     if (__builtin_amdgcn_ballot_w64(odd_scales<BITS>(most(sh.ks[0], sh.ks[1])))) {
       if (page < 0 || t + 16 * u + (int32_t)n >= s.n) sh.ks[0] = sh.ks[1] = 0u;
+      gone |= gone_keys(sh.ks);
       if (shrink<BITS>(sh.ks)) factor[u] = kShrunk;
     }
+    hidden |= (gone >> (4u * b4) & 15u) << (4 * u);
+    some |= gone;
     key_operands<BITS, true>(sh, kh[u], kl[u]);
   }
   float acc[16];
@@ -1336,7 +1350,7 @@ __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a
 #pragma unroll
     for (int i = 0; i < 16; ++i) sc[i] = raw[i >> 2][i & 3] * (f * factor[i >> 2]);
     cap_scores<16>(a, sc);
-    if (!absent && t >= all_lo && t + 64 <= all_hi) {
+    if (!some && t >= all_lo && t + 64 <= all_hi) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[i] += __builtin_amdgcn_exp2f(sc[i] - ls);
     } else {
@@ -1346,7 +1360,7 @@ __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a
       for (int i = 0; i < 16; ++i) {
         const int32_t tok = t + 16 * (i >> 2) + 4 * (int32_t)b4 + (i & 3);
         const float p = __builtin_amdgcn_exp2f(sc[i] - ls);
-        acc[i] += bool((tok >= row_lo) & (tok < row_hi) & !((absent >> (i >> 2)) & 1u)) ? p : 0.0f;
+        acc[i] += bool((tok >= row_lo) & (tok < row_hi) & !((hidden >> i) & 1u)) ? p : 0.0f;
       }
     }
   }

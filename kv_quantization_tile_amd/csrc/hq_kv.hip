@@ -389,7 +389,8 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
 
 // Moves the tokens that stay: 16 lanes take four consecutive destination tokens, which are one block of V, so
 // that a lane stores its group's codes and scales of all four at once.  Values lie by blocks of four tokens,
-// so where a quarter of the tokens stay nearly all of V is read; that traffic bounds the kernel.
+// so where a quarter of the tokens stay nearly all of V is read; that traffic bounds the kernel.  A token of an
+// absent page that stays gets zeros, with the sign set in its keys' scales: it takes no part where it goes either.
 template <int BITS>
 __global__ __launch_bounds__(kBlock) void evict_move_kernel(EvictArgs a, uint32_t blocks) {
   const uint32_t l = threadIdx.x & 15u, bh = blockIdx.x / blocks, b = bh / a.heads, h = bh % a.heads;
@@ -401,16 +402,17 @@ __global__ __launch_bounds__(kBlock) void evict_move_kernel(EvictArgs a, uint32_
   if ((uint32_t)dp >= a.pages) return;
   const uint64_t size = (uint64_t)P * Page<BITS>::kToken;
   uint8_t* d = a.cache + ((uint64_t)dp * a.heads + h) * size;
-  int32_t src[4];
+  int32_t src[4];  // -1: absent; -2: no token
   const uint8_t* page[4];
   bool whole = true;
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i) {
     src[i] = j + i < a.budget ? kept[j + i] : -1;
+    if (src[i] < 0) src[i] = -2;
     const int32_t sp = src[i] >= 0 ? a.table[(uint64_t)b * a.width + ((uint32_t)src[i] >> a.page_log2)] : -1;
-    if ((uint32_t)sp >= a.pages) src[i] = -1;
+    if (src[i] >= 0 && (uint32_t)sp >= a.pages) src[i] = -1;
     page[i] = a.cache + ((uint64_t)(src[i] < 0 ? 0 : sp) * a.heads + h) * size;
-    whole &= src[i] >= 0;
+    whole &= src[i] != -2;
   }
   typedef uint32_t piece __attribute__((ext_vector_type(BITS / 4)));
   piece v[4];
@@ -420,6 +422,10 @@ __global__ __launch_bounds__(kBlock) void evict_move_kernel(EvictArgs a, uint32_
     const uint32_t so = (uint32_t)(src[i] < 0 ? 0 : src[i]) & (P - 1u);
     v[i] = *reinterpret_cast<const piece*>(page[i] + Page<BITS>::v_code(P, so, l));
     s[i] = *reinterpret_cast<const uint16_t*>(page[i] + Page<BITS>::v_scale(P, so, l));
+    if (src[i] < 0) {
+      v[i] = (piece)0u;
+      s[i] = 0u;
+    }
   }
   // keys: the lane's quarter of one of the four vectors
   const uint32_t which = l >> 2, part = l & 3u;
@@ -427,9 +433,13 @@ __global__ __launch_bounds__(kBlock) void evict_move_kernel(EvictArgs a, uint32_
   const uint8_t* kp = which == 0 ? page[0] : which == 1 ? page[1] : which == 2 ? page[2] : page[3];
   const uint32_t ko = (uint32_t)(ks < 0 ? 0 : ks) & (P - 1u);
   const uint4* kc = reinterpret_cast<const uint4*>(kp + Page<BITS>::k_code(P, ko) + part * 4u * BITS);
-  const uint4 k0 = kc[0], k1 = kc[BITS / 8];
-  const uint2 kscale = *reinterpret_cast<const uint2*>(kp + Page<BITS>::k_scale(P, ko) + 8u * part);
-  if (ks >= 0) {
+  uint4 k0 = kc[0], k1 = kc[BITS / 8];
+  uint2 kscale = *reinterpret_cast<const uint2*>(kp + Page<BITS>::k_scale(P, ko) + 8u * part);
+  if (ks < 0) {
+    k0 = k1 = make_uint4(0u, 0u, 0u, 0u);
+    kscale = make_uint2(0x80008000u, 0x80008000u);
+  }
+  if (ks != -2) {
     uint4* kd = reinterpret_cast<uint4*>(d + Page<BITS>::k_code(P, to + which) + part * 4u * BITS);
     kd[0] = k0;
     if (BITS == 8) kd[1] = k1;
@@ -448,7 +458,7 @@ __global__ __launch_bounds__(kBlock) void evict_move_kernel(EvictArgs a, uint32_
   } else {
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i)
-      if (src[i] >= 0) {
+      if (src[i] != -2) {
         reinterpret_cast<piece*>(vd)[i] = v[i];
         reinterpret_cast<uint16_t*>(sd)[i] = (uint16_t)s[i];
       }

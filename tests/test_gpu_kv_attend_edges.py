@@ -1,5 +1,6 @@
 """GPU: attention over the paged SRFT cache at the edges of what a call may ask: fewer queries computed than a sequence has,
-small and large cached values, batches that are mostly single tokens.
+small and large cached values, batches that are mostly single tokens,
+tokens that an eviction kept without having them.
 
 Bounds are kv_reference.attend's; cases are those of test_gpu_kv_attend."""
 import numpy as np
@@ -176,3 +177,48 @@ def test_many_sequences_beside_a_chunk_of_32768():
         assert not out[a:b - 410].any() and bool(out[b - 410:b].any(-1).all())
         alone = hq.hq_kv_attend(cache, torch.cat([q[:a], q[b:]]), torch.cat([table[:77], table[78:]]), torch.cat([lens[:77], lens[78:]]), max_len=410)
         assert torch.equal(torch.cat([out[:a], out[b:]]), alone)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("group,m", [(2, 1), (2, 40), (2, 140)])
+def test_absent_tokens_that_an_eviction_keeps(orc, monkeypatch, group, m, bits):
+    """Tokens of absent pages that stay (first, last or within the budget) take no part after the move either, whatever their
+    new slots held, nor after a second move."""
+    say(f"case: attend after an eviction that keeps absent tokens, group {group}, {m} queries, {bits} bits")
+    c = Case(orc, [250, 230], [m, m], heads=2, group=group, bits=bits)
+    c.table[0, 0] = c.table[0, 7] = c.table[1, 3] = c.table[1, 14] = -1
+    pages, want_pages, budget = c.cache.shape[0], 12, 180
+    cache = torch.cat([c.cache, c.cache[torch.randint(0, pages, (48,), device="cuda")]])  # fresh pages hold other tokens
+    lens = dev(np.array(c.lens, np.int32))
+    weights = torch.rand(2, 2, 250, device="cuda")
+    dst = pages + np.arange(24, dtype=np.int32).reshape(2, 12)
+    kept, left, wk = hq.hq_kv_evict(cache, dev(c.table), lens, weights, budget, 20, 30, dev(dst), bits=bits)
+    assert left.tolist() == [budget, budget]
+    old = [[ref.coordinates(host(c.cache), bits, c.table[b], c.lens[b], h, np.ones(128), np.ones(128)) for h in range(2)] for b in range(2)]
+
+    def moved(kept):
+        def of(_, __, row, n, head, ___, ____):
+            k, v, there = old[row][head]
+            at = kept[row, head, :n]
+            return k[at], v[at], there[at]
+        return of
+
+    kh = host(kept)
+    assert any(not old[b][h][2][kh[b, h]].all() for b in range(2) for h in range(2))
+    second = pages + 24 + np.arange(24, dtype=np.int32).reshape(2, 12)
+    kept2, left2, _ = hq.hq_kv_evict(cache, dev(dst), left, wk, 150, 20, 30, dev(second), bits=bits)
+    kh2 = np.take_along_axis(kh, host(kept2), 2)
+    for table, n, index in ((dst, budget, kh), (second, 150, kh2)):
+        monkeypatch.setattr(ref, "coordinates", moved(index))
+        for precise in (False, True):
+            want, tol, ww, wtol = ref.attend(orc, cache, c.q, [0, 1], [n, n], [m, m], bits, SEED, scale=c.scale, precise=precise)
+            w = torch.zeros(2, 2, n, device="cuda") if precise else None
+            out = torch.full(c.q.shape, float("nan"), device="cuda")
+            hq.hq_kv_attend(cache, dev(c.q), dev(table), torch.full_like(left, n), max_len=n, bits=bits, seed=SEED, weights=w, out=out)
+            within(host(out), want, tol)
+            if precise:
+                got = host(w).astype(np.float64)
+                assert (np.abs(got - ww) <= wtol + 2.0 ** -23 * ww).all()
+                assert all((got[b, h][~old[b][h][2][index[b, h]]] == 0).all() for b in range(2) for h in range(2))
+    slots = dev((dst[0, 0] * 16 + np.arange(16)).astype(np.int64))  # the first tokens of the first sequence were absent
+    assert not any(x.any() for x in hq.hq_kv_read(cache, slots, bits=bits, seed=SEED))
