@@ -38,6 +38,7 @@ constexpr int kAttWaves = 4;
 constexpr int kPad = kD + 4;         // row of a tile in LDS, in floats
 constexpr float kPScaleLog2 = 8.0f;  // P is stored as p 2^8
 constexpr float kSlack = 6.0f;       // the reference may lag the maximum by this much (log2)
+constexpr float kLowest = -3.402823466e38f;  // the reference before the first score: no finite score is below it
 
 struct AttendArgs {
   const uint8_t* cache;
@@ -548,7 +549,7 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
   // the tokens every existing row sees need no mask (rows past the last are products with zero)
   if (rows) rows_common(a, s, r0, rows, &all_lo, &all_hi);
 
-  float m = -1.0e30f, sum = 0.0f, poison = 0.0f;
+  float m = kLowest, sum = 0.0f, poison = 0.0f;
   f32x4 o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -727,7 +728,7 @@ __global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables
   rows_range(a, s, r0, tile_rows, &lo, &hi);
   if (a.pages == 0) hi = lo;
   const uint32_t s0 = hi > lo ? (uint32_t)lo / chunk : 0u, s1 = hi > lo ? ((uint32_t)hi + chunk - 1u) / chunk : 0u;
-  float m = -1.0e30f, sum = 0.0f, y[8];
+  float m = kLowest, sum = 0.0f, y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = 0.0f;
   for (uint32_t i = s0 + (WIDE ? g : 0u); i < s1; i += WIDE ? 16u : 1u) {
@@ -1002,7 +1003,7 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
     }
     qf[q] = have ? a.qf[row] : 1.0f;
     eff[q] = cap ? 1.0f : qf[q];  // scores are eff sc: the product with qf waits for the exponent's fma
-    m[q] = -1.0e30f;
+    m[q] = kLowest;
     sum[q] = poison[q] = 0.0f;
     row_lo[q] = row_hi[q] = 0;
     if (w0 + 16u * q + n < rows) visible(a, s, (int32_t)query_of(a, w0 + 16u * q + n), &row_lo[q], &row_hi[q]);

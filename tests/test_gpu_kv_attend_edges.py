@@ -1,6 +1,6 @@
 """GPU: attention over the paged SRFT cache at the edges of what a call may ask: fewer queries computed than a sequence has,
 small and large cached values, batches that are mostly single tokens,
-tokens that an eviction kept without having them.
+tokens that an eviction kept without having them, and scores of any size.
 
 Bounds are kv_reference.attend's; cases are those of test_gpu_kv_attend."""
 import numpy as np
@@ -222,3 +222,54 @@ def test_absent_tokens_that_an_eviction_keeps(orc, monkeypatch, group, m, bits):
                 assert all((got[b, h][~old[b][h][2][index[b, h]]] == 0).all() for b in range(2) for h in range(2))
     slots = dev((dst[0, 0] * 16 + np.arange(16)).astype(np.int64))  # the first tokens of the first sequence were absent
     assert not any(x.any() for x in hq.hq_kv_read(cache, slots, bits=bits, seed=SEED))
+
+
+@pytest.mark.parametrize("m", [1, 40, 140])
+def test_large_scores_pick_one_token(orc, m):
+    """Where the best score of a row leads by more than its error allows, the row is that token's value."""
+    say(f"case: attend with scores of thousands, {m} queries")
+    c = Case(orc, [256, 190], [m, m], heads=1, group=2)
+    c.q *= 1000
+    T = ref.transform(orc, SEED)
+    runs = [host(c.run()), host(c.run(weights=torch.zeros(2, 1, 256, device="cuda")))]
+    rows = 0
+    for b, n in enumerate(c.lens):
+        k, v, _ = ref.coordinates(host(c.cache), 4, c.table[b], n, 0, np.ones(128), np.ones(128))
+        for i in range(m):
+            for j in range(2):
+                seen = n - m + i + 1
+                y = c.q[b * m + i, j].astype(np.float64) @ T.T * c.scale
+                s, size = k[:seen] @ y, (np.abs(k[:seen]) @ np.abs(y)).max()
+                best = int(np.argmax(s))
+                lead = s[best] - np.max(np.delete(s, best))
+                # scores are off by (2^-10 + 2^-17) of their sum of magnitudes; e^-20 of 256 others is below 2^-20
+                if lead <= 2 * (2.0 ** -10 + 2.0 ** -17) * size + 20:
+                    continue
+                rows += 1
+                for out in runs:
+                    want = v[best] @ T
+                    assert np.linalg.norm(out[b * m + i, j] - want) <= (3 * 2.0 ** -11 + 2.0 ** -17) * np.linalg.norm(v[best])
+    assert rows >= m  # of 4 m
+
+
+@pytest.mark.parametrize("m", [1, 40, 140])
+@pytest.mark.parametrize("size", [-1e3, -1e28, -1e34, 1e34])
+def test_scores_far_from_zero(orc, size, m):
+    """Equal scores of any size, far below zero too, average the values that a row sees."""
+    say(f"case: attend with scores about {size}, {m} queries")
+    c = Case(orc, [150, 190], [m, m], heads=1, group=2)
+    slots = torch.arange(c.cache.shape[0] * 16, device="cuda")
+    key = torch.ones(slots.numel(), 1, 128, device="cuda")
+    v = hq.hq_kv_read(c.cache, slots, out_dtype=torch.float32, **c.fmt)[1]
+    hq.hq_kv_append(c.cache, key, v, slots, **c.fmt)
+    c.q[:] = size
+    T = ref.transform(orc, SEED)
+    for w in (None, torch.zeros(2, 1, 190, device="cuda")):
+        got = host(c.run(weights=w))
+        for b, n in enumerate(c.lens):
+            _, v, _ = ref.coordinates(host(c.cache), 4, c.table[b], n, 0, np.ones(128), np.ones(128))
+            for i in range(m):
+                v_seen = v[:n - m + i + 1]
+                want = v_seen.mean(0) @ T
+                bound = (3 * 2.0 ** -11 + 2.0 ** -17) * np.linalg.norm(np.abs(v_seen).mean(0))
+                assert (np.linalg.norm(got[b * m + i] - want, axis=-1) <= bound).all()
