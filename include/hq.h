@@ -372,8 +372,8 @@ typedef struct {
 int hq_kv_attend_workspace_size(const hq_kv_cache *cache, const hq_kv_attend_args *args, size_t *bytes);
 
 /* HQ_ERR_INVALID_ARG: null or misaligned pointers, sizes outside their ranges, q_heads not a multiple of
- * heads, q_start == NULL with total_q not a multiple of seqs, a scale or softcap that is not finite, a
- * negative softcap, weights_stride < max_len, max_len over 2^30, a launch of 2^32 threads or more (2^28
+ * heads, q_start == NULL with total_q not a multiple of seqs, a scale that is not a number in
+ * [-2^126, 2^126], a softcap that is neither 0 nor in [2^-125, 2^125], weights_stride < max_len, max_len over 2^30, a launch of 2^32 threads or more (2^28
  * rows of queries and heads), or a workspace that is too small.  Rows of `out` that no sequence's queries name are not written. */
 int hq_kv_attend(const hq_kv_cache *cache, const hq_kv_attend_args *args, void *workspace,
                  size_t workspace_bytes, hq_stream_t stream);

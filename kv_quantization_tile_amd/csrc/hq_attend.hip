@@ -1549,7 +1549,9 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   if (int rc = check_attend(cache, args)) return rc;
   const hq_kv_attend_args& g = *args;
   if ((g.q_dtype != HQ_F32 && g.q_dtype != HQ_BF16) || (g.out_dtype != HQ_F32 && g.out_dtype != HQ_BF16)) return HQ_ERR_INVALID_ARG;
-  if (!std::isfinite(g.scale) || !std::isfinite(g.softcap) || g.softcap < 0.0f) return HQ_ERR_INVALID_ARG;
+  // log2(e) times the scale and the cap, and its reciprocal, are normal binary32 numbers (NaN fails too)
+  if (!(std::fabs(g.scale) <= 0x1p126f)) return HQ_ERR_INVALID_ARG;
+  if (g.softcap != 0.0f && !(g.softcap >= 0x1p-125f && g.softcap <= 0x1p125f)) return HQ_ERR_INVALID_ARG;
   if (g.weights && g.weights_stride < g.max_len) return HQ_ERR_INVALID_ARG;
   Tables T;
   if (!make_tables(*cache, false, &T)) return HQ_ERR_INVALID_ARG;

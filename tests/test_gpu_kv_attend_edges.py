@@ -273,3 +273,19 @@ def test_scores_far_from_zero(orc, size, m):
                 want = v_seen.mean(0) @ T
                 bound = (3 * 2.0 ** -11 + 2.0 ** -17) * np.linalg.norm(np.abs(v_seen).mean(0))
                 assert (np.linalg.norm(got[b * m + i] - want, axis=-1) <= bound).all()
+
+
+@pytest.mark.parametrize("softcap", [2.0 ** -125, 1e-20, 1e20, 2.0 ** 125])
+@pytest.mark.parametrize("m", [1, 40])
+def test_caps_of_any_size(orc, m, softcap):
+    """A cap far above the scores leaves them, one far below makes them equal; one that binary32 cannot hold is refused."""
+    say(f"case: attend with a cap of {softcap}, {m} queries")
+    c = Case(orc, [150, 190], [m, m], heads=1, group=2, softcap=softcap)
+    if softcap > 1:
+        c.kw["softcap"] = 0.0
+    want, tol, _, _ = c.want()
+    c.kw["softcap"] = softcap
+    within(host(c.run()), want, tol)
+    for kw in (dict(softcap=3e38), dict(softcap=1e-39), dict(scale=3e38)):
+        with pytest.raises(hq.HqError):
+            c.run(**kw)

@@ -55,6 +55,19 @@ def test_equal_sequences_take_what_they_took():
             assert 0 < workspace(seqs, seqs * m, m, offsets=offsets) <= rows_bytes(seqs * m, False) + 2048 * 256 * 520 + 2048 * 16 * 520 + MIB
 
 
+@pytest.mark.parametrize("kw", [dict(softcap=3e38), dict(softcap=1e-39), dict(scale=3e38), dict(scale=-2.0 ** 127), dict(softcap=-1e-40)])
+def test_factors_that_binary32_cannot_hold_in_log2_units(kw):
+    """log2(e) times the scale or the cap, or its reciprocal, would be infinite or lose its bits: refused, not computed."""
+    c = hq.HqKvCache(data=1 << 20, pages=8, heads=2, page=64, bits=4)
+    a = dict(q=1 << 20, out=1 << 20, q_dtype=1, out_dtype=1, q_stride_token=1024, q_stride_head=128, total_q=4, q_heads=8, seqs=4, max_q=1, max_len=512,
+             table=1 << 20, table_width=8, lens=1 << 20, scale=0.1)
+    # without a workspace nothing is launched whatever the factors: a good call is told from a refused one by none being asked for
+    good = hq.HqKvAttendArgs(**a | dict(total_q=0))
+    assert hq.lib().hq_kv_attend(ctypes.byref(c), ctypes.byref(good), None, 0, None) == hq.HQ_OK
+    bad = hq.HqKvAttendArgs(**a | dict(total_q=0) | kw)
+    assert hq.lib().hq_kv_attend(ctypes.byref(c), ctypes.byref(bad), None, 0, None) == hq.HQ_ERR_INVALID_ARG
+
+
 def test_sizes_past_a_launch_are_refused():
     for kw in (dict(seqs=1 << 24, total_q=1 << 24, max_q=1), dict(seqs=1, total_q=1 << 30, max_q=1 << 30), dict(seqs=1, total_q=1 << 27, max_q=1 << 27)):
         assert workspace(**kw) == hq.HQ_ERR_INVALID_ARG
