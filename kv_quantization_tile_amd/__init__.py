@@ -422,9 +422,21 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _stream_on(stream, device):
-    """The handle of `stream`, or of the device's current stream (without the Stream object, which takes 3 us to make)."""
-    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(device.index)
+def _launch(what, device, stream, call, *args):
+    """Calls `call`(*args, stream's handle) with `device` current: the handle of `stream`, or of the device's current stream
+    (without the Stream object, which takes 3 us to make)."""
+    torch = _torch()
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device == device:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"{what}: the stream is on {stream.device}, the cache on {device}")
+    if torch.cuda.current_device() == device.index:
+        _check(call(*args, handle), what)
+    else:
+        with torch.cuda.device(device):
+            _check(call(*args, handle), what)
 
 
 def _row_strides(t, name, heads, device):
@@ -447,8 +459,8 @@ def hq_kv_append(cache, k, v, slots, bits: int = 4, seed: int = 0, lam_k=None, l
     if k.dtype != v.dtype or v.shape[0] != tokens:
         raise ValueError("k and v must have one type and length")
     _check_tensor(slots, "slots", _torch().int64, (tokens,), dev)
-    _check(lib().hq_kv_append(ctypes.byref(c), k.data_ptr(), v.data_ptr(), _dtype_code(k), tokens, _Strides4(ks[0], ks[1], vs[0], vs[1]),
-                              slots.data_ptr(), _stream_on(stream, dev)), "hq_kv_append")
+    _launch("hq_kv_append", dev, stream, lib().hq_kv_append, ctypes.byref(c), k.data_ptr(), v.data_ptr(), _dtype_code(k), tokens,
+            _Strides4(ks[0], ks[1], vs[0], vs[1]), slots.data_ptr())
     return cache
 
 
@@ -469,8 +481,7 @@ def hq_kv_read(cache, slots, bits: int = 4, seed: int = 0, lam_k=None, lam_v=Non
         v = _empty(shape, dt, dev, stream)
     else:
         _check_tensor(v, "v", dt, shape, dev)
-    _check(lib().hq_kv_read(ctypes.byref(c), slots.data_ptr(), tokens, k.data_ptr(), v.data_ptr(), _dtype_code(k),
-                            _stream_on(stream, dev)), "hq_kv_read")
+    _launch("hq_kv_read", dev, stream, lib().hq_kv_read, ctypes.byref(c), slots.data_ptr(), tokens, k.data_ptr(), v.data_ptr(), _dtype_code(k))
     return k, v
 
 
@@ -521,7 +532,7 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
         ws = _empty(need.value, torch.uint8, dev, stream)
     elif not (ws.is_contiguous() and ws.device == dev and ws.dtype == torch.uint8):
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
-    _check(L.hq_kv_attend(cp, ap, ws.data_ptr(), ws.numel(), _stream_on(stream, dev)), "hq_kv_attend")
+    _launch("hq_kv_attend", dev, stream, L.hq_kv_attend, cp, ap, ws.data_ptr(), ws.numel())
     return out
 
 
@@ -557,7 +568,7 @@ def hq_kv_evict(cache, table, lens, weights, budget: int, sink: int, recent: int
                       min(top, width * c.page) if max_len is None else _size(max_len, "max_len"), budget, _size(sink, "sink"),
                       _size(recent, "recent"), dst_table.data_ptr(), dst_width, kept.data_ptr(), new_lens.data_ptr(),
                       new_weights.data_ptr())
-    _check(lib().hq_kv_evict(ctypes.byref(c), ctypes.byref(a), _stream_on(stream, dev)), "hq_kv_evict")
+    _launch("hq_kv_evict", dev, stream, lib().hq_kv_evict, ctypes.byref(c), ctypes.byref(a))
     return kept, new_lens, new_weights
 
 
