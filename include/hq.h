@@ -388,7 +388,9 @@ typedef struct {
   const int32_t *lens;       /* DEVICE, [seqs]                                             */
   const float *weights;      /* DEVICE, as hq_kv_attend's                                  */
   uint64_t weights_stride;
-  uint32_t seqs, table_width, max_len;
+  uint32_t seqs, table_width;
+  uint32_t max_len;          /* most tokens of a sequence, at most weights_stride; a larger
+                                length counts as this: tokens past it are not kept         */
   uint32_t budget, sink, recent;   /* sink + recent <= budget <= dst_width * page           */
   const int32_t *dst_table;  /* DEVICE, [seqs][dst_width]                                  */
   uint32_t dst_width;

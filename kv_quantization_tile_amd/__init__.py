@@ -370,7 +370,7 @@ def hq_srft_decode(codes, scales, n: int, seed: int = 0, bits: int = 4, lam=None
     return out
 
 
-# ---- the paged SRFT cache ---------------------------------------------------------------------------
+# ---- the paged SRFT cache (for inference: no gradient passes through these calls) --------------------
 
 def hq_kv_token_bytes(bits: int = 4) -> int:
     """Bytes of one token of one head, K and V."""
@@ -493,8 +493,8 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
     table int32 [seqs][width], lens int32 [seqs] (tokens cached, the queries' own among them); q_start int32
     [seqs + 1] offsets of each sequence's queries (None: as many each); max_q, max_len bounds on a sequence's
     queries and tokens (None: all queries, what the table's width or the weights hold).  weights float32
-    [seqs][heads][>= max_len] gets each token's softmax weights added.  Returns out ([queries][q heads][128], bf16
-    unless given)."""
+    [seqs][heads][>= max_len] gets each token's softmax weights added (and has the scores computed in two parts, so out may
+    differ in its last bits).  Returns out ([queries][q heads][128], bf16 unless given)."""
     torch = _torch()
     c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
     dev = cache.device
@@ -540,7 +540,8 @@ def hq_kv_evict(cache, table, lens, weights, budget: int, sink: int, recent: int
                 kept=None, new_lens=None, new_weights=None, stream=None):
     """Keep, of each (sequence, head)'s tokens, at most `budget`: the first `sink`, the last `recent`, and the
     others of most weight (ties to the lowest index), moved in order into the pages of dst_table (int32 [seqs][width],
-    none of them in `table`).  Returns (kept int32 [seqs][heads][budget], -1 past the end; new_lens int32 [seqs];
+    none of them in `table`).  max_len bounds a sequence's tokens (None: what the table's width and the weights hold);
+    tokens past it are not kept, so weights has to reach over every length.  Returns (kept int32 [seqs][heads][budget], -1 past the end; new_lens int32 [seqs];
     new_weights float32 [seqs][heads][budget])."""
     torch = _torch()
     c, _ = _cache_arg(cache, bits, 0, None, None)
