@@ -1103,7 +1103,8 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
         whole = true;
       }
     }
-#pragma unroll 2
+    constexpr int kUnroll = PREC ? 2 : 1;  // without PREC the count depends on `whole`: such a loop is not unrolled
+#pragma unroll kUnroll
     for (int w = whole ? kTok / 32 : 0; w < kTok / 32; ++w) {
       const int32_t tw = t + 32 * w;
       if (tw >= whi || tw + 32 <= wlo || tw >= t1) continue;
