@@ -480,14 +480,15 @@ __device__ __forceinline__ int32_t page_in(const AttendArgs& a, int32_t entry) {
 __device__ __forceinline__ int32_t page_of(const AttendArgs& a, uint32_t b, int32_t tt, int32_t end) { return page_in(a, entry_of(a, b, tt, end)); }
 
 // ---------------------------------------------------------------------------------------------
-// Tiles of up to 16 rows: the single-token step, and the single tokens and last rows of a batch that has longer
-// chunks too (left to the other kernel they take as long there as 256 rows: 181 us, against 108 and 23 here, for
-// 4 x 129 and 4 x 1 queries).  A workgroup takes one split of the tokens; its four wavefronts take 32 tokens in
+// Light tiles, of up to 16 rows: the single-token step, and the single tokens and last rows of a batch that has longer
+// chunks too (with the full tiles they take as long as 256 rows: 181 us for 4 x 129 and 4 x 1 queries, against 107 there and
+// 28 here).  A workgroup takes one split of the tokens; its four wavefronts take 32 tokens in
 // turn, the next 32 already on their way, and join at the end.  The rows are a fraction of the products' 16
 // columns, which costs nothing here.  The cache's bytes bound it where there are many: 16 sequences of up to
-// 32768 tokens, 535 MB, in 145 us (3.7 TB/s; a sum over 1 GiB reads 3.9, a 2 GiB copy moves 4.9); an extra
-// wavefront a SIMD (128 registers, some spilled) left that at 160 us.  One sequence of 301 tokens takes 9 us:
-// 2 until the codes are asked for, 1.5 for the rows, 4.2 for three turns, 1 for the join.
+// 32768 tokens, 535 MB, in 148 us with the join (3.6 TB/s; a sum over 1 GiB reads 3.9, a 2 GiB copy moves 4.9); an extra
+// wavefront a SIMD (128 registers, some spilled) took 160 us.  Scales out of the ordinary are looked for where the codes
+// beside them are first used: one look at a step's scales waits for its last load (151 us).  One sequence of 301 tokens
+// takes 10.5 us: about 2 until the codes are asked for, 1.5 for the rows, 4.2 for three turns, 1 for the join.
 template <int BITS, bool PREC>
 __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kernel(AttendArgs a, Tables K) {
   __shared__ __align__(16) float s_o[kAttWaves][16][kPad];
@@ -839,7 +840,7 @@ __device__ void plan_tiles(const AttendArgs& a) {
 
 // Many rows: the queries' rows transformed once, to the workspace; the first workgroup counts the tiles.  A workgroup
 // takes `span` rows of a head, 16 at a time: 64 where that leaves four workgroups a CU, so that the twiddles are fetched
-// once for four (262144 rows: 45 us, 53 us with 16; 16640 rows: 12 us with 64, 11.5 us with 16).
+// once for four (262144 rows: 45 us, 53 us with 16; 16640 rows: 12 us with 64, 11 us with 16).
 template <int BITS>
 __global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Tables K, int parts, uint32_t span) {
   __shared__ __align__(16) _Float16 s_q[2][16][kD + 8];
@@ -874,7 +875,7 @@ __global__ __launch_bounds__(kAttBlock) void rotate_rows_kernel(AttendArgs a, Ta
 // ones' codes are in flight meanwhile.  Two wavefronts a SIMD, so that one's softmax runs beside the
 // other's products; R = 2 is what 256 registers hold (at R = 4 and one wavefront a SIMD nothing overlapped:
 // 1.2 ms for a prompt of 8192 tokens).  Two stages of LDS, one with the keys in two parts (160 KB hold no more).
-// A prompt of 8192 tokens, 550 GFLOP, takes 645 to 715 us (770 to 850 TFLOP/s, less the longer the card
+// A prompt of 8192 tokens, 550 GFLOP, takes 635 to 740 us (740 to 865 TFLOP/s, less the longer the card
 // has been at it; a 16-bit product of 8192^3 reaches 1050 to 1100).
 // A turn of 128 tokens was 12800 cycles: 4350 of matrix instructions, about 6800 of vector instructions and 4100
 // of LDS a SIMD, in phases that the two wavefronts share (scores 700, softmax 700, output 750, four times; 1750
