@@ -366,9 +366,10 @@ typedef struct {
 } hq_kv_attend_args;
 
 /* Workspace bytes of hq_kv_attend for these sizes (host only; pointers are not read; the errors are
- * hq_kv_attend's).  About 264 bytes a row of total_q x q_heads (520 with weights; none where no sequence
- * has more than 16 rows a KV head), and up to 300 MB for the outputs of split tiles.  The workspace needs no
- * initialisation, is 256-byte aligned, and serves one call in flight. */
+ * hq_kv_attend's).  About 264 bytes a row of total_q x q_heads (520 with weights), and up to 300 MB for the
+ * outputs of split tiles; where no sequence has more than 16 rows a KV head, 4 bytes a row and, with weights,
+ * 4 bytes for each of max_len tokens a row.  The workspace needs no initialisation, is 256-byte aligned, and
+ * serves one call in flight. */
 int hq_kv_attend_workspace_size(const hq_kv_cache *cache, const hq_kv_attend_args *args, size_t *bytes);
 
 /* HQ_ERR_INVALID_ARG: null or misaligned pointers, sizes outside their ranges, q_heads not a multiple of
