@@ -492,7 +492,8 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
 
     table int32 [seqs][width], lens int32 [seqs] (tokens cached, the queries' own among them); q_start int32
     [seqs + 1] offsets of each sequence's queries (None: as many each); max_q, max_len bounds on a sequence's
-    queries and tokens (None: all queries, what the table's width or the weights hold).  weights float32
+    queries and tokens (None: all queries, what the table's width or the weights hold): further queries are not computed,
+    and a longer length counts as max_len.  weights float32
     [seqs][heads][>= max_len] gets each token's softmax weights added (and has the scores computed in two parts, so out may
     differ in its last bits).  Returns out ([queries][q heads][128], bf16 unless given)."""
     torch = _torch()
