@@ -379,6 +379,88 @@ int hq_kv_attend_workspace_size(const hq_kv_cache *cache, const hq_kv_attend_arg
 int hq_kv_attend(const hq_kv_cache *cache, const hq_kv_attend_args *args, void *workspace,
                  size_t workspace_bytes, hq_stream_t stream);
 
+/* hq_kv_attend for a tree of drafted tokens.  The last m cached tokens of a sequence are drafts, the tokens of its m
+ * queries in order, and parents[i] (DEVICE, int32 [total_q]) is the draft, counted within its sequence, that query i's
+ * draft follows; a value that is not in [0, i) means that it follows the n - m tokens held before the drafts.  Query i
+ * sees those and, of the drafts, its own and its ancestors; with window > 0 only the last `window` of what it sees.
+ * args->causal must not be 0 and args->weights must be NULL (a rejected draft's weights could not be taken back);
+ * args->max_q is at most 256.  Workspace: hq_kv_attend_workspace_size.  Errors as hq_kv_attend. */
+int hq_kv_attend_tree(const hq_kv_cache *cache, const hq_kv_attend_args *args, const int32_t *parents,
+                      void *workspace, size_t workspace_bytes, hq_stream_t stream);
+
+/* Places for tokens: pages come from, and go back to, a stack of free ones.  counts[b] > 0: sequence b gets that many
+ * more tokens; < 0: its last -counts[b] tokens go (all of them, if there are fewer) and the pages that they leave empty
+ * return, their table entries becoming -1.  Pages return from the last sequence's last to the first's first, an entry
+ * outside [0, pages) does not, and what the stack cannot hold is dropped; then sequences grow in order, each taking its
+ * pages from the top.  A sequence whose table is too narrow takes nothing; from the first that the stack cannot serve on,
+ * no sequence grows.  So a call with the counts that a call granted, negated, undoes it.
+ * Sequence b's new tokens are `slots` and `positions` q_start[b] .. q_start[b + 1] - 1 (q_start counts what was asked for): token i of them
+ * stands at position t = lens[b] + i in slot table[b][t / page] page + t mod page, or -1 if the sequence did not grow or
+ * the entry is outside [0, pages).  Places past the last have slot -1 and position 0.
+ * Asynchronous, allocates nothing, may be captured. */
+typedef struct {
+  int32_t *table;            /* DEVICE, [seqs][table_width], in and out                              */
+  int32_t *lens;             /* DEVICE, [seqs], in and out: tokens held (cut to 0 .. table_width page) */
+  const int32_t *counts;     /* DEVICE, [seqs]                                                       */
+  int32_t *free;             /* DEVICE, [pages], in and out: free[0 .. *free_count - 1] are free        */
+  int32_t *free_count;       /* DEVICE, in and out (cut to 0 .. pages)                               */
+  uint32_t seqs, table_width, pages, page;  /* page: tokens of a page, a power of two from 16 to 4096 */
+  uint64_t tokens;           /* places in slots and positions                                       */
+  int64_t *slots;            /* DEVICE, [tokens]                                                    */
+  int32_t *positions;        /* DEVICE or NULL, [tokens]                                            */
+  int32_t *q_start;          /* DEVICE, [seqs + 1]; saturates at 2^31 - 1                           */
+  int32_t *granted;          /* DEVICE, [seqs]: by how much the sequence's length changed              */
+} hq_kv_reserve_args;
+/* HQ_ERR_INVALID_ARG: null or misaligned pointers, a bad page, over 2^31 tokens, pages, or table_width page, a table of 2^31
+ * entries or more. */
+int hq_kv_reserve(const hq_kv_reserve_args *args, hq_stream_t stream);
+
+/* Acceptance of drafted tokens.  Draft i of a sequence's m drafts (its last m cached tokens, m and the offsets as in
+ * hq_kv_attend_tree) is token tokens[i] behind parents[i], and the model's choice behind it is target[i].  Draft 0, which
+ * an earlier step chose, is accepted; behind the accepted draft i the first draft j with parents[j] = i and
+ * tokens[j] = target[i] is, and so on.  The K and V of the accepted drafts move, head by head, to tokens n - m, n - m + 1, ...;
+ * those behind them are left as they are.  An absent page's draft becomes one that takes no part (zeros, K scales -0).
+ * path [seqs][max_q]: the accepted drafts, then -1; accepted [seqs]: how many; next [seqs]: the target behind the last
+ * (-1 without drafts); change [seqs]: accepted - m, the change of the sequence's length (hq_kv_reserve takes it).
+ * Only the first max_q drafts are looked at, at most 256.  lens is not changed. */
+typedef struct {
+  const int32_t *table;      /* DEVICE, [seqs][table_width]                                */
+  const int32_t *lens;       /* DEVICE, [seqs], the drafts among them                      */
+  const int32_t *q_start;    /* DEVICE, [seqs + 1], or NULL: total_q / seqs drafts each       */
+  const int32_t *tokens, *target, *parents;  /* DEVICE, [total_q]                           */
+  uint64_t total_q;
+  uint32_t seqs, table_width, max_q;
+  int32_t *path, *accepted, *next, *change;  /* DEVICE                                      */
+} hq_kv_accept_args;
+/* HQ_ERR_INVALID_ARG: null or misaligned pointers, a bad cache, max_q over 256, sizes outside hq_kv_attend's ranges,
+ * q_start == NULL with total_q not a multiple of seqs.  Asynchronous, allocates nothing, may be captured. */
+int hq_kv_accept(const hq_kv_cache *cache, const hq_kv_accept_args *args, hq_stream_t stream);
+
+/* Softmax attention within packed prompts, on queries, keys and values as they are: what a model computes for a whole
+ * prompt beside appending it to the cache.  Sequence b is rows start[b] .. start[b + 1] - 1 of q, k and v; query i of
+ * it sees its tokens up to i (all of them when causal == 0), and with window > 0 only the last `window` of those up to
+ * i.  Scores are scale q.k, then softcap tanh(score / softcap) when softcap > 0.  Query head j reads KV head
+ * j / (q_heads / heads).  Types: bf16; 128 values a head.  Products are bf16 x bf16 into binary32; the softmax's
+ * weights enter the second one as bf16, each off by at most 2^-8 of itself; scores, maxima, sums and outputs are
+ * binary32.  A value that a row does not see does not reach it, whatever it holds. */
+typedef struct {
+  const void *q, *k, *v;     /* DEVICE, 16-byte aligned: value c of head j of row i at q[i q_stride[0] + j q_stride[1] + c] */
+  void *out;                 /* DEVICE, [rows][q_heads][128], 16-byte aligned                       */
+  int32_t dtype, out_dtype;  /* dtype: HQ_BF16                                                      */
+  int64_t q_stride[2], k_stride[2], v_stride[2];  /* in values, multiples of 8                        */
+  uint64_t rows;
+  uint32_t q_heads, heads;   /* q_heads a multiple of heads                                         */
+  uint32_t seqs;
+  const int32_t *start;      /* DEVICE, seqs + 1 offsets that do not decrease (cut to [0, rows])        */
+  float scale, softcap;
+  int32_t causal;
+  uint32_t window;           /* 0: none                                                             */
+} hq_attend_prompt_args;
+/* Asynchronous, allocates nothing, may be captured.  HQ_ERR_INVALID_ARG: null or misaligned pointers, strides that are not
+ * multiples of 8, another dtype, sizes outside their ranges (2^30 rows, 2^28 rows times query heads), a scale or softcap as
+ * hq_kv_attend's.  Rows of `out` that no sequence names are not written. */
+int hq_attend_prompt(const hq_attend_prompt_args *args, hq_stream_t stream);
+
 /* Eviction by accumulated weight.  Of each (sequence, head)'s n tokens, m = min(n, budget) stay: the first
  * `sink`, the last `recent`, and of the others those of most weight (ties to the lowest index; NaN counts
  * least).  They move, in order, to tokens 0..m-1 of the pages of dst_table, which must not be pages that

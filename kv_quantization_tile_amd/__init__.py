@@ -6,8 +6,9 @@ fallback: if the library is missing the calls raise.
 
 Entry points mirror the C ABI: ``hq_encode``, ``hq_decode``, ``hq_rate``, ``hq_codes``,
 ``hq_status``, ``hq_fallbacks``, ``hq_workspace_size``, ``hq_stream_fixed_bytes``, ``hq_encode_bound``,
-``hq_version``, ``hq_strerror``; the paged SRFT cache: ``hq_kv_cache``, ``hq_kv_append``, ``hq_kv_read``,
-``hq_kv_attend``, ``hq_kv_evict``.
+``hq_version``, ``hq_strerror``; the paged SRFT cache: ``hq_kv_cache``, ``hq_kv_reserve``, ``hq_kv_append``,
+``hq_kv_read``, ``hq_kv_attend`` (with ``parents``: ``hq_kv_attend_tree``), ``hq_kv_accept``, ``hq_kv_evict``; beside it
+``hq_attend_prompt``.
 """
 from __future__ import annotations
 
@@ -27,7 +28,8 @@ EXPORTS = ("hq_version", "hq_strerror", "hq_workspace_size", "hq_stream_fixed_by
            "hq_encode", "hq_encode_noalloc", "hq_decode", "hq_status", "hq_fallbacks", "hq_codes",
            "hq_gemv_workspace_size", "hq_gemv",
            "hq_haar_matrix", "hq_rotate", "hq_srft_encode", "hq_srft_decode",
-           "hq_kv_append", "hq_kv_read", "hq_kv_attend_workspace_size", "hq_kv_attend", "hq_kv_evict")
+           "hq_kv_append", "hq_kv_read", "hq_kv_attend_workspace_size", "hq_kv_attend", "hq_kv_attend_tree", "hq_kv_evict",
+           "hq_kv_reserve", "hq_kv_accept", "hq_attend_prompt")
 
 
 class HqParams(ctypes.Structure):
@@ -58,6 +60,28 @@ class HqKvAttendArgs(ctypes.Structure):
                 ("q_start", ctypes.c_void_p), ("table", ctypes.c_void_p), ("table_width", ctypes.c_uint32),
                 ("lens", ctypes.c_void_p), ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("causal", ctypes.c_int32),
                 ("window", ctypes.c_uint32), ("weights", ctypes.c_void_p), ("weights_stride", ctypes.c_uint64)]
+
+
+class HqKvReserveArgs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("counts", ctypes.c_void_p), ("free", ctypes.c_void_p),
+                ("free_count", ctypes.c_void_p), ("seqs", ctypes.c_uint32), ("table_width", ctypes.c_uint32), ("pages", ctypes.c_uint32),
+                ("page", ctypes.c_uint32), ("tokens", ctypes.c_uint64), ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p), ("granted", ctypes.c_void_p)]
+
+
+class HqKvAcceptArgs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("target", ctypes.c_void_p), ("parents", ctypes.c_void_p), ("total_q", ctypes.c_uint64), ("seqs", ctypes.c_uint32),
+                ("table_width", ctypes.c_uint32), ("max_q", ctypes.c_uint32), ("path", ctypes.c_void_p), ("accepted", ctypes.c_void_p),
+                ("next", ctypes.c_void_p), ("change", ctypes.c_void_p)]
+
+
+class HqAttendPromptArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("out", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2),
+                ("v_stride", ctypes.c_int64 * 2), ("rows", ctypes.c_uint64), ("q_heads", ctypes.c_uint32), ("heads", ctypes.c_uint32),
+                ("seqs", ctypes.c_uint32), ("start", ctypes.c_void_p), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("causal", ctypes.c_int32), ("window", ctypes.c_uint32)]
 
 
 class HqKvEvictArgs(ctypes.Structure):
@@ -108,7 +132,11 @@ def lib():
         L.hq_kv_read.argtypes = [P, P, u64, P, P, i32, P]
         L.hq_kv_attend_workspace_size.argtypes = [P, P, ctypes.POINTER(sz)]
         L.hq_kv_attend.argtypes = [P, P, P, sz, P]
+        L.hq_kv_attend_tree.argtypes = [P, P, P, P, sz, P]
         L.hq_kv_evict.argtypes = [P, P, P]
+        L.hq_kv_reserve.argtypes = [P, P]
+        L.hq_kv_accept.argtypes = [P, P, P]
+        L.hq_attend_prompt.argtypes = [P, P]
         for name in EXPORTS:
             getattr(L, name).restype = getattr(L, name).restype or ctypes.c_int
         _lib = L
@@ -487,7 +515,7 @@ def hq_kv_read(cache, slots, bits: int = 4, seed: int = 0, lam_k=None, lam_v=Non
 
 def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, bits: int = 4, seed: int = 0, lam_k=None,
                  lam_v=None, scale=None, causal: bool = True, window: int = 0, softcap: float = 0.0, weights=None, out=None,
-                 ws=None, stream=None):
+                 ws=None, stream=None, parents=None):
     """Softmax attention of q ([queries][q heads][128] bf16 or float32, any strides but the last) over the cache.
 
     table int32 [seqs][width], lens int32 [seqs] (tokens cached, the queries' own among them); q_start int32
@@ -495,7 +523,11 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
     queries and tokens (None: all queries, what the table's width or the weights hold): further queries are not computed,
     and a longer length counts as max_len.  weights float32
     [seqs][heads][>= max_len] gets each token's softmax weights added (and has the scores computed in two parts, so out may
-    differ in its last bits).  Returns out ([queries][q heads][128], bf16 unless given)."""
+    differ in its last bits).  Returns out ([queries][q heads][128], bf16 unless given).
+
+    parents int32 [queries] makes the queries a tree of drafted tokens, a sequence's last cached ones (C: hq_kv_attend_tree): draft
+    parents[i] of the sequence comes before draft i, -1 for one that follows the held tokens.  A draft sees the held tokens, its
+    ancestors and itself, and with a window the last `window` of those.  At most 256 drafts of a sequence are computed; no weights."""
     torch = _torch()
     c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
     dev = cache.device
@@ -510,6 +542,12 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
         _check_tensor(q_start, "q_start", torch.int32, (seqs + 1,), dev)
     if max_q is None:
         max_q = total if q_start is not None else total // max(seqs, 1)
+        if parents is not None:
+            max_q = min(max_q, 256)
+    if parents is not None:
+        _check_tensor(parents, "parents", torch.int32, (total,), dev)
+        if not causal or weights is not None or max_q > 256:
+            raise ValueError("drafts (parents) attend causally, without weights, at most 256 (max_q) a sequence")
     if out is None:
         out = _empty((total, heads, 128), torch.bfloat16, dev, stream)
     else:
@@ -533,7 +571,118 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
         ws = _empty(need.value, torch.uint8, dev, stream)
     elif not (ws.is_contiguous() and ws.device == dev and ws.dtype == torch.uint8):
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
-    _launch("hq_kv_attend", dev, stream, L.hq_kv_attend, cp, ap, ws.data_ptr(), ws.numel())
+    if parents is None:
+        _launch("hq_kv_attend", dev, stream, L.hq_kv_attend, cp, ap, ws.data_ptr(), ws.numel())
+    else:
+        _launch("hq_kv_attend", dev, stream, L.hq_kv_attend_tree, cp, ap, parents.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+def _out(t, name, shape, dtype, device, stream):
+    """The caller's output buffer, checked, or one of the call's own."""
+    if t is None:
+        return _empty(shape, dtype, device, stream)
+    _check_tensor(t, name, dtype, shape, device)
+    return t
+
+
+def hq_kv_reserve(table, lens, counts, free, free_count, page: int, tokens: int, slots=None, positions=None, q_start=None, granted=None,
+                  stream=None):
+    """Places for the sequences' new tokens, or their last tokens' places back.
+
+    table int32 [seqs][width] and lens int32 [seqs] are updated: sequence b gets counts[b] (int32 [seqs]) more tokens, its pages
+    taken from the stack free[:free_count] (int32 [pages], int32 [1], updated), or loses its last -counts[b], the pages that they
+    leave empty returning and their entries becoming -1.  A sequence whose table is too narrow gets nothing; from the first one that
+    the stack cannot serve on, no sequence grows.  `tokens` is the number of places to fill in (at least the sum of the positive counts,
+    or what a captured graph has room for).  Returns (slots int64 [tokens] for hq_kv_append, -1 for a token that got no place and past the last one;
+    positions int32 [tokens]; q_start int32 [seqs + 1] for hq_kv_attend; granted int32 [seqs], each length's change)."""
+    torch = _torch()
+    if not table.is_cuda or table.dim() != 2:
+        raise TypeError("table must be an int32 CUDA tensor [seqs][width]")
+    dev, i32 = table.device, torch.int32
+    seqs, width = table.shape
+    if free.dim() != 1:
+        raise ValueError("free must be [pages]")
+    pages = free.shape[0]
+    _check_tensor(table, "table", i32, (seqs, width), dev)
+    _check_tensor(lens, "lens", i32, (seqs,), dev)
+    _check_tensor(counts, "counts", i32, (seqs,), dev)
+    _check_tensor(free, "free", i32, (pages,), dev)
+    _check_tensor(free_count, "free_count", i32, (1,), dev)
+    tokens, page = _size(tokens, "tokens"), _size(page, "page")
+    slots = _out(slots, "slots", (tokens,), torch.int64, dev, stream)
+    positions = _out(positions, "positions", (tokens,), i32, dev, stream)
+    q_start = _out(q_start, "q_start", (seqs + 1,), i32, dev, stream)
+    granted = _out(granted, "granted", (seqs,), i32, dev, stream)
+    a = HqKvReserveArgs(table.data_ptr(), lens.data_ptr(), counts.data_ptr(), free.data_ptr(), free_count.data_ptr(), seqs, width, pages, page,
+                        tokens, slots.data_ptr(), positions.data_ptr(), q_start.data_ptr(), granted.data_ptr())
+    _launch("hq_kv_reserve", dev, stream, lib().hq_kv_reserve, ctypes.byref(a))
+    return slots, positions, q_start, granted
+
+
+def hq_kv_accept(cache, table, lens, tokens, target, parents, q_start=None, max_q=None, bits: int = 4, path=None, accepted=None, next=None,
+                 change=None, stream=None):
+    """Accept drafted tokens (a sequence's last cached ones, as hq_kv_attend's with `parents`) and move them up in the cache.
+
+    tokens, target, parents int32 [drafts]: each draft's token, the model's choice behind it, and the draft before it.  Draft 0 of a
+    sequence is accepted, and behind an accepted one the first of its children that is its target.  Their K and V move, in order, to the
+    drafts' first places.  max_q bounds a sequence's drafts (None: all, at most 256); further ones are not looked at.  Returns (path int32
+    [seqs][max_q], -1 past the end; accepted int32 [seqs]; next int32 [seqs], the target behind the last, -1 without drafts; change
+    int32 [seqs], accepted less drafts: what hq_kv_reserve takes to give the others' places back)."""
+    torch = _torch()
+    c, _ = _cache_arg(cache, bits, 0, None, None)
+    dev, i32 = cache.device, torch.int32
+    seqs, width, total = lens.numel(), table.shape[-1], tokens.numel()
+    _check_tensor(lens, "lens", i32, (seqs,), dev)
+    _check_tensor(table, "table", i32, (seqs, width), dev)
+    _check_tensor(tokens, "tokens", i32, (total,), dev)
+    _check_tensor(target, "target", i32, (total,), dev)
+    _check_tensor(parents, "parents", i32, (total,), dev)
+    if q_start is not None:
+        _check_tensor(q_start, "q_start", i32, (seqs + 1,), dev)
+    if max_q is None:
+        max_q = min(total if q_start is not None else total // max(seqs, 1), 256)
+    if not 0 <= max_q <= 256:
+        raise ValueError("at most 256 drafts (max_q) a sequence")
+    path = _out(path, "path", (seqs, max_q), i32, dev, stream)
+    accepted = _out(accepted, "accepted", (seqs,), i32, dev, stream)
+    next = _out(next, "next", (seqs,), i32, dev, stream)
+    change = _out(change, "change", (seqs,), i32, dev, stream)
+    a = HqKvAcceptArgs(table.data_ptr(), lens.data_ptr(), q_start.data_ptr() if q_start is not None else None, tokens.data_ptr(), target.data_ptr(),
+                       parents.data_ptr(), total, seqs, width, max_q, path.data_ptr(), accepted.data_ptr(), next.data_ptr(), change.data_ptr())
+    _launch("hq_kv_accept", dev, stream, lib().hq_kv_accept, ctypes.byref(c), ctypes.byref(a))
+    return path, accepted, next, change
+
+
+_Strides2 = ctypes.c_int64 * 2
+
+
+def hq_attend_prompt(q, k, v, start, scale=None, causal: bool = True, window: int = 0, softcap: float = 0.0, out=None, stream=None):
+    """Softmax attention within packed prompts: q [rows][q heads][128], k and v [rows][heads][128], bf16, rows 16-byte aligned (any
+    strides that are multiples of 8 values); sequence b is rows start[b] .. start[b + 1] - 1 (int32 [seqs + 1]).  Masks, scale and cap as
+    hq_kv_attend's, whose form on the cache a later step uses.  Returns out ([rows][q heads][128], bf16 unless given)."""
+    torch = _torch()
+    if not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    dev = q.device
+    qs, ks, vs = _row_strides(q, "q", None, dev), _row_strides(k, "k", None, dev), _row_strides(v, "v", k.shape[1], dev)
+    rows, q_heads, _ = q.shape
+    heads = k.shape[1]
+    if k.shape[0] != rows or v.shape[0] != rows or heads == 0 or q_heads == 0 or q_heads % heads:
+        raise ValueError("q, k and v must have one length, and q heads a multiple of the heads")
+    if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise TypeError("q, k and v must be bfloat16")
+    if start.dim() != 1 or start.shape[0] == 0:
+        raise ValueError("start must be int32 [seqs + 1]")
+    _check_tensor(start, "start", torch.int32, start.shape, dev)
+    if out is None:
+        out = _empty((rows, q_heads, 128), torch.bfloat16, dev, stream)
+    else:
+        _check_tensor(out, "out", out.dtype, (rows, q_heads, 128), dev)
+    a = HqAttendPromptArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), HQ_BF16, _dtype_code(out), _Strides2(qs[0], qs[1]),
+                           _Strides2(ks[0], ks[1]), _Strides2(vs[0], vs[1]), rows, q_heads, heads, start.shape[0] - 1, start.data_ptr(),
+                           128 ** -0.5 if scale is None else scale, softcap, 1 if causal else 0, _size(window, "window"))
+    _launch("hq_attend_prompt", dev, stream, lib().hq_attend_prompt, ctypes.byref(a))
     return out
 
 

@@ -10,7 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libhq.so")
 BUILD = os.path.join(HERE, "_build")
-SOURCES = ["hq_kernels.hip", "hq_api.hip", "hq_rotate.hip", "hq_srft.hip", "hq_kv.hip", "hq_attend.hip"]
+SOURCES = ["hq_kernels.hip", "hq_api.hip", "hq_rotate.hip", "hq_srft.hip", "hq_kv.hip", "hq_attend.hip",
+           "hq_kv_steps.hip", "hq_prompt.hip"]
 
 # Floating-point flags: every binary32 operation that decides an integer code must be rounded
 # exactly once in program order (no contraction into FMA, no fast-math, denormals kept, correctly

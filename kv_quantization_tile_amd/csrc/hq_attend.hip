@@ -45,6 +45,7 @@ struct AttendArgs {
   const void* q;
   void* out;
   const int32_t *q_start, *table, *lens;
+  const int32_t* parents;  // of drafted tokens, or null
   float* weights;
   uint64_t wstride, total_q;
   int64_t qt, qh;  // strides of q in values
@@ -106,7 +107,9 @@ __device__ __forceinline__ void visible(const AttendArgs& a, const Seq& s, int32
   *lo = l > h ? h : (int32_t)l;
   *hi = h;
 }
-// Tokens that some row of [r0, r0 + count) sees, as one range.
+// Tokens that some row of [r0, r0 + count) sees, as one range.  In a tree, draft i sees drafts up to itself, and no fewer held
+// tokens than the root.
+template <bool TREE>
 __device__ __forceinline__ void rows_range(const AttendArgs& a, const Seq& s, uint32_t r0, uint32_t count, int32_t* lo, int32_t* hi) {
   const uint32_t rows = (uint32_t)s.m * a.group;
   if (r0 >= rows) {
@@ -115,19 +118,63 @@ __device__ __forceinline__ void rows_range(const AttendArgs& a, const Seq& s, ui
   }
   const uint32_t r1 = r0 + count < rows ? r0 + count - 1u : rows - 1u;
   int32_t l0, h0, l1, h1;
-  visible(a, s, (int32_t)query_of(a, r0), &l0, &h0);
+  visible(a, s, TREE ? 0 : (int32_t)query_of(a, r0), &l0, &h0);
   visible(a, s, (int32_t)query_of(a, r1), &l1, &h1);
   *lo = l0;
   *hi = h1;
 }
 
-// Tokens that every row of [r0, r0 + count) sees; none if some of the rows do not exist.
+// Tokens that every row of [r0, r0 + count) sees; none if some of the rows do not exist.  In a tree, held ones: those that
+// a draft as deep as its index sees.
+template <bool TREE>
 __device__ __forceinline__ void rows_common(const AttendArgs& a, const Seq& s, uint32_t r0, uint32_t count, int32_t* lo, int32_t* hi) {
   *lo = *hi = 0;
   if (r0 + count > (uint32_t)s.m * a.group) return;
   int32_t x;
   visible(a, s, (int32_t)query_of(a, r0 + count - 1u), lo, &x);
   visible(a, s, (int32_t)query_of(a, r0), &x, hi);
+  if (TREE) *hi = s.back > 0 ? s.back : 0;
+}
+
+// A tree of drafted tokens: the last tokens of a sequence are its queries' own, and query i sees, of them, itself and
+// its ancestors.  parents[i] is the draft that draft i follows; one that is not before i means that draft i follows the held
+// tokens.  A bit each for up to kMaxTree drafts, for the queries of one tile.
+constexpr int kMaxTree = 256;
+template <int QUERIES>
+struct Tree {
+  int32_t parent[kMaxTree];
+  uint32_t seen[QUERIES][kMaxTree / 32];
+  uint32_t depth[QUERIES];
+};
+// Walks up from queries [i0, i0 + count) with the workgroup's threads.  With a window, of a query's path the last `window`.
+template <int QUERIES>
+__device__ __forceinline__ void climb(const AttendArgs& a, const Seq& s, uint32_t i0, uint32_t count, Tree<QUERIES>& t) {
+  for (uint32_t i = threadIdx.x; i < i0 + count; i += blockDim.x) {
+    const int32_t p = a.parents[(uint64_t)s.q0 + i];
+    t.parent[i] = p >= 0 && p < (int32_t)i ? p : -1;
+  }
+  __syncthreads();
+  for (uint32_t q = threadIdx.x; q < count; q += blockDim.x) {
+#pragma unroll
+    for (int w = 0; w < kMaxTree / 32; ++w) t.seen[q][w] = 0;
+    uint32_t depth = 0;
+    for (int32_t i = (int32_t)(i0 + q); i >= 0; i = t.parent[i], ++depth)
+      if (a.window == 0 || depth < a.window) t.seen[q][i >> 5] |= 1u << (i & 31);
+    t.depth[q] = depth - 1u;
+  }
+  __syncthreads();
+}
+// The first held token that a query of this depth sees.
+__device__ __forceinline__ int32_t tree_lo(const AttendArgs& a, const Seq& s, uint32_t depth) {
+  const int64_t l = a.window ? (int64_t)s.back + depth + 1 - (int64_t)a.window : 0;
+  return l < 0 ? 0 : l > 0x7FFFFFFF ? 0x7FFFFFFF : (int32_t)l;
+}
+// Whether a query sees token `tok`, which some query of its tile sees.
+template <int QUERIES>
+__device__ __forceinline__ bool tree_sees(const Tree<QUERIES>& t, int32_t back, uint32_t query, int32_t lo, int32_t tok) {
+  if (tok < back) return tok >= lo;
+  const uint32_t j = (uint32_t)(tok - back) & (kMaxTree - 1);
+  return (t.seen[query][j >> 5] >> (j & 31u)) & 1u;
 }
 
 __device__ __forceinline__ float swap16_max(float x) {
@@ -489,7 +536,7 @@ __device__ __forceinline__ int32_t page_of(const AttendArgs& a, uint32_t b, int3
 // wavefront a SIMD (128 registers, some spilled) took 160 us.  Scales out of the ordinary are looked for where the codes
 // beside them are first used: one look at a step's scales waits for its last load (151 us).  One sequence of 301 tokens
 // takes 10.5 us: about 2 until the codes are asked for, 1.5 for the rows, 4.2 for three turns, 1 for the join.
-template <int BITS, bool PREC>
+template <int BITS, bool PREC, bool TREE>
 __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kernel(AttendArgs a, Tables K) {
   __shared__ __align__(16) float s_o[kAttWaves][16][kPad];
   __shared__ __align__(16) _Float16 s_q[PREC ? 2 : 1][16][kD + 8];
@@ -500,7 +547,7 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
   const uint32_t r0 = last_tile(a, s), rows = (uint32_t)s.m * a.group - r0;  // of this tile
   if (rows == 0 || rows > 16u) return;
   int32_t lo, hi;
-  rows_range(a, s, r0, 16, &lo, &hi);
+  rows_range<TREE>(a, s, r0, 16, &lo, &hi);
   int32_t t0 = (int32_t)(split * a.lchunk), t1 = t0 + (int32_t)a.lchunk;
   t0 = t0 > (lo & ~15) ? t0 : lo & ~15;
   t1 = t1 < hi ? t1 : hi;
@@ -546,9 +593,21 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
   }
   const float qf = s_f[n];
   int32_t row_lo = 0, row_hi = 0, all_lo = hi, all_hi = lo;
-  if (n < rows) visible(a, s, (int32_t)query_of(a, r0 + n), &row_lo, &row_hi);
+  __shared__ Tree<TREE ? 16 : 1> s_tree;
+  uint32_t query = 0;
+  if constexpr (TREE) {
+    // splits of held tokens alone need no tree, unless a window ends among them
+    if (a.window || t1 > s.back) {
+      const uint32_t i0 = query_of(a, r0);
+      climb(a, s, i0, query_of(a, r0 + rows - 1u) - i0 + 1u, s_tree);
+      if (n < rows) query = query_of(a, r0 + n) - i0;
+      row_lo = tree_lo(a, s, s_tree.depth[query]);
+    }
+  } else {
+    if (n < rows) visible(a, s, (int32_t)query_of(a, r0 + n), &row_lo, &row_hi);
+  }
   // the tokens every existing row sees need no mask (rows past the last are products with zero)
-  if (rows) rows_common(a, s, r0, rows, &all_lo, &all_hi);
+  if (rows) rows_common<TREE>(a, s, r0, rows, &all_lo, &all_hi);
 
   float m = kLowest, sum = 0.0f, poison = 0.0f;
   f32x4 o[8];
@@ -594,7 +653,8 @@ __global__ __launch_bounds__(kAttBlock, BITS == 4 ? 3 : 2) void attend_few_kerne
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int32_t tok = t + 16 * (i >> 2) + 4 * (int32_t)b4 + (i & 3);
-        if (!there[i >> 2] || tok < row_lo || tok >= row_hi || tok >= t1) sc[i] = -__builtin_inff();
+        const bool sees = TREE ? tree_sees(s_tree, s.back, query, row_lo, tok) : tok >= row_lo && tok < row_hi;
+        if (!there[i >> 2] || !sees || tok >= t1) sc[i] = -__builtin_inff();
       }
     }
     if (a.scores && n < rows) {
@@ -726,7 +786,8 @@ __global__ __launch_bounds__(kAttBlock) void combine_kernel(AttendArgs a, Tables
   const uint32_t r = r0 + row, rows = (uint32_t)s.m * a.group;
   if (r >= rows || (LIGHT && rows - r0 > 16u)) return;
   int32_t lo, hi;
-  rows_range(a, s, r0, tile_rows, &lo, &hi);
+  if (a.parents) rows_range<true>(a, s, r0, tile_rows, &lo, &hi);
+  else rows_range<false>(a, s, r0, tile_rows, &lo, &hi);
   if (a.pages == 0) hi = lo;
   const uint32_t s0 = hi > lo ? (uint32_t)lo / chunk : 0u, s1 = hi > lo ? ((uint32_t)hi + chunk - 1u) / chunk : 0u;
   float m = kLowest, sum = 0.0f, y[8];
@@ -777,7 +838,7 @@ __global__ __launch_bounds__(kAttBlock) void weights_few_kernel(AttendArgs a, ui
   const uint32_t rows = (uint32_t)s.m * a.group;
   const int32_t t = (int32_t)((blockIdx.x % blocks) * kAttBlock + threadIdx.x);
   int32_t lo, hi;
-  rows_range(a, s, 0, 16, &lo, &hi);
+  rows_range<false>(a, s, 0, 16, &lo, &hi);
   if (a.pages == 0 || t < (lo & ~15) || t >= hi) return;
   float w = 0.0f;
   for (uint32_t r = 0; r < rows; ++r) {
@@ -892,7 +953,7 @@ struct Stage {
 template <bool PREC>
 constexpr size_t many_lds() { return sizeof(Stage<PREC>) * (PREC ? 1 : 2); }
 
-template <int BITS, bool PREC, int R>
+template <int BITS, bool PREC, int R, bool TREE>
 __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a, Tables K) {
   constexpr int32_t kTok = 16 * kManyWaves;
   extern __shared__ __align__(16) uint8_t raw[];
@@ -914,9 +975,9 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
   const uint32_t rows = (uint32_t)s.m * a.group, r0 = (f - a.first[b]) * a.tile_rows, w0 = r0 + wave * 16u * R;
   if (r0 >= rows) return;
   int32_t lo, hi, wlo, whi, all_lo, all_hi;
-  rows_range(a, s, r0, a.tile_rows, &lo, &hi);
-  rows_range(a, s, w0, 16u * R, &wlo, &whi);
-  rows_common(a, s, w0, 16u * R, &all_lo, &all_hi);
+  rows_range<TREE>(a, s, r0, a.tile_rows, &lo, &hi);
+  rows_range<TREE>(a, s, w0, 16u * R, &wlo, &whi);
+  rows_common<TREE>(a, s, w0, 16u * R, &all_lo, &all_hi);
   int32_t t0 = (int32_t)(split * chunk), t1 = t0 + (int32_t)chunk;
   t0 = t0 > (lo & ~15) ? t0 : lo & ~15;
   t1 = t1 < hi ? t1 : hi;
@@ -987,6 +1048,15 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
   if (t < t1) load(t + mine, page);
   int32_t next = entry_of(a, b, t + kTok + mine, t1);
 
+  __shared__ Tree<TREE ? 16 * kManyWaves * R : 1> s_tree;
+  uint32_t query[R];
+  const bool climbs = TREE && (a.window || t1 > s.back);  // as for few rows
+  const uint32_t i0 = query_of(a, r0);
+  if constexpr (TREE) {
+    const uint32_t last = (r0 + a.tile_rows < rows ? r0 + a.tile_rows : rows) - 1u;
+    if (climbs) climb(a, s, i0, query_of(a, last) - i0 + 1u, s_tree);
+  }
+
   const bool cap = a.cap_in > 0.0f;
   f16x8 qh[R][4], ql[R][4];
   float qf[R], eff[R], m[R], sum[R], poison[R];
@@ -1007,7 +1077,16 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
     m[q] = kLowest;
     sum[q] = poison[q] = 0.0f;
     row_lo[q] = row_hi[q] = 0;
-    if (w0 + 16u * q + n < rows) visible(a, s, (int32_t)query_of(a, w0 + 16u * q + n), &row_lo[q], &row_hi[q]);
+    query[q] = 0;
+    if constexpr (TREE) {
+      if (climbs && w0 + 16u * q + n < rows) {
+        query[q] = query_of(a, w0 + 16u * q + n) - i0;
+        row_lo[q] = tree_lo(a, s, s_tree.depth[query[q]]);
+      }
+      row_hi[q] = w0 + 16u * q + n < rows ? 1 : 0;  // rows that are not there see nothing
+    } else {
+      if (w0 + 16u * q + n < rows) visible(a, s, (int32_t)query_of(a, w0 + 16u * q + n), &row_lo[q], &row_hi[q]);
+    }
     ones[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[q][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -1159,7 +1238,8 @@ __global__ __launch_bounds__(kManyBlock, 2) void attend_many_kernel(AttendArgs a
             for (int i = 0; i < 4; ++i) {
               const int32_t tok = tw + 16 * u + 4 * (int32_t)b4 + i;
               const uint32_t fl = (u ? f1.x : f0.x) >> (4 * b4 + i);
-              if ((fl & 0x10000u) || tok < row_lo[q] || tok >= row_hi[q] || tok >= t1) sc[q][u][i] = -__builtin_inff();
+              const bool sees = TREE ? row_hi[q] && tree_sees(s_tree, s.back, query[q], row_lo[q], tok) : tok >= row_lo[q] && tok < row_hi[q];
+              if ((fl & 0x10000u) || !sees || tok >= t1) sc[q][u][i] = -__builtin_inff();
               else if (fl & 1u) poison[q] = __builtin_nanf("");
             }
       }
@@ -1327,9 +1407,9 @@ __global__ __launch_bounds__(kAttBlock, 2) void weights_many_kernel(AttendArgs a
     __syncthreads();
     if (r0 + 16 < r1) fetch(r0 + 16);
     int32_t lo, hi, all_lo, all_hi;
-    rows_range(a, s, r0, 16, &lo, &hi);
+    rows_range<false>(a, s, r0, 16, &lo, &hi);
     if (t >= hi || t + 64 <= lo) continue;
-    rows_common(a, s, r0, 16, &all_lo, &all_hi);
+    rows_common<false>(a, s, r0, 16, &all_lo, &all_hi);
     f16x8 oh[4], ol[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -1472,13 +1552,13 @@ int plan_of(const hq_kv_cache& c, const hq_kv_attend_args& g, Plan* out) {
   return HQ_OK;
 }
 
-template <int BITS, bool PREC, int R>
+template <int BITS, bool PREC, int R, bool TREE>
 hipError_t launch_many(const AttendArgs& a, const Tables& T, uint32_t grid, hipStream_t st) {
   // more dynamic LDS than the default limit: asked for once per kernel (the attribute holds for every device)
-  static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_many_kernel<BITS, PREC, R>),
+  static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_many_kernel<BITS, PREC, R, TREE>),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)many_lds<PREC>());
   if (set != hipSuccess) return set;
-  hipLaunchKernelGGL((attend_many_kernel<BITS, PREC, R>), dim3(grid), dim3(kManyBlock), many_lds<PREC>(), st, a, T);
+  hipLaunchKernelGGL((attend_many_kernel<BITS, PREC, R, TREE>), dim3(grid), dim3(kManyBlock), many_lds<PREC>(), st, a, T);
   return hipSuccess;
 }
 
@@ -1502,13 +1582,18 @@ hipError_t launch_attend(const AttendArgs& a, const Tables& T, const Plan& p, hi
   }
   if (p.few || p.light) {
     const dim3 grid(sh * a.lsplits);
-    if (prec) hipLaunchKernelGGL((attend_few_kernel<BITS, true>), grid, block, 0, st, a, T);
-    else hipLaunchKernelGGL((attend_few_kernel<BITS, false>), grid, block, 0, st, a, T);
+    if (a.parents) hipLaunchKernelGGL((attend_few_kernel<BITS, false, true>), grid, block, 0, st, a, T);
+    else if (prec) hipLaunchKernelGGL((attend_few_kernel<BITS, true, false>), grid, block, 0, st, a, T);
+    else hipLaunchKernelGGL((attend_few_kernel<BITS, false, false>), grid, block, 0, st, a, T);
     if (a.lsplits > 1) launch_combine<BITS, true>(a, T, sh, rows < 16 ? rows : 16, st);
   }
   if (p.grid) {
-    const hipError_t e = a.tile_rows == 128 ? prec ? launch_many<BITS, true, 1>(a, T, p.grid, st) : launch_many<BITS, false, 1>(a, T, p.grid, st)
-                                            : prec ? launch_many<BITS, true, 2>(a, T, p.grid, st) : launch_many<BITS, false, 2>(a, T, p.grid, st);
+    const hipError_t e = a.parents          ? a.tile_rows == 128 ? launch_many<BITS, false, 1, true>(a, T, p.grid, st)
+                                                                 : launch_many<BITS, false, 2, true>(a, T, p.grid, st)
+                         : a.tile_rows == 128 ? prec ? launch_many<BITS, true, 1, false>(a, T, p.grid, st)
+                                                     : launch_many<BITS, false, 1, false>(a, T, p.grid, st)
+                         : prec ? launch_many<BITS, true, 2, false>(a, T, p.grid, st)
+                                : launch_many<BITS, false, 2, false>(a, T, p.grid, st);
     if (e != hipSuccess) return e;
     // of split tiles there are half as many as parts
     const uint32_t items = a.bound * a.heads, per = rows < a.tile_rows ? (rows + 15) / 16 * 16 : a.tile_rows;
@@ -1533,21 +1618,8 @@ int check_attend(const hq_kv_cache* cache, const hq_kv_attend_args* g) {
   return HQ_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int hq_kv_attend_workspace_size(const hq_kv_cache* cache, const hq_kv_attend_args* args, size_t* bytes) {
-  if (!bytes) return HQ_ERR_INVALID_ARG;
-  if (int rc = check_attend(cache, args)) return rc;
-  Plan p;
-  if (int rc = plan_of(*cache, *args, &p)) return rc;
-  *bytes = p.bytes;
-  return HQ_OK;
-}
-
-int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* workspace, size_t workspace_bytes,
-                 hq_stream_t stream) {
+int attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, const int32_t* parents, void* workspace, size_t workspace_bytes,
+           hq_stream_t stream) {
   if (int rc = check_attend(cache, args)) return rc;
   const hq_kv_attend_args& g = *args;
   if ((g.q_dtype != HQ_F32 && g.q_dtype != HQ_BF16) || (g.out_dtype != HQ_F32 && g.out_dtype != HQ_BF16)) return HQ_ERR_INVALID_ARG;
@@ -1572,6 +1644,7 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   a.q_start = g.q_start;
   a.table = g.table;
   a.lens = g.lens;
+  a.parents = parents;
   a.weights = g.weights;
   a.wstride = g.weights_stride;
   a.total_q = g.total_q;
@@ -1624,6 +1697,31 @@ int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* 
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const hipError_t e = cache->bits == 4 ? launch_attend<4>(a, T, p, st) : launch_attend<8>(a, T, p, st);
   return e == hipSuccess ? HQ_OK : HQ_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hq_kv_attend_workspace_size(const hq_kv_cache* cache, const hq_kv_attend_args* args, size_t* bytes) {
+  if (!bytes) return HQ_ERR_INVALID_ARG;
+  if (int rc = check_attend(cache, args)) return rc;
+  Plan p;
+  if (int rc = plan_of(*cache, *args, &p)) return rc;
+  *bytes = p.bytes;
+  return HQ_OK;
+}
+
+int hq_kv_attend(const hq_kv_cache* cache, const hq_kv_attend_args* args, void* workspace, size_t workspace_bytes,
+                 hq_stream_t stream) {
+  return attend(cache, args, nullptr, workspace, workspace_bytes, stream);
+}
+
+int hq_kv_attend_tree(const hq_kv_cache* cache, const hq_kv_attend_args* args, const int32_t* parents, void* workspace,
+                      size_t workspace_bytes, hq_stream_t stream) {
+  if (!args || !args->causal || args->weights || args->max_q > (uint32_t)kMaxTree) return HQ_ERR_INVALID_ARG;
+  if (((uintptr_t)parents & 3u) || (!parents && args->total_q && args->seqs && args->max_q)) return HQ_ERR_INVALID_ARG;
+  return attend(cache, args, parents, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,428 @@
+// hq_prompt.hip -- softmax attention within packed prompts, on bf16 queries, keys and values.
+//
+//   o_i = sum_t p_it v_t,  p_it = exp(s_it - m_i) / sum_u exp(s_iu - m_i),  s_it = scale q_i.k_t (capped)
+//
+// in one pass over the keys: a running reference m (at most 2^6 below the running maximum, in powers of two), the
+// running sum, and the output in registers.
+//
+// A row is one (query, head of the KV head's group), so that a tile of rows spans few queries and the causal
+// mask wastes little.  A wavefront owns 32 rows; S^t = K Q^t on v_mfma_f32_32x32x16_bf16 leaves lane (n, h)
+// (n = lane mod 32, h = lane / 32) the scores of row n for tokens 8 i + 4 h + 0..3 of 32: register for
+// register the operand P^t of O^t = V^t P^t, if V^t is read for the same order of tokens.  K and V lie in LDS as they
+// lie in memory, a token a row of 256 bytes; V^t comes out of it by transposing reads (four tokens of 16 columns to
+// 16 lanes).  A row's 16-byte pieces are permuted so that a read meets every bank once: K's by the token modulo 16
+// (a read takes one piece of 16 tokens), V's by the token modulo 4 (a read takes four pieces of four tokens).
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "../../include/hq.h"
+#include "hq_kv_device.h"
+#include "hq_kv_internal.h"
+
+namespace hq_kv {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kPromptSlack = 6.0f;                 // the reference may lag the maximum by this much (log2)
+constexpr float kPromptLowest = -3.402823466e38f;    // the reference before the first score
+constexpr int kPromptTok = 64;                       // tokens of a step
+constexpr uint32_t kPromptTile = kPromptTok * 256u;  // their bytes, K or V
+
+struct PromptArgs {
+  const uint16_t *q, *k, *v;
+  void* out;
+  const int32_t* start;
+  int64_t qt, qh, kt, kh, vt, vh;
+  uint64_t total;
+  uint32_t heads, group, q_heads, seqs, window;
+  uint32_t group_mul, group_shift;
+  int causal, out_f32, zero, flip;  // scale 0: queries count as 0 (NaN stays); below 0: their signs flip
+  float scale_log2, cap_in, cap_out;
+};
+
+__device__ __forceinline__ uint32_t prompt_query(const PromptArgs& a, uint32_t r) { return (uint32_t)(((uint64_t)r * a.group_mul) >> a.group_shift); }
+
+// Rows start[b] .. start[b + 1] - 1, cut to the rows there are.
+__device__ __forceinline__ uint32_t prompt_rows(const PromptArgs& a, uint32_t b, uint32_t* first) {
+  const int64_t x = a.start[b], y = a.start[b + 1], top = (int64_t)a.total;
+  const int64_t s = x < 0 ? 0 : x > top ? top : x, e = y < s ? s : y > top ? top : y;
+  *first = (uint32_t)s;
+  return (uint32_t)(e - s);
+}
+
+__device__ __forceinline__ uint32_t wave_sum(uint32_t x) {
+#pragma unroll
+  for (uint32_t d = 1; d < 64; d <<= 1) x += (uint32_t)__builtin_amdgcn_ds_bpermute((int)(((threadIdx.x & 63u) ^ d) << 2), (int)x);
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
+}
+
+// The tile with the index-th most work, by the wavefront: tiles later in a sequence see more tokens, so of all
+// sequences' tiles those of one place in their sequence form a level, the last levels first.  False if there are
+// not so many tiles.  `tile`: its place in the sequence.
+template <int ROWS>
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, uint32_t index, uint32_t* seq, uint32_t* tile) {
+  const uint32_t lane = threadIdx.x & 63u;
+  auto tiles_of = [&](uint32_t b) {
+    uint32_t first;
+    return b < a.seqs ? (uint32_t)(((uint64_t)prompt_rows(a, b, &first) * a.group + ROWS - 1u) / ROWS) : 0u;
+  };
+  const uint32_t mine = tiles_of(lane);
+  // tiles at or past a level
+  auto past = [&](uint32_t level) {
+    uint32_t sum = mine > level ? mine - level : 0u;
+    for (uint32_t b = 64u + lane; b < a.seqs; b += 64u) {
+      const uint32_t n = tiles_of(b);
+      sum += n > level ? n - level : 0u;
+    }
+    return wave_sum(sum);
+  };
+  if (past(0) <= index) return false;
+  uint32_t lo = 0, hi = (uint32_t)((a.total * a.group + ROWS - 1u) / ROWS);  // past(lo) > index >= past(hi)
+  if (a.seqs == 1) {
+    *seq = 0;
+    *tile = (uint32_t)__builtin_amdgcn_readfirstlane((int)mine) - 1u - index;
+    return true;
+  }
+  while (hi - lo > 1u) {
+    const uint32_t mid = lo + (hi - lo) / 2u;
+    if (past(mid) > index) lo = mid;
+    else hi = mid;
+  }
+  uint32_t skip = index - past(lo + 1u);
+  for (uint32_t b0 = 0; b0 < a.seqs; b0 += 64u) {
+    const uint32_t n = b0 ? tiles_of(b0 + lane) : mine;
+    uint64_t votes = __builtin_amdgcn_ballot_w64(n > lo);
+    const uint32_t here = (uint32_t)__builtin_popcountll(votes);
+    if (skip < here) {
+      for (; skip; --skip) votes &= votes - 1u;
+      *seq = b0 + (uint32_t)__builtin_ctzll(votes);
+      *tile = lo;
+      return true;
+    }
+    skip -= here;
+  }
+  return false;
+}
+
+__device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
+}
+
+// 1 - 2 / (e^2x + 1) away from zero (it saturates by itself), the odd series to x^5 below 2^-4 (the next term is below
+// 2^-27 of x); s in units of the cap.
+__device__ __forceinline__ float cap_tanh(float x) {
+  const float e = __builtin_amdgcn_exp2f(x * 2.885390081777927f), x2 = x * x;
+  const float big = __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f);
+  const float small = x * __builtin_fmaf(x2, __builtin_fmaf(x2, 2.0f / 15.0f, -1.0f / 3.0f), 1.0f);
+  return fabsf(x) < 0.0625f ? small : big;
+}
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+template <int WAVES, bool CAP>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void prompt_kernel(PromptArgs a) {
+  constexpr uint32_t kRows = 32u * WAVES;
+  __shared__ __align__(16) uint8_t s_k0[kPromptTile], s_k1[kPromptTile], s_v0[kPromptTile], s_v1[kPromptTile];
+  const uint32_t lane = threadIdx.x & 63u, wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), n32 = lane & 31u, half = lane >> 5;
+  const uint32_t head = blockIdx.x % a.heads;
+  uint32_t b, place;
+  if (!find_tile<(int)kRows>(a, blockIdx.x / a.heads, &b, &place)) return;
+  uint32_t first;
+  const uint32_t n = prompt_rows(a, b, &first), rows = n * a.group, r0 = place * kRows, w0 = r0 + 32u * wave;
+  // tokens that the tile's rows see, and this wavefront's
+  auto range = [&](uint32_t x, uint32_t count, int32_t* lo, int32_t* hi, int32_t* all_lo, int32_t* all_hi) {
+    if (x >= rows) {
+      *lo = *hi = *all_lo = *all_hi = 0;
+      return;
+    }
+    const int32_t i0 = (int32_t)prompt_query(a, x), i1 = (int32_t)prompt_query(a, (x + count < rows ? x + count : rows) - 1u);
+    const int64_t w0 = (int64_t)i0 + 1 - (int64_t)a.window, w1 = (int64_t)i1 + 1 - (int64_t)a.window;
+    *lo = a.window && w0 > 0 ? (int32_t)w0 : 0;
+    *hi = a.causal ? i1 + 1 : (int32_t)n;
+    *all_lo = a.window && w1 > 0 ? (int32_t)w1 : 0;
+    *all_hi = a.causal ? i0 + 1 : (int32_t)n;
+  };
+  int32_t lo, hi, wlo, whi, all_lo, all_hi, x0, x1;
+  range(r0, kRows, &lo, &hi, &x0, &x1);
+  range(w0, 32u, &wlo, &whi, &all_lo, &all_hi);
+  lo &= ~(kPromptTok - 1);
+  const int32_t steps = (hi - lo + kPromptTok - 1) / kPromptTok;
+
+  // global to LDS: 1024 bytes, four tokens, an instruction
+  constexpr int kLoads = 16 / WAVES;
+  const uint16_t* kbase = a.k + (int64_t)first * a.kt + (int64_t)head * a.kh;
+  const uint16_t* vbase = a.v + (int64_t)first * a.vt + (int64_t)head * a.vh;
+  auto load = [&](const uint16_t* base, int64_t stride, uint32_t mask, uint32_t shift, int32_t t, uint8_t* lds) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t row0 = 4u * (wave * kLoads + i), row = row0 + (lane >> 4), piece = (lane & 15u) ^ ((row & mask) << shift);
+      uint32_t tok = (uint32_t)t + row;
+      tok = tok < n ? tok : n - 1u;  // past the sequence: its last token again, masked below
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + (int64_t)tok * stride + 8u * piece),
+                                       (__attribute__((address_space(3))) void*)(lds + row0 * 256u), 16, 0, 0);
+    }
+  };
+  load(kbase, a.kt, 15u, 0u, lo, s_k0);
+  load(vbase, a.vt, 3u, 2u, lo, s_v0);
+
+  // this lane's row: piece 2 s + half of its query
+  bf16x8 q[8];
+  const uint32_t r = w0 + n32;
+  const bool have = r < rows;
+  const uint32_t qi = prompt_query(a, have ? r : rows - 1u), qg = (have ? r : rows - 1u) - qi * a.group;
+  {
+    const uint16_t* p = a.q + (int64_t)(first + qi) * a.qt + (int64_t)(head * a.group + qg) * a.qh + 8u * half;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      u32x4 u = *reinterpret_cast<const u32x4*>(p + 16 * s);
+      if (a.flip) u ^= 0x80008000u;
+      if (a.zero) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = u[i];
+          u[i] = ((x & 0x7F80u) == 0x7F80u ? 0x7FC0u : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0x7FC00000u : 0u);
+        }
+      }
+      q[s] = __builtin_bit_cast(bf16x8, u);
+    }
+  }
+  const int32_t row_hi = a.causal ? (int32_t)qi + 1 : (int32_t)n;
+  const int64_t rl = (int64_t)qi + 1 - (int64_t)a.window;
+  const int32_t row_lo = a.window && rl > 0 ? (int32_t)rl : 0;
+
+  uint32_t ka[8], va[4];
+#pragma unroll
+  for (uint32_t s = 0; s < 8; ++s) ka[s] = n32 * 256u + (((2u * s + half) ^ (lane & 15u)) * 16u);
+#pragma unroll
+  for (uint32_t d = 0; d < 4; ++d) {
+    const uint32_t i = lane & 15u, tok = 4u * half + (i >> 2), piece = (4u * d + 2u * ((lane >> 4) & 1u) + ((i & 3u) >> 1)) ^ ((i >> 2) << 2);
+    va[d] = tok * 256u + piece * 16u + (i & 1u) * 8u;
+  }
+
+  float m = kPromptLowest, sum = 0.0f;
+  f32x16 o[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) o[d] = (f32x16)0.0f;
+
+  auto scores = [&](const uint8_t* kb, f32x16* s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      s[u] = (f32x16)0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[u] = mfma32(*reinterpret_cast<const bf16x8*>(kb + u * 8192 + ka[j]), q[j], s[u]);
+    }
+  };
+  auto value = [&](const uint8_t* vb, int d, int step) __attribute__((always_inline)) {
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds_u8*)(vb + va[d] + step * 4096));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds_u8*)(vb + va[d] + step * 4096 + 2048));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  // whether the lane's row sees its score i of block u
+  auto sees = [&](int32_t t, int u, int i) __attribute__((always_inline)) {
+    const int32_t tok = t + 32 * u + 8 * (i >> 2) + 4 * (int32_t)half + (i & 3);
+    return tok >= row_lo && tok < row_hi;
+  };
+  auto finish = [&](const uint8_t* vb, int32_t t, f32x16* s) __attribute__((always_inline)) {
+    const bool masked = t < all_lo || t + kPromptTok > all_hi;
+    if (CAP) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[u][i] = cap_tanh(s[u][i] * a.cap_in);
+    }
+    if (masked) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!sees(t, u, i)) s[u][i] = -__builtin_inff();
+    }
+    const float c = CAP ? a.cap_out : a.scale_log2;
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i >> 4][i & 15]);
+    top *= c;
+    if (__builtin_amdgcn_ballot_w64(top > m + kPromptSlack)) {
+      const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+      const float mn = fmaxf(m, fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]))), f = __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      sum *= f;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] *= f;
+    }
+    bf16x8 p[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      u32x4 x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = 8 * (w & 1) + 2 * i;
+        const uint32_t pair = bf16_pack(__builtin_amdgcn_exp2f(__builtin_fmaf(s[w >> 1][e], c, -m)), __builtin_amdgcn_exp2f(__builtin_fmaf(s[w >> 1][e + 1], c, -m)));
+        // the sum of the rounded weights, those that the output is made with
+        sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, 0x3F803F80u), sum, false);
+        x[i] = pair;
+      }
+      p[w] = __builtin_bit_cast(bf16x8, x);
+    }
+    if (masked) {
+      // 0 times a value that is not finite would reach rows that do not see it
+      uint32_t worst = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(vb + (64 * i + lane) * 16u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          worst = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, worst), __builtin_bit_cast(u16x2, x[j] & 0x7FFF7FFFu)));
+      }
+      if (__builtin_amdgcn_ballot_w64((worst & 0xFFFFu) >= 0x7F80u || worst >= 0x7F800000u)) {
+        // what is not finite is taken out of the product and counted for the rows that see it: infinities, by sign, and NaN
+#pragma unroll 1
+        for (uint32_t kind = 0; kind < 4; ++kind) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            f32x16 count = (f32x16)0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              u32x4 x = __builtin_bit_cast(u32x4, value(vb, d, w)), one;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t y = 0;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t z = (x[i] >> (16 * e)) & 0xFFFFu, mag = z & 0x7FFFu;
+                  const uint32_t is = mag < 0x7F80u ? 0u : mag > 0x7F80u ? 3u : z == 0x7F80u ? 1u : 2u;
+                  y |= (kind == 0 ? (is ? 0u : z) : is == kind ? 0x3F80u : 0u) << (16 * e);
+                }
+                x[i] = y;
+                const int s0 = 8 * (w & 1) + 2 * i;
+                one[i] = (sees(t, w >> 1, s0) ? 0x3F80u : 0u) | (sees(t, w >> 1, s0 + 1) ? 0x3F800000u : 0u);
+              }
+              if (kind == 0) o[d] = mfma32(__builtin_bit_cast(bf16x8, x), p[w], o[d]);
+              else count = mfma32(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, one), count);
+            }
+            const float add = kind == 1 ? __builtin_inff() : kind == 2 ? -__builtin_inff() : __builtin_nanf("");
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (count[i] > 0.0f) o[d][i] += add;
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] = mfma32(value(vb, d, w), p[w], o[d]);
+  };
+  auto arrived = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the loads into LDS have landed
+    __syncthreads();
+  };
+
+  f32x16 s[2];
+  for (int32_t j = 0; j < steps; j += 2) {
+    const int32_t t = lo + kPromptTok * j;
+    arrived();
+    if (j + 1 < steps) {
+      load(kbase, a.kt, 15u, 0u, t + kPromptTok, s_k1);
+      load(vbase, a.vt, 3u, 2u, t + kPromptTok, s_v1);
+    }
+    if (t < whi && t + kPromptTok > wlo) {
+      scores(s_k0, s);
+      finish(s_v0, t, s);
+    }
+    if (j + 1 >= steps) break;
+    arrived();
+    if (j + 2 < steps) {
+      load(kbase, a.kt, 15u, 0u, t + 2 * kPromptTok, s_k0);
+      load(vbase, a.vt, 3u, 2u, t + 2 * kPromptTok, s_v0);
+    }
+    if (t + kPromptTok < whi && t + 2 * kPromptTok > wlo) {
+      scores(s_k1, s);
+      finish(s_v1, t + kPromptTok, s);
+    }
+  }
+
+  const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
+  const float total = __uint_as_float(x[0]) + __uint_as_float(x[1]), inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const uint64_t at = ((uint64_t)(first + qi) * a.q_heads + head * a.group + qg) * kD;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    o[d] *= inv;
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      // lane h has columns 8 j + 4 h + 0..3 and 8 more: half 0 takes columns 8 j .. 8 j + 7, half 1 the next eight
+      if (a.out_f32) {
+        if (have) {
+          float* p = static_cast<float*>(a.out) + at + 32 * d + 8 * j + 4 * half;
+          *reinterpret_cast<f32x4*>(p) = (f32x4){o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
+          *reinterpret_cast<f32x4*>(p + 8) = (f32x4){o[d][4 * j + 4], o[d][4 * j + 5], o[d][4 * j + 6], o[d][4 * j + 7]};
+        }
+      } else {
+        const auto y0 = __builtin_amdgcn_permlane32_swap(bf16_pack(o[d][4 * j], o[d][4 * j + 1]), bf16_pack(o[d][4 * j + 4], o[d][4 * j + 5]), false, false);
+        const auto y1 = __builtin_amdgcn_permlane32_swap(bf16_pack(o[d][4 * j + 2], o[d][4 * j + 3]), bf16_pack(o[d][4 * j + 6], o[d][4 * j + 7]), false, false);
+        if (have) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + at + 32 * d + 8 * j + 8 * half) = (u32x4){y0[0], y1[0], y0[1], y1[1]};
+      }
+    }
+  }
+}
+
+}  // namespace hq_kv
+
+using namespace hq_kv;
+
+extern "C" int hq_attend_prompt(const hq_attend_prompt_args* g, hq_stream_t stream) {
+  if (!g || g->heads == 0 || g->q_heads == 0 || g->q_heads % g->heads || g->q_heads > 65535u) return HQ_ERR_INVALID_ARG;
+  if (g->dtype != HQ_BF16 || (g->out_dtype != HQ_F32 && g->out_dtype != HQ_BF16)) return HQ_ERR_INVALID_ARG;
+  if (g->rows > (1ull << 30) || g->rows * g->q_heads > (1ull << 28)) return HQ_ERR_INVALID_ARG;
+  if (!(std::fabs(g->scale) <= 0x1p126f)) return HQ_ERR_INVALID_ARG;
+  if (g->softcap != 0.0f && !(g->softcap >= 0x1p-125f && g->softcap <= 0x1p125f)) return HQ_ERR_INVALID_ARG;
+  if ((g->q_stride[0] | g->q_stride[1] | g->k_stride[0] | g->k_stride[1] | g->v_stride[0] | g->v_stride[1]) & 7) return HQ_ERR_INVALID_ARG;
+  if (g->rows == 0 || g->seqs == 0) return HQ_OK;
+  if (!g->q || !g->k || !g->v || !g->out || !g->start || ((uintptr_t)g->start & 3u)) return HQ_ERR_INVALID_ARG;
+  if (((uintptr_t)g->q | (uintptr_t)g->k | (uintptr_t)g->v | (uintptr_t)g->out) & 15u) return HQ_ERR_INVALID_ARG;
+  PromptArgs a;
+  a.q = static_cast<const uint16_t*>(g->q);
+  a.k = static_cast<const uint16_t*>(g->k);
+  a.v = static_cast<const uint16_t*>(g->v);
+  a.out = g->out;
+  a.start = g->start;
+  a.qt = g->q_stride[0];
+  a.qh = g->q_stride[1];
+  a.kt = g->k_stride[0];
+  a.kh = g->k_stride[1];
+  a.vt = g->v_stride[0];
+  a.vh = g->v_stride[1];
+  a.total = g->rows;
+  a.heads = g->heads;
+  a.group = g->q_heads / g->heads;
+  a.q_heads = g->q_heads;
+  a.seqs = g->seqs;
+  a.window = g->window;
+  uint32_t sh = 0;
+  while ((1u << sh) < a.group) ++sh;
+  a.group_mul = (uint32_t)((1ull << (31u + sh)) / a.group + 1u);
+  a.group_shift = 31u + sh;
+  a.causal = g->causal != 0;
+  a.out_f32 = g->out_dtype == HQ_F32;
+  a.zero = g->scale == 0.0f;
+  a.flip = g->scale < 0.0f;
+  const double log2e = 1.4426950408889634074, scale = std::fabs((double)g->scale);
+  a.scale_log2 = a.zero ? 1.0f : (float)(scale * log2e);
+  a.cap_in = g->softcap > 0.0f ? (float)((a.zero ? 1.0 : scale) / g->softcap) : 0.0f;
+  a.cap_out = (float)(g->softcap * log2e);
+  const uint64_t rows = g->rows * a.group, tiles = (rows + 255u * (uint64_t)(g->seqs < rows ? g->seqs : rows)) / 256u, grid = tiles * a.heads;
+  if (grid > kMaxThreads / 512u) return HQ_ERR_INVALID_ARG;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (g->softcap > 0.0f) hipLaunchKernelGGL((prompt_kernel<8, true>), dim3((uint32_t)grid), dim3(512), 0, st, a);
+  else hipLaunchKernelGGL((prompt_kernel<8, false>), dim3((uint32_t)grid), dim3(512), 0, st, a);
+  return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
+}
