@@ -32,6 +32,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr float kPromptSlack = 6.0f;                 // the reference may lag the maximum by this much (log2)
 constexpr float kPromptLowest = -3.402823466e38f;    // the reference before the first score
 constexpr int kPromptTok = 64;                       // tokens of a step
+constexpr int64_t kPromptStride = 1 << 23;            // K's and V's rows are nearer than this, in values
 constexpr uint32_t kPromptTile = kPromptTok * 256u;  // their bytes, K or V
 
 struct PromptArgs {
@@ -42,7 +43,8 @@ struct PromptArgs {
   uint64_t total;
   uint32_t heads, group, q_heads, seqs, window;
   uint32_t group_mul, group_shift;
-  int causal, out_f32, zero, flip;  // scale 0: queries count as 0 (NaN stays); below 0: their signs flip
+  int causal, out_f32;
+  uint32_t flip;  // of pairs of a query's values: their signs, for a scale below 0
   float scale_log2, cap_in, cap_out;
 };
 
@@ -56,10 +58,15 @@ __device__ __forceinline__ uint32_t prompt_rows(const PromptArgs& a, uint32_t b,
   return (uint32_t)(e - s);
 }
 
+// Sum over the wavefront: within 16 lanes by shifts, then the four ends.
+template <int SHIFT>
+__device__ __forceinline__ uint32_t add_shifted(uint32_t x) {
+  return x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x110 + SHIFT, 0xF, 0xF, true);  // row_shr, zeros from outside
+}
 __device__ __forceinline__ uint32_t wave_sum(uint32_t x) {
-#pragma unroll
-  for (uint32_t d = 1; d < 64; d <<= 1) x += (uint32_t)__builtin_amdgcn_ds_bpermute((int)(((threadIdx.x & 63u) ^ d) << 2), (int)x);
-  return (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
+  x = add_shifted<8>(add_shifted<4>(add_shifted<2>(add_shifted<1>(x))));
+  return (uint32_t)(__builtin_amdgcn_readlane((int)x, 15) + __builtin_amdgcn_readlane((int)x, 31) + __builtin_amdgcn_readlane((int)x, 47) +
+                    __builtin_amdgcn_readlane((int)x, 63));
 }
 
 // The tile with the index-th most work, by the wavefront: tiles later in a sequence see more tokens, so of all
@@ -73,6 +80,12 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, uint32_t index, u
     return b < a.seqs ? (uint32_t)(((uint64_t)prompt_rows(a, b, &first) * a.group + ROWS - 1u) / ROWS) : 0u;
   };
   const uint32_t mine = tiles_of(lane);
+  if (a.seqs == 1) {
+    const uint32_t count = (uint32_t)__builtin_amdgcn_readfirstlane((int)mine);
+    *seq = 0;
+    *tile = count - 1u - index;
+    return index < count;
+  }
   // tiles at or past a level
   auto past = [&](uint32_t level) {
     uint32_t sum = mine > level ? mine - level : 0u;
@@ -84,11 +97,6 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, uint32_t index, u
   };
   if (past(0) <= index) return false;
   uint32_t lo = 0, hi = (uint32_t)((a.total * a.group + ROWS - 1u) / ROWS);  // past(lo) > index >= past(hi)
-  if (a.seqs == 1) {
-    *seq = 0;
-    *tile = (uint32_t)__builtin_amdgcn_readfirstlane((int)mine) - 1u - index;
-    return true;
-  }
   while (hi - lo > 1u) {
     const uint32_t mid = lo + (hi - lo) / 2u;
     if (past(mid) > index) lo = mid;
@@ -128,8 +136,9 @@ __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) { return 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 template <int WAVES, bool CAP>
-__global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
   constexpr uint32_t kRows = 32u * WAVES;
+  // arrays of their own: a read of one does not wait for loads into another
   __shared__ __align__(16) uint8_t s_k0[kPromptTile], s_k1[kPromptTile], s_v0[kPromptTile], s_v1[kPromptTile];
   const uint32_t lane = threadIdx.x & 63u, wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), n32 = lane & 31u, half = lane >> 5;
   const uint32_t head = blockIdx.x % a.heads;
@@ -137,66 +146,48 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void prompt_kernel(
   if (!find_tile<(int)kRows>(a, blockIdx.x / a.heads, &b, &place)) return;
   uint32_t first;
   const uint32_t n = prompt_rows(a, b, &first), rows = n * a.group, r0 = place * kRows, w0 = r0 + 32u * wave;
-  // tokens that the tile's rows see, and this wavefront's
-  auto range = [&](uint32_t x, uint32_t count, int32_t* lo, int32_t* hi, int32_t* all_lo, int32_t* all_hi) {
-    if (x >= rows) {
-      *lo = *hi = *all_lo = *all_hi = 0;
-      return;
-    }
-    const int32_t i0 = (int32_t)prompt_query(a, x), i1 = (int32_t)prompt_query(a, (x + count < rows ? x + count : rows) - 1u);
-    const int64_t w0 = (int64_t)i0 + 1 - (int64_t)a.window, w1 = (int64_t)i1 + 1 - (int64_t)a.window;
-    *lo = a.window && w0 > 0 ? (int32_t)w0 : 0;
-    *hi = a.causal ? i1 + 1 : (int32_t)n;
-    *all_lo = a.window && w1 > 0 ? (int32_t)w1 : 0;
-    *all_hi = a.causal ? i0 + 1 : (int32_t)n;
+  // tokens from `lo` to `hi` that some of the tile's rows see, in steps; those that all of the wavefront's see
+  const uint32_t last = rows - 1u;
+  auto query = [&](uint32_t x) { return (int32_t)prompt_query(a, x < last ? x : last); };
+  auto from = [&](int32_t i) {  // the first token that query i sees
+    const int64_t x = (int64_t)i + 1 - (int64_t)a.window;
+    return a.window && x > 0 ? (int32_t)x : 0;
   };
-  int32_t lo, hi, wlo, whi, all_lo, all_hi, x0, x1;
-  range(r0, kRows, &lo, &hi, &x0, &x1);
-  range(w0, 32u, &wlo, &whi, &all_lo, &all_hi);
-  lo &= ~(kPromptTok - 1);
+  const int32_t lo = from(query(r0)) & ~(kPromptTok - 1), hi = a.causal ? query(r0 + kRows - 1u) + 1 : (int32_t)n;
+  const int32_t all_lo = from(query(w0 + 31u)), all_hi = a.causal ? query(w0) + 1 : (int32_t)n;
   const int32_t steps = (hi - lo + kPromptTok - 1) / kPromptTok;
 
   // global to LDS: 1024 bytes, four tokens, an instruction
   constexpr int kLoads = 16 / WAVES;
   const uint16_t* kbase = a.k + (int64_t)first * a.kt + (int64_t)head * a.kh;
   const uint16_t* vbase = a.v + (int64_t)first * a.vt + (int64_t)head * a.vh;
-  auto load = [&](const uint16_t* base, int64_t stride, uint32_t mask, uint32_t shift, int32_t t, uint8_t* lds) __attribute__((always_inline)) {
+  auto load = [&](const uint16_t* base, uint32_t stride, bool keys, int32_t step, uint8_t* lds) __attribute__((always_inline)) {
+    const uint32_t t = (uint32_t)(lo + kPromptTok * step), most = n - 1u - t;  // past the sequence: its last token again, masked below
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(base + (uint64_t)t * stride);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const uint32_t row0 = 4u * (wave * kLoads + i), row = row0 + (lane >> 4), piece = (lane & 15u) ^ ((row & mask) << shift);
-      uint32_t tok = (uint32_t)t + row;
-      tok = tok < n ? tok : n - 1u;  // past the sequence: its last token again, masked below
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + (int64_t)tok * stride + 8u * piece),
+      const uint32_t row0 = 4u * (wave * kLoads + i), row = row0 + (lane >> 4), piece = (lane & 15u) ^ (keys ? row & 15u : (row & 3u) << 2);
+      const uint32_t at = (row < most ? row : most) * (2u * stride) + 16u * piece;  // below 2^31
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + at),
                                        (__attribute__((address_space(3))) void*)(lds + row0 * 256u), 16, 0, 0);
     }
   };
-  load(kbase, a.kt, 15u, 0u, lo, s_k0);
-  load(vbase, a.vt, 3u, 2u, lo, s_v0);
+  auto load_k = [&](int32_t step, uint8_t* lds) __attribute__((always_inline)) { load(kbase, (uint32_t)a.kt, true, step, lds); };
+  auto load_v = [&](int32_t step, uint8_t* lds) __attribute__((always_inline)) { load(vbase, (uint32_t)a.vt, false, step, lds); };
+  load_k(0, s_k0);
+  load_v(0, s_v0);
 
   // this lane's row: piece 2 s + half of its query
   bf16x8 q[8];
   const uint32_t r = w0 + n32;
   const bool have = r < rows;
-  const uint32_t qi = prompt_query(a, have ? r : rows - 1u), qg = (have ? r : rows - 1u) - qi * a.group;
+  const uint32_t qi = (uint32_t)query(r), qg = (have ? r : last) - qi * a.group;
   {
     const uint16_t* p = a.q + (int64_t)(first + qi) * a.qt + (int64_t)(head * a.group + qg) * a.qh + 8u * half;
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      u32x4 u = *reinterpret_cast<const u32x4*>(p + 16 * s);
-      if (a.flip) u ^= 0x80008000u;
-      if (a.zero) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x = u[i];
-          u[i] = ((x & 0x7F80u) == 0x7F80u ? 0x7FC0u : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0x7FC00000u : 0u);
-        }
-      }
-      q[s] = __builtin_bit_cast(bf16x8, u);
-    }
+    for (int s = 0; s < 8; ++s) q[s] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p + 16 * s) ^ a.flip);
   }
-  const int32_t row_hi = a.causal ? (int32_t)qi + 1 : (int32_t)n;
-  const int64_t rl = (int64_t)qi + 1 - (int64_t)a.window;
-  const int32_t row_lo = a.window && rl > 0 ? (int32_t)rl : 0;
+  const int32_t row_hi = a.causal ? (int32_t)qi + 1 : (int32_t)n, row_lo = from((int32_t)qi);
 
   uint32_t ka[8], va[4];
 #pragma unroll
@@ -207,50 +198,46 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void prompt_kernel(
     va[d] = tok * 256u + piece * 16u + (i & 1u) * 8u;
   }
 
-  float m = kPromptLowest, sum = 0.0f;
+  float m = kPromptLowest, sum = 0.0f, bad = 0.0f;  // bad: NaN once a masked step has met a value that is not finite
   f32x16 o[4];
 #pragma unroll
   for (int d = 0; d < 4; ++d) o[d] = (f32x16)0.0f;
+  const float c = CAP ? a.cap_out : a.scale_log2;
 
-  auto scores = [&](const uint8_t* kb, f32x16* s) __attribute__((always_inline)) {
+  // raw scores of 32 tokens, half u of a step
+  auto scores = [&](const uint8_t* kb, int u, f32x16& s) __attribute__((always_inline)) {
+    s = (f32x16)0.0f;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      s[u] = (f32x16)0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[u] = mfma32(*reinterpret_cast<const bf16x8*>(kb + u * 8192 + ka[j]), q[j], s[u]);
-    }
+    for (int j = 0; j < 8; ++j) s = mfma32(*reinterpret_cast<const bf16x8*>(kb + u * 8192 + ka[j]), q[j], s);
   };
-  auto value = [&](const uint8_t* vb, int d, int step) __attribute__((always_inline)) {
-    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds_u8*)(vb + va[d] + step * 4096));
-    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds_u8*)(vb + va[d] + step * 4096 + 2048));
+  auto value = [&](const uint8_t* vb, int d, int w) __attribute__((always_inline)) {
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds_u8*)(vb + va[d] + w * 4096));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds_u8*)(vb + va[d] + w * 4096 + 2048));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  // whether the lane's row sees its score i of block u
-  auto sees = [&](int32_t t, int u, int i) __attribute__((always_inline)) {
-    const int32_t tok = t + 32 * u + 8 * (i >> 2) + 4 * (int32_t)half + (i & 3);
-    return tok >= row_lo && tok < row_hi;
-  };
-  auto finish = [&](const uint8_t* vb, int32_t t, f32x16* s) __attribute__((always_inline)) {
-    const bool masked = t < all_lo || t + kPromptTok > all_hi;
+  auto cap = [&](f32x16& s) __attribute__((always_inline)) {
     if (CAP) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[u][i] = cap_tanh(s[u][i] * a.cap_in);
+      for (int i = 0; i < 16; ++i) s[i] = cap_tanh(s[i] * a.cap_in);
     }
-    if (masked) {
+  };
+  // takes the tokens that the row does not see, of 32 from t, out
+  auto hide = [&](int32_t t, f32x16& s) __attribute__((always_inline)) {
+    const int32_t a0 = row_lo - t - 4 * (int32_t)half, a1 = row_hi - t - 4 * (int32_t)half;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!sees(t, u, i)) s[u][i] = -__builtin_inff();
+    for (int i = 0; i < 16; ++i) {
+      const int tok = 8 * (i >> 2) + (i & 3);
+      if (tok < a0 || tok >= a1) s[i] = -__builtin_inff();
     }
-    const float c = CAP ? a.cap_out : a.scale_log2;
-    float top = s[0][0];
+  };
+  // a new reference, if a score is far above the present one; whether there is
+  auto raise = [&](const f32x16& s) __attribute__((always_inline)) {
+    float top = s[0];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i >> 4][i & 15]);
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
     top *= c;
-    if (__builtin_amdgcn_ballot_w64(top > m + kPromptSlack)) {
+    const bool rise = __builtin_amdgcn_ballot_w64(top > m + kPromptSlack) != 0u;
+    if (rise) {
       const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
       const float mn = fmaxf(m, fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]))), f = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
@@ -258,96 +245,146 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void prompt_kernel(
 #pragma unroll
       for (int d = 0; d < 4; ++d) o[d] *= f;
     }
-    bf16x8 p[4];
+    return rise;
+  };
+  auto weigh = [&](const f32x16& s, bf16x8* p) __attribute__((always_inline)) {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < 2; ++w) {
       u32x4 x;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int e = 8 * (w & 1) + 2 * i;
-        const uint32_t pair = bf16_pack(__builtin_amdgcn_exp2f(__builtin_fmaf(s[w >> 1][e], c, -m)), __builtin_amdgcn_exp2f(__builtin_fmaf(s[w >> 1][e + 1], c, -m)));
+        const int e = 8 * w + 2 * i;
+        const uint32_t pair = bf16_pack(__builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -m)), __builtin_amdgcn_exp2f(__builtin_fmaf(s[e + 1], c, -m)));
         // the sum of the rounded weights, those that the output is made with
         sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, 0x3F803F80u), sum, false);
         x[i] = pair;
       }
       p[w] = __builtin_bit_cast(bf16x8, x);
     }
-    if (masked) {
-      // 0 times a value that is not finite would reach rows that do not see it
-      uint32_t worst = 0;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(vb + (64 * i + lane) * 16u);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          worst = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, worst), __builtin_bit_cast(u16x2, x[j] & 0x7FFF7FFFu)));
-      }
-      if (__builtin_amdgcn_ballot_w64((worst & 0xFFFFu) >= 0x7F80u || worst >= 0x7F800000u)) {
-        // what is not finite is taken out of the product and counted for the rows that see it: infinities, by sign, and NaN
-#pragma unroll 1
-        for (uint32_t kind = 0; kind < 4; ++kind) {
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            f32x16 count = (f32x16)0.0f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              u32x4 x = __builtin_bit_cast(u32x4, value(vb, d, w)), one;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t y = 0;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const uint32_t z = (x[i] >> (16 * e)) & 0xFFFFu, mag = z & 0x7FFFu;
-                  const uint32_t is = mag < 0x7F80u ? 0u : mag > 0x7F80u ? 3u : z == 0x7F80u ? 1u : 2u;
-                  y |= (kind == 0 ? (is ? 0u : z) : is == kind ? 0x3F80u : 0u) << (16 * e);
-                }
-                x[i] = y;
-                const int s0 = 8 * (w & 1) + 2 * i;
-                one[i] = (sees(t, w >> 1, s0) ? 0x3F80u : 0u) | (sees(t, w >> 1, s0 + 1) ? 0x3F800000u : 0u);
-              }
-              if (kind == 0) o[d] = mfma32(__builtin_bit_cast(bf16x8, x), p[w], o[d]);
-              else count = mfma32(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, one), count);
-            }
-            const float add = kind == 1 ? __builtin_inff() : kind == 2 ? -__builtin_inff() : __builtin_nanf("");
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (count[i] > 0.0f) o[d][i] += add;
-          }
-        }
-        return;
-      }
-    }
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-#pragma unroll
-      for (int d = 0; d < 4; ++d) o[d] = mfma32(value(vb, d, w), p[w], o[d]);
   };
+  auto products = [&](const uint8_t* vb, int u, const bf16x8* p) __attribute__((always_inline)) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] = mfma32(value(vb, d, 2 * u + w), p[w], o[d]);
+  };
+
   auto arrived = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the loads into LDS have landed
     __syncthreads();
   };
-
-  f32x16 s[2];
-  for (int32_t j = 0; j < steps; j += 2) {
-    const int32_t t = lo + kPromptTok * j;
+  // A step's two halves: one's weights are made among the other's products.
+  auto step = [&](auto parity, int32_t j) __attribute__((always_inline)) {
+    constexpr bool odd = decltype(parity)::value;
+    const uint8_t *kb = odd ? s_k1 : s_k0, *vb = odd ? s_v1 : s_v0;
     arrived();
     if (j + 1 < steps) {
-      load(kbase, a.kt, 15u, 0u, t + kPromptTok, s_k1);
-      load(vbase, a.vt, 3u, 2u, t + kPromptTok, s_v1);
+      load_k(j + 1, odd ? s_k0 : s_k1);
+      load_v(j + 1, odd ? s_v0 : s_v1);
     }
-    if (t < whi && t + kPromptTok > wlo) {
-      scores(s_k0, s);
-      finish(s_v0, t, s);
+    const int32_t t = lo + kPromptTok * j;
+    const bool masked = t < all_lo || t + kPromptTok > all_hi;
+    f32x16 s0, s1;
+    bf16x8 p0[2], p1[2];
+    __builtin_amdgcn_s_setprio(1);  // its products before the other workgroup's vector work (4096 tokens: 141 us against 149)
+    scores(kb, 0, s0);
+    __builtin_amdgcn_s_setprio(0);
+    cap(s0);
+    if (masked) hide(t, s0);
+    raise(s0);
+    scores(kb, 1, s1);
+    const float before = sum;
+    weigh(s0, p0);
+    cap(s1);
+    if (masked) hide(t + 32, s1);
+    {
+      const float with = sum;
+      sum = before;
+      if (raise(s1)) weigh(s0, p0);  // the first half's weights, not used yet, follow
+      else sum = with;
     }
-    if (j + 1 >= steps) break;
-    arrived();
-    if (j + 2 < steps) {
-      load(kbase, a.kt, 15u, 0u, t + 2 * kPromptTok, s_k0);
-      load(vbase, a.vt, 3u, 2u, t + 2 * kPromptTok, s_v0);
+    __builtin_amdgcn_s_setprio(1);
+    products(vb, 0, p0);
+    weigh(s1, p1);
+    products(vb, 1, p1);
+    __builtin_amdgcn_s_setprio(0);
+    if (masked) {
+      // 0 times a value that is not finite reaches rows that do not see it: such a tile is done again, below
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(vb + (64 * i + lane) * 16u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t y = x[e];
+          bad = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, y), __builtin_bit_cast(bf16x2, 0u), bad, false);
+        }
+      }
     }
-    if (t + kPromptTok < whi && t + 2 * kPromptTok > wlo) {
-      scores(s_k1, s);
-      finish(s_v1, t + kPromptTok, s);
+  };
+
+  __shared__ int s_again;
+  if (threadIdx.x == 0) s_again = 0;
+  for (int32_t j = 0; j < steps; j += 2) {
+    step(std::false_type{}, j);
+    if (j + 1 < steps) step(std::true_type{}, j + 1);
+  }
+
+  // Again, where a step that hides tokens has values that are not finite: they count as 0 in the products, and are added
+  // to the rows that see them.
+  if (__builtin_amdgcn_ballot_w64(bad != 0.0f)) s_again = 1;
+  __syncthreads();
+  if (s_again) {
+    m = kPromptLowest;
+    sum = 0.0f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] = (f32x16)0.0f;
+#pragma unroll 1
+    for (int32_t j = 0; j < steps; ++j) {
+      const int32_t t = lo + kPromptTok * j;
+      __syncthreads();
+      load_k(j, s_k0);
+      load_v(j, s_v0);
+      arrived();
+      bf16x8 p[4];
+      f32x16 s[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        scores(s_k0, u, s[u]);
+        cap(s[u]);
+        hide(t + 32 * u, s[u]);
+        raise(s[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) weigh(s[u], p + 2 * u);
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          u32x4 x = __builtin_bit_cast(u32x4, value(s_v0, d, w));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t y = x[i];
+            x[i] = ((y & 0x7F80u) == 0x7F80u ? 0u : y & 0xFFFFu) | ((y & 0x7F800000u) == 0x7F800000u ? 0u : y & 0xFFFF0000u);
+          }
+          o[d] = mfma32(__builtin_bit_cast(bf16x8, x), p[w], o[d]);
+        }
+#pragma unroll 1
+      for (int32_t tok = 0; tok < kPromptTok; ++tok) {
+        const bool sees = t + tok >= row_lo && t + tok < row_hi;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // columns 32 d + 8 e + 4 half + 0..3
+            const uint32_t piece = (uint32_t)(4 * d + e) ^ (((uint32_t)tok & 3u) << 2);
+            const uint2 x = *reinterpret_cast<const uint2*>(s_v0 + (uint32_t)tok * 256u + piece * 16u + half * 8u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t y = i & 1 ? (i & 2 ? x.y : x.x) & 0xFFFF0000u : (i & 2 ? x.y : x.x) << 16;
+              if (sees && (y & 0x7F800000u) == 0x7F800000u) o[d][4 * e + i] += __uint_as_float(y);
+            }
+          }
+      }
     }
   }
 
@@ -386,6 +423,8 @@ extern "C" int hq_attend_prompt(const hq_attend_prompt_args* g, hq_stream_t stre
   if (!(std::fabs(g->scale) <= 0x1p126f)) return HQ_ERR_INVALID_ARG;
   if (g->softcap != 0.0f && !(g->softcap >= 0x1p-125f && g->softcap <= 0x1p125f)) return HQ_ERR_INVALID_ARG;
   if ((g->q_stride[0] | g->q_stride[1] | g->k_stride[0] | g->k_stride[1] | g->v_stride[0] | g->v_stride[1]) & 7) return HQ_ERR_INVALID_ARG;
+  // a step's 64 rows lie within 2^31 bytes of each other
+  if (g->k_stride[0] < 0 || g->k_stride[0] >= kPromptStride || g->v_stride[0] < 0 || g->v_stride[0] >= kPromptStride) return HQ_ERR_INVALID_ARG;
   if (g->rows == 0 || g->seqs == 0) return HQ_OK;
   if (!g->q || !g->k || !g->v || !g->out || !g->start || ((uintptr_t)g->start & 3u)) return HQ_ERR_INVALID_ARG;
   if (((uintptr_t)g->q | (uintptr_t)g->k | (uintptr_t)g->v | (uintptr_t)g->out) & 15u) return HQ_ERR_INVALID_ARG;
@@ -413,16 +452,16 @@ extern "C" int hq_attend_prompt(const hq_attend_prompt_args* g, hq_stream_t stre
   a.group_shift = 31u + sh;
   a.causal = g->causal != 0;
   a.out_f32 = g->out_dtype == HQ_F32;
-  a.zero = g->scale == 0.0f;
-  a.flip = g->scale < 0.0f;
-  const double log2e = 1.4426950408889634074, scale = std::fabs((double)g->scale);
-  a.scale_log2 = a.zero ? 1.0f : (float)(scale * log2e);
-  a.cap_in = g->softcap > 0.0f ? (float)((a.zero ? 1.0 : scale) / g->softcap) : 0.0f;
+  a.flip = g->scale < 0.0f ? 0x80008000u : 0u;
+  // Hidden scores are -inf, which a factor of 0 would make NaN: a scale of 0 is 2^-126, the same for scores up to 2^100.
+  const double log2e = 1.4426950408889634074, scale = std::fmax(std::fabs((double)g->scale), 0x1p-126);
+  a.scale_log2 = (float)(scale * log2e);
+  a.cap_in = g->softcap > 0.0f ? (float)std::fmin(scale / g->softcap, 0x1p126) : 0.0f;
   a.cap_out = (float)(g->softcap * log2e);
-  const uint64_t rows = g->rows * a.group, tiles = (rows + 255u * (uint64_t)(g->seqs < rows ? g->seqs : rows)) / 256u, grid = tiles * a.heads;
-  if (grid > kMaxThreads / 512u) return HQ_ERR_INVALID_ARG;
+  const uint64_t rows = g->rows * a.group, tiles = (rows + 127u * (uint64_t)(g->seqs < rows ? g->seqs : rows)) / 128u, grid = tiles * a.heads;
+  if (grid > kMaxThreads / 256u) return HQ_ERR_INVALID_ARG;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (g->softcap > 0.0f) hipLaunchKernelGGL((prompt_kernel<8, true>), dim3((uint32_t)grid), dim3(512), 0, st, a);
-  else hipLaunchKernelGGL((prompt_kernel<8, false>), dim3((uint32_t)grid), dim3(512), 0, st, a);
+  if (g->softcap > 0.0f) hipLaunchKernelGGL((prompt_kernel<4, true>), dim3((uint32_t)grid), dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((prompt_kernel<4, false>), dim3((uint32_t)grid), dim3(256), 0, st, a);
   return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
 }
