@@ -135,6 +135,11 @@ __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) { return 
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
+// Classes of instructions that sched_group_barrier names.
+constexpr int kSchedVector = 0x2, kSchedMatrix = 0x8, kSchedRead = 0x100, kSchedExp = 0x400;
+// x is made here, and not moved to where it is used.
+__device__ __forceinline__ void keep(const bf16x8& x) { asm volatile("" ::"v"(x)); }
+
 template <int WAVES, bool CAP>
 __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
   constexpr uint32_t kRows = 32u * WAVES;
@@ -204,11 +209,15 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
   for (int d = 0; d < 4; ++d) o[d] = (f32x16)0.0f;
   const float c = CAP ? a.cap_out : a.scale_log2;
 
-  // raw scores of 32 tokens, half u of a step
-  auto scores = [&](const uint8_t* kb, int u, f32x16& s) __attribute__((always_inline)) {
+  // the keys of 32 tokens, half u of a step, as operands; their raw scores
+  auto keys = [&](const uint8_t* kb, int u, bf16x8* k) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k[j] = *reinterpret_cast<const bf16x8*>(kb + u * 8192 + ka[j]);
+  };
+  auto scores = [&](const bf16x8* k, f32x16& s) __attribute__((always_inline)) {
     s = (f32x16)0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = mfma32(*reinterpret_cast<const bf16x8*>(kb + u * 8192 + ka[j]), q[j], s);
+    for (int j = 0; j < 8; ++j) s = mfma32(k[j], q[j], s);
   };
   auto value = [&](const uint8_t* vb, int d, int w) __attribute__((always_inline)) {
     const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds_u8*)(vb + va[d] + w * 4096));
@@ -285,16 +294,20 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
     const int32_t t = lo + kPromptTok * j;
     const bool masked = t < all_lo || t + kPromptTok > all_hi;
     f32x16 s0, s1;
-    bf16x8 p0[2], p1[2];
+    bf16x8 k0[8], k1[8], p0[2], p1[2];
+    keys(kb, 0, k0);
+    keys(kb, 1, k1);
     __builtin_amdgcn_s_setprio(1);  // its products before the other workgroup's vector work (4096 tokens: 141 us against 149)
-    scores(kb, 0, s0);
+    scores(k0, s0);
     __builtin_amdgcn_s_setprio(0);
     cap(s0);
     if (masked) hide(t, s0);
     raise(s0);
-    scores(kb, 1, s1);
+    scores(k1, s1);
     const float before = sum;
     weigh(s0, p0);
+    keep(p0[0]);
+    keep(p0[1]);
     cap(s1);
     if (masked) hide(t + 32, s1);
     {
@@ -306,7 +319,23 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
     __builtin_amdgcn_s_setprio(1);
     products(vb, 0, p0);
     weigh(s1, p1);
+    keep(p1[0]);
+    keep(p1[1]);
     products(vb, 1, p1);
+    // the order of these: reads four products ahead, and an eighth of the second half's weights beside each of the first's products
+    __builtin_amdgcn_sched_group_barrier(kSchedRead, 8, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedVector, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedExp, 2, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 0);
+    }
     __builtin_amdgcn_s_setprio(0);
     if (masked) {
       // 0 times a value that is not finite reaches rows that do not see it: such a tile is done again, below
@@ -349,7 +378,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
       f32x16 s[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        scores(s_k0, u, s[u]);
+        bf16x8 k[8];
+        keys(s_k0, u, k);
+        scores(k, s[u]);
         cap(s[u]);
         hide(t + 32 * u, s[u]);
         raise(s[u]);
