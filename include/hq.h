@@ -384,7 +384,8 @@ int hq_kv_attend(const hq_kv_cache *cache, const hq_kv_attend_args *args, void *
  * draft follows; a value that is not in [0, i) means that it follows the n - m tokens held before the drafts.  Query i
  * sees those and, of the drafts, its own and its ancestors; with window > 0 only the last `window` of what it sees.
  * args->causal must not be 0 and args->weights must be NULL (a rejected draft's weights could not be taken back);
- * args->max_q is at most 256.  Workspace: hq_kv_attend_workspace_size.  Errors as hq_kv_attend. */
+ * args->max_q is at most 256.  The workspace is hq_kv_attend's kind, of its own size.  Errors as hq_kv_attend. */
+int hq_kv_attend_tree_workspace_size(const hq_kv_cache *cache, const hq_kv_attend_args *args, size_t *bytes);
 int hq_kv_attend_tree(const hq_kv_cache *cache, const hq_kv_attend_args *args, const int32_t *parents,
                       void *workspace, size_t workspace_bytes, hq_stream_t stream);
 

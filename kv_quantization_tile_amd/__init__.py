@@ -28,7 +28,8 @@ EXPORTS = ("hq_version", "hq_strerror", "hq_workspace_size", "hq_stream_fixed_by
            "hq_encode", "hq_encode_noalloc", "hq_decode", "hq_status", "hq_fallbacks", "hq_codes",
            "hq_gemv_workspace_size", "hq_gemv",
            "hq_haar_matrix", "hq_rotate", "hq_srft_encode", "hq_srft_decode",
-           "hq_kv_append", "hq_kv_read", "hq_kv_attend_workspace_size", "hq_kv_attend", "hq_kv_attend_tree", "hq_kv_evict",
+           "hq_kv_append", "hq_kv_read", "hq_kv_attend_workspace_size", "hq_kv_attend", "hq_kv_attend_tree_workspace_size",
+           "hq_kv_attend_tree", "hq_kv_evict",
            "hq_kv_reserve", "hq_kv_accept", "hq_attend_prompt")
 
 
@@ -132,6 +133,7 @@ def lib():
         L.hq_kv_read.argtypes = [P, P, u64, P, P, i32, P]
         L.hq_kv_attend_workspace_size.argtypes = [P, P, ctypes.POINTER(sz)]
         L.hq_kv_attend.argtypes = [P, P, P, sz, P]
+        L.hq_kv_attend_tree_workspace_size.argtypes = [P, P, ctypes.POINTER(sz)]
         L.hq_kv_attend_tree.argtypes = [P, P, P, P, sz, P]
         L.hq_kv_evict.argtypes = [P, P, P]
         L.hq_kv_reserve.argtypes = [P, P]
@@ -567,7 +569,8 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
     L, cp, ap = lib(), ctypes.byref(c), ctypes.byref(a)
     if ws is None:
         need = ctypes.c_size_t()
-        _check(L.hq_kv_attend_workspace_size(cp, ap, ctypes.byref(need)), "hq_kv_attend")
+        size = L.hq_kv_attend_workspace_size if parents is None else L.hq_kv_attend_tree_workspace_size
+        _check(size(cp, ap, ctypes.byref(need)), "hq_kv_attend")
         ws = _empty(need.value, torch.uint8, dev, stream)
     elif not (ws.is_contiguous() and ws.device == dev and ws.dtype == torch.uint8):
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")

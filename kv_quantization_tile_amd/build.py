@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libhq.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["hq_kernels.hip", "hq_api.hip", "hq_rotate.hip", "hq_srft.hip", "hq_kv.hip", "hq_attend.hip",
-           "hq_kv_steps.hip", "hq_prompt.hip"]
+           "hq_kv_steps.hip", "hq_prompt.hip", "hq_tree.hip"]
 
 # Floating-point flags: every binary32 operation that decides an integer code must be rounded
 # exactly once in program order (no contraction into FMA, no fast-math, denormals kept, correctly

@@ -1,0 +1,514 @@
+// hq_tree.hip -- attention of a tree of drafted tokens over the paged SRFT cache (the mathematics and the operands'
+// layout: hq_attend.hip).
+//
+// The drafts are a sequence's last cached tokens.  Draft i sees the held tokens before them and, of the drafts, its path from
+// the root: a bit each, found by walking up from the draft in LDS.  Held tokens need no bits, so only the steps that reach the
+// drafts look at them.
+//
+// A tile is R times 16 rows (queries x heads of the group), of a sequence and a KV head.  A workgroup takes a tile
+// and one split of the tokens; its four wavefronts take 32 tokens in turn, every wavefront with all the rows, so that
+// codes become operands once in registers for all of them and nothing is shared but the join at the end.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/hq.h"
+#include "hq_attend_device.h"
+
+namespace hq_kv {
+
+constexpr int kMaxTree = 256;  // drafts of a sequence
+
+struct TreeArgs {
+  const int32_t* parents;
+  uint32_t tiles, splits, chunk;  // of a sequence, at most; of a tile, and their tokens
+  float *po, *pml;                // [seqs][tiles][heads][splits][16 R], 128 and 2 values
+};
+
+// Tokens that some row of [r0, r0 + count) sees, as one range: draft i sees drafts up to itself, and no fewer held tokens
+// than a root.
+__device__ __forceinline__ void tree_range(const AttendArgs& a, const Seq& s, uint32_t r0, uint32_t count, int32_t* lo, int32_t* hi) {
+  const uint32_t rows = (uint32_t)s.m * a.group;
+  if (r0 >= rows) {
+    *lo = *hi = 0;
+    return;
+  }
+  int32_t x;
+  visible(a, s, 0, lo, &x);
+  visible(a, s, (int32_t)query_of(a, (r0 + count < rows ? r0 + count : rows) - 1u), &x, hi);
+  if (*lo > *hi) *lo = *hi;
+}
+// Held tokens that every row up to query `last` sees: those that a draft as deep as its index sees.
+__device__ __forceinline__ void tree_common(const AttendArgs& a, const Seq& s, uint32_t last, int32_t* lo, int32_t* hi) {
+  int32_t x;
+  visible(a, s, (int32_t)last, lo, &x);
+  *hi = s.back > 0 ? s.back : 0;
+}
+
+template <int QUERIES>
+struct Tree {
+  int32_t parent[kMaxTree];
+  uint32_t seen[QUERIES][kMaxTree / 32];
+  uint32_t depth[QUERIES];
+};
+// Walks up from queries [i0, i0 + count) with the workgroup's threads.  With a window, of a query's path the last `window`.  A
+// parent that is not before its draft counts as none.
+template <int QUERIES>
+__device__ __forceinline__ void climb(const AttendArgs& a, const int32_t* parents, const Seq& s, uint32_t i0, uint32_t count, Tree<QUERIES>& t) {
+  for (uint32_t i = threadIdx.x; i < i0 + count; i += kAttBlock) {
+    const int32_t p = parents[(uint64_t)s.q0 + i];
+    t.parent[i] = p >= 0 && p < (int32_t)i ? p : -1;
+  }
+  __syncthreads();
+  for (uint32_t q = threadIdx.x; q < count; q += kAttBlock) {
+#pragma unroll
+    for (int w = 0; w < kMaxTree / 32; ++w) t.seen[q][w] = 0;
+    uint32_t depth = 0;
+    for (int32_t i = (int32_t)(i0 + q); i >= 0; i = t.parent[i], ++depth)
+      if (a.window == 0 || depth < a.window) t.seen[q][i >> 5] |= 1u << (i & 31);
+    t.depth[q] = depth - 1u;
+  }
+  __syncthreads();
+}
+// The first held token that a query of this depth sees.
+__device__ __forceinline__ int32_t tree_lo(const AttendArgs& a, const Seq& s, uint32_t depth) {
+  const int64_t l = a.window ? (int64_t)s.back + depth + 1 - (int64_t)a.window : 0;
+  return l < 0 ? 0 : l > 0x7FFFFFFF ? 0x7FFFFFFF : (int32_t)l;
+}
+
+template <int BITS, int R>
+__global__ __launch_bounds__(kAttBlock, R == 2 || BITS == 8 ? 2 : 3) void attend_tree_kernel(AttendArgs a, TreeArgs g, Tables K) {
+  constexpr uint32_t kRows = 16u * R;
+  __shared__ __align__(16) float s_o[kAttWaves][16][kPad];
+  __shared__ __align__(16) _Float16 s_q[kRows][kD + 8];
+  __shared__ float s_f[kRows], s_m[kAttWaves][kRows], s_l[kAttWaves][kRows], s_lam[2][kD];
+  __shared__ Tree<(int)kRows> s_tree;
+  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
+  // Consecutive workgroups go to the 8 XCDs in turn: the tiles of one (sequence, head, split), which read the same codes, meet
+  // in one XCD's L2.
+  const uint32_t item = blockIdx.x / (8u * g.tiles) * 8u + blockIdx.x % 8u, tile = blockIdx.x / 8u % g.tiles;
+  const uint32_t split = item % g.splits, h = item / g.splits % a.heads, b = item / g.splits / a.heads;
+  if (b >= a.seqs) return;
+  const Seq s = seq_of(a, b);
+  const uint32_t r0 = tile * kRows, all = (uint32_t)s.m * a.group;
+  if (r0 >= all) return;
+  const uint32_t rows = all - r0 < kRows ? all - r0 : kRows, i0 = query_of(a, r0), last = query_of(a, r0 + rows - 1u);
+  int32_t lo, hi;
+  tree_range(a, s, r0, kRows, &lo, &hi);
+  int32_t t0 = (int32_t)(split * g.chunk), t1 = t0 + (int32_t)g.chunk;
+  t0 = t0 > (lo & ~15) ? t0 : lo & ~15;
+  t1 = t1 < hi ? t1 : hi;
+  if (a.pages == 0) t1 = t0;
+  if (t0 >= t1 && g.splits > 1) return;  // the same for the whole workgroup
+  const uint32_t P = 1u << a.page_log2;
+  const uint64_t page_size = (uint64_t)P * Page<BITS>::kToken;
+
+  Share<BITS> cur[2], nxt[2];
+  auto load = [&](int32_t t, int32_t page, Share<BITS>& sh) __attribute__((always_inline)) {
+    // an absent page's place is taken by page 0, masked below
+    const uint8_t* p = a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + h) * page_size;
+    load_keys<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
+    load_values<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
+  };
+  constexpr int32_t kStep = 32 * kAttWaves;
+  int32_t t = t0 + 32 * (int32_t)wave;
+  int32_t pg0 = page_of(a, b, t, t1), pg1 = page_of(a, b, t + 16, t1);
+  if (t < t1) {
+    load(t, pg0, cur[0]);
+    load(t + 16, pg1, cur[1]);
+  }
+  int32_t en0 = entry_of(a, b, t + kStep, t1), en1 = entry_of(a, b, t + kStep + 16, t1);
+
+  stage_tables(K, s_lam);
+  {  // the rows: 16 at a time, four to a wavefront, 16 lanes each
+    const LaneForward forward = lane_forward(K, n);
+#pragma unroll 1
+    for (uint32_t r = threadIdx.x >> 4; r < kRows; r += 16u) {
+      float f = 1.0f;
+      if ((r & ~3u) < rows) f = rotate_row<BITS>(a, K, s_lam[0], h, (uint32_t)s.q0 * a.group + r0 + r, r < rows, n, forward, s_q[r], nullptr);
+      else *reinterpret_cast<f16x8*>(&s_q[r][8 * n]) = (f16x8)(_Float16)0.0f;
+      if (n == 0) s_f[r] = f;
+    }
+  }
+  // splits of held tokens alone need no tree, unless a window ends among them
+  const bool climbs = a.window || t1 > s.back;
+  if (climbs) climb(a, g.parents, s, i0, last - i0 + 1u, s_tree);
+  else __syncthreads();
+
+  const bool cap = a.cap_in > 0.0f;
+  f16x8 q[R][4];
+  float qf[R], eff[R], m[R], poison[R];
+  uint32_t query[R];
+  int32_t row_lo[R];
+  f32x4 o[R][8], ones[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[r][j] = *reinterpret_cast<const f16x8*>(&s_q[16 * r + n][8 * (4 * b4 + j)]);
+    qf[r] = s_f[16 * r + n];
+    eff[r] = cap ? 1.0f : qf[r];  // scores are eff sc: the product with qf waits for the exponent's fma
+    m[r] = kLowest;
+    poison[r] = 0.0f;
+    query[r] = 16u * r + n < rows ? query_of(a, r0 + 16u * r + n) - i0 : 0u;
+    row_lo[r] = climbs ? tree_lo(a, s, s_tree.depth[query[r]]) : 0;
+    ones[r] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[r][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // the tokens every row sees need no mask (rows past the last are products with zero)
+  int32_t all_lo, all_hi;
+  tree_common(a, s, last, &all_lo, &all_hi);
+  // whether row r sees token tok, which the tile sees
+  auto sees = [&](int r, int32_t tok) __attribute__((always_inline)) {
+    const uint32_t j = (uint32_t)(tok - s.back) & (kMaxTree - 1);
+    const bool draft = (s_tree.seen[query[r]][j >> 5] >> (j & 31u)) & 1u;
+    return bool(((tok < s.back) & (tok >= row_lo[r])) | ((tok >= s.back) & draft));
+  };
+
+  for (; t < t1; t += kStep) {
+    const bool there[2] = {pg0 >= 0, pg1 >= 0};
+    pg0 = page_in(a, en0);
+    pg1 = page_in(a, en1);
+    en0 = entry_of(a, b, t + 2 * kStep, t1);
+    en1 = entry_of(a, b, t + 2 * kStep + 16, t1);
+    if (t + kStep < t1) {
+      load(t + kStep, pg0, nxt[0]);
+      load(t + kStep + 16, pg1, nxt[1]);
+    }
+    uint32_t large = 0, gone = 0;  // bit u: shrunk keys, bit 2 + u: shrunk values; tokens that take no part
+    f32x4 sc[R][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (__builtin_amdgcn_ballot_w64(odd_scales<BITS>(most(cur[u].ks[0], cur[u].ks[1])))) {
+        const int32_t tok = t + 16 * u + (int32_t)n;
+        if (!there[u] || tok < lo || tok >= t1) cur[u].ks[0] = cur[u].ks[1] = 0u;  // a token that no row sees may hold anything
+        gone |= gone_keys(cur[u].ks) << (16 * u);
+        if (shrink<BITS>(cur[u].ks)) large |= 1u << u;
+      }
+      f16x8 kh[4], kl[4];
+      key_operands<BITS, false>(cur[u], kh, kl);
+#pragma unroll
+      for (int r = 0; r < R; ++r) sc[r][u] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) sc[r][u] = mfma(kh[j], q[r][j], sc[r][u]);
+    }
+    if (large & 3u) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) sc[r][u] *= (large >> u) & 1u ? kShrunk : 1.0f;
+    }
+    if (cap) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sc[r][i >> 2][i & 3] = a.cap_out * tanh32(sc[r][i >> 2][i & 3] * qf[r] * a.cap_in);
+    }
+    // Value vectors with NaN scales make the rows that see them NaN and no other (0 NaN in the product would reach every row):
+    // their scales count as 0, and the rows are poisoned.
+    uint32_t bad[2] = {0u, 0u};
+    const bool odd = __builtin_amdgcn_ballot_w64(odd_scales<BITS>(__builtin_elementwise_max(most(cur[0].vs[0], cur[0].vs[1]), most(cur[1].vs[0], cur[1].vs[1])))) != 0u;
+    if (odd) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t drop = bad[u] = bad_scales(cur[u].vs);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t tok = t + 16 * u + 4 * (int32_t)b4 + i;
+          if (!there[u] || tok < lo || tok >= t1) drop |= 1u << i;  // as with the keys
+        }
+        // the 16 lanes of a token hold one group each: a vector with one NaN scale is NaN as a whole, and poisons by each of them
+        drop_scales(cur[u].vs, drop);
+        if (shrink<BITS>(cur[u].vs)) large |= 4u << u;
+      }
+    }
+    if (gone || !(there[0] && there[1] && t >= all_lo && t + 32 <= all_hi && t + 32 <= t1)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int32_t tok = t + 16 * (i >> 2) + 4 * (int32_t)b4 + (i & 3);
+          const bool hidden = (gone >> (4u * b4) >> (16 * (i >> 2) + (i & 3))) & 1u;
+          const bool shown = !hidden & there[i >> 2] & (tok < t1) & sees(r, tok);
+          sc[r][i >> 2][i & 3] = shown ? sc[r][i >> 2][i & 3] : -__builtin_inff();
+        }
+    }
+    if (odd) {
+      // which of 16 tokens have a NaN scale in some lane
+      uint32_t word[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        word[u] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t votes = __builtin_amdgcn_ballot_w64((bad[u] >> i) & 1u);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) word[u] |= (votes >> (16 * k)) & 0xFFFFu ? 1u << (4 * k + i) : 0u;
+        }
+        drop_scales(cur[u].vs, (word[u] >> (4 * b4)) & 15u);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if ((word[i >> 2] >> (4 * b4 + (i & 3))) & 1u && sc[r][i >> 2][i & 3] != -__builtin_inff()) poison[r] = __builtin_nanf("");
+    }
+    float top[R];
+    bool rise = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      top[r] = sc[r][0][0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top[r] = fmaxf(top[r], sc[r][i >> 2][i & 3]);
+      top[r] *= eff[r];
+      rise |= top[r] > m[r] + kSlack;
+    }
+    // with shrunk values, P goes up to 2^15 against the maximum itself
+    if (large >= 4u || __builtin_amdgcn_ballot_w64(rise)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float mn = fmaxf(m[r], blocks_max(top[r])), f = __builtin_amdgcn_exp2f(m[r] - mn);
+        m[r] = mn;
+        ones[r] *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[r][i] *= f;
+      }
+    }
+    f16x8 p[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float base = kPScaleLog2 - m[r];
+      U32x4 x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r][i >> 1][2 * (i & 1)], eff[r], base));
+        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r][i >> 1][2 * (i & 1) + 1], eff[r], base));
+        x.v[i] = u2((f16x2){(_Float16)p0, (_Float16)p1});
+      }
+      p[r] = frag(x);
+      // the sum of the rounded P, the one the output is weighted with, is one more product
+      ones[r] = mfma((f16x8)(_Float16)1.0f, p[r], ones[r]);
+      if (large >= 4u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[r][i] *= (large >> (2 + (i >> 2))) & 1u ? (_Float16)kShrunk : (_Float16)1.0f;
+      }
+    }
+    uint32_t v0[8][2], v1[8][2];
+    value_operands<BITS>(cur[0], v0);
+    value_operands<BITS>(cur[1], v1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const U32x4 v = {{v0[i][0], v0[i][1], v1[i][0], v1[i][1]}};
+#pragma unroll
+      for (int r = 0; r < R; ++r) o[r][i] = mfma(frag(v), p[r], o[r][i]);
+    }
+    cur[0] = nxt[0];
+    cur[1] = nxt[1];
+  }
+
+  // the wavefronts' parts, joined in order, 16 rows at a time
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    poison[r] = blocks_sum(poison[r]);
+    if (b4 == 0) {
+      s_m[wave][16 * r + n] = m[r];
+      s_l[wave][16 * r + n] = ones[r][0];
+    }
+  }
+  __syncthreads();
+  const uint32_t row = threadIdx.x >> 4;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (16u * r >= rows) break;  // the same for the whole workgroup
+    float mm = s_m[0][16 * r + n];
+#pragma unroll
+    for (int w = 1; w < kAttWaves; ++w) mm = fmaxf(mm, s_m[w][16 * r + n]);
+    const float f = __builtin_amdgcn_exp2f(m[r] - mm);
+    if (r) __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<f32x4*>(&s_o[wave][n][8 * (4 * b4 + c) + i]) =
+            (f32x4){o[r][i][c] * f + poison[r], o[r][i + 1][c] * f + poison[r], o[r][i + 2][c] * f + poison[r], o[r][i + 3][c] * f + poison[r]};
+    __syncthreads();
+    const uint32_t x = 16u * r + row;
+    if ((x & ~3u) >= rows) continue;
+    float total = 0.0f, mr = s_m[0][x], y[8];
+#pragma unroll
+    for (int w = 1; w < kAttWaves; ++w) mr = fmaxf(mr, s_m[w][x]);
+#pragma unroll
+    for (int w = 0; w < kAttWaves; ++w) total += s_l[w][x] * __builtin_amdgcn_exp2f(s_m[w][x] - mr);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = s_o[0][row][8 * n + i];
+#pragma unroll
+    for (int w = 1; w < kAttWaves; ++w)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] += s_o[w][row][8 * n + i];
+    if (g.splits == 1) {
+      store_row<BITS>(a, K, s_lam[1], s, h, r0 + x, n, lane_inverse(K, n), y, total);
+      continue;
+    }
+    const uint64_t p = ((((uint64_t)b * g.tiles + tile) * a.heads + h) * g.splits + split) * kRows + x;
+    *reinterpret_cast<f32x4*>(g.po + p * kD + 8 * n) = (f32x4){y[0], y[1], y[2], y[3]};
+    *reinterpret_cast<f32x4*>(g.po + p * kD + 8 * n + 4) = (f32x4){y[4], y[5], y[6], y[7]};
+    if (n == 0) *reinterpret_cast<f32x2*>(g.pml + p * 2) = (f32x2){mr, total};
+  }
+}
+
+// Joins a row's splits, turns it back and stores it.  WIDE: one workgroup a row, its 16 groups of 16 lanes take
+// the splits in turn and join in LDS; otherwise 16 lanes take a row and all its splits.
+template <int BITS, bool WIDE>
+__global__ __launch_bounds__(kAttBlock) void join_tree_kernel(AttendArgs a, TreeArgs g, Tables K, uint32_t tile_rows, uint32_t most_rows) {
+  __shared__ float s_y[WIDE ? 16 : 1][kD + 4], s_m[16], s_l[16];
+  const uint32_t l = threadIdx.x & 15u, k = threadIdx.x >> 4;
+  const uint32_t index = WIDE ? blockIdx.x : blockIdx.x * 16u + k;
+  // rows of a (sequence, head) in order; none of a wavefront's or all of its four are in a tile of the sequence
+  const uint32_t r = index % most_rows, h = index / most_rows % a.heads, b = index / most_rows / a.heads;
+  if (b >= a.seqs) return;
+  const Seq s = seq_of(a, b);
+  if ((r & ~3u) >= (uint32_t)s.m * a.group) return;
+  const uint32_t tile = r / tile_rows, r0 = tile * tile_rows;
+  int32_t lo, hi;
+  tree_range(a, s, r0, tile_rows, &lo, &hi);
+  if (a.pages == 0) hi = lo;
+  const uint32_t s0 = hi > lo ? (uint32_t)lo / g.chunk : 0u, s1 = hi > lo ? ((uint32_t)hi + g.chunk - 1u) / g.chunk : 0u;
+  const uint64_t first = (((uint64_t)b * g.tiles + tile) * a.heads + h) * g.splits;
+  float m = kLowest, sum = 0.0f, y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+  for (uint32_t i = s0 + (WIDE ? k : 0u); i < s1; i += WIDE ? 16u : 1u) {
+    const uint64_t p = (first + i) * tile_rows + r - r0;
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(g.pml + p * 2);
+    const f32x4 u0 = *reinterpret_cast<const f32x4*>(g.po + p * kD + 8 * l), u1 = *reinterpret_cast<const f32x4*>(g.po + p * kD + 8 * l + 4);
+    const float mn = fmaxf(m, ml[0]), f0 = __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(ml[0] - mn);
+    m = mn;
+    sum = sum * f0 + ml[1] * f1;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      y[c] = y[c] * f0 + u0[c] * f1;
+      y[4 + c] = y[4 + c] * f0 + u1[c] * f1;
+    }
+  }
+  if (WIDE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_y[WIDE ? k : 0][8 * l + i] = y[i];
+    if (l == 0) {
+      s_m[k] = m;
+      s_l[k] = sum;
+    }
+    __syncthreads();
+    if (k) return;
+    m = s_m[0];
+    for (int i = 1; i < 16; ++i) m = fmaxf(m, s_m[i]);
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+    for (int i = 0; i < 16; ++i) {
+      const float f = __builtin_amdgcn_exp2f(s_m[i] - m);
+      sum += s_l[i] * f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) y[c] += s_y[WIDE ? i : 0][8 * l + c] * f;
+    }
+  }
+  store_row<BITS>(a, K, K.v, s, h, r, l, lane_inverse(K, l), y, sum);
+}
+
+}  // namespace hq_kv
+
+using namespace hq_kv;
+
+namespace {
+
+bool is_tree(const hq_kv_attend_args* g) { return g && g->causal && !g->weights && g->max_q <= (uint32_t)kMaxTree; }
+
+struct TreePlan {
+  uint32_t max_q, rows, r, tiles, splits, chunk;
+  uint64_t grid, joins, pml, po, bytes;
+};
+
+// HQ_OK, or an error for a call that the launches cannot take.
+int plan_tree(const hq_kv_cache& c, const hq_kv_attend_args& g, TreePlan* out) {
+  TreePlan p;
+  const uint64_t each = g.q_start || g.seqs == 0 ? g.total_q : g.total_q / g.seqs;
+  p.max_q = (uint32_t)(each < g.max_q ? each : g.max_q);
+  const uint64_t rows = (uint64_t)p.max_q * (g.q_heads / c.heads), sh = (uint64_t)g.seqs * c.heads;
+  if (g.total_q * (g.q_heads / c.heads) > 0x7FFFFF00ull || rows > 0x7FFFFF00ull / 64u) return HQ_ERR_INVALID_ARG;
+  p.rows = (uint32_t)rows;
+  p.r = rows <= 16 ? 1 : 2;
+  p.tiles = rows ? (uint32_t)((rows + 16u * p.r - 1u) / (16u * p.r)) : 1u;
+  const uint64_t items = sh * p.tiles, target = p.r == 1 ? 2048 : 512;
+  uint64_t splits = items ? (target + items - 1) / items : 1;
+  const uint64_t most = ((uint64_t)g.max_len + 511) / 512;
+  if (splits > most) splits = most;
+  if (splits < 1) splits = 1;
+  p.chunk = (uint32_t)(((g.max_len + splits - 1) / splits + 127) / 128 * 128);
+  if (p.chunk == 0) p.chunk = 128;
+  p.splits = (g.max_len + p.chunk - 1) / p.chunk;
+  if (p.splits == 0) p.splits = 1;
+  p.grid = (sh * p.splits + 7) / 8 * 8 * p.tiles;
+  p.joins = sh * ((rows + 15) / 16 * 16);
+  if (p.grid > kMaxThreads / kAttBlock || p.joins > kMaxThreads / 16) return HQ_ERR_INVALID_ARG;
+  const uint64_t parts = p.splits > 1 ? items * p.splits * 16u * p.r : 0;
+  p.pml = 0;
+  p.po = (parts * 8 + 255) / 256 * 256;
+  p.bytes = p.po + parts * kD * 4;
+  *out = p;
+  return HQ_OK;
+}
+
+template <int BITS>
+void launch_tree(const AttendArgs& a, const TreeArgs& g, const Tables& T, const TreePlan& p, hipStream_t st) {
+  const dim3 grid((uint32_t)p.grid), block(kAttBlock);
+  if (p.r == 1) hipLaunchKernelGGL((attend_tree_kernel<BITS, 1>), grid, block, 0, st, a, g, T);
+  else hipLaunchKernelGGL((attend_tree_kernel<BITS, 2>), grid, block, 0, st, a, g, T);
+  if (p.splits == 1) return;
+  // A workgroup a row while those are at most 16 a CU, 16 lanes a row beyond, as in hq_attend.hip.
+  const uint32_t each = (p.rows + 15u) / 16u * 16u;
+  if (p.joins <= 4096) hipLaunchKernelGGL((join_tree_kernel<BITS, true>), dim3((uint32_t)p.joins), block, 0, st, a, g, T, 16u * p.r, each);
+  else hipLaunchKernelGGL((join_tree_kernel<BITS, false>), dim3((uint32_t)(p.joins / 16)), block, 0, st, a, g, T, 16u * p.r, each);
+}
+
+}  // namespace
+
+extern "C" {
+
+int hq_kv_attend_tree_workspace_size(const hq_kv_cache* cache, const hq_kv_attend_args* args, size_t* bytes) {
+  if (!bytes || !is_tree(args)) return HQ_ERR_INVALID_ARG;
+  if (int rc = check_attend(cache, args)) return rc;
+  TreePlan p;
+  if (int rc = plan_tree(*cache, *args, &p)) return rc;
+  *bytes = p.bytes;
+  return HQ_OK;
+}
+
+int hq_kv_attend_tree(const hq_kv_cache* cache, const hq_kv_attend_args* args, const int32_t* parents, void* workspace,
+                      size_t workspace_bytes, hq_stream_t stream) {
+  if (!is_tree(args)) return HQ_ERR_INVALID_ARG;
+  if (int rc = check_attend(cache, args)) return rc;
+  AttendArgs a = {};
+  Tables T;
+  bool nothing;
+  if (int rc = attend_args(*cache, *args, &a, &T, &nothing)) return rc;
+  if (nothing) return HQ_OK;
+  if (!parents || ((uintptr_t)parents & 3u)) return HQ_ERR_INVALID_ARG;
+  TreePlan p;
+  if (int rc = plan_tree(*cache, *args, &p)) return rc;
+  if (p.bytes && (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < p.bytes)) return HQ_ERR_INVALID_ARG;
+  a.max_q = p.max_q;
+  TreeArgs g;
+  g.parents = parents;
+  g.tiles = p.tiles;
+  g.splits = p.splits;
+  g.chunk = p.chunk;
+  g.pml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.pml);
+  g.po = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.po);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (cache->bits == 4) launch_tree<4>(a, g, T, p, st);
+  else launch_tree<8>(a, g, T, p, st);
+  return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
+}
+
+}  // extern "C"

@@ -67,6 +67,16 @@ def test_accept_refusals(kw):
     assert accept(cache(), **kw) == E
 
 
+def test_tree_workspace():
+    L, c, size = hq.lib(), cache(), ctypes.c_size_t(0)
+    call = lambda a, s=size: L.hq_kv_attend_tree_workspace_size(ctypes.byref(c), ctypes.byref(a), ctypes.byref(s) if s is not None else None)  # noqa: E731
+    assert call(attend_args(), None) == E and call(attend_args(causal=0)) == E and call(attend_args(max_q=257, total_q=4 * 257)) == E
+    for q in (1, 4, 7, 16, 33, 200):
+        a = attend_args(max_q=q, total_q=4 * q, max_len=40000, table_width=700)
+        assert call(a) == hq.HQ_OK and size.value % 256 == 0
+        assert tree(c, a, size=size.value - 1) == E
+
+
 def test_accept_of_nothing():
     assert hq.lib().hq_kv_accept(ctypes.byref(cache()), None, None) == E
     assert accept(cache(), seqs=0, total_q=0, lens=None, accepted=None, next=None, change=None, path=None, table=None) == hq.HQ_OK
@@ -81,7 +91,8 @@ def test_tree_refusals(kw):
 def test_tree_parents():
     assert tree(cache(), attend_args(), parents=None) == E and tree(cache(), attend_args(), parents=OK + 2) == E
     assert hq.lib().hq_kv_attend_tree(ctypes.byref(cache()), None, OK, OK, 1 << 30, None) == E
-    assert tree(cache(), attend_args(), size=16) == E and tree(cache(), attend_args(), ws=None) == E
+    a = attend_args(max_len=40000, table_width=700)
+    assert tree(cache(), a, size=16) == E and tree(cache(), a, ws=None) == E and tree(cache(), a, ws=OK + 16) == E
     assert tree(cache(), attend_args(total_q=0), parents=None, ws=None, size=0) == hq.HQ_OK
 
 
@@ -148,7 +159,7 @@ def world(monkeypatch):
             return hq.HQ_OK
         return call
 
-    names = ("hq_kv_reserve", "hq_kv_attend_workspace_size", "hq_kv_attend", "hq_kv_attend_tree", "hq_kv_accept", "hq_attend_prompt")
+    names = ("hq_kv_reserve", "hq_kv_attend_tree_workspace_size", "hq_kv_attend", "hq_kv_attend_tree", "hq_kv_accept", "hq_attend_prompt")
     monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
     monkeypatch.setattr(torch.cuda, "device", Current)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 1000 + i, raising=False)
