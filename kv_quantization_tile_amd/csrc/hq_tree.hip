@@ -5,9 +5,10 @@
 // the root: a bit each, found by walking up from the draft in LDS.  Held tokens need no bits, so only the steps that reach the
 // drafts look at them.
 //
-// A tile is R times 16 rows (queries x heads of the group), of a sequence and a KV head.  A workgroup takes a tile
-// and one split of the tokens; its four wavefronts take 32 tokens in turn, every wavefront with all the rows, so that
-// codes become operands once in registers for all of them and nothing is shared but the join at the end.
+// Rows are queries x heads of the group, of a sequence and a KV head; a workgroup takes a tile of them and one split of the
+// tokens.  Up to 32 rows: its four wavefronts take 32 tokens in turn, every wavefront with all the rows, so that codes become
+// operands in registers and nothing is shared but the join at the end.  More: operands are made once, 16 tokens by each
+// wavefront, and shared through LDS, and each wavefront owns 16 or 32 rows.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -76,6 +77,24 @@ __device__ __forceinline__ int32_t tree_lo(const AttendArgs& a, const Seq& s, ui
   return l < 0 ? 0 : l > 0x7FFFFFFF ? 0x7FFFFFFF : (int32_t)l;
 }
 
+// Whether a query sees token `tok`, which its tile sees; `lo` is the first held token it sees.
+template <int QUERIES>
+__device__ __forceinline__ bool tree_sees(const Tree<QUERIES>& t, int32_t back, uint32_t query, int32_t lo, int32_t tok) {
+  const uint32_t j = (uint32_t)(tok - back) & (kMaxTree - 1);
+  const bool draft = (t.seen[query][j >> 5] >> (j & 31u)) & 1u;
+  return bool(((tok < back) & (tok >= lo)) | ((tok >= back) & draft));
+}
+
+// What a workgroup takes.  Consecutive workgroups go to the 8 XCDs in turn: the tiles of one (sequence, head, split), which
+// read the same codes, meet in one XCD's L2.
+struct TreeItem {
+  uint32_t b, h, split, tile;
+};
+__device__ __forceinline__ TreeItem tree_item(const AttendArgs& a, const TreeArgs& g) {
+  const uint32_t item = blockIdx.x / (8u * g.tiles) * 8u + blockIdx.x % 8u;
+  return {item / g.splits / a.heads, item / g.splits % a.heads, item % g.splits, blockIdx.x / 8u % g.tiles};
+}
+
 template <int BITS, int R>
 __global__ __launch_bounds__(kAttBlock, R == 2 || BITS == 8 ? 2 : 3) void attend_tree_kernel(AttendArgs a, TreeArgs g, Tables K) {
   constexpr uint32_t kRows = 16u * R;
@@ -84,10 +103,8 @@ __global__ __launch_bounds__(kAttBlock, R == 2 || BITS == 8 ? 2 : 3) void attend
   __shared__ float s_f[kRows], s_m[kAttWaves][kRows], s_l[kAttWaves][kRows], s_lam[2][kD];
   __shared__ Tree<(int)kRows> s_tree;
   const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
-  // Consecutive workgroups go to the 8 XCDs in turn: the tiles of one (sequence, head, split), which read the same codes, meet
-  // in one XCD's L2.
-  const uint32_t item = blockIdx.x / (8u * g.tiles) * 8u + blockIdx.x % 8u, tile = blockIdx.x / 8u % g.tiles;
-  const uint32_t split = item % g.splits, h = item / g.splits % a.heads, b = item / g.splits / a.heads;
+  const TreeItem at = tree_item(a, g);
+  const uint32_t b = at.b, h = at.h, split = at.split, tile = at.tile;
   if (b >= a.seqs) return;
   const Seq s = seq_of(a, b);
   const uint32_t r0 = tile * kRows, all = (uint32_t)s.m * a.group;
@@ -158,13 +175,6 @@ __global__ __launch_bounds__(kAttBlock, R == 2 || BITS == 8 ? 2 : 3) void attend
   // the tokens every row sees need no mask (rows past the last are products with zero)
   int32_t all_lo, all_hi;
   tree_common(a, s, last, &all_lo, &all_hi);
-  // whether row r sees token tok, which the tile sees
-  auto sees = [&](int r, int32_t tok) __attribute__((always_inline)) {
-    const uint32_t j = (uint32_t)(tok - s.back) & (kMaxTree - 1);
-    const bool draft = (s_tree.seen[query[r]][j >> 5] >> (j & 31u)) & 1u;
-    return bool(((tok < s.back) & (tok >= row_lo[r])) | ((tok >= s.back) & draft));
-  };
-
   for (; t < t1; t += kStep) {
     const bool there[2] = {pg0 >= 0, pg1 >= 0};
     pg0 = page_in(a, en0);
@@ -231,7 +241,7 @@ __global__ __launch_bounds__(kAttBlock, R == 2 || BITS == 8 ? 2 : 3) void attend
         for (int i = 0; i < 8; ++i) {
           const int32_t tok = t + 16 * (i >> 2) + 4 * (int32_t)b4 + (i & 3);
           const bool hidden = (gone >> (4u * b4) >> (16 * (i >> 2) + (i & 3))) & 1u;
-          const bool shown = !hidden & there[i >> 2] & (tok < t1) & sees(r, tok);
+          const bool shown = !hidden & there[i >> 2] & (tok < t1) & tree_sees(s_tree, s.back, query[r], row_lo[r], tok);
           sc[r][i >> 2][i & 3] = shown ? sc[r][i >> 2][i & 3] : -__builtin_inff();
         }
     }
@@ -358,6 +368,364 @@ __global__ __launch_bounds__(kAttBlock, R == 2 || BITS == 8 ? 2 : 3) void attend
   }
 }
 
+// More rows: the queries' rows transformed once, to the workspace, 16 a workgroup.
+template <int BITS>
+__global__ __launch_bounds__(kAttBlock) void rotate_tree_kernel(AttendArgs a, Tables K) {
+  __shared__ __align__(16) _Float16 s_q[16][kD + 8];
+  __shared__ float s_lam[2][kD];
+  stage_tables(K, s_lam);
+  const uint32_t l = threadIdx.x & 15u, k = threadIdx.x >> 4, per = (a.rows + 15u) / 16u, h = blockIdx.x / per, row = blockIdx.x % per * 16u + k;
+  const float f = rotate_row<BITS>(a, K, s_lam[0], h, row, row < a.rows, l, lane_forward(K, l), s_q[k], nullptr);
+  // a row is written and read by the same wavefront
+  wave_sync();
+  if (row >= a.rows) return;
+  const uint64_t at = (uint64_t)h * a.rows + row;
+  if (l == 0) a.qf[at] = f;
+  *reinterpret_cast<f16x8*>(a.qhi + at * kD + 8 * l) = *reinterpret_cast<const f16x8*>(&s_q[k][8 * l]);
+}
+
+struct TreeStage {
+  f16x8 k[kAttWaves][4][64];      // [16 tokens][step][lane]
+  f16x8 v[kAttWaves / 2][8][64];  // [32 tokens][coordinate][lane]
+};
+
+// R = 1 (up to 64 rows): one stage, four workgroups a CU.  R = 2: two stages, so that a turn has one barrier, and two workgroups.
+template <int R>
+constexpr size_t tree_lds() { return R == 1 ? sizeof(float) * kAttWaves * 16 * kPad : 2 * sizeof(TreeStage); }
+
+template <int BITS, int R>
+__global__ __launch_bounds__(kAttBlock, R == 1 ? 4 : 2) void attend_tree_many_kernel(AttendArgs a, TreeArgs g, Tables K) {
+  constexpr int32_t kTok = 16 * kAttWaves;
+  constexpr uint32_t kRows = 16u * R * kAttWaves;
+  extern __shared__ __align__(16) uint8_t raw[];
+  TreeStage* st = reinterpret_cast<TreeStage*>(raw);
+  float(*s_o)[16][kPad] = reinterpret_cast<float(*)[16][kPad]>(raw);  // [wavefront], after the last product
+  // bits 0..15: tokens with NaN value scales, 16..31: tokens that take no part; bits 0 and 1: shrunk keys, values
+  __shared__ uint2 s_flags[2][kAttWaves];
+  __shared__ Tree<(int)kRows> s_tree;
+  const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15u, b4 = lane >> 4;
+  const TreeItem at = tree_item(a, g);
+  if (at.b >= a.seqs) return;
+  const uint32_t h = at.h;
+  const Seq s = seq_of(a, at.b);
+  const uint32_t rows = (uint32_t)s.m * a.group, r0 = at.tile * kRows, w0 = r0 + wave * 16u * R;
+  if (r0 >= rows) return;
+  const uint32_t i0 = query_of(a, r0), last = query_of(a, (r0 + kRows < rows ? r0 + kRows : rows) - 1u);
+  int32_t lo, hi, wlo, whi, all_lo, all_hi;
+  tree_range(a, s, r0, kRows, &lo, &hi);
+  tree_range(a, s, w0, 16u * R, &wlo, &whi);
+  tree_common(a, s, last, &all_lo, &all_hi);
+  if (w0 + 16u * R > rows) all_lo = all_hi = 0;  // rows that are not there see nothing
+  int32_t t0 = (int32_t)(at.split * g.chunk), t1 = t0 + (int32_t)g.chunk;
+  t0 = t0 > (lo & ~15) ? t0 : lo & ~15;
+  t1 = t1 < hi ? t1 : hi;
+  if (a.pages == 0) t1 = t0;
+  if (t0 >= t1 && g.splits > 1) return;  // the same for the whole workgroup
+  const uint32_t b = at.b;
+  const uint32_t P = 1u << a.page_log2;
+  const uint64_t page_size = (uint64_t)P * Page<BITS>::kToken;
+
+  Share<BITS> sh;
+  auto load = [&](int32_t t, int32_t page) __attribute__((always_inline)) {
+    const uint8_t* p = a.cache + ((uint64_t)(page < 0 ? 0 : page) * a.heads + h) * page_size;
+    load_keys<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
+    load_values<BITS>(p, P, (uint32_t)t & (P - 1u), lane, sh);
+  };
+  // this wavefront's 16 tokens at t, as operands
+  auto stage = [&](TreeStage& d, uint2* flags, int32_t t, int32_t page) __attribute__((always_inline)) {
+    uint32_t word = page < 0 ? 0xFFFF0000u : 0u, large = 0;
+    if (__builtin_amdgcn_ballot_w64(odd_scales<BITS>(most(sh.ks[0], sh.ks[1])))) {
+      const int32_t tok = t + (int32_t)n;
+      if (page < 0 || tok < lo || tok >= t1) sh.ks[0] = sh.ks[1] = 0u;  // a token that no row sees may hold anything
+      word |= gone_keys(sh.ks) << 16;
+      if (shrink<BITS>(sh.ks)) large |= 1u;
+    }
+    f16x8 kh[4], kl[4];
+    key_operands<BITS, false>(sh, kh, kl);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d.k[wave][j][lane] = kh[j];
+    if (__builtin_amdgcn_ballot_w64(odd_scales<BITS>(most(sh.vs[0], sh.vs[1])))) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int32_t tok = t + 4 * (int32_t)b4 + i;
+        if (page < 0 || tok < lo || tok >= t1) drop_scales(sh.vs, 1u << i);
+      }
+      const uint32_t bad = bad_scales(sh.vs);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t votes = __builtin_amdgcn_ballot_w64((bad >> i) & 1u);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) word |= (votes >> (16 * q)) & 0xFFFFu ? 1u << (4 * q + i) : 0u;
+      }
+      // a value vector with one NaN scale is NaN as a whole: its rows are poisoned, its scales count as 0
+      drop_scales(sh.vs, (word >> (4 * b4)) & 15u);
+      if (shrink<BITS>(sh.vs)) large |= 2u;
+    }
+    if (lane == 0) flags[wave] = make_uint2(word, large);
+    uint32_t v[8][2];
+    value_operands<BITS>(sh, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      reinterpret_cast<uint2*>(&d.v[wave >> 1][i][lane])[wave & 1u] = make_uint2(v[i][0], v[i][1]);
+  };
+  const int32_t mine = 16 * (int32_t)wave;
+  int32_t t = t0, page = page_of(a, b, t + mine, t1);
+  if (t < t1) load(t + mine, page);
+  int32_t next = entry_of(a, b, t + kTok + mine, t1);
+
+  uint32_t query[R];
+  const bool climbs = a.window || t1 > s.back;  // as for few rows
+  if (climbs) climb(a, g.parents, s, i0, last - i0 + 1u, s_tree);
+
+  const bool cap = a.cap_in > 0.0f;
+  f16x8 qh[R][4];
+  float qf[R], eff[R], m[R], poison[R];
+  int32_t row_lo[R];
+  bool have[R];
+  f32x4 o[R][8], ones[R];
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const uint64_t row = (uint64_t)h * a.rows + (uint64_t)s.q0 * a.group + w0 + 16u * q + n;
+    const bool some = w0 + 16u * q < rows;  // the last 16 may have rows of the next sequence among them: they see nothing
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      qh[q][j] = (f16x8)(_Float16)0.0f;
+      if (some) qh[q][j] = *reinterpret_cast<const f16x8*>(a.qhi + row * kD + 8 * (4 * b4 + j));
+    }
+    qf[q] = some ? a.qf[row] : 1.0f;
+    eff[q] = cap ? 1.0f : qf[q];  // scores are eff sc: the product with qf waits for the exponent's fma
+    m[q] = kLowest;
+    poison[q] = 0.0f;
+    have[q] = w0 + 16u * q + n < rows;
+    query[q] = have[q] ? query_of(a, w0 + 16u * q + n) - i0 : 0u;
+    row_lo[q] = climbs ? tree_lo(a, s, s_tree.depth[query[q]]) : 0;
+    ones[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[q][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // a new reference for the rows' exponentials
+  auto raise = [&](const float* top) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const float mn = fmaxf(m[q], blocks_max(top[q]));
+      const float f = __builtin_amdgcn_exp2f(m[q] - mn);
+      m[q] = mn;
+      ones[q] *= f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[q][i] *= f;
+    }
+  };
+  uint32_t buf = 0;
+  if (t < t1) {
+    stage(st[0], s_flags[0], t + mine, page);
+    __syncthreads();
+  }
+  for (; t < t1; t += kTok) {
+    const bool more = t + kTok < t1;
+    if (more) {
+      page = page_in(a, next);
+      load(t + kTok + mine, page);
+      next = entry_of(a, b, t + 2 * kTok + mine, t1);
+    }
+    const TreeStage& d = st[buf];
+    // blocks of 16 tokens with a flag, asked for once and not between the products
+    const uint2 flags = s_flags[buf][lane & (kAttWaves - 1)];
+    const uint32_t flagged = (uint32_t)__builtin_amdgcn_ballot_w64(lane < (uint32_t)kAttWaves && (flags.x | flags.y) != 0u);
+    bool whole = false;
+    {
+      if (!cap && !flagged && t >= all_lo && t + kTok <= all_hi && t + kTok <= t1) {
+        // every row sees every token: each step's scores are under way during the softmax of the one before
+        f32x4 sc[2][R][2];
+        auto products = [&](int w, f32x4 (*x)[2]) __attribute__((always_inline)) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int q = 0; q < R; ++q) x[q][u] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const f16x8 kh = d.k[2 * w + u][j][lane];
+#pragma unroll
+              for (int q = 0; q < R; ++q) x[q][u] = mfma(kh, qh[q][j], x[q][u]);
+            }
+          }
+        };
+        products(0, sc[0]);
+#pragma unroll
+        for (int w = 0; w < kTok / 32; ++w) {
+          f32x4(*x)[2] = sc[w & 1];
+          float top[R];
+          bool rise = false;
+#pragma unroll
+          for (int q = 0; q < R; ++q) {
+            top[q] = x[q][0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) top[q] = fmaxf(top[q], x[q][i >> 2][i & 3]);
+            top[q] *= eff[q];
+            rise |= top[q] > m[q] + kSlack;
+          }
+          if (__builtin_amdgcn_ballot_w64(rise)) raise(top);
+          if (w + 1 < kTok / 32) products(w + 1, sc[(w + 1) & 1]);
+          f16x8 pf[R];
+#pragma unroll
+          for (int q = 0; q < R; ++q) {
+            const float base = kPScaleLog2 - m[q];
+            U32x4 p;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int u = i >> 1, c = 2 * (i & 1);
+              const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[q][u][c], eff[q], base));
+              const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[q][u][c + 1], eff[q], base));
+              p.v[i] = u2((f16x2){(_Float16)p0, (_Float16)p1});
+            }
+            pf[q] = frag(p);
+            ones[q] = mfma((f16x8)(_Float16)1.0f, pf[q], ones[q]);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const f16x8 v = d.v[w][i][lane];
+#pragma unroll
+            for (int q = 0; q < R; ++q) o[q][i] = mfma(v, pf[q], o[q][i]);
+          }
+        }
+        whole = true;
+      }
+    }
+#pragma unroll 1
+    for (int w = whole ? kTok / 32 : 0; w < kTok / 32; ++w) {
+      const int32_t tw = t + 32 * w;
+      if (tw >= whi || tw + 32 <= wlo || tw >= t1) continue;
+      f32x4 sc[R][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) sc[q][u] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f16x8 kh = d.k[2 * w + u][j][lane];
+#pragma unroll
+          for (int q = 0; q < R; ++q) sc[q][u] = mfma(kh, qh[q][j], sc[q][u]);
+        }
+      }
+      auto unshrink = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float k = s_flags[buf][2 * w + u].y & 1u ? kShrunk : 1.0f;
+#pragma unroll
+          for (int q = 0; q < R; ++q) sc[q][u] *= k;
+        }
+      };
+      uint32_t large = 0;  // blocks of shrunk values
+      if (cap) {
+        if (flagged >> (2 * w) & 3u) unshrink();
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[q][u][i] = a.cap_out * tanh32(sc[q][u][i] * qf[q] * a.cap_in);
+      }
+      if ((flagged >> (2 * w) & 3u) || tw < all_lo || tw + 32 > all_hi || tw + 32 > t1) {
+        const uint2 f0 = s_flags[buf][2 * w], f1 = s_flags[buf][2 * w + 1];
+        large = uniform(f0.y >> 1 | (f1.y & 2u));
+        if (!cap) unshrink();
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int32_t tok = tw + 16 * u + 4 * (int32_t)b4 + i;
+              const uint32_t fl = (u ? f1.x : f0.x) >> (4 * b4 + i);
+              const bool shown = have[q] & !(fl & 0x10000u) & (tok < t1) & tree_sees(s_tree, s.back, query[q], row_lo[q], tok);
+              sc[q][u][i] = shown ? sc[q][u][i] : -__builtin_inff();
+              poison[q] = shown & (fl & 1u) ? __builtin_nanf("") : poison[q];
+            }
+      }
+      float top[R];
+      bool rise = false;
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        top[q] = sc[q][0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top[q] = fmaxf(top[q], sc[q][i >> 2][i & 3]);
+        top[q] *= eff[q];
+        rise |= top[q] > m[q] + kSlack;
+      }
+      // with shrunk values, P goes up to 2^15 against the maximum itself
+      if (large || __builtin_amdgcn_ballot_w64(rise)) raise(top);
+      f16x8 pf[R];
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const float base = kPScaleLog2 - m[q];
+        U32x4 p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int u = i >> 1, c = 2 * (i & 1);
+          const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][u][c], eff[q], base));
+          const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][u][c + 1], eff[q], base));
+          p.v[i] = u2((f16x2){(_Float16)p0, (_Float16)p1});
+        }
+        pf[q] = frag(p);
+        // the sum of the rounded P, the one the output is weighted with, is one more product
+        ones[q] = mfma((f16x8)(_Float16)1.0f, pf[q], ones[q]);
+      }
+      if (large) {
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pf[q][i] *= (large >> (i >> 2)) & 1u ? (_Float16)kShrunk : (_Float16)1.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const f16x8 v = d.v[w][i][lane];
+#pragma unroll
+        for (int q = 0; q < R; ++q) o[q][i] = mfma(v, pf[q], o[q][i]);
+      }
+    }
+    if (more) {
+      if (R == 1) __syncthreads();
+      else buf ^= 1u;
+      stage(st[buf], s_flags[buf], t + kTok + mine, page);
+    }
+    __syncthreads();
+  }
+
+  // each wavefront's rows, 16 at a time, through its part of LDS: a row's values to 16 lanes
+  __syncthreads();
+  const uint64_t first_part = ((((uint64_t)b * g.tiles + at.tile) * a.heads + h) * g.splits + at.split) * kRows + wave * 16u * R;
+  const LaneInverse inv = lane_inverse(K, n);
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const float total = ones[q][0], bad = blocks_sum(poison[q]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<f32x4*>(&s_o[wave][n][8 * (4 * b4 + r) + i]) =
+            (f32x4){o[q][i][r] + bad, o[q][i + 1][r] + bad, o[q][i + 2][r] + bad, o[q][i + 3][r] + bad};
+    const uint64_t part = first_part + 16u * q;
+    if (b4 == 0 && g.splits > 1) *reinterpret_cast<f32x2*>(g.pml + (part + n) * 2) = (f32x2){m[q], total};
+    wave_sync();
+#pragma unroll 1
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint32_t r = 4u * k + b4;
+      if (w0 + 16u * q + 4u * k >= rows) break;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = s_o[wave][r][8 * n + i];
+      const float tr = row_get_any(total, r);
+      if (g.splits == 1) {
+        store_row<BITS>(a, K, K.v, s, h, w0 + 16u * q + r, n, inv, y, tr);
+      } else {
+        float* d = g.po + (part + r) * kD + 8 * n;
+        *reinterpret_cast<f32x4*>(d) = (f32x4){y[0], y[1], y[2], y[3]};
+        *reinterpret_cast<f32x4*>(d + 4) = (f32x4){y[4], y[5], y[6], y[7]};
+      }
+    }
+    wave_sync();
+  }
+}
+
 // Joins a row's splits, turns it back and stores it.  WIDE: one workgroup a row, its 16 groups of 16 lanes take
 // the splits in turn and join in LDS; otherwise 16 lanes take a row and all its splits.
 template <int BITS, bool WIDE>
@@ -425,8 +793,8 @@ namespace {
 bool is_tree(const hq_kv_attend_args* g) { return g && g->causal && !g->weights && g->max_q <= (uint32_t)kMaxTree; }
 
 struct TreePlan {
-  uint32_t max_q, rows, r, tiles, splits, chunk;
-  uint64_t grid, joins, pml, po, bytes;
+  uint32_t max_q, rows, all, tile_rows, tiles, splits, chunk;
+  uint64_t grid, joins, pml, po, qf, qhi, bytes;
 };
 
 // HQ_OK, or an error for a call that the launches cannot take.
@@ -434,12 +802,13 @@ int plan_tree(const hq_kv_cache& c, const hq_kv_attend_args& g, TreePlan* out) {
   TreePlan p;
   const uint64_t each = g.q_start || g.seqs == 0 ? g.total_q : g.total_q / g.seqs;
   p.max_q = (uint32_t)(each < g.max_q ? each : g.max_q);
-  const uint64_t rows = (uint64_t)p.max_q * (g.q_heads / c.heads), sh = (uint64_t)g.seqs * c.heads;
-  if (g.total_q * (g.q_heads / c.heads) > 0x7FFFFF00ull || rows > 0x7FFFFF00ull / 64u) return HQ_ERR_INVALID_ARG;
+  const uint64_t rows = (uint64_t)p.max_q * (g.q_heads / c.heads), sh = (uint64_t)g.seqs * c.heads, all = g.total_q * (g.q_heads / c.heads);
+  if (all > 0x7FFFFF00ull || all * c.heads > kMaxThreads / 16 || rows > 0x7FFFFF00ull / 128u) return HQ_ERR_INVALID_ARG;
   p.rows = (uint32_t)rows;
-  p.r = rows <= 16 ? 1 : 2;
-  p.tiles = rows ? (uint32_t)((rows + 16u * p.r - 1u) / (16u * p.r)) : 1u;
-  const uint64_t items = sh * p.tiles, target = p.r == 1 ? 2048 : 512;
+  p.all = (uint32_t)all;
+  p.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  p.tiles = rows ? (uint32_t)((rows + p.tile_rows - 1u) / p.tile_rows) : 1u;
+  const uint64_t items = sh * p.tiles, target = p.tile_rows == 16 ? 2048 : p.tile_rows == 64 ? 1024 : 512;
   uint64_t splits = items ? (target + items - 1) / items : 1;
   const uint64_t most = ((uint64_t)g.max_len + 511) / 512;
   if (splits > most) splits = most;
@@ -451,24 +820,50 @@ int plan_tree(const hq_kv_cache& c, const hq_kv_attend_args& g, TreePlan* out) {
   p.grid = (sh * p.splits + 7) / 8 * 8 * p.tiles;
   p.joins = sh * ((rows + 15) / 16 * 16);
   if (p.grid > kMaxThreads / kAttBlock || p.joins > kMaxThreads / 16) return HQ_ERR_INVALID_ARG;
-  const uint64_t parts = p.splits > 1 ? items * p.splits * 16u * p.r : 0;
-  p.pml = 0;
-  p.po = (parts * 8 + 255) / 256 * 256;
-  p.bytes = p.po + parts * kD * 4;
+  uint64_t at = 0;
+  auto take = [&](uint64_t n) {
+    const uint64_t here = at;
+    at = (at + n + 255) / 256 * 256;
+    return here;
+  };
+  // 16 rows are read together from any row on
+  const uint64_t parts = p.splits > 1 ? items * p.splits * p.tile_rows : 0, held = p.tile_rows > 32 ? all * c.heads + 16 : 0;
+  p.pml = take(parts * 8);
+  p.po = take(parts * kD * 4);
+  p.qf = take(held * 4);
+  p.qhi = take(held * kD * 2);
+  p.bytes = at;
   *out = p;
   return HQ_OK;
 }
 
+template <int BITS, int R>
+hipError_t launch_tree_many(const AttendArgs& a, const TreeArgs& g, const Tables& T, const TreePlan& p, hipStream_t st) {
+  // dynamic LDS, which may be more than the default limit: asked for once per kernel (the attribute holds for every device)
+  static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_tree_many_kernel<BITS, R>),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)(tree_lds<R>()));
+  if (set != hipSuccess) return set;
+  hipLaunchKernelGGL((rotate_tree_kernel<BITS>), dim3((a.rows + 15u) / 16u * a.heads), dim3(kAttBlock), 0, st, a, T);
+  hipLaunchKernelGGL((attend_tree_many_kernel<BITS, R>), dim3((uint32_t)p.grid), dim3(kAttBlock), tree_lds<R>(), st, a, g, T);
+  return hipSuccess;
+}
+
 template <int BITS>
-void launch_tree(const AttendArgs& a, const TreeArgs& g, const Tables& T, const TreePlan& p, hipStream_t st) {
+hipError_t launch_tree(const AttendArgs& a, const TreeArgs& g, const Tables& T, const TreePlan& p, hipStream_t st) {
   const dim3 grid((uint32_t)p.grid), block(kAttBlock);
-  if (p.r == 1) hipLaunchKernelGGL((attend_tree_kernel<BITS, 1>), grid, block, 0, st, a, g, T);
-  else hipLaunchKernelGGL((attend_tree_kernel<BITS, 2>), grid, block, 0, st, a, g, T);
-  if (p.splits == 1) return;
-  // A workgroup a row while those are at most 16 a CU, 16 lanes a row beyond, as in hq_attend.hip.
-  const uint32_t each = (p.rows + 15u) / 16u * 16u;
-  if (p.joins <= 4096) hipLaunchKernelGGL((join_tree_kernel<BITS, true>), dim3((uint32_t)p.joins), block, 0, st, a, g, T, 16u * p.r, each);
-  else hipLaunchKernelGGL((join_tree_kernel<BITS, false>), dim3((uint32_t)(p.joins / 16)), block, 0, st, a, g, T, 16u * p.r, each);
+  hipError_t e = hipSuccess;
+  if (p.tile_rows == 16) hipLaunchKernelGGL((attend_tree_kernel<BITS, 1>), grid, block, 0, st, a, g, T);
+  else if (p.tile_rows == 32) hipLaunchKernelGGL((attend_tree_kernel<BITS, 2>), grid, block, 0, st, a, g, T);
+  else if (p.tile_rows == 64) e = launch_tree_many<BITS, 1>(a, g, T, p, st);
+  else e = launch_tree_many<BITS, 2>(a, g, T, p, st);
+  if (e != hipSuccess) return e;
+  if (p.splits > 1) {
+    // A workgroup a row while those are at most 16 a CU, 16 lanes a row beyond, as in hq_attend.hip.
+    const uint32_t each = (p.rows + 15u) / 16u * 16u;
+    if (p.joins <= 4096) hipLaunchKernelGGL((join_tree_kernel<BITS, true>), dim3((uint32_t)p.joins), block, 0, st, a, g, T, p.tile_rows, each);
+    else hipLaunchKernelGGL((join_tree_kernel<BITS, false>), dim3((uint32_t)(p.joins / 16)), block, 0, st, a, g, T, p.tile_rows, each);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -498,17 +893,20 @@ int hq_kv_attend_tree(const hq_kv_cache* cache, const hq_kv_attend_args* args, c
   if (int rc = plan_tree(*cache, *args, &p)) return rc;
   if (p.bytes && (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < p.bytes)) return HQ_ERR_INVALID_ARG;
   a.max_q = p.max_q;
+  a.rows = p.all;
+  char* w = static_cast<char*>(workspace);
+  a.qf = reinterpret_cast<float*>(w + p.qf);
+  a.qhi = reinterpret_cast<_Float16*>(w + p.qhi);
   TreeArgs g;
   g.parents = parents;
   g.tiles = p.tiles;
   g.splits = p.splits;
   g.chunk = p.chunk;
-  g.pml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.pml);
-  g.po = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.po);
+  g.pml = reinterpret_cast<float*>(w + p.pml);
+  g.po = reinterpret_cast<float*>(w + p.po);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (cache->bits == 4) launch_tree<4>(a, g, T, p, st);
-  else launch_tree<8>(a, g, T, p, st);
-  return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
+  const hipError_t e = cache->bits == 4 ? launch_tree<4>(a, g, T, p, st) : launch_tree<8>(a, g, T, p, st);
+  return e == hipSuccess ? HQ_OK : HQ_ERR_HIP;
 }
 
 }  // extern "C"
