@@ -581,12 +581,12 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
     return out
 
 
-def _out(t, name, shape, dtype, device, stream):
-    """The caller's output buffer, checked, or one of the call's own."""
-    if t is None:
-        return _empty(shape, dtype, device, stream)
-    _check_tensor(t, name, dtype, shape, device)
-    return t
+def _out(t, name, shape, like, stream):
+    """The caller's output buffer of like's type, checked, or one of the call's own (made from `like`, which takes less host time)."""
+    if t is not None:
+        _check_tensor(t, name, like.dtype, shape, like.device)
+        return t
+    return like.new_empty(shape) if stream is None else _empty(shape, like.dtype, like.device, stream)
 
 
 def hq_kv_reserve(table, lens, counts, free, free_count, page: int, tokens: int, slots=None, positions=None, q_start=None, granted=None,
@@ -613,10 +613,13 @@ def hq_kv_reserve(table, lens, counts, free, free_count, page: int, tokens: int,
     _check_tensor(free, "free", i32, (pages,), dev)
     _check_tensor(free_count, "free_count", i32, (1,), dev)
     tokens, page = _size(tokens, "tokens"), _size(page, "page")
-    slots = _out(slots, "slots", (tokens,), torch.int64, dev, stream)
-    positions = _out(positions, "positions", (tokens,), i32, dev, stream)
-    q_start = _out(q_start, "q_start", (seqs + 1,), i32, dev, stream)
-    granted = _out(granted, "granted", (seqs,), i32, dev, stream)
+    if slots is None:
+        slots = _empty((tokens,), torch.int64, dev, stream)
+    else:
+        _check_tensor(slots, "slots", torch.int64, (tokens,), dev)
+    positions = _out(positions, "positions", (tokens,), lens, stream)
+    q_start = _out(q_start, "q_start", (seqs + 1,), lens, stream)
+    granted = _out(granted, "granted", (seqs,), lens, stream)
     a = HqKvReserveArgs(table.data_ptr(), lens.data_ptr(), counts.data_ptr(), free.data_ptr(), free_count.data_ptr(), seqs, width, pages, page,
                         tokens, slots.data_ptr(), positions.data_ptr(), q_start.data_ptr(), granted.data_ptr())
     _launch("hq_kv_reserve", dev, stream, lib().hq_kv_reserve, ctypes.byref(a))
@@ -647,10 +650,10 @@ def hq_kv_accept(cache, table, lens, tokens, target, parents, q_start=None, max_
         max_q = min(total if q_start is not None else total // max(seqs, 1), 256)
     if not 0 <= max_q <= 256:
         raise ValueError("at most 256 drafts (max_q) a sequence")
-    path = _out(path, "path", (seqs, max_q), i32, dev, stream)
-    accepted = _out(accepted, "accepted", (seqs,), i32, dev, stream)
-    next = _out(next, "next", (seqs,), i32, dev, stream)
-    change = _out(change, "change", (seqs,), i32, dev, stream)
+    path = _out(path, "path", (seqs, max_q), lens, stream)
+    accepted = _out(accepted, "accepted", (seqs,), lens, stream)
+    next = _out(next, "next", (seqs,), lens, stream)
+    change = _out(change, "change", (seqs,), lens, stream)
     a = HqKvAcceptArgs(table.data_ptr(), lens.data_ptr(), q_start.data_ptr() if q_start is not None else None, tokens.data_ptr(), target.data_ptr(),
                        parents.data_ptr(), total, seqs, width, max_q, path.data_ptr(), accepted.data_ptr(), next.data_ptr(), change.data_ptr())
     _launch("hq_kv_accept", dev, stream, lib().hq_kv_accept, ctypes.byref(c), ctypes.byref(a))
