@@ -112,8 +112,7 @@ __global__ __launch_bounds__(kAttBlock, R == 2 || BITS == 8 ? 2 : 3) void attend
   const uint32_t rows = all - r0 < kRows ? all - r0 : kRows, i0 = query_of(a, r0), last = query_of(a, r0 + rows - 1u);
   int32_t lo, hi;
   tree_range(a, s, r0, kRows, &lo, &hi);
-  int32_t t0 = (int32_t)(split * g.chunk), t1 = t0 + (int32_t)g.chunk;
-  t0 = t0 > (lo & ~15) ? t0 : lo & ~15;
+  int32_t t0 = (lo & ~15) + (int32_t)(split * g.chunk), t1 = t0 + (int32_t)g.chunk;
   t1 = t1 < hi ? t1 : hi;
   if (a.pages == 0) t1 = t0;
   if (t0 >= t1 && g.splits > 1) return;  // the same for the whole workgroup
@@ -416,8 +415,7 @@ __global__ __launch_bounds__(kAttBlock, R == 1 ? 4 : 2) void attend_tree_many_ke
   tree_range(a, s, w0, 16u * R, &wlo, &whi);
   tree_common(a, s, last, &all_lo, &all_hi);
   if (w0 + 16u * R > rows) all_lo = all_hi = 0;  // rows that are not there see nothing
-  int32_t t0 = (int32_t)(at.split * g.chunk), t1 = t0 + (int32_t)g.chunk;
-  t0 = t0 > (lo & ~15) ? t0 : lo & ~15;
+  int32_t t0 = (lo & ~15) + (int32_t)(at.split * g.chunk), t1 = t0 + (int32_t)g.chunk;
   t1 = t1 < hi ? t1 : hi;
   if (a.pages == 0) t1 = t0;
   if (t0 >= t1 && g.splits > 1) return;  // the same for the whole workgroup
@@ -742,12 +740,12 @@ __global__ __launch_bounds__(kAttBlock) void join_tree_kernel(AttendArgs a, Tree
   int32_t lo, hi;
   tree_range(a, s, r0, tile_rows, &lo, &hi);
   if (a.pages == 0) hi = lo;
-  const uint32_t s0 = hi > lo ? (uint32_t)lo / g.chunk : 0u, s1 = hi > lo ? ((uint32_t)hi + g.chunk - 1u) / g.chunk : 0u;
+  const uint32_t s1 = hi > lo ? ((uint32_t)(hi - (lo & ~15)) + g.chunk - 1u) / g.chunk : 0u;
   const uint64_t first = (((uint64_t)b * g.tiles + tile) * a.heads + h) * g.splits;
   float m = kLowest, sum = 0.0f, y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-  for (uint32_t i = s0 + (WIDE ? k : 0u); i < s1; i += WIDE ? 16u : 1u) {
+  for (uint32_t i = WIDE ? k : 0u; i < s1; i += WIDE ? 16u : 1u) {
     const uint64_t p = (first + i) * tile_rows + r - r0;
     const f32x2 ml = *reinterpret_cast<const f32x2*>(g.pml + p * 2);
     const f32x4 u0 = *reinterpret_cast<const f32x4*>(g.po + p * kD + 8 * l), u1 = *reinterpret_cast<const f32x4*>(g.po + p * kD + 8 * l + 4);
@@ -808,14 +806,19 @@ int plan_tree(const hq_kv_cache& c, const hq_kv_attend_args& g, TreePlan* out) {
   p.all = (uint32_t)all;
   p.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   p.tiles = rows ? (uint32_t)((rows + p.tile_rows - 1u) / p.tile_rows) : 1u;
-  const uint64_t items = sh * p.tiles, target = p.tile_rows == 16 ? 2048 : p.tile_rows == 64 ? 1024 : 512;
+  // Workgroups: about three rounds of up to 16 rows, as in hq_attend.hip; of more rows, whose starts cost more, as many as the chip
+  // holds at once, and half as many again where four fit a CU (16 drafts on 16 x 8192 ragged tokens, 64 rows: 68 us at 1536, 79 at
+  // 1024, 81 at 2048; 64 on 32768, 128 rows a tile: 73 at 512, 84 at 768; 13 on 64 x 2001, 32 rows: 43 at 512, 54 at 768).
+  // Splits count from the first token that a tile sees, of at least 512 tokens.
+  const uint64_t items = sh * p.tiles, target = p.tile_rows == 16 ? 2048 : p.tile_rows == 64 ? 1536 : 512;
+  const uint64_t seen = (uint64_t)g.window + p.max_q + 15, span = g.window && seen < g.max_len ? seen : g.max_len;
   uint64_t splits = items ? (target + items - 1) / items : 1;
-  const uint64_t most = ((uint64_t)g.max_len + 511) / 512;
+  const uint64_t most = (span + 511) / 512;
   if (splits > most) splits = most;
   if (splits < 1) splits = 1;
-  p.chunk = (uint32_t)(((g.max_len + splits - 1) / splits + 127) / 128 * 128);
+  p.chunk = (uint32_t)(((span + splits - 1) / splits + 127) / 128 * 128);
   if (p.chunk == 0) p.chunk = 128;
-  p.splits = (g.max_len + p.chunk - 1) / p.chunk;
+  p.splits = (uint32_t)((span + p.chunk - 1) / p.chunk);
   if (p.splits == 0) p.splits = 1;
   p.grid = (sh * p.splits + 7) / 8 * 8 * p.tiles;
   p.joins = sh * ((rows + 15) / 16 * 16);
