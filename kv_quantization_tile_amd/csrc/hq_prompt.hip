@@ -122,12 +122,19 @@ __device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
 }
 
-// 1 - 2 / (e^2x + 1) away from zero (it saturates by itself), the odd series to x^5 below 2^-4 (the next term is below
-// 2^-27 of x); s in units of the cap.
-__device__ __forceinline__ float cap_tanh(float x) {
-  const float e = __builtin_amdgcn_exp2f(x * 2.885390081777927f), x2 = x * x;
+// How scores are capped: not, by kCapPlain, by kCapExact.
+enum { kCapNone = 0, kCapPlain = 1, kCapExact = 2 };
+constexpr float kCapPlainMost = 256.0f;
+// cap tanh(x) = cap - 2 cap / (e^2x + 1), of which the softmax does not see the constant: -1 / (e^2x + 1) is the score in units of
+// 2 cap.  It is off by 2^-22, the capped score by 2^-21 of the cap: 2^-13 at kCapPlainMost, a 32nd of a bf16 weight's
+// rounding.  Four operations where the exact form takes thirteen (2 x 4001 tokens, 28 heads, window 1024: 147 us against 180).
+__device__ __forceinline__ float cap_plain(float x2) { return __builtin_amdgcn_rcpf(-1.0f - __builtin_amdgcn_exp2f(x2)); }
+// A larger cap needs small scores to their own precision: 1 - 2 / (e^2x + 1) away from zero (it saturates by itself), the
+// odd series to x^5 below 2^-4 (the next term is below 2^-27 of x).
+__device__ __forceinline__ float cap_exact(float x2) {
+  const float x = x2 * 0.34657359027997264f, e = __builtin_amdgcn_exp2f(x2), x4 = x * x;
   const float big = __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f);
-  const float small = x * __builtin_fmaf(x2, __builtin_fmaf(x2, 2.0f / 15.0f, -1.0f / 3.0f), 1.0f);
+  const float small = x * __builtin_fmaf(x4, __builtin_fmaf(x4, 2.0f / 15.0f, -1.0f / 3.0f), 1.0f);
   return fabsf(x) < 0.0625f ? small : big;
 }
 
@@ -140,7 +147,7 @@ constexpr int kSchedVector = 0x2, kSchedMatrix = 0x8, kSchedRead = 0x100, kSched
 // x is made here, and not moved to where it is used.
 __device__ __forceinline__ void keep(const bf16x8& x) { asm volatile("" ::"v"(x)); }
 
-template <int WAVES, bool CAP>
+template <int WAVES, int CAP>
 __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
   constexpr uint32_t kRows = 32u * WAVES;
   // arrays of their own: a read of one does not wait for loads into another
@@ -207,7 +214,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
   f32x16 o[4];
 #pragma unroll
   for (int d = 0; d < 4; ++d) o[d] = (f32x16)0.0f;
-  const float c = CAP ? a.cap_out : a.scale_log2;
+  const float c = CAP == kCapNone ? a.scale_log2 : a.cap_out;
 
   // the keys of 32 tokens, half u of a step, as operands; their raw scores
   auto keys = [&](const uint8_t* kb, int u, bf16x8* k) __attribute__((always_inline)) {
@@ -225,9 +232,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
   };
   auto cap = [&](f32x16& s) __attribute__((always_inline)) {
-    if (CAP) {
+    if (CAP != kCapNone) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = cap_tanh(s[i] * a.cap_in);
+      for (int i = 0; i < 16; ++i) s[i] = CAP == kCapPlain ? cap_plain(s[i] * a.cap_in) : cap_exact(s[i] * a.cap_in);
     }
   };
   // takes the tokens that the row does not see, of 32 from t, out
@@ -487,12 +494,15 @@ extern "C" int hq_attend_prompt(const hq_attend_prompt_args* g, hq_stream_t stre
   // Hidden scores are -inf, which a factor of 0 would make NaN: a scale of 0 is 2^-126, the same for scores up to 2^100.
   const double log2e = 1.4426950408889634074, scale = std::fmax(std::fabs((double)g->scale), 0x1p-126);
   a.scale_log2 = (float)(scale * log2e);
-  a.cap_in = g->softcap > 0.0f ? (float)std::fmin(scale / g->softcap, 0x1p126) : 0.0f;
-  a.cap_out = (float)(g->softcap * log2e);
+  const bool plain = g->softcap <= kCapPlainMost;
+  a.cap_in = g->softcap > 0.0f ? (float)std::fmin(2.0 * log2e * scale / g->softcap, 0x1p126) : 0.0f;  // 2 x log2 e of a raw score
+  a.cap_out = (float)(g->softcap * log2e * (plain ? 2.0 : 1.0));
   const uint64_t rows = g->rows * a.group, tiles = (rows + 127u * (uint64_t)(g->seqs < rows ? g->seqs : rows)) / 128u, grid = tiles * a.heads;
   if (grid > kMaxThreads / 256u) return HQ_ERR_INVALID_ARG;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (g->softcap > 0.0f) hipLaunchKernelGGL((prompt_kernel<4, true>), dim3((uint32_t)grid), dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((prompt_kernel<4, false>), dim3((uint32_t)grid), dim3(256), 0, st, a);
+  const dim3 blocks((uint32_t)grid), block(256);
+  if (g->softcap == 0.0f) hipLaunchKernelGGL((prompt_kernel<4, kCapNone>), blocks, block, 0, st, a);
+  else if (plain) hipLaunchKernelGGL((prompt_kernel<4, kCapPlain>), blocks, block, 0, st, a);
+  else hipLaunchKernelGGL((prompt_kernel<4, kCapExact>), blocks, block, 0, st, a);
   return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
 }
