@@ -90,7 +90,9 @@ __device__ __forceinline__ void place(const ReserveArgs& a, uint64_t i, uint32_t
 }
 
 // One workgroup: sums over the sequences say where each one's pages and tokens begin, and a sequence's share
-// of them is spread over all threads, so that one long sequence costs no more than many short ones.
+// of them is spread over all threads, so that one long sequence costs no more than many short ones.  What it moves is a few
+// kilobytes: the chain of loads, sums and barriers bounds it (4 sequences 6.2 us, 333 sequences with 34000 tokens 9.7 us and 2.9 for
+// their places), and several workgroups would need a launch between returning pages and taking them.
 __global__ __launch_bounds__(kPlan) void reserve_kernel(ReserveArgs a) {
   __shared__ uint64_t s_wave[kPlanWaves];
   __shared__ uint32_t s_start[kPlan], s_first[kPlan], s_tokens[kPlan], s_old[kPlan];
@@ -202,7 +204,7 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(ReserveArgs a) {
   }
 }
 
-// The places of many tokens, a thread each.
+// The places of many tokens, a thread each, where one workgroup would write them for too long (hq_kv_reserve).
 __global__ __launch_bounds__(kStepBlock) void slots_kernel(ReserveArgs a) {
   const uint64_t i = (uint64_t)blockIdx.x * kStepBlock + threadIdx.x;
   if (i >= a.tokens) return;
@@ -245,7 +247,8 @@ struct Piece {
 // A workgroup takes a head of a sequence.  Its first wavefront follows the accepted drafts (64 candidates a
 // look), which costs less than a launch of its own; then the wavefronts move the drafts' bytes, 16 at a time,
 // all of them read before one is written: a draft moves towards the front, so what a turn overwrites no later
-// one reads.
+// one reads.  Latency bounds it, a chain of four loads and a few looks: 5.5 us for one sequence's 8 drafts and 8 heads, 9.2 us for
+// 64 sequences' 64 drafts at 8 bits, 512 workgroups that move 2.6 MB.
 template <int BITS>
 __global__ __launch_bounds__(kStepBlock) void accept_kernel(AcceptArgs a) {
   __shared__ int32_t s_token[kDrafts], s_target[kDrafts], s_parent[kDrafts], s_path[kDrafts];
@@ -376,6 +379,7 @@ int hq_kv_reserve(const hq_kv_reserve_args* g, hq_stream_t stream) {
   a.width = g->table_width;
   a.pages = g->pages;
   a.page_log2 = 31u - (uint32_t)__builtin_clz(g->page);
+  // One launch or two, us a call: 512 tokens 8.2 and 10.1, 2048 8.7 and 10.2, 4096 9.9 and 10.2, 8192 12.0 and 10.2.
   a.here = g->tokens <= 4096;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   hipLaunchKernelGGL(reserve_kernel, dim3(1), dim3(kPlan), 0, st, a);
