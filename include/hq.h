@@ -448,7 +448,8 @@ typedef struct {
   const void *q, *k, *v;     /* DEVICE, 16-byte aligned: value c of head j of row i at q[i q_stride[0] + j q_stride[1] + c] */
   void *out;                 /* DEVICE, [rows][q_heads][128], 16-byte aligned                       */
   int32_t dtype, out_dtype;  /* dtype: HQ_BF16                                                      */
-  int64_t q_stride[2], k_stride[2], v_stride[2];  /* in values, multiples of 8                        */
+  int64_t q_stride[2], k_stride[2], v_stride[2];  /* in values, multiples of 8; of k and v rows: 0 to
+                                2^23 - 8.  Those of one row or one head are not looked at              */
   uint64_t rows;
   uint32_t q_heads, heads;   /* q_heads a multiple of heads                                         */
   uint32_t seqs;
@@ -457,8 +458,8 @@ typedef struct {
   int32_t causal;
   uint32_t window;           /* 0: none                                                             */
 } hq_attend_prompt_args;
-/* Asynchronous, allocates nothing, may be captured.  HQ_ERR_INVALID_ARG: null or misaligned pointers, strides that are not
- * multiples of 8, another dtype, sizes outside their ranges (2^30 rows, 2^28 rows times query heads), a scale or softcap as
+/* Asynchronous, allocates nothing, may be captured.  HQ_ERR_INVALID_ARG: null or misaligned pointers, strides outside
+ * their ranges, another dtype, sizes outside their ranges (2^30 rows, 2^28 rows times query heads), a scale or softcap as
  * hq_kv_attend's.  Rows of `out` that no sequence names are not written. */
 int hq_attend_prompt(const hq_attend_prompt_args *args, hq_stream_t stream);
 

@@ -178,6 +178,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
   };
   const int32_t lo = from(query(r0)) & ~(kPromptTok - 1), hi = a.causal ? query(r0 + kRows - 1u) + 1 : (int32_t)n;
   const int32_t all_lo = from(query(w0 + 31u)), all_hi = a.causal ? query(w0) + 1 : (int32_t)n;
+  // those that all of the tile's rows see
+  const int32_t some_lo = from(query(r0 + kRows - 1u)), some_hi = a.causal ? query(r0) + 1 : (int32_t)n;
   const int32_t steps = (hi - lo + kPromptTok - 1) / kPromptTok;
 
   // global to LDS: 1024 bytes, four tokens, an instruction
@@ -355,11 +357,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
       __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 0);
     }
     __builtin_amdgcn_s_setprio(0);
-    if (masked) {
-      // 0 times a value that is not finite reaches rows that do not see it: such a tile is done again, below
+    if (t < some_lo || t + kPromptTok > some_hi) {
+      // 0 times a value that is not finite reaches rows that do not see it: such a tile is done again, below.  Each wavefront looks at
+      // its share of the step's values.
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(vb + (64 * i + lane) * 16u);
+      for (int i = 0; i < kLoads; ++i) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(vb + (64u * (wave * kLoads + i) + lane) * 16u);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t y = x[e];
@@ -471,9 +474,15 @@ extern "C" int hq_attend_prompt(const hq_attend_prompt_args* g, hq_stream_t stre
   if (g->rows > (1ull << 30) || g->rows * g->q_heads > (1ull << 28)) return HQ_ERR_INVALID_ARG;
   if (!(std::fabs(g->scale) <= 0x1p126f)) return HQ_ERR_INVALID_ARG;
   if (g->softcap != 0.0f && !(g->softcap >= 0x1p-125f && g->softcap <= 0x1p125f)) return HQ_ERR_INVALID_ARG;
-  if ((g->q_stride[0] | g->q_stride[1] | g->k_stride[0] | g->k_stride[1] | g->v_stride[0] | g->v_stride[1]) & 7) return HQ_ERR_INVALID_ARG;
+  // a stride that leads nowhere, of one row or one head, may be any
+  const bool many = g->rows > 1;
+  const struct {
+    int64_t qt, qh, kt, kh, vt, vh;
+  } st = {many ? g->q_stride[0] : 0, g->q_heads > 1 ? g->q_stride[1] : 0, many ? g->k_stride[0] : 0,
+          g->heads > 1 ? g->k_stride[1] : 0, many ? g->v_stride[0] : 0, g->heads > 1 ? g->v_stride[1] : 0};
+  if ((st.qt | st.qh | st.kt | st.kh | st.vt | st.vh) & 7) return HQ_ERR_INVALID_ARG;
   // a step's 64 rows lie within 2^31 bytes of each other
-  if (g->k_stride[0] < 0 || g->k_stride[0] >= kPromptStride || g->v_stride[0] < 0 || g->v_stride[0] >= kPromptStride) return HQ_ERR_INVALID_ARG;
+  if (st.kt < 0 || st.kt >= kPromptStride || st.vt < 0 || st.vt >= kPromptStride) return HQ_ERR_INVALID_ARG;
   if (g->rows == 0 || g->seqs == 0) return HQ_OK;
   if (!g->q || !g->k || !g->v || !g->out || !g->start || ((uintptr_t)g->start & 3u)) return HQ_ERR_INVALID_ARG;
   if (((uintptr_t)g->q | (uintptr_t)g->k | (uintptr_t)g->v | (uintptr_t)g->out) & 15u) return HQ_ERR_INVALID_ARG;
@@ -483,12 +492,12 @@ extern "C" int hq_attend_prompt(const hq_attend_prompt_args* g, hq_stream_t stre
   a.v = static_cast<const uint16_t*>(g->v);
   a.out = g->out;
   a.start = g->start;
-  a.qt = g->q_stride[0];
-  a.qh = g->q_stride[1];
-  a.kt = g->k_stride[0];
-  a.kh = g->k_stride[1];
-  a.vt = g->v_stride[0];
-  a.vh = g->v_stride[1];
+  a.qt = st.qt;
+  a.qh = st.qh;
+  a.kt = st.kt;
+  a.kh = st.kh;
+  a.vt = st.vt;
+  a.vh = st.vh;
   a.total = g->rows;
   a.heads = g->heads;
   a.group = g->q_heads / g->heads;
@@ -510,10 +519,10 @@ extern "C" int hq_attend_prompt(const hq_attend_prompt_args* g, hq_stream_t stre
   a.cap_out = (float)(g->softcap * log2e * (plain ? 2.0 : 1.0));
   const uint64_t rows = g->rows * a.group, tiles = (rows + 127u * (uint64_t)(g->seqs < rows ? g->seqs : rows)) / 128u, grid = tiles * a.heads;
   if (grid > kMaxThreads / 256u) return HQ_ERR_INVALID_ARG;
-  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const hipStream_t on = static_cast<hipStream_t>(stream);
   const dim3 blocks((uint32_t)grid), block(256);
-  if (g->softcap == 0.0f) hipLaunchKernelGGL((prompt_kernel<4, kCapNone>), blocks, block, 0, st, a);
-  else if (plain) hipLaunchKernelGGL((prompt_kernel<4, kCapPlain>), blocks, block, 0, st, a);
-  else hipLaunchKernelGGL((prompt_kernel<4, kCapExact>), blocks, block, 0, st, a);
+  if (g->softcap == 0.0f) hipLaunchKernelGGL((prompt_kernel<4, kCapNone>), blocks, block, 0, on, a);
+  else if (plain) hipLaunchKernelGGL((prompt_kernel<4, kCapPlain>), blocks, block, 0, on, a);
+  else hipLaunchKernelGGL((prompt_kernel<4, kCapExact>), blocks, block, 0, on, a);
   return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
 }

@@ -156,6 +156,17 @@ def test_what_is_not_seen_does_not_reach(what, causal, window):
     assert torch.equal(got, clean)
 
 
+def test_strides_that_lead_nowhere():
+    """Of one row, or one head, any stride will do."""
+    say("case: prompt strides of one row and one head")
+    q, k, v, start = inputs([1], heads=2, group=2)
+    odd = lambda x: torch.as_strided(x, x.shape, ((1 << 24) + 1, 128, 1))  # noqa: E731
+    assert torch.equal(hq.hq_attend_prompt(odd(q), odd(k), odd(v), start), hq.hq_attend_prompt(q, k, v, start))
+    q, k, v, start = inputs([33], heads=1, group=1)
+    odd = lambda x: torch.as_strided(x, x.shape, (128, 3, 1))  # noqa: E731
+    assert torch.equal(hq.hq_attend_prompt(odd(q), odd(k), odd(v), start), hq.hq_attend_prompt(q, k, v, start))
+
+
 def test_offsets():
     """Rows that no sequence names stay as they were; offsets are cut to the rows there are."""
     say("case: prompt offsets")

@@ -101,6 +101,7 @@ def test_tree_parents():
     dict(rows=1 << 26), dict(scale=float("nan")), dict(scale=float("inf")), dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")),
     dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(start=None), dict(q=OK + 8), dict(k=OK + 2), dict(v=OK + 4), dict(out=OK + 8),
     dict(start=OK + 2), dict(q_stride=(1024, 129)), dict(k_stride=(257, 128)), dict(v_stride=(260, 128)),
+    dict(k_stride=(1 << 23, 128)), dict(v_stride=(-256, 128)),
 ])
 def test_prompt_refusals(kw):
     assert prompt(**kw) == E
