@@ -6,8 +6,8 @@
 // drafts look at them.
 //
 // Rows are queries x heads of the group, of a sequence and a KV head; a workgroup takes a tile of them and one split of the
-// tokens.  Up to 32 rows: its four wavefronts take 32 tokens in turn, every wavefront with all the rows, so that codes become
-// operands in registers and nothing is shared but the join at the end.  More: operands are made once, 16 tokens by each
+// tokens.  Up to 32 rows, or little work: its four wavefronts take 32 tokens in turn, every wavefront with all the rows, so that codes become
+// operands in registers and nothing is shared but the join at the end.  Otherwise operands are made once, 16 tokens by each
 // wavefront, and shared through LDS, and each wavefront owns 16 or 32 rows.  (32 rows a workgroup for 64 and 256 of them makes
 // the operands two and eight times: 92 us against 71 for 16 drafts on 16 x 8192 tokens, 95 against 75 for 64 on 32768;
 // 64 rows in one wavefront's registers, one wavefront a SIMD, 142 and 136.)
@@ -813,14 +813,17 @@ int plan_tree(const hq_kv_cache& c, const hq_kv_attend_args& g, TreePlan* out) {
   if (all > 0x7FFFFF00ull || all * c.heads > kMaxThreads / 16 || rows > 0x7FFFFF00ull / 128u) return HQ_ERR_INVALID_ARG;
   p.rows = (uint32_t)rows;
   p.all = (uint32_t)all;
-  p.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const uint64_t seen = (uint64_t)g.window + p.max_q + 15, span = g.window && seen < g.max_len ? seen : g.max_len;
+  // Operands in registers, 32 rows a tile, up to 2^24 rows x tokens: LDS starts later and takes a launch for the rows.  8 heads,
+  // 4 query heads each, us in registers and in LDS: 64 drafts on 301 tokens 18 and 35, on 8192 (2^24) 40 and 44, on 16384 58 and
+  // 53, on 32768 92 and 74; 16 drafts on 8192 23 and 30; 32 on 16384 (2^24) 38 and 40, on 32768 55 and 50.
+  p.tile_rows = rows <= 16 ? 16 : rows <= 32 || sh * rows * span <= 1ull << 24 ? 32 : rows <= 64 ? 64 : 128;
   p.tiles = rows ? (uint32_t)((rows + p.tile_rows - 1u) / p.tile_rows) : 1u;
   // Workgroups: about three rounds of up to 16 rows, as in hq_attend.hip; of more rows, whose starts cost more, as many as the chip
   // holds at once, and half as many again where four fit a CU (16 drafts on 16 x 8192 ragged tokens, 64 rows: 68 us at 1536, 79 at
   // 1024, 81 at 2048; 64 on 32768, 128 rows a tile: 73 at 512, 84 at 768; 13 on 64 x 2001, 32 rows: 43 at 512, 54 at 768).
   // Splits count from the first token that a tile sees, of at least 512 tokens.
   const uint64_t items = sh * p.tiles, target = p.tile_rows == 16 ? 2048 : p.tile_rows == 64 ? 1536 : 512;
-  const uint64_t seen = (uint64_t)g.window + p.max_q + 15, span = g.window && seen < g.max_len ? seen : g.max_len;
   uint64_t splits = items ? (target + items - 1) / items : 1;
   const uint64_t most = (span + 511) / 512;
   if (splits > most) splits = most;

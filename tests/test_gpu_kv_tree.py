@@ -325,3 +325,60 @@ def test_accept_ties_absent_pages_and_cuts():
     none = cache[:0]
     out = hq.hq_kv_accept(none, i32(0, 1, 2).view(1, 3), i32(40), i32(*tok), i32(*tgt), i32(*tree))
     assert out[1].tolist() == [3]
+
+
+# ---- operands through LDS ------------------------------------------------------------------------
+
+WORK = 1 << 24  # rows x tokens from which operands go through LDS
+
+
+@pytest.mark.parametrize("name", ["mid", "tile_128", "tile_256", "all_256", "tiles", "cap_many", "mixed", "group_8", "splits", "more_drafts_than_tokens"])
+def test_much_work(orc, name):
+    """The kernels for much work, which max_len announces, on the same inputs; whole and in splits."""
+    say(f"case: tree through LDS, {name}")
+    kw = dict(CASES[name])
+    if kw.pop("window", 0):
+        kw["lens"] = [1200]
+    c = Case(orc, **kw)
+    rows = len(c.lens) * c.cache.shape[1] * max(c.q_lens) * c.q.shape[1] // c.cache.shape[1]
+    want, tol = c.want()
+    bound = tol + 2.0 ** -20 * np.linalg.norm(want, axis=-1)
+    for max_len in (WORK // rows + 600, 1 << 24):  # more than WORK; the second: one split holds all
+        got = c.run(max_len=max_len)
+        err = np.linalg.norm(host(got).astype(np.float64) - want, axis=-1)
+        assert np.isfinite(host(got)).all() and (err <= bound).all(), np.max(err / np.maximum(bound, 1e-30))
+        assert torch.equal(c.run(max_len=max_len), got)
+
+
+def test_much_work_window(orc):
+    """A window's edge in the kernels for much work, against those for little: the same operands, so rows differ by the weights'
+    roundings, 2 2^-11 in either, and by the order of sums (below 2^-10 for scores up to 64): 2^-8 of the longest value."""
+    say("case: tree through LDS, window")
+    c = Case(orc, [5000], [64], heads=8, group=8, window=4500, page=64)
+    assert 8 * 512 * (4500 + 64 + 15) > WORK >= 8 * 64 * 4600
+    slots = dev(np.array([c.table[0, t // 64] * 64 + t % 64 for t in range(5000)], np.int64))
+    longest = float(hq.hq_kv_read(c.cache, slots, out_dtype=torch.float32, **c.fmt)[1].norm(dim=-1).max())
+    much, little = c.run(), c.run(max_q=8)
+    assert torch.isfinite(much).all() and float((much[:8] - little[:8]).norm(dim=-1).max()) <= 2.0 ** -8 * longest
+
+
+@pytest.mark.parametrize("group,m", [(2, 20), (2, 40), (1, 140)])
+def test_much_work_absent_pages_and_nan(orc, group, m):
+    say(f"case: tree through LDS, absent pages and NaN, group {group}, {m} drafts")
+    c = Case(orc, [190, 170], [m, m], heads=2, group=group)
+    c.table[0, 2], c.table[0, 11], c.table[1, 0] = -1, c.cache.shape[0], 1 << 30
+    want, tol = c.want()
+    clean = host(c.run(max_len=1 << 24))
+    assert (np.linalg.norm(clean - want, axis=-1) <= tol + 2.0 ** -20 * np.linalg.norm(want, axis=-1)).all()
+    bad = 170 - m + m // 2
+    slot = dev(np.array([c.table[1, bad // 16] * 16 + bad % 16], np.int64))
+    for side in range(2):
+        held = c.cache.clone()
+        pair = list(hq.hq_kv_read(c.cache, slot, out_dtype=torch.float32, **c.fmt))
+        pair[side][:, 1] = float("nan")
+        hq.hq_kv_append(c.cache, *pair, slot, **c.fmt)
+        got, sees = host(c.run(max_len=1 << 24)), c.sees[1][:, bad]
+        assert np.isnan(got[m:, group:][sees]).all()
+        got[m:, group:][sees] = 0
+        assert np.isfinite(got).all()
+        c.cache = held
