@@ -459,8 +459,8 @@ typedef struct {
   uint32_t window;           /* 0: none                                                             */
 } hq_attend_prompt_args;
 /* Asynchronous, allocates nothing, may be captured.  HQ_ERR_INVALID_ARG: null or misaligned pointers, strides outside
- * their ranges, another dtype, sizes outside their ranges (2^30 rows, 2^28 rows times query heads), a scale or softcap as
- * hq_kv_attend's.  Rows of `out` that no sequence names are not written. */
+ * their ranges, another dtype, sizes outside their ranges (2^30 rows, 2^28 rows times query heads, 2^31 - 1 sequences), a scale
+ * or softcap as hq_kv_attend's.  Rows of `out` that no sequence names are not written. */
 int hq_attend_prompt(const hq_attend_prompt_args *args, hq_stream_t stream);
 
 /* Eviction by accumulated weight.  Of each (sequence, head)'s n tokens, m = min(n, budget) stay: the first

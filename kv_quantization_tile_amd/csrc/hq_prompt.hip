@@ -472,6 +472,8 @@ extern "C" int hq_attend_prompt(const hq_attend_prompt_args* g, hq_stream_t stre
   if (!g || g->heads == 0 || g->q_heads == 0 || g->q_heads % g->heads || g->q_heads > 65535u) return HQ_ERR_INVALID_ARG;
   if (g->dtype != HQ_BF16 || (g->out_dtype != HQ_F32 && g->out_dtype != HQ_BF16)) return HQ_ERR_INVALID_ARG;
   if (g->rows > (1ull << 30) || g->rows * g->q_heads > (1ull << 28)) return HQ_ERR_INVALID_ARG;
+  // find_tile's index of a sequence goes up to 127 past the last one
+  if (g->seqs > 0x7FFFFFFFu) return HQ_ERR_INVALID_ARG;
   if (!(std::fabs(g->scale) <= 0x1p126f)) return HQ_ERR_INVALID_ARG;
   if (g->softcap != 0.0f && !(g->softcap >= 0x1p-125f && g->softcap <= 0x1p125f)) return HQ_ERR_INVALID_ARG;
   // a stride that leads nowhere, of one row or one head, may be any
