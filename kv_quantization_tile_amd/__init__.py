@@ -537,7 +537,7 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
     total, heads, _ = q.shape
     if heads == 0 or heads % c.heads:
         raise ValueError("q must be [queries][q heads][128], q heads a multiple of the cache's heads")
-    seqs, width = lens.numel(), table.shape[-1]
+    seqs, width = _size(lens.numel(), "the number of sequences"), _size(table.shape[-1], "the table's width")
     _check_tensor(lens, "lens", torch.int32, (seqs,), dev)
     _check_tensor(table, "table", torch.int32, (seqs, width), dev)
     if q_start is not None:
@@ -603,10 +603,10 @@ def hq_kv_reserve(table, lens, counts, free, free_count, page: int, tokens: int,
     if not table.is_cuda or table.dim() != 2:
         raise TypeError("table must be an int32 CUDA tensor [seqs][width]")
     dev, i32 = table.device, torch.int32
-    seqs, width = table.shape
+    seqs, width = _size(table.shape[0], "the number of sequences"), _size(table.shape[1], "the table's width")
     if free.dim() != 1:
         raise ValueError("free must be [pages]")
-    pages = free.shape[0]
+    pages = _size(free.shape[0], "the number of pages")
     _check_tensor(table, "table", i32, (seqs, width), dev)
     _check_tensor(lens, "lens", i32, (seqs,), dev)
     _check_tensor(counts, "counts", i32, (seqs,), dev)
@@ -638,7 +638,7 @@ def hq_kv_accept(cache, table, lens, tokens, target, parents, q_start=None, max_
     torch = _torch()
     c, _ = _cache_arg(cache, bits, 0, None, None)
     dev, i32 = cache.device, torch.int32
-    seqs, width, total = lens.numel(), table.shape[-1], tokens.numel()
+    seqs, width, total = _size(lens.numel(), "the number of sequences"), _size(table.shape[-1], "the table's width"), tokens.numel()
     _check_tensor(lens, "lens", i32, (seqs,), dev)
     _check_tensor(table, "table", i32, (seqs, width), dev)
     _check_tensor(tokens, "tokens", i32, (total,), dev)
@@ -680,13 +680,14 @@ def hq_attend_prompt(q, k, v, start, scale=None, causal: bool = True, window: in
         raise TypeError("q, k and v must be bfloat16")
     if start.dim() != 1 or start.shape[0] == 0:
         raise ValueError("start must be int32 [seqs + 1]")
+    seqs = _size(start.shape[0] - 1, "the number of sequences")
     _check_tensor(start, "start", torch.int32, start.shape, dev)
     if out is None:
         out = _empty((rows, q_heads, 128), torch.bfloat16, dev, stream)
     else:
         _check_tensor(out, "out", out.dtype, (rows, q_heads, 128), dev)
     a = HqAttendPromptArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), HQ_BF16, _dtype_code(out), _Strides2(qs[0], qs[1]),
-                           _Strides2(ks[0], ks[1]), _Strides2(vs[0], vs[1]), rows, q_heads, heads, start.shape[0] - 1, start.data_ptr(),
+                           _Strides2(ks[0], ks[1]), _Strides2(vs[0], vs[1]), rows, q_heads, heads, seqs, start.data_ptr(),
                            128 ** -0.5 if scale is None else scale, softcap, 1 if causal else 0, _size(window, "window"))
     _launch("hq_attend_prompt", dev, stream, lib().hq_attend_prompt, ctypes.byref(a))
     return out
@@ -701,7 +702,8 @@ def hq_kv_evict(cache, table, lens, weights, budget: int, sink: int, recent: int
     new_weights float32 [seqs][heads][budget])."""
     torch = _torch()
     c, _ = _cache_arg(cache, bits, 0, None, None)
-    dev, heads, seqs, width, dst_width, top = cache.device, c.heads, lens.numel(), table.shape[-1], dst_table.shape[-1], weights.shape[-1]
+    dev, heads, top = cache.device, c.heads, weights.shape[-1]
+    seqs, width, dst_width = _size(lens.numel(), "the number of sequences"), _size(table.shape[-1], "the table's width"), _size(dst_table.shape[-1], "dst_table's width")
     _check_tensor(lens, "lens", torch.int32, (seqs,), dev)
     _check_tensor(table, "table", torch.int32, (seqs, width), dev)
     _check_tensor(weights, "weights", torch.float32, (seqs, heads, top), dev)

@@ -15,3 +15,34 @@ torch = pytest.importorskip("torch")
 def test_prompt_sequences(seqs):
     """A workgroup looks for its tile over all sequences, 64 at a time: an index past them has to fit 32 bits."""
     assert prompt(seqs=seqs) == E
+
+
+def i32(*shape, device="cpu"):
+    return OnDevice(torch.empty(*shape, dtype=torch.int32, device=device))
+
+
+def far(*shape):
+    return i32(*shape, device="meta")  # of a size, without memory
+
+
+CACHE = OnDevice(torch.zeros(4, 2, 64 * hq.hq_kv_token_bytes(4), dtype=torch.uint8))
+ROWS = OnDevice(torch.zeros(3, 2, 128, dtype=torch.bfloat16))
+WIDE = 2 ** 32 + 16  # 16 to a 32-bit field
+
+
+@pytest.mark.parametrize("call", [
+    lambda: hq.hq_attend_prompt(ROWS, ROWS, ROWS, far(WIDE + 1)),
+    lambda: hq.hq_kv_reserve(far(1, WIDE), i32(1), i32(1), i32(9), i32(1), 16, 5),
+    lambda: hq.hq_kv_reserve(i32(1, 4), i32(1), i32(1), far(WIDE), i32(1), 16, 5),
+    lambda: hq.hq_kv_reserve(far(WIDE, 4), far(WIDE), far(WIDE), i32(9), i32(1), 16, 5, q_start=far(WIDE + 1), granted=far(WIDE)),
+    lambda: hq.hq_kv_accept(CACHE, far(1, WIDE), i32(1), i32(3), i32(3), i32(3)),
+    lambda: hq.hq_kv_attend(CACHE, ROWS, far(1, WIDE), i32(1), max_len=100),
+    lambda: hq.hq_kv_attend(CACHE, ROWS, far(1, WIDE), i32(1), max_len=100, parents=i32(3)),
+    lambda: hq.hq_kv_attend(CACHE, ROWS, far(WIDE, 1), far(WIDE), q_start=far(WIDE + 1)),
+    lambda: hq.hq_kv_evict(CACHE, far(1, WIDE), i32(1), OnDevice(torch.zeros(1, 2, 8)), 4, 1, 1, i32(1, 1)),
+    lambda: hq.hq_kv_evict(CACHE, i32(1, 1), i32(1), OnDevice(torch.zeros(1, 2, 8)), 4, 1, 1, far(1, WIDE)),
+])
+def test_sizes_past_32_bits_are_not_cut(world, call):  # noqa: F811
+    with pytest.raises(ValueError):
+        call()
+    assert not world[1]
