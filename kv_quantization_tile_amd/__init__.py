@@ -529,7 +529,8 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
 
     parents int32 [queries] makes the queries a tree of drafted tokens, a sequence's last cached ones (C: hq_kv_attend_tree): draft
     parents[i] of the sequence comes before draft i, -1 for one that follows the held tokens.  A draft sees the held tokens, its
-    ancestors and itself, and with a window the last `window` of those.  At most 256 drafts of a sequence are computed; no weights."""
+    ancestors and itself, and with a window the last `window` of those.  At most 256 drafts of a sequence are computed (more
+    are refused where q_start is None and max_q does not say fewer); no weights."""
     torch = _torch()
     c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
     dev = cache.device
@@ -544,8 +545,8 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
         _check_tensor(q_start, "q_start", torch.int32, (seqs + 1,), dev)
     if max_q is None:
         max_q = total if q_start is not None else total // max(seqs, 1)
-        if parents is not None:
-            max_q = min(max_q, 256)
+        if parents is not None and (q_start is not None or seqs == 0):
+            max_q = min(max_q, 256)  # how many a sequence has is known on the device alone
     if parents is not None:
         _check_tensor(parents, "parents", torch.int32, (total,), dev)
         if not causal or weights is not None or max_q > 256:

@@ -46,3 +46,24 @@ def test_sizes_past_32_bits_are_not_cut(world, call):  # noqa: F811
     with pytest.raises(ValueError):
         call()
     assert not world[1]
+
+
+# ---- drafts ---------------------------------------------------------------------------------------
+
+
+def drafts(n, seqs=1, **kw):
+    q = OnDevice(torch.zeros(n, 2, 128, dtype=torch.bfloat16))
+    return hq.hq_kv_attend(CACHE, q, i32(seqs, 1), i32(seqs), parents=i32(n), **kw)
+
+
+def test_drafts_that_would_not_be_computed(world):  # noqa: F811
+    """Without q_start the drafts of a sequence are known: more than 256 are refused, unless max_q says which are asked for."""
+    drafts(256)
+    drafts(3 * 256, seqs=3)
+    drafts(300, max_q=256)
+    drafts(300, seqs=2, q_start=i32(3))
+    assert len(world[1]) == 4
+    for n, seqs in ((257, 1), (3 * 257, 3), (1 << 16, 1)):
+        with pytest.raises(ValueError):
+            drafts(n, seqs)
+    assert len(world[1]) == 4
