@@ -567,18 +567,18 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
                        _size(max_q, "max_q"), _size(max_len, "max_len"), q_start.data_ptr() if q_start is not None else None,
                        table.data_ptr(), width, lens.data_ptr(), 128 ** -0.5 if scale is None else scale, softcap, 1 if causal else 0,
                        _size(window, "window"), weights.data_ptr() if weights is not None else None, stride)
-    L, cp, ap = lib(), ctypes.byref(c), ctypes.byref(a)
+    L, cp, ap, what = lib(), ctypes.byref(c), ctypes.byref(a), "hq_kv_attend" if parents is None else "hq_kv_attend_tree"
     if ws is None:
         need = ctypes.c_size_t()
         size = L.hq_kv_attend_workspace_size if parents is None else L.hq_kv_attend_tree_workspace_size
-        _check(size(cp, ap, ctypes.byref(need)), "hq_kv_attend")
+        _check(size(cp, ap, ctypes.byref(need)), what)
         ws = _empty(need.value, torch.uint8, dev, stream)
     elif not (ws.is_contiguous() and ws.device == dev and ws.dtype == torch.uint8):
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
     if parents is None:
-        _launch("hq_kv_attend", dev, stream, L.hq_kv_attend, cp, ap, ws.data_ptr(), ws.numel())
+        _launch(what, dev, stream, L.hq_kv_attend, cp, ap, ws.data_ptr(), ws.numel())
     else:
-        _launch("hq_kv_attend", dev, stream, L.hq_kv_attend_tree, cp, ap, parents.data_ptr(), ws.data_ptr(), ws.numel())
+        _launch(what, dev, stream, L.hq_kv_attend_tree, cp, ap, parents.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 

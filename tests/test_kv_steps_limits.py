@@ -67,3 +67,14 @@ def test_drafts_that_would_not_be_computed(world):  # noqa: F811
         with pytest.raises(ValueError):
             drafts(n, seqs)
     assert len(world[1]) == 4
+
+
+def test_a_failed_call_names_itself(world, monkeypatch):  # noqa: F811
+    """An error of a tree's call, or of its workspace's size, names the C entry that failed."""
+    for failing in ("hq_kv_attend_tree", "hq_kv_attend_tree_workspace_size"):
+        L = types.SimpleNamespace(**{n: lambda *a: hq.HQ_OK for n in ("hq_kv_attend_tree", "hq_kv_attend_tree_workspace_size")})
+        setattr(L, failing, lambda *a: E)
+        monkeypatch.setattr(hq, "lib", lambda: L)
+        monkeypatch.setattr(hq, "strerror", lambda code: str(code))
+        with pytest.raises(hq.HqError, match="hq_kv_attend_tree"):
+            drafts(4)
