@@ -3,7 +3,7 @@
 Prompts of different lengths are attended among themselves (hq_attend_prompt) and appended.  Then every step drafts a small tree
 behind each sequence's last token, attends all of it in one call (hq_kv_attend with `parents`), accepts what the model
 would have chosen (hq_kv_accept moves it up in the cache) and gives the other drafts' places back.  Pages, block
-tables and slots stay on the GPU throughout (hq_kv_reserve).  The layer's weights are random; drafts are guesses over a small
+tables and slots stay on the GPU throughout (hq_kv_reserve); a sequence for which there is no room waits.  The layer's weights are random; drafts are guesses over a small
 vocabulary, so some of them are right.
 
     python examples/drafts.py [--steps N] [--bits 4|8]
@@ -51,13 +51,15 @@ class DraftedLayer:
         """tokens [sum(counts)]: the token chosen behind each prompt."""
         q, k, v = self._rows(tokens)
         slots, _, start, granted = self._reserve(torch.tensor(counts, dtype=torch.int32, device="cuda"), len(tokens))
+        if granted.tolist() != list(counts):
+            raise RuntimeError("the prompts need more pages, or wider tables")
         hq.hq_kv_append(self.cache, k, v, slots, bits=self.bits, seed=self.seed)
         out = hq.hq_attend_prompt(q, k, v, start)
         return self._choose(out[(start[1:] - 1).long()])
 
     def step(self, last):
-        """last [seqs]: the tokens chosen before, not cached yet.  Returns (accepted drafts [seqs][len(TREE)], -1 past the end,
-        their tokens; the tokens chosen behind them)."""
+        """last [seqs]: the tokens chosen before, not cached yet.  Returns (accepted drafts [seqs][len(TREE)], -1 past the end and
+        throughout for a sequence without room; their tokens; the tokens chosen behind them)."""
         seqs, m = len(last), len(TREE)
         tokens = torch.randint(0, self.vocabulary, (seqs, m), generator=self.g, device="cuda", dtype=torch.int32)
         tokens[:, 0] = last
@@ -65,12 +67,16 @@ class DraftedLayer:
         q, k, v = self._rows(tokens.flatten())
         slots, _, start, granted = self._reserve(torch.full_like(last, m), seqs * m)
         hq.hq_kv_append(self.cache, k, v, slots, bits=self.bits, seed=self.seed)
-        out = hq.hq_kv_attend(self.cache, q, self.table, self.lens, q_start=start, max_q=m, parents=parents, bits=self.bits, seed=self.seed)
-        path, accepted, nxt, change = hq.hq_kv_accept(self.cache, self.table, self.lens, tokens.flatten(), self._choose(out), parents, q_start=start,
+        # a sequence that got no places has no drafts in the cache: with a length of 0 none of its tokens are taken for some
+        here = granted > 0
+        held = torch.where(here, self.lens, 0)
+        out = hq.hq_kv_attend(self.cache, q, self.table, held, q_start=start, max_q=m, parents=parents, bits=self.bits, seed=self.seed)
+        path, accepted, nxt, change = hq.hq_kv_accept(self.cache, self.table, held, tokens.flatten(), self._choose(out), parents, q_start=start,
                                                        max_q=m, bits=self.bits)
-        self._reserve(change, 0)
+        self._reserve(torch.where(here, change, 0), 0)
+        path = torch.where(here[:, None], path, -1)
         taken = torch.where(path >= 0, tokens.gather(1, path.clamp(min=0).long()), path)
-        return path, taken, nxt
+        return path, taken, torch.where(here, nxt, last)
 
 
 def generate(steps=20, bits=4, prompts=(100, 37, 1, 64), seed=0, **layer):

@@ -398,6 +398,9 @@ int hq_kv_attend_tree(const hq_kv_cache *cache, const hq_kv_attend_args *args, c
  * Sequence b's new tokens are `slots` and `positions` q_start[b] .. q_start[b + 1] - 1 (q_start counts what was asked for): token i of them
  * stands at position t = lens[b] + i in slot table[b][t / page] page + t mod page, or -1 if the sequence did not grow or
  * the entry is outside [0, pages).  Places past the last have slot -1 and position 0.
+ * A sequence that did not grow (granted[b] == 0 where counts[b] > 0) still has its rows in q_start, but its last tokens are not
+ * those rows': for hq_kv_attend, hq_kv_attend_tree and hq_kv_accept it is given a length of 0 until it grows (its rows see
+ * nothing and nothing of it moves), and the change that hq_kv_accept returns for it is left out.
  * Asynchronous, allocates nothing, may be captured. */
 typedef struct {
   int32_t *table;            /* DEVICE, [seqs][table_width], in and out                              */
@@ -423,7 +426,8 @@ int hq_kv_reserve(const hq_kv_reserve_args *args, hq_stream_t stream);
  * those behind them are left as they are.  An absent page's draft becomes one that takes no part (zeros, K scales -0).
  * path [seqs][max_q]: the accepted drafts, then -1; accepted [seqs]: how many; next [seqs]: the target behind the last
  * (-1 without drafts); change [seqs]: accepted - m, the change of the sequence's length (hq_kv_reserve takes it).
- * Only the first max_q drafts are looked at, at most 256.  lens is not changed. */
+ * Only the first max_q drafts are looked at, at most 256.  lens is not changed.  Of a sequence whose drafts are not cached, as it got
+ * no places for them, held tokens would be taken for drafts: see hq_kv_reserve for what it is given instead. */
 typedef struct {
   const int32_t *table;      /* DEVICE, [seqs][table_width]                                */
   const int32_t *lens;       /* DEVICE, [seqs], the drafts among them                      */

@@ -599,7 +599,11 @@ def hq_kv_reserve(table, lens, counts, free, free_count, page: int, tokens: int,
     leave empty returning and their entries becoming -1.  A sequence whose table is too narrow gets nothing; from the first one that
     the stack cannot serve on, no sequence grows.  `tokens` is the number of places to fill in (at least the sum of the positive counts,
     or what a captured graph has room for).  Returns (slots int64 [tokens] for hq_kv_append, -1 for a token that got no place and past the last one;
-    positions int32 [tokens]; q_start int32 [seqs + 1] for hq_kv_attend; granted int32 [seqs], each length's change)."""
+    positions int32 [tokens]; q_start int32 [seqs + 1] for hq_kv_attend; granted int32 [seqs], each length's change).
+
+    q_start counts what was asked for, so a sequence that got nothing has rows whose tokens are not cached: hq_kv_attend and
+    hq_kv_accept take its last held tokens for them unless it is given a length of 0, torch.where(granted > 0, lens, 0); the change that
+    hq_kv_accept returns for it is then left out, torch.where(granted > 0, change, 0)."""
     torch = _torch()
     if not table.is_cuda or table.dim() != 2:
         raise TypeError("table must be an int32 CUDA tensor [seqs][width]")
