@@ -60,15 +60,19 @@ def attend(c, large=False):
     T, cache = kv_reference.transform(c.orc, SEED), host(c.cache)
     lam_k, lam_v = (np.ones(D) if x is None else x.astype(np.float64) for x in c.lam)
     heads, hq_heads = cache.shape[1], c.q.shape[1]
-    ks = kv_reference.parts(cache, c.bits)[1].view(np.uint16)
     out, tol, at = np.zeros(c.q.shape), np.zeros(c.q.shape[:2]), 0
     for b, (n, see) in enumerate(zip(c.lens, c.sees)):
         m = len(see)
+        # the sequence's pages alone
+        row = c.table[b, :-(-n // c.page)]
+        named = (row >= 0) & (row < len(cache))
+        pages = cache[np.where(named, row, 0)]
+        row = np.where(named, np.arange(len(row)), -1)
+        ks = kv_reference.parts(pages, c.bits)[1].view(np.uint16)
         for a in range(heads if m else 0):
-            k, v, there = kv_reference.coordinates(cache, c.bits, c.table[b], n, a, lam_k, lam_v)
+            k, v, there = kv_reference.coordinates(pages, c.bits, row, n, a, lam_k, lam_v)
             t = np.arange(n)
-            page = np.where(there, c.table[b][t // c.page], 0)
-            there = there & (ks[page, a, t % c.page, 0] != 0x8000)
+            there = there & (ks[t // c.page, a, t % c.page, 0] != 0x8000)
             k, v, w = k[there], v[there], see[:, there]
             for j in range(a * hq_heads // heads, (a + 1) * hq_heads // heads):
                 y = c.q[at:at + m, j].astype(np.float64) @ T.T * c.kw["scale"]
