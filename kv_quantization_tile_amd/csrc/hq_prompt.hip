@@ -45,6 +45,7 @@ constexpr float kPromptLowest = -3.402823466e38f;    // the reference before the
 constexpr int kPromptTok = 64;                       // tokens of a step
 constexpr int64_t kPromptStride = 1 << 23;            // K's and V's rows are nearer than this, in values
 constexpr uint32_t kPromptTile = kPromptTok * 256u;  // their bytes, K or V
+constexpr uint32_t kPromptMany = 64;                 // tiles of more sequences than this go by place
 
 struct PromptArgs {
   const uint16_t *q, *k, *v;
@@ -54,6 +55,7 @@ struct PromptArgs {
   uint64_t total;
   uint32_t heads, group, q_heads, seqs, window;
   uint32_t group_mul, group_shift;
+  int by_place;  // workgroups take their tiles by place_of, not find_tile
   int causal, out_f32;
   uint32_t flip;  // of pairs of a query's values: their signs, for a scale below 0
   float scale_log2, cap_in, cap_out;
@@ -80,7 +82,7 @@ __device__ __forceinline__ uint32_t wave_sum(uint32_t x) {
                     __builtin_amdgcn_readlane((int)x, 63));
 }
 
-// The tile with the index-th most work, by the wavefront: tiles later in a sequence see more tokens, so of all
+// The tile with the index-th most work, by the wavefront, of few sequences (each look walks all of them): tiles later in a sequence see more tokens, so of all
 // sequences' tiles those of one place in their sequence form a level, the last levels first.  False if there are
 // not so many tiles.  `tile`: its place in the sequence.
 template <int ROWS>
@@ -129,6 +131,31 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, uint32_t index, u
   return false;
 }
 
+// The tile of the index-th place, by the wavefront, of many sequences.  A sequence of n rows from row s has places from
+// floor(s / ROWS) + b on (rows of all the group's heads): as ceil(y) <= floor(x + y) - floor(x) + 1, they suffice and no two
+// sequences share one.  The sequence is found among 64 offsets a look, and its last tile goes first.  False if the place has no tile.
+template <int ROWS>
+__device__ __forceinline__ bool place_of(const PromptArgs& a, uint32_t index, uint32_t* seq, uint32_t* tile) {
+  const uint32_t lane = threadIdx.x & 63u;
+  uint32_t lo = 0, count = a.seqs, first;  // the last sequence that starts at or before `index` is one of `count` from lo on
+  while (count > 1u) {
+    const uint32_t stride = (count + 63u) / 64u, at = lane * stride;
+    bool before = false;
+    if (at < count) {
+      prompt_rows(a, lo + at, &first);
+      before = first * a.group / ROWS + lo + at <= index;
+    }
+    const uint64_t votes = __builtin_amdgcn_ballot_w64(before);
+    const uint32_t k = votes ? 63u - (uint32_t)__builtin_clzll(votes) : 0u;
+    lo += k * stride;
+    count = count - k * stride < stride ? count - k * stride : stride;
+  }
+  const uint32_t tiles = (prompt_rows(a, lo, &first) * a.group + ROWS - 1u) / ROWS, place = index - (first * a.group / ROWS + lo);
+  *seq = lo;
+  *tile = tiles - 1u - place;
+  return place < tiles;  // unsigned: not before the sequence's first place either
+}
+
 __device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
 }
@@ -166,7 +193,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
   const uint32_t lane = threadIdx.x & 63u, wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), n32 = lane & 31u, half = lane >> 5;
   const uint32_t head = blockIdx.x % a.heads;
   uint32_t b, place;
-  if (!find_tile<(int)kRows>(a, blockIdx.x / a.heads, &b, &place)) return;
+  if (a.by_place ? !place_of<(int)kRows>(a, blockIdx.x / a.heads, &b, &place) : !find_tile<(int)kRows>(a, blockIdx.x / a.heads, &b, &place)) return;
   uint32_t first;
   const uint32_t n = prompt_rows(a, b, &first), rows = n * a.group, r0 = place * kRows, w0 = r0 + 32u * wave;
   // tokens from `lo` to `hi` that some of the tile's rows see, in steps; those that all of the wavefront's see
@@ -472,7 +499,7 @@ extern "C" int hq_attend_prompt(const hq_attend_prompt_args* g, hq_stream_t stre
   if (!g || g->heads == 0 || g->q_heads == 0 || g->q_heads % g->heads || g->q_heads > 65535u) return HQ_ERR_INVALID_ARG;
   if (g->dtype != HQ_BF16 || (g->out_dtype != HQ_F32 && g->out_dtype != HQ_BF16)) return HQ_ERR_INVALID_ARG;
   if (g->rows > (1ull << 30) || g->rows * g->q_heads > (1ull << 28)) return HQ_ERR_INVALID_ARG;
-  // find_tile's index of a sequence goes up to 127 past the last one
+  // an index of a sequence goes up to 127 past the last one (find_tile)
   if (g->seqs > 0x7FFFFFFFu) return HQ_ERR_INVALID_ARG;
   if (!(std::fabs(g->scale) <= 0x1p126f)) return HQ_ERR_INVALID_ARG;
   if (g->softcap != 0.0f && !(g->softcap >= 0x1p-125f && g->softcap <= 0x1p125f)) return HQ_ERR_INVALID_ARG;
@@ -519,8 +546,14 @@ extern "C" int hq_attend_prompt(const hq_attend_prompt_args* g, hq_stream_t stre
   const bool plain = g->softcap <= kCapPlainMost;
   a.cap_in = g->softcap > 0.0f ? (float)std::fmin(2.0 * log2e * scale / g->softcap, 0x1p126) : 0.0f;  // 2 x log2 e of a raw score
   a.cap_out = (float)(g->softcap * log2e * (plain ? 2.0 : 1.0));
-  const uint64_t rows = g->rows * a.group, tiles = (rows + 127u * (uint64_t)(g->seqs < rows ? g->seqs : rows)) / 128u, grid = tiles * a.heads;
-  if (grid > kMaxThreads / 256u) return HQ_ERR_INVALID_ARG;
+  const uint64_t rows = g->rows * a.group, tiles = (rows + 127u * (uint64_t)(g->seqs < rows ? g->seqs : rows)) / 128u, most = kMaxThreads / 256u;
+  // Tiles by level or by place, us (8 heads, 4 query heads each): 64 prompts of 100 tokens 47 and 45, 65 51 and 41, 256 252 and 151, 1024
+  // 2315 and 593, 4096 32100 and 2473; 4096 of 8 tokens 6424 and 389; 100 of up to 2048 1893 and 1495; one of 8192 among 64 of 50
+  // 535 and 522, first or last.  A launch has no room for a place to each of 2^24 / heads sequences, mostly empty ones: they go by level.
+  const uint64_t places = rows / 128u + g->seqs;
+  a.by_place = g->seqs > kPromptMany && places * a.heads <= most;
+  const uint64_t grid = (a.by_place ? places : tiles) * a.heads;
+  if (grid > most) return HQ_ERR_INVALID_ARG;
   const hipStream_t on = static_cast<hipStream_t>(stream);
   const dim3 blocks((uint32_t)grid), block(256);
   if (g->softcap == 0.0f) hipLaunchKernelGGL((prompt_kernel<4, kCapNone>), blocks, block, 0, on, a);

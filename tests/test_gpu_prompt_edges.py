@@ -22,6 +22,39 @@ def test_thousands_of_sequences(seqs, most, long):
     check(inputs([int(n) for n in lens], heads=2, group=3), {})
 
 
+def test_more_sequences_than_a_launch_has_places():
+    """2^24 / heads sequences and more, of which few have tokens."""
+    say("case: prompt 270000 sequences, 64 heads")
+    lens = np.zeros(270000, int)
+    lens[[0, 1, 63, 64, 5000, 140000, 269998, 269999]] = [3, 1, 130, 2, 40, 65, 1, 7]
+    check(inputs([int(n) for n in lens], heads=64, group=1), {})
+
+
+def test_time_grows_with_the_sequences():
+    """16 times as many prompts of one token take about 16 times as long, not 256 times: 64 lies between."""
+    say("case: prompt, time of 1024 and 16384 sequences")
+
+    def time_of(seqs):
+        x = torch.randn(seqs, 48, 128, device="cuda").to(torch.bfloat16)
+        q, k, v = x[:, :32], x[:, 32:40], x[:, 40:]
+        start = torch.arange(seqs + 1, dtype=torch.int32, device="cuda")
+        out = hq.hq_attend_prompt(q, k, v, start)
+        # a row that sees itself alone
+        assert torch.equal(out, v.repeat_interleave(4, 1))
+        times = []
+        for _ in range(3):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(4):
+                hq.hq_attend_prompt(q, k, v, start, out=out)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    assert time_of(16384) < 64 * time_of(1024)
+
+
 def test_rows_past_32_bits():
     """Rows 8 MiB apart, 4.6 GB of each operand from first to last: what rows side by side give."""
     say("case: prompt, rows far apart")
