@@ -43,6 +43,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr float kPromptSlack = 6.0f;                 // the reference may lag the maximum by this much (log2)
 constexpr float kPromptLowest = -3.402823466e38f;    // the reference before the first score
 constexpr int kPromptTok = 64;                       // tokens of a step
+constexpr int kPromptWaves = 4;                      // wavefronts of a workgroup, 32 rows each
+constexpr uint32_t kPromptRows = 32u * kPromptWaves;
 constexpr int64_t kPromptStride = 1 << 23;            // K's and V's rows are nearer than this, in values
 constexpr uint32_t kPromptTile = kPromptTok * 256u;  // their bytes, K or V
 constexpr uint32_t kPromptMany = 64;                 // tiles of more sequences than this go by place
@@ -85,12 +87,11 @@ __device__ __forceinline__ uint32_t wave_sum(uint32_t x) {
 // The tile with the index-th most work, by the wavefront, of few sequences (each look walks all of them): tiles later in a sequence see more tokens, so of all
 // sequences' tiles those of one place in their sequence form a level, the last levels first.  False if there are
 // not so many tiles.  `tile`: its place in the sequence.
-template <int ROWS>
 __device__ __forceinline__ bool find_tile(const PromptArgs& a, uint32_t index, uint32_t* seq, uint32_t* tile) {
   const uint32_t lane = threadIdx.x & 63u;
   auto tiles_of = [&](uint32_t b) {
     uint32_t first;
-    return b < a.seqs ? (uint32_t)(((uint64_t)prompt_rows(a, b, &first) * a.group + ROWS - 1u) / ROWS) : 0u;
+    return b < a.seqs ? (uint32_t)(((uint64_t)prompt_rows(a, b, &first) * a.group + kPromptRows - 1u) / kPromptRows) : 0u;
   };
   const uint32_t mine = tiles_of(lane);
   if (a.seqs == 1) {
@@ -109,7 +110,7 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, uint32_t index, u
     return wave_sum(sum);
   };
   if (past(0) <= index) return false;
-  uint32_t lo = 0, hi = (uint32_t)((a.total * a.group + ROWS - 1u) / ROWS);  // past(lo) > index >= past(hi)
+  uint32_t lo = 0, hi = (uint32_t)((a.total * a.group + kPromptRows - 1u) / kPromptRows);  // past(lo) > index >= past(hi)
   while (hi - lo > 1u) {
     const uint32_t mid = lo + (hi - lo) / 2u;
     if (past(mid) > index) lo = mid;
@@ -132,9 +133,8 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, uint32_t index, u
 }
 
 // The tile of the index-th place, by the wavefront, of many sequences.  A sequence of n rows from row s has places from
-// floor(s / ROWS) + b on (rows of all the group's heads): as ceil(y) <= floor(x + y) - floor(x) + 1, they suffice and no two
+// floor(s / kPromptRows) + b on (rows of all the group's heads): as ceil(y) <= floor(x + y) - floor(x) + 1, they suffice and no two
 // sequences share one.  The sequence is found among 64 offsets a look, and its last tile goes first.  False if the place has no tile.
-template <int ROWS>
 __device__ __forceinline__ bool place_of(const PromptArgs& a, uint32_t index, uint32_t* seq, uint32_t* tile) {
   const uint32_t lane = threadIdx.x & 63u;
   uint32_t lo = 0, count = a.seqs, first;  // the last sequence that starts at or before `index` is one of `count` from lo on
@@ -143,14 +143,14 @@ __device__ __forceinline__ bool place_of(const PromptArgs& a, uint32_t index, ui
     bool before = false;
     if (at < count) {
       prompt_rows(a, lo + at, &first);
-      before = first * a.group / ROWS + lo + at <= index;
+      before = first * a.group / kPromptRows + lo + at <= index;
     }
     const uint64_t votes = __builtin_amdgcn_ballot_w64(before);
     const uint32_t k = votes ? 63u - (uint32_t)__builtin_clzll(votes) : 0u;
     lo += k * stride;
     count = count - k * stride < stride ? count - k * stride : stride;
   }
-  const uint32_t tiles = (prompt_rows(a, lo, &first) * a.group + ROWS - 1u) / ROWS, place = index - (first * a.group / ROWS + lo);
+  const uint32_t tiles = (prompt_rows(a, lo, &first) * a.group + kPromptRows - 1u) / kPromptRows, place = index - (first * a.group / kPromptRows + lo);
   *seq = lo;
   *tile = tiles - 1u - place;
   return place < tiles;  // unsigned: not before the sequence's first place either
@@ -185,17 +185,16 @@ constexpr int kSchedVector = 0x2, kSchedMatrix = 0x8, kSchedRead = 0x100, kSched
 // x is made here, and not moved to where it is used.
 __device__ __forceinline__ void keep(const bf16x8& x) { asm volatile("" ::"v"(x)); }
 
-template <int WAVES, int CAP>
-__global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
-  constexpr uint32_t kRows = 32u * WAVES;
+template <int CAP>
+__global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_kernel(PromptArgs a) {
   // arrays of their own: a read of one does not wait for loads into another
   __shared__ __align__(16) uint8_t s_k0[kPromptTile], s_k1[kPromptTile], s_v0[kPromptTile], s_v1[kPromptTile];
   const uint32_t lane = threadIdx.x & 63u, wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), n32 = lane & 31u, half = lane >> 5;
   const uint32_t head = blockIdx.x % a.heads;
   uint32_t b, place;
-  if (a.by_place ? !place_of<(int)kRows>(a, blockIdx.x / a.heads, &b, &place) : !find_tile<(int)kRows>(a, blockIdx.x / a.heads, &b, &place)) return;
+  if (a.by_place ? !place_of(a, blockIdx.x / a.heads, &b, &place) : !find_tile(a, blockIdx.x / a.heads, &b, &place)) return;
   uint32_t first;
-  const uint32_t n = prompt_rows(a, b, &first), rows = n * a.group, r0 = place * kRows, w0 = r0 + 32u * wave;
+  const uint32_t n = prompt_rows(a, b, &first), rows = n * a.group, r0 = place * kPromptRows, w0 = r0 + 32u * wave;
   // tokens from `lo` to `hi` that some of the tile's rows see, in steps; those that all of the wavefront's see
   const uint32_t last = rows - 1u;
   auto query = [&](uint32_t x) { return (int32_t)prompt_query(a, x < last ? x : last); };
@@ -203,14 +202,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a) {
     const int64_t x = (int64_t)i + 1 - (int64_t)a.window;
     return a.window && x > 0 ? (int32_t)x : 0;
   };
-  const int32_t lo = from(query(r0)) & ~(kPromptTok - 1), hi = a.causal ? query(r0 + kRows - 1u) + 1 : (int32_t)n;
+  const int32_t lo = from(query(r0)) & ~(kPromptTok - 1), hi = a.causal ? query(r0 + kPromptRows - 1u) + 1 : (int32_t)n;
   const int32_t all_lo = from(query(w0 + 31u)), all_hi = a.causal ? query(w0) + 1 : (int32_t)n;
   // those that all of the tile's rows see
-  const int32_t some_lo = from(query(r0 + kRows - 1u)), some_hi = a.causal ? query(r0) + 1 : (int32_t)n;
+  const int32_t some_lo = from(query(r0 + kPromptRows - 1u)), some_hi = a.causal ? query(r0) + 1 : (int32_t)n;
   const int32_t steps = (hi - lo + kPromptTok - 1) / kPromptTok;
 
   // global to LDS: 1024 bytes, four tokens, an instruction
-  constexpr int kLoads = 16 / WAVES;
+  constexpr int kLoads = 16 / kPromptWaves;
   const uint16_t* kbase = a.k + (int64_t)first * a.kt + (int64_t)head * a.kh;
   const uint16_t* vbase = a.v + (int64_t)first * a.vt + (int64_t)head * a.vh;
   auto load = [&](const uint16_t* base, uint32_t stride, bool keys, int32_t step, uint8_t* lds) __attribute__((always_inline)) {
@@ -546,18 +545,19 @@ extern "C" int hq_attend_prompt(const hq_attend_prompt_args* g, hq_stream_t stre
   const bool plain = g->softcap <= kCapPlainMost;
   a.cap_in = g->softcap > 0.0f ? (float)std::fmin(2.0 * log2e * scale / g->softcap, 0x1p126) : 0.0f;  // 2 x log2 e of a raw score
   a.cap_out = (float)(g->softcap * log2e * (plain ? 2.0 : 1.0));
-  const uint64_t rows = g->rows * a.group, tiles = (rows + 127u * (uint64_t)(g->seqs < rows ? g->seqs : rows)) / 128u, most = kMaxThreads / 256u;
+  const uint64_t rows = g->rows * a.group, some = g->seqs < rows ? g->seqs : rows;  // sequences with tokens, at most
+  const uint64_t tiles = (rows + (kPromptRows - 1u) * some) / kPromptRows, most = kMaxThreads / (64u * kPromptWaves);
   // Tiles by level or by place, us (8 heads, 4 query heads each): 64 prompts of 100 tokens 47 and 45, 65 51 and 41, 256 252 and 151, 1024
   // 2315 and 593, 4096 32100 and 2473; 4096 of 8 tokens 6424 and 389; 100 of up to 2048 1893 and 1495; one of 8192 among 64 of 50
   // 535 and 522, first or last.  A launch has no room for a place to each of 2^24 / heads sequences, mostly empty ones: they go by level.
-  const uint64_t places = rows / 128u + g->seqs;
+  const uint64_t places = rows / kPromptRows + g->seqs;
   a.by_place = g->seqs > kPromptMany && places * a.heads <= most;
   const uint64_t grid = (a.by_place ? places : tiles) * a.heads;
   if (grid > most) return HQ_ERR_INVALID_ARG;
   const hipStream_t on = static_cast<hipStream_t>(stream);
-  const dim3 blocks((uint32_t)grid), block(256);
-  if (g->softcap == 0.0f) hipLaunchKernelGGL((prompt_kernel<4, kCapNone>), blocks, block, 0, on, a);
-  else if (plain) hipLaunchKernelGGL((prompt_kernel<4, kCapPlain>), blocks, block, 0, on, a);
-  else hipLaunchKernelGGL((prompt_kernel<4, kCapExact>), blocks, block, 0, on, a);
+  const dim3 blocks((uint32_t)grid), block(64 * kPromptWaves);
+  if (g->softcap == 0.0f) hipLaunchKernelGGL((prompt_kernel<kCapNone>), blocks, block, 0, on, a);
+  else if (plain) hipLaunchKernelGGL((prompt_kernel<kCapPlain>), blocks, block, 0, on, a);
+  else hipLaunchKernelGGL((prompt_kernel<kCapExact>), blocks, block, 0, on, a);
   return hipGetLastError() == hipSuccess ? HQ_OK : HQ_ERR_HIP;
 }
