@@ -384,7 +384,7 @@ int hq_kv_attend(const hq_kv_cache *cache, const hq_kv_attend_args *args, void *
  * draft follows; a value that is not in [0, i) means that it follows the n - m tokens held before the drafts.  Query i
  * sees those and, of the drafts, its own and its ancestors; with window > 0 only the last `window` of what it sees.
  * args->causal must not be 0 and args->weights must be NULL (a rejected draft's weights could not be taken back);
- * args->max_q is at most 256.  The workspace is hq_kv_attend's kind, of its own size.  Errors as hq_kv_attend. */
+ * args->max_q is at most 256; the launch is sized for sequences of that many drafts, so the most that there are is best.  The workspace is hq_kv_attend's kind, of its own size.  Errors as hq_kv_attend. */
 int hq_kv_attend_tree_workspace_size(const hq_kv_cache *cache, const hq_kv_attend_args *args, size_t *bytes);
 int hq_kv_attend_tree(const hq_kv_cache *cache, const hq_kv_attend_args *args, const int32_t *parents,
                       void *workspace, size_t workspace_bytes, hq_stream_t stream);
@@ -447,7 +447,7 @@ int hq_kv_accept(const hq_kv_cache *cache, const hq_kv_accept_args *args, hq_str
  * i.  Scores are scale q.k, then softcap tanh(score / softcap) when softcap > 0.  Query head j reads KV head
  * j / (q_heads / heads).  Types: bf16; 128 values a head.  Products are bf16 x bf16 into binary32; the softmax's
  * weights enter the second one as bf16, each off by at most 2^-8 of itself; scores, maxima, sums and outputs are
- * binary32.  A value that a row does not see does not reach it, whatever it holds. */
+ * binary32, and a capped score is off by up to 2^-21 of softcap more.  A value that a row does not see does not reach it, whatever it holds. */
 typedef struct {
   const void *q, *k, *v;     /* DEVICE, 16-byte aligned: value c of head j of row i at q[i q_stride[0] + j q_stride[1] + c] */
   void *out;                 /* DEVICE, [rows][q_heads][128], 16-byte aligned                       */

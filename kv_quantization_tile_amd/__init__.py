@@ -529,8 +529,9 @@ def hq_kv_attend(cache, q, table, lens, q_start=None, max_q=None, max_len=None, 
 
     parents int32 [queries] makes the queries a tree of drafted tokens, a sequence's last cached ones (C: hq_kv_attend_tree): draft
     parents[i] of the sequence comes before draft i, -1 for one that follows the held tokens.  A draft sees the held tokens, its
-    ancestors and itself, and with a window the last `window` of those.  At most 256 drafts of a sequence are computed (more
-    are refused where q_start is None and max_q does not say fewer); no weights."""
+    ancestors and itself, and with a window the last `window` of those.  max_q should be the most drafts of a sequence, as
+    the launch is sized for it (16 sequences of 16 drafts on 8192 tokens: 96 us with 16, 364 us without).  At most 256 are computed
+    (more are refused where q_start is None and max_q does not say fewer); no weights."""
     torch = _torch()
     c, keep = _cache_arg(cache, bits, seed, lam_k, lam_v)
     dev = cache.device
@@ -671,7 +672,8 @@ _Strides2 = ctypes.c_int64 * 2
 def hq_attend_prompt(q, k, v, start, scale=None, causal: bool = True, window: int = 0, softcap: float = 0.0, out=None, stream=None):
     """Softmax attention within packed prompts: q [rows][q heads][128], k and v [rows][heads][128], bf16, rows 16-byte aligned (any
     strides that are multiples of 8 values); sequence b is rows start[b] .. start[b + 1] - 1 (int32 [seqs + 1]).  Masks, scale and cap as
-    hq_kv_attend's, whose form on the cache a later step uses.  Returns out ([rows][q heads][128], bf16 unless given)."""
+    hq_kv_attend's, whose form on the cache a later step uses.  For inference: no gradient passes through the call.  Returns out ([rows][q
+    heads][128], bf16 unless given; rows that no sequence names are not written)."""
     torch = _torch()
     if not q.is_cuda:
         raise TypeError("q must be a CUDA tensor")

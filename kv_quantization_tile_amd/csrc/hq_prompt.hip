@@ -22,7 +22,8 @@
 // One MI355X, 8 heads and 32 query heads: 16384 tokens 2.03 ms, 1080 TFLOP/s (a 16-bit product of 8192^3 reaches 1050 to 1165, and
 // the clock falls to 1.8 GHz under either); matrix instructions are under way half of the cycles, LDS reads a quarter.
 // Middling prompts lose to what a tile pays once (its place, Q, the first keys, the join of its halves, about 5 us of which the
-// other workgroup hides a part) and to the masked step at its end: 16 of up to 2048 tokens, 750 to 800 TFLOP/s.
+// other workgroup hides a part) and to the masked step at its end: 16 of up to 2048 tokens, 345 to 369 us on several cards, 730 to 780
+// TFLOP/s.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -165,7 +166,8 @@ enum { kCapNone = 0, kCapPlain = 1, kCapExact = 2 };
 constexpr float kCapPlainMost = 256.0f;
 // cap tanh(x) = cap - 2 cap / (e^2x + 1), of which the softmax does not see the constant: -1 / (e^2x + 1) is the score in units of
 // 2 cap.  It is off by 2^-22, the capped score by 2^-21 of the cap: 2^-13 at kCapPlainMost, a 32nd of a bf16 weight's
-// rounding.  Four operations where the exact form takes thirteen (2 x 4001 tokens, 28 heads, window 1024: 147 us against 180).
+// rounding.  Four operations where the exact form takes thirteen (2 x 4001 tokens, 28 heads, window 1024: 149 us, and 180 with the
+// exact form).
 __device__ __forceinline__ float cap_plain(float x2) { return __builtin_amdgcn_rcpf(-1.0f - __builtin_amdgcn_exp2f(x2)); }
 // A larger cap needs small scores to their own precision: 1 - 2 / (e^2x + 1) away from zero (it saturates by itself), the
 // odd series to x^5 below 2^-4 (the next term is below 2^-27 of x).

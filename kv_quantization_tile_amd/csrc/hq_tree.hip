@@ -79,7 +79,9 @@ __device__ __forceinline__ int32_t tree_lo(const AttendArgs& a, const Seq& s, ui
   return l < 0 ? 0 : l > 0x7FFFFFFF ? 0x7FFFFFFF : (int32_t)l;
 }
 
-// Whether a query sees token `tok`, which its tile sees; `lo` is the first held token it sees.
+// Whether a query sees token `tok`, which its tile sees; `lo` is the first held token it sees.  Without branches, here and where a score
+// is hidden by it: with short-circuit conditions around stores to single scores, scores were seen to stay unmasked in this compiler's
+// output (ROCm 7.2.0's clang at -O3; the same source masked them with a printf beside it).
 template <int QUERIES>
 __device__ __forceinline__ bool tree_sees(const Tree<QUERIES>& t, int32_t back, uint32_t query, int32_t lo, int32_t tok) {
   const uint32_t j = (uint32_t)(tok - back) & (kMaxTree - 1);
@@ -97,8 +99,8 @@ __device__ __forceinline__ TreeItem tree_item(const AttendArgs& a, const TreeArg
   return {item / g.splits / a.heads, item / g.splits % a.heads, item % g.splits, blockIdx.x / 8u % g.tiles};
 }
 
-// 32 rows on 32 x 4096 tokens: 56 us with the join, 201 MB at 3.6 TB/s; 26 rows on 64 ragged sequences of up to 2001 at 8 bits
-// 45 us.  A step of 32 tokens and 32 rows is about 560 vector instructions, 380 of them for the operands, which bound it where
+// 32 rows on 32 x 4096 tokens: 58 us with the join, 201 MB at 3.5 TB/s; 26 rows on 64 ragged sequences of up to 2001 at 8 bits
+// 46 us.  A step of 32 tokens and 32 rows is about 560 vector instructions, 380 of them for the operands, which bound it where
 // memory does not.  One sequence of 301 tokens takes 15 us: 2 until its codes are asked for, 3 for its rows, 1 for the
 // tree, 4 for three steps, 3 for the join and the way back.
 template <int BITS, int R>
@@ -394,7 +396,7 @@ struct TreeStage {
   f16x8 v[kAttWaves / 2][8][64];  // [32 tokens][coordinate][lane]
 };
 
-// 64 drafts (256 rows) on 32768 tokens: 63 us, 545 TFLOP/s; 16 (64 rows) on 16 ragged sequences of up to 8192: 58 us, 390 TFLOP/s.
+// 64 drafts (256 rows) on 32768 tokens: 66 us, 520 TFLOP/s; 16 (64 rows) on 16 ragged sequences of up to 8192: 59 us, 385 TFLOP/s.
 // Matrix instructions take a fifth of the cycles and vector instructions a third: a turn of 64 tokens is a chain of loads,
 // operands, a barrier and products, which two to four workgroups a CU overlap in part, and starts and ends are 28 % of the launch.
 // R = 1 (up to 64 rows): one stage, four workgroups a CU.  R = 2: two stages, so that a turn has one barrier, and two workgroups.
@@ -423,7 +425,9 @@ __global__ __launch_bounds__(kAttBlock, R == 1 ? 4 : 2) void attend_tree_many_ke
   tree_range(a, s, r0, kRows, &lo, &hi);
   tree_range(a, s, w0, 16u * R, &wlo, &whi);
   tree_common(a, s, last, &all_lo, &all_hi);
-  if (w0 + 16u * R > rows) all_lo = all_hi = 0;  // rows that are not there see nothing
+  // Rows that are not there see nothing.  Such a wavefront takes the masked loop for every token, and the others wait for it: 60 drafts
+  // x 4 heads on 32768 tokens 107 us, 64 x 4 78; 15 x 4 on 16 x 8192 123, 16 x 4 86.
+  if (w0 + 16u * R > rows) all_lo = all_hi = 0;
   int32_t t0 = (lo & ~15) + (int32_t)(at.split * g.chunk), t1 = t0 + (int32_t)g.chunk;
   t1 = t1 < hi ? t1 : hi;
   if (a.pages == 0) t1 = t0;
@@ -541,7 +545,8 @@ __global__ __launch_bounds__(kAttBlock, R == 1 ? 4 : 2) void attend_tree_many_ke
     bool whole = false;
     {
       if (!cap && !flagged && t >= all_lo && t + kTok <= all_hi && t + kTok <= t1) {
-        // every row sees every token: each step's scores are under way during the softmax of the one before
+        // Every row sees every token: each step's scores are under way during the softmax of the one before.  Capped scores, a dozen
+        // vector instructions more each, take the loop below (64 drafts on 32768 tokens 108 us, 78 without a cap; here they were not tried).
         f32x4 sc[2][R][2];
         auto products = [&](int w, f32x4 (*x)[2]) __attribute__((always_inline)) {
 #pragma unroll
@@ -814,15 +819,25 @@ int plan_tree(const hq_kv_cache& c, const hq_kv_attend_args& g, TreePlan* out) {
   p.rows = (uint32_t)rows;
   p.all = (uint32_t)all;
   const uint64_t seen = (uint64_t)g.window + p.max_q + 15, span = g.window && seen < g.max_len ? seen : g.max_len;
-  // Operands in registers, 32 rows a tile, up to 2^24 rows x tokens: LDS starts later and takes a launch for the rows.  8 heads,
-  // 4 query heads each, us in registers and in LDS: 64 drafts on 301 tokens 18 and 35, on 8192 (2^24) 40 and 44, on 16384 58 and
-  // 53, on 32768 92 and 74; 16 drafts on 8192 23 and 30; 32 on 16384 (2^24) 38 and 40, on 32768 55 and 50.
+  // Operands in registers, 32 rows a tile, up to 2^24 rows x tokens: LDS starts later and takes a launch for the rows.  us in
+  // registers and in LDS, 4 query heads a KV head, 4 bits unless said:
+  //   64 drafts, 8 heads, on 4096 tokens 32 and 40, on 8192 (2^24) 40 and 42, on 16384 57 and 51, on 32768 92 and 73; at 8 bits 33 and
+  //   41, 40 and 43, 57 and 52, 90 and 73; one head, on 32768 29 and 38, 65536 (2^24) 40 and 43, 131072 58 and 53
+  //   16 drafts of 16 sequences, 8 heads, on 1024 28 and 32, 2048 (2^24) 37 and 39, 4096 54 and 53, 8192 89 and 86; at 8 bits 28 and 35,
+  //   38 and 42, 54 and 57
+  //   16 drafts of 64 sequences on 256 34 and 33, 512 (2^24) 43 and 40, 1024 60 and 60, 2048 93 and 94
+  //   100 drafts of 16 sequences, 2 heads, on 1024 49 and 61, 2048 (2^24.6) 65 and 67, 4096 101 and 104
+  // It is off where rows are many and tokens few (64 drafts of 64 sequences, 8 heads, on 128 tokens (2^24) 113 and 80), and where 64-row
+  // tiles are half empty (9 drafts, 36 rows, of 64 sequences on 2048 93 and 114).
   p.tile_rows = rows <= 16 ? 16 : rows <= 32 || sh * rows * span <= 1ull << 24 ? 32 : rows <= 64 ? 64 : 128;
   p.tiles = rows ? (uint32_t)((rows + p.tile_rows - 1u) / p.tile_rows) : 1u;
   // Workgroups: about three rounds of up to 16 rows, as in hq_attend.hip; of more rows, whose starts cost more, as many as the chip
   // holds at once, and half as many again where four fit a CU (16 drafts on 16 x 8192 ragged tokens, 64 rows: 68 us at 1536, 79 at
   // 1024, 81 at 2048; 64 on 32768, 128 rows a tile: 73 at 512, 84 at 768; 13 on 64 x 2001, 32 rows: 43 at 512, 54 at 768).
-  // Splits count from the first token that a tile sees, of at least 512 tokens.
+  // Splits count from the first token that a tile sees, at most one for each 512 tokens begun; in whole 128 tokens, of 384 or more where
+  // there are several.
+  // Rows are counted by max_q: 16 sequences of 16 drafts on 8192 tokens take 96 us with 16 and 364 with 256 (tiles for rows that no
+  // sequence has, and no splits), one of 64 drafts among 15 of 4 342 with 64.
   const uint64_t items = sh * p.tiles, target = p.tile_rows == 16 ? 2048 : p.tile_rows == 64 ? 1536 : 512;
   uint64_t splits = items ? (target + items - 1) / items : 1;
   const uint64_t most = (span + 511) / 512;
