@@ -330,3 +330,51 @@ def test_steps_reference_agrees(orc):
         c = Case(orc, **kw)
         for x, y in zip(attend(c), ref.attend(orc, host(c.cache), c.q, c.table, c.lens, c.sees, c.bits, SEED, *c.lam, **c.kw)):
             assert np.allclose(x, y, rtol=1e-9, atol=1e-12)
+
+
+# ---- graphs, and calls at once ------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("name", [64, 128])
+def test_graphs_through_lds(orc, name):
+    """Captured with launches of their own for rows and joins, replayed on other queries, trees, lengths and pages."""
+    say(f"case: tree graph, {name} rows a tile")
+    kw, max_len, tile = shape(name, window=0)
+    c = Case(orc, **kw)
+    assert planned(c, max_len)[0] == tile
+    q, table, lens, parents, start = (dev(x) for x in (c.q, c.table, np.array(c.lens, np.int32), c.parents, c.start))
+    call = lambda: hq.hq_kv_attend(c.cache, q, table, lens, q_start=start, max_q=max(c.q_lens), max_len=max_len, parents=parents, **c.kw, **c.fmt)  # noqa: E731
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = call()
+    g = np.random.default_rng(2)
+    for i in range(4):
+        q.normal_()
+        parents.copy_(torch.tensor(sum((some_tree(g, m) for m in c.q_lens), []), dtype=torch.int32))
+        lens.copy_(torch.tensor([n - 37 * i for n in c.lens], dtype=torch.int32))
+        table.copy_(dev(c.table[::-1].copy() if i == 2 else c.table))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held, call())
+
+
+def test_calls_at_once(orc):
+    """Trees of every kernel and prompts on streams of their own, their launches among one another's, give what they give alone."""
+    say("case: trees and prompts on several streams")
+    cases = [(Case(orc, **shape(name)[0]), shape(name)[1]) for name in SHAPES]
+    rows = [torch.randn(n, 6, D, device="cuda").to(torch.bfloat16) for n in (700, 300)]
+    starts = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 100, 101, 700], list(range(0, 301, 3)))]
+    calls = [lambda s, c=c, n=n: c.run(max_len=n, stream=s) for c, n in cases]
+    calls += [lambda s, x=x, st=st: hq.hq_attend_prompt(x[:, :4], x[:, 4:5], x[:, 5:], st, stream=s) for x, st in zip(rows, starts)]
+    want = [f(None) for f in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for f, s in zip(calls, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):  # the case's own buffers too
+                got.append(f(s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

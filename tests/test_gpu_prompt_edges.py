@@ -30,6 +30,29 @@ def test_more_sequences_than_a_launch_has_places():
     check(inputs([int(n) for n in lens], heads=64, group=1), {})
 
 
+@pytest.mark.parametrize("seqs", [64, 65, 300])
+def test_offsets_of_many_sequences(seqs):
+    """Rows before the first offset, behind the last and of no sequence stay as they were; offsets are cut to the rows there are; empty
+    sequences at either end."""
+    say(f"case: prompt offsets of {seqs} sequences")
+    g = np.random.default_rng(seqs)
+    lens = g.integers(0, 9, seqs)
+    lens[[0, 1, seqs - 1]], lens[seqs // 2] = 0, 200
+    q, k, v, _ = inputs([int(lens.sum()) + 50], heads=2, group=2)
+    for first, clamp in ((0, False), (13, False), (50, False), (0, True)):
+        start = (first + np.concatenate([[0], np.cumsum(lens)])).astype(np.int32)
+        if clamp:  # what lies outside the rows is none
+            start[:2], start[-2:] = (-1 << 31, -7), (q.shape[0], (1 << 31) - 1)
+        out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+        hq.hq_attend_prompt(q, k, v, torch.from_numpy(start).cuda(), out=out)
+        lo, hi = np.clip(start[[0, -1]], 0, q.shape[0])
+        assert torch.isnan(out[:lo]).all() and torch.isnan(out[hi:]).all()
+        for a, b in zip(start.clip(0, q.shape[0])[:-1], start.clip(0, q.shape[0])[1:]):
+            if a < b:
+                one = hq.hq_attend_prompt(q[a:b], k[a:b], v[a:b], torch.tensor([0, b - a], dtype=torch.int32, device="cuda"))
+                assert torch.equal(out[a:b], one)
+
+
 def test_time_grows_with_the_sequences():
     """16 times as many prompts of one token take about 16 times as long, not 256 times: 64 lies between."""
     say("case: prompt, time of 1024 and 16384 sequences")
